@@ -10,6 +10,9 @@ vLLM MiniMax-M3 sparse attention pages and TensorRT-LLM PR #17171 describe it:
                    request, cu_seqlens_q)
   combine()        merge of split-K partials
   decode_step()    the three stages back to back on one stream
+  append_kv()      the step before: new keys and values rotated, quantised and
+                   written to the paged cache, the query rotated
+                   (append_kv_prefill() for prefill batches)
 
 Every function here only checks and marshals torch tensors into the C ABI of
 libmsa.so (include/msa.h); all arithmetic runs in that library's CUDA kernels.
@@ -18,7 +21,10 @@ There is no CPU fallback: if the library is missing, calls raise.
 Tensor layouts (see include/msa.h): q bf16 [T, Hq, 128] with T = B * qlen
 request-major; kv fp8 e4m3 [num_blocks, Hkv, 128, 256] (K bytes 0..127, V bytes
 128..255), given as uint8 or float8_e4m3fn; block_table int32 [B, S];
-seq_lens int32 [B]; scores fp32 [Hkv, T, S]; topk int32 [T, Hkv, 16].
+seq_lens int32 [B]; scores fp32 [Hkv, T, S]; topk int32 [T, Hkv, 16].  Every
+function that reads the cache takes kv_scales=, page scales fp32 [num_blocks,
+Hkv, 2] (a page's K and V factor per KV head, as append_kv keeps them), which
+multiply k_scale and v_scale (msa_*_scaled).
 """
 from __future__ import annotations
 
@@ -39,7 +45,7 @@ MAX_QLEN = 32
 
 __all__ = ["score", "topk", "sparse_decode", "sparse_decode_select", "sparse_prefill",
            "sparse_prefill_select", "dense_decode", "dense_splits",
-           "combine", "decode_step",
+           "combine", "decode_step", "append_kv", "append_kv_prefill",
            "fused_selection", "FUSED_MAX_BLOCKS", "workspace_bytes",
            "choose_splits", "get_error", "set_input_overlap", "set_union_tile", "DecodeBuffers",
            "MSAError"]
@@ -116,11 +122,21 @@ def _fp8(q, q_scale: float) -> bool:
     return True
 
 
+def _page_scales(kv_scales, name: str, dev, num_blocks: int, num_kv_heads: int, sides: int):
+    """Checks page scales fp32 [num_blocks, Hkv, sides] and returns their address."""
+    _need(kv_scales, name, (torch.float32,), dev)
+    if tuple(kv_scales.shape) != (num_blocks, num_kv_heads, sides):
+        raise ValueError(f"{name} must be [num_blocks, Hkv, {sides}]")
+    return kv_scales.data_ptr()
+
+
 def score(q, kv, block_table, seq_lens, qlen: int, sm_scale: float, k_scale: float = 1.0,
-          scores: torch.Tensor | None = None, stream=None, q_scale: float = 1.0) -> torch.Tensor:
+          scores: torch.Tensor | None = None, stream=None, q_scale: float = 1.0,
+          kv_scales: torch.Tensor | None = None) -> torch.Tensor:
     """Block scores fp32 [Hkv, T, S] (msa_score; msa_score_q8 for an fp8 q of
     value q * q_scale).  `kv` may be the packed K|V cache [NB, Hkv, 128, 256]
-    or a K-only (index-K) cache [NB, Hkv, 128, 128] (msa_score_kcache)."""
+    or a K-only (index-K) cache [NB, Hkv, 128, 128] (msa_score_kcache).
+    kv_scales: page scales [NB, Hkv, 2] ([NB, Hkv, 1] of a K-only cache)."""
     dev, B, S, Hq, Hkv, NB = _geometry(q, kv, block_table, seq_lens, qlen, k_only_ok=True)
     if scores is None:
         scores = torch.empty((Hkv, B * qlen, S), dtype=torch.float32, device=dev)
@@ -130,7 +146,11 @@ def score(q, kv, block_table, seq_lens, qlen: int, sm_scale: float, k_scale: flo
     args = (kv.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), scores.data_ptr(), B, qlen,
             Hq, Hkv, S, NB, float(sm_scale), float(k_scale), _stream(dev, stream))
     k_only = kv.shape[3] == HEAD_DIM
-    if _fp8(q, q_scale):
+    if kv_scales is not None:
+        sc = _page_scales(kv_scales, "kv_scales", dev, NB, Hkv, 1 if k_only else 2)
+        st = _lib().msa_score_scaled(q.data_ptr(), float(q_scale) if _fp8(q, q_scale) else 0.0,
+                                     args[0], sc, int(k_only), *args[1:])
+    elif _fp8(q, q_scale):
         f = _lib().msa_score_kcache_q8 if k_only else _lib().msa_score_q8
         st = f(q.data_ptr(), float(q_scale), *args)
     else:
@@ -165,9 +185,11 @@ def topk(scores: torch.Tensor, seq_lens: torch.Tensor, qlen: int, k: int = TOPK,
 def sparse_decode(q, kv, block_table, seq_lens, topk_idx, qlen: int, sm_scale: float,
                   k_scale: float = 1.0, v_scale: float = 1.0, out: torch.Tensor | None = None,
                   num_splits: int = 0, workspace: torch.Tensor | None = None,
-                  stream=None, q_scale: float = 1.0) -> torch.Tensor:
+                  stream=None, q_scale: float = 1.0,
+                  kv_scales: torch.Tensor | None = None) -> torch.Tensor:
     """Attention over the selected pages, bf16 [T, Hq, 128] (msa_sparse_decode;
-    with more than one split the merge runs on the same stream)."""
+    with more than one split the merge runs on the same stream).  kv_scales:
+    page scales [NB, Hkv, 2]."""
     dev, B, S, Hq, Hkv, NB = _geometry(q, kv, block_table, seq_lens, qlen)
     _need(topk_idx, "topk", (torch.int32,), dev)
     if tuple(topk_idx.shape) != (B * qlen, Hkv, TOPK):
@@ -184,7 +206,11 @@ def sparse_decode(q, kv, block_table, seq_lens, topk_idx, qlen: int, sm_scale: f
     args = (kv.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), topk_idx.data_ptr(), ws_ptr,
             ws_bytes, out.data_ptr(), B, qlen, Hq, Hkv, S, NB, float(sm_scale), float(k_scale),
             float(v_scale), splits, _stream(dev, stream))
-    if _fp8(q, q_scale):
+    if kv_scales is not None:
+        sc = _page_scales(kv_scales, "kv_scales", dev, NB, Hkv, 2)
+        st = _lib().msa_sparse_decode_scaled(
+            q.data_ptr(), float(q_scale) if _fp8(q, q_scale) else 0.0, args[0], sc, *args[1:])
+    elif _fp8(q, q_scale):
         st = _lib().msa_sparse_decode_q8(q.data_ptr(), float(q_scale), *args)
     else:
         st = _lib().msa_sparse_decode(q.data_ptr(), *args)
@@ -201,9 +227,10 @@ def dense_splits(stride: int) -> int:
 def dense_decode(q, kv, block_table, seq_lens, qlen: int, sm_scale: float, k_scale: float = 1.0,
                  v_scale: float = 1.0, out: torch.Tensor | None = None,
                  workspace: torch.Tensor | None = None, stream=None,
-                 q_scale: float = 1.0) -> torch.Tensor:
+                 q_scale: float = 1.0, kv_scales: torch.Tensor | None = None) -> torch.Tensor:
     """Attention over every visible block, bf16 [T, Hq, 128] (msa_dense_decode;
-    with more than one split the merge runs on the same stream)."""
+    with more than one split the merge runs on the same stream).  kv_scales:
+    page scales [NB, Hkv, 2]."""
     dev, B, S, Hq, Hkv, NB = _geometry(q, kv, block_table, seq_lens, qlen)
     if out is None:
         out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
@@ -219,7 +246,11 @@ def dense_decode(q, kv, block_table, seq_lens, qlen: int, sm_scale: float, k_sca
     args = (kv.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), ws_ptr, ws_bytes,
             out.data_ptr(), B, qlen, Hq, Hkv, S, NB, float(sm_scale), float(k_scale),
             float(v_scale), _stream(dev, stream))
-    if _fp8(q, q_scale):
+    if kv_scales is not None:
+        sc = _page_scales(kv_scales, "kv_scales", dev, NB, Hkv, 2)
+        st = _lib().msa_dense_decode_scaled(
+            q.data_ptr(), float(q_scale) if _fp8(q, q_scale) else 0.0, args[0], sc, *args[1:])
+    elif _fp8(q, q_scale):
         st = _lib().msa_dense_decode_q8(q.data_ptr(), float(q_scale), *args)
     else:
         st = _lib().msa_dense_decode(q.data_ptr(), *args)
@@ -243,10 +274,12 @@ def sparse_decode_select(q, kv, block_table, seq_lens, scores, qlen: int, sm_sca
                          k_scale: float = 1.0, v_scale: float = 1.0,
                          topk_out: torch.Tensor | None = None, out: torch.Tensor | None = None,
                          num_splits: int = 0, workspace: torch.Tensor | None = None,
-                         stream=None, q_scale: float = 1.0):
+                         stream=None, q_scale: float = 1.0,
+                         kv_scales: torch.Tensor | None = None):
     """Selection and attention in one kernel (msa_sparse_decode_select): the
     top-16 blocks of every (token, KV head) row are selected from `scores`
-    (any strides, as msa_topk) and attended.  Returns (topk [T, Hkv, 16], out)."""
+    (any strides, as msa_topk) and attended.  kv_scales: page scales [NB, Hkv,
+    2].  Returns (topk [T, Hkv, 16], out)."""
     dev, B, S, Hq, Hkv, NB = _geometry(q, kv, block_table, seq_lens, qlen)
     # any strided view, as for topk()
     if not (isinstance(scores, torch.Tensor) and scores.is_cuda and scores.dtype == torch.float32
@@ -271,7 +304,11 @@ def sparse_decode_select(q, kv, block_table, seq_lens, scores, qlen: int, sm_sca
     args = (kv.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), scores.data_ptr(), sh, st,
             sn, topk_out.data_ptr(), ws_ptr, ws_bytes, out.data_ptr(), B, qlen, Hq, Hkv, S, NB,
             float(sm_scale), float(k_scale), float(v_scale), splits, _stream(dev, stream))
-    if _fp8(q, q_scale):
+    if kv_scales is not None:
+        psc = _page_scales(kv_scales, "kv_scales", dev, NB, Hkv, 2)
+        status = _lib().msa_sparse_decode_select_scaled(
+            q.data_ptr(), float(q_scale) if _fp8(q, q_scale) else 0.0, args[0], psc, *args[1:])
+    elif _fp8(q, q_scale):
         status = _lib().msa_sparse_decode_select_q8(q.data_ptr(), float(q_scale), *args)
     else:
         status = _lib().msa_sparse_decode_select(q.data_ptr(), *args)
@@ -303,11 +340,13 @@ def _prefill_splits(T: int, Hq: int, Hkv: int, num_splits: int, workspace, dev):
 def sparse_prefill(q, kv, block_table, seq_lens, cu_seqlens_q, topk_idx, sm_scale: float,
                    k_scale: float = 1.0, v_scale: float = 1.0, out: torch.Tensor | None = None,
                    num_splits: int = 0, workspace: torch.Tensor | None = None, stream=None,
-                   q_scale: float = 1.0) -> torch.Tensor:
+                   q_scale: float = 1.0,
+                   kv_scales: torch.Tensor | None = None) -> torch.Tensor:
     """Sparse attend of a prefill or chunked-prefill batch (msa_sparse_prefill):
     request b's query tokens are q[cu_seqlens_q[b] : cu_seqlens_q[b + 1]], the
     last ones of its seq_lens[b]; each token attends its own list
-    topk_idx [T, Hkv, 16].  Returns bf16 [T, Hq, 128]."""
+    topk_idx [T, Hkv, 16].  kv_scales: page scales [NB, Hkv, 2].  Returns bf16
+    [T, Hq, 128]."""
     dev, B, T, S, Hq, Hkv, NB = _prefill_geometry(q, kv, block_table, seq_lens, cu_seqlens_q)
     _need(topk_idx, "topk", (torch.int32,), dev)
     if tuple(topk_idx.shape) != (T, Hkv, TOPK):
@@ -319,7 +358,11 @@ def sparse_prefill(q, kv, block_table, seq_lens, cu_seqlens_q, topk_idx, sm_scal
     args = (kv.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), cu_seqlens_q.data_ptr(),
             topk_idx.data_ptr(), ws_ptr, ws_bytes, out.data_ptr(), B, T, Hq, Hkv, S, NB,
             float(sm_scale), float(k_scale), float(v_scale), splits, _stream(dev, stream))
-    if _fp8(q, q_scale):
+    if kv_scales is not None:
+        sc = _page_scales(kv_scales, "kv_scales", dev, NB, Hkv, 2)
+        st = _lib().msa_sparse_prefill_scaled(
+            q.data_ptr(), float(q_scale) if _fp8(q, q_scale) else 0.0, args[0], sc, *args[1:])
+    elif _fp8(q, q_scale):
         st = _lib().msa_sparse_prefill_q8(q.data_ptr(), float(q_scale), *args)
     else:
         st = _lib().msa_sparse_prefill(q.data_ptr(), *args)
@@ -331,10 +374,12 @@ def sparse_prefill_select(q, kv, block_table, seq_lens, cu_seqlens_q, scores, sm
                           k_scale: float = 1.0, v_scale: float = 1.0,
                           topk_out: torch.Tensor | None = None, out: torch.Tensor | None = None,
                           num_splits: int = 0, workspace: torch.Tensor | None = None,
-                          stream=None, q_scale: float = 1.0):
+                          stream=None, q_scale: float = 1.0,
+                          kv_scales: torch.Tensor | None = None):
     """Per-token causal top-16 selected from `scores` [Hkv, T, >= S] (any
     strides) and attended, for a prefill-style batch
-    (msa_sparse_prefill_select).  Returns (topk [T, Hkv, 16], out)."""
+    (msa_sparse_prefill_select).  kv_scales: page scales [NB, Hkv, 2].  Returns
+    (topk [T, Hkv, 16], out)."""
     dev, B, T, S, Hq, Hkv, NB = _prefill_geometry(q, kv, block_table, seq_lens, cu_seqlens_q)
     if not (isinstance(scores, torch.Tensor) and scores.is_cuda and scores.dtype == torch.float32
             and scores.device == dev):
@@ -354,7 +399,11 @@ def sparse_prefill_select(q, kv, block_table, seq_lens, cu_seqlens_q, scores, sm
             scores.data_ptr(), sh, st, sn, topk_out.data_ptr(), ws_ptr, ws_bytes, out.data_ptr(),
             B, T, Hq, Hkv, S, NB, float(sm_scale), float(k_scale), float(v_scale), splits,
             _stream(dev, stream))
-    if _fp8(q, q_scale):
+    if kv_scales is not None:
+        psc = _page_scales(kv_scales, "kv_scales", dev, NB, Hkv, 2)
+        status = _lib().msa_sparse_prefill_select_scaled(
+            q.data_ptr(), float(q_scale) if _fp8(q, q_scale) else 0.0, args[0], psc, *args[1:])
+    elif _fp8(q, q_scale):
         status = _lib().msa_sparse_prefill_select_q8(q.data_ptr(), float(q_scale), *args)
     else:
         status = _lib().msa_sparse_prefill_select(q.data_ptr(), *args)
@@ -404,14 +453,17 @@ class DecodeBuffers:
 def decode_step(q, kv, block_table, seq_lens, qlen: int, sm_scale: float, k_scale: float = 1.0,
                 v_scale: float = 1.0, buffers: DecodeBuffers | None = None, stream=None,
                 q_scale: float = 1.0, index_k: torch.Tensor | None = None,
-                index_k_scale: float | None = None):
+                index_k_scale: float | None = None, kv_scales: torch.Tensor | None = None,
+                index_scales: torch.Tensor | None = None):
     """One decode step in one library call (msa_decode_step): score, then
     selection + attention on one stream, no host sync -- in one kernel
     (msa_sparse_decode_select) while rows have at most FUSED_MAX_BLOCKS
     candidate blocks, else msa_topk then msa_sparse_decode (-> combine when
     split).  With `index_k` (a K-only cache [NB, Hkv, 128, 128] on the same
     block table, scale index_k_scale, default k_scale) the blocks are scored
-    on it instead of kv's K halves.  Returns (scores, topk, out)."""
+    on it instead of kv's K halves.  kv_scales: page scales [NB, Hkv, 2] of kv,
+    with index_scales [NB, Hkv, 1] those of index_k (msa_decode_step_scaled).
+    Returns (scores, topk, out)."""
     dev, B, S, Hq, Hkv, NB = _geometry(q, kv, block_table, seq_lens, qlen)
     if buffers is None:
         buffers = DecodeBuffers.allocate(B, qlen, Hq, Hkv, S, dev)
@@ -432,14 +484,135 @@ def decode_step(q, kv, block_table, seq_lens, qlen: int, sm_scale: float, k_scal
     ws_bytes = ws.numel() * ws.element_size() if ws is not None else 0
     fp8 = _fp8(q, q_scale)
     ik_scale = (k_scale if index_k_scale is None else index_k_scale) if index_k is not None else 0.0
-    st = _lib().msa_decode_step(
-        q.data_ptr(), float(q_scale) if fp8 else 0.0, kv.data_ptr(),
-        index_k.data_ptr() if index_k is not None else None, float(ik_scale),
+    if index_scales is not None and (index_k is None or kv_scales is None):
+        raise ValueError("index_scales go with index_k and kv_scales")
+    head = (q.data_ptr(), float(q_scale) if fp8 else 0.0, kv.data_ptr())
+    index = (index_k.data_ptr() if index_k is not None else None, float(ik_scale))
+    if kv_scales is not None:
+        f = _lib().msa_decode_step_scaled
+        head += (_page_scales(kv_scales, "kv_scales", dev, NB, Hkv, 2),)
+        index += (None if index_scales is None else
+                  _page_scales(index_scales, "index_scales", dev, NB, Hkv, 1),)
+    else:
+        f = _lib().msa_decode_step
+    st = f(
+        *head, *index,
         block_table.data_ptr(), seq_lens.data_ptr(), bf.scores.data_ptr(), bf.topk.data_ptr(),
         ws_ptr, ws_bytes, bf.out.data_ptr(), B, qlen, Hq, Hkv, S, NB, float(sm_scale),
         float(k_scale), float(v_scale), bf.num_splits, _stream(dev, stream))
     _native.check(st, "msa_decode_step")
     return bf.scores, bf.topk, bf.out
+
+
+def _rows(t, name: str, heads: int, tokens: int, dev):
+    """Checks bf16 rows [T, heads, 128] whose heads lie one behind the other and
+    returns the tokens' distance in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+    if t.dim() != 3 or t.shape[0] != tokens or t.shape[1] != heads or t.shape[2] != HEAD_DIM:
+        raise ValueError(f"{name} must be [{tokens}, {heads}, 128]")
+    st, sh, sd = t.stride()
+    if sd != 1 or (heads > 1 and sh != HEAD_DIM):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    if tokens <= 1:
+        return heads * HEAD_DIM
+    if st % 8 or st < heads * HEAD_DIM:
+        raise ValueError(f"{name}: tokens must be a multiple of 8 elements apart and not overlap")
+    return st
+
+
+def _append(fn, k, v, kv, block_table, seq_lens, tokens, cu, qlen, k_scale, v_scale, kv_scales,
+            cos_sin, interleaved, q, q_out, q_scale, stream):
+    _need(kv, "kv", _KV_DTYPES)
+    dev = kv.device
+    _need(block_table, "block_table", (torch.int32,), dev)
+    _need(seq_lens, "seq_lens", (torch.int32,), dev)
+    sides = 1 if v is None else 2
+    if kv.dim() != 4 or kv.shape[2] != PAGE_SIZE or kv.shape[3] != sides * HEAD_DIM:
+        raise ValueError("kv must be [num_blocks, Hkv, 128, 256], or without v a K-only "
+                         "[num_blocks, Hkv, 128, 128]")
+    if block_table.dim() != 2 or seq_lens.dim() != 1 or block_table.shape[0] != seq_lens.shape[0]:
+        raise ValueError("block_table must be [B, S] and seq_lens [B]")
+    B, S = block_table.shape
+    NB, Hkv = kv.shape[0], kv.shape[1]
+    Hq = GROUP * Hkv
+    if tokens is None:
+        tokens = B * qlen
+    ks = _rows(k, "k", Hkv, tokens, dev)
+    vs = _rows(v, "v", Hkv, tokens, dev) if v is not None else 0
+    qs = qp = qo = None
+    q8 = 0.0
+    if q is not None:
+        qs, qp = _rows(q, "q", Hq, tokens, dev), q.data_ptr()
+        if q_out is None:
+            q_out = torch.empty((tokens, Hq, HEAD_DIM), dtype=torch.bfloat16, device=dev)
+        _need(q_out, "q_out", (torch.bfloat16,) + ((_FP8_Q,) if _FP8_Q is not None else ()), dev)
+        if tuple(q_out.shape) != (tokens, Hq, HEAD_DIM):
+            raise ValueError("q_out must be [T, Hq, 128]")
+        qo = q_out.data_ptr()
+        if _fp8(q_out, q_scale):
+            q8 = float(q_scale)
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    sc = None
+    if kv_scales is not None:
+        sc = _page_scales(kv_scales, "kv_scales", dev, NB, Hkv, sides)
+    tab, max_pos, rot = None, 0, 0
+    if cos_sin is not None:
+        _need(cos_sin, "cos_sin", (torch.float32,), dev)
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be [max_pos, rot_dim]")
+        tab, (max_pos, rot) = cos_sin.data_ptr(), cos_sin.shape
+        if rot == 0 or rot > HEAD_DIM or rot % 16:
+            raise ValueError("rot_dim must be a multiple of 16 up to 128")
+    if B == 0 and tokens == 0:
+        return q_out        # empty tensors have no address to check
+    mid = () if cu is None else (cu.data_ptr(),)
+    st = getattr(_lib(), fn)(
+        k.data_ptr(), ks, v.data_ptr() if v is not None else None, vs, qp, qs or 0, tab, max_pos,
+        rot, 1 if interleaved else 0, kv.data_ptr(), sc, qo, q8, block_table.data_ptr(),
+        seq_lens.data_ptr(), *mid, B, tokens if cu is not None else qlen, Hq, Hkv, S, NB,
+        float(k_scale), float(v_scale), _stream(dev, stream))
+    _native.check(st, fn)
+    return q_out
+
+
+def append_kv(k, v, kv, block_table, seq_lens, qlen: int, k_scale: float = 1.0,
+              v_scale: float = 1.0, kv_scales: torch.Tensor | None = None,
+              cos_sin: torch.Tensor | None = None, interleaved: bool = False, q=None,
+              q_out: torch.Tensor | None = None, q_scale: float = 1.0, stream=None):
+    """Writes a decode step's keys and values into the paged cache (msa_append_kv).
+
+    k, v bf16 [T, Hkv, 128], T = B * qlen, possibly slices of one projection's
+    output (a token's heads contiguous); v None for a K-only cache.  Token j of
+    request b goes to position seq_lens[b] - qlen + j (seq_lens counts the new
+    tokens).  cos_sin fp32 [max_pos, rot_dim] (cosines, then sines of each
+    position) rotates the first rot_dim dims of k, and of q [T, Hq, 128] into
+    q_out (bf16, or fp8 e4m3 codes of q / q_scale; q itself for in place), in
+    halves or, with `interleaved`, in neighbouring pairs.  kv_scales [NB, Hkv,
+    2] (or 1): page scales, updated; else codes are x / k_scale, x / v_scale.
+    Returns q_out (None without q)."""
+    return _append("msa_append_kv", k, v, kv, block_table, seq_lens, None, None, qlen, k_scale,
+                   v_scale, kv_scales, cos_sin, interleaved, q, q_out, q_scale, stream)
+
+
+def append_kv_prefill(k, v, kv, block_table, seq_lens, cu_seqlens_q, k_scale: float = 1.0,
+                      v_scale: float = 1.0, kv_scales: torch.Tensor | None = None,
+                      cos_sin: torch.Tensor | None = None, interleaved: bool = False, q=None,
+                      q_out: torch.Tensor | None = None, q_scale: float = 1.0, stream=None):
+    """append_kv of a prefill or chunked-prefill batch (msa_append_kv_prefill):
+    request b's tokens are rows cu_seqlens_q[b] .. cu_seqlens_q[b + 1] - 1 of k,
+    v and q, the last ones of its seq_lens[b]."""
+    _need(cu_seqlens_q, "cu_seqlens_q", (torch.int32,), seq_lens.device)
+    if tuple(cu_seqlens_q.shape) != (seq_lens.shape[0] + 1,):
+        raise ValueError("cu_seqlens_q must be [B + 1]")
+    return _append("msa_append_kv_prefill", k, v, kv, block_table, seq_lens, k.shape[0],
+                   cu_seqlens_q, None, k_scale, v_scale, kv_scales, cos_sin, interleaved, q, q_out,
+                   q_scale, stream)
 
 
 def set_union_tile(enable: bool) -> bool:

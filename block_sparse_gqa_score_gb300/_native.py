@@ -16,6 +16,8 @@ ERR_PAGE_RANGE = 0x04
 ERR_SEQ_RANGE = 0x08
 ERR_SCORE_NAN = 0x10
 ERR_TIMEOUT = 0x20
+ERR_POS_RANGE = 0x40
+ERR_SCALE = 0x80
 
 #: Every symbol include/msa.h declares.
 EXPORTS = ("msa_score", "msa_topk", "msa_workspace_bytes", "msa_choose_splits",
@@ -25,7 +27,11 @@ EXPORTS = ("msa_score", "msa_topk", "msa_workspace_bytes", "msa_choose_splits",
            "msa_sparse_decode_select_q8", "msa_dense_decode_q8", "msa_sparse_prefill",
            "msa_sparse_prefill_select", "msa_sparse_prefill_q8", "msa_sparse_prefill_select_q8",
            "msa_score_kcache", "msa_score_kcache_q8", "msa_decode_step",
-           "msa_set_input_overlap", "msa_set_union_tile", "msa_test_wait_timeout")
+           "msa_set_input_overlap", "msa_set_union_tile", "msa_test_wait_timeout",
+           "msa_append_kv", "msa_append_kv_prefill", "msa_score_scaled",
+           "msa_sparse_decode_scaled", "msa_sparse_decode_select_scaled",
+           "msa_dense_decode_scaled", "msa_sparse_prefill_scaled",
+           "msa_sparse_prefill_select_scaled", "msa_decode_step_scaled")
 
 _lib = None
 _lock = threading.Lock()
@@ -91,6 +97,21 @@ def load(path: str | None = None):
         # the whole step: (q, q_scale, kv, index_k, index_k_scale, ...)
         lib.msa_decode_step.argtypes = [P, f32, P, P, f32, P, P, P, P, P, sz, P, i32, i32, i32,
                                         i32, i32, i64, f32, f32, f32, i32, P]
+        # page scales: (q, q_scale, kv, kv_scales) in place of (q, kv)
+        for scaled, plain in (("sparse_decode", lib.msa_sparse_decode),
+                              ("sparse_decode_select", lib.msa_sparse_decode_select),
+                              ("dense_decode", lib.msa_dense_decode),
+                              ("sparse_prefill", lib.msa_sparse_prefill),
+                              ("sparse_prefill_select", lib.msa_sparse_prefill_select)):
+            getattr(lib, f"msa_{scaled}_scaled").argtypes = [P, f32, P, P] + plain.argtypes[2:]
+        lib.msa_score_scaled.argtypes = [P, f32, P, P, i32] + lib.msa_score.argtypes[2:]
+        lib.msa_decode_step_scaled.argtypes = ([P, f32, P, P, P, f32, P] +
+                                               lib.msa_decode_step.argtypes[5:])
+        # the cache append
+        rows = [P, i64, P, i64, P, i64, P, i32, i32, i32, P, P, P, f32, P, P]
+        sizes = [i32, i32, i32, i32, i32, i64, f32, f32, P]
+        lib.msa_append_kv.argtypes = rows + sizes
+        lib.msa_append_kv_prefill.argtypes = rows + [P] + sizes
         lib.msa_set_input_overlap.argtypes = [i32]
         lib.msa_set_union_tile.argtypes = [i32]
         lib.msa_test_wait_timeout.argtypes = [ctypes.c_ulonglong, P]
@@ -104,7 +125,11 @@ def load(path: str | None = None):
                      "msa_dense_decode_q8", "msa_sparse_prefill", "msa_sparse_prefill_select",
                      "msa_sparse_prefill_q8", "msa_sparse_prefill_select_q8",
                      "msa_score_kcache", "msa_score_kcache_q8", "msa_decode_step",
-                     "msa_set_input_overlap", "msa_set_union_tile", "msa_test_wait_timeout"):
+                     "msa_set_input_overlap", "msa_set_union_tile", "msa_test_wait_timeout",
+                     "msa_append_kv", "msa_append_kv_prefill", "msa_score_scaled",
+                     "msa_sparse_decode_scaled", "msa_sparse_decode_select_scaled",
+                     "msa_dense_decode_scaled", "msa_sparse_prefill_scaled",
+                     "msa_sparse_prefill_select_scaled", "msa_decode_step_scaled"):
             getattr(lib, name).restype = i32
         _lib = lib
         return lib

@@ -164,11 +164,11 @@ namespace {
 int prepare_score(const void* q, float q_scale, const void* kv, const int32_t* block_table,
                   const int32_t* seq_lens, float* scores, int B, int Q, int Hq, int Hkv, int S,
                   int64_t num_blocks, float sm_scale, float k_scale, bool k_only,
-                  msa::ScoreParams* p, CUtensorMap* map) {
+                  const float* kv_scales, msa::ScoreParams* p, CUtensorMap* map) {
   int st = check_common(q, kv, block_table, seq_lens, B, Q, Hq, Hkv, S, num_blocks);
   if (st != MSA_OK) return st;
   if (!scores || !aligned(scores, 4) || !finite_pos(sm_scale) || !finite_pos(k_scale) ||
-      !(q_scale == 0.f || finite_pos(q_scale)))
+      !(q_scale == 0.f || finite_pos(q_scale)) || !aligned(kv_scales, k_only ? 4 : 8))
     return MSA_EINVAL;
   if (B == 0) return MSA_OK;
   DeviceState* dev;
@@ -192,20 +192,26 @@ int prepare_score(const void* q, float q_scale, const void* kv, const int32_t* b
   p->ctas = dev->sm_count;
   p->num_blocks = num_blocks;
   p->scale = sm_scale * k_scale;
+  p->kv_scales = kv_scales;
+  p->scale_sides = k_only ? 1 : 2;
   return MSA_OK;
+}
+
+int enqueue_score(const CUtensorMap& map, const msa::ScoreParams& p, cudaStream_t s, bool pdl) {
+  return from_cuda(p.kv_scales ? msa::launch_score_scaled(map, p, s, pdl)
+                               : msa::launch_score(map, p, s, pdl));
 }
 
 int score(const void* q, float q_scale, const void* kv, const int32_t* block_table,
           const int32_t* seq_lens, float* scores, int B, int Q, int Hq, int Hkv, int S,
           int64_t num_blocks, float sm_scale, float k_scale, msa_stream_t stream,
-          bool k_only = false) {
+          bool k_only = false, const float* kv_scales = nullptr) {
   msa::ScoreParams p;
   CUtensorMap map;
   const int st = prepare_score(q, q_scale, kv, block_table, seq_lens, scores, B, Q, Hq, Hkv, S,
-                               num_blocks, sm_scale, k_scale, k_only, &p, &map);
+                               num_blocks, sm_scale, k_scale, k_only, kv_scales, &p, &map);
   if (st != MSA_OK || B == 0) return st;
-  return from_cuda(
-      msa::launch_score(map, p, reinterpret_cast<cudaStream_t>(stream), input_overlap()));
+  return enqueue_score(map, p, reinterpret_cast<cudaStream_t>(stream), input_overlap());
 }
 
 }  // namespace
@@ -317,9 +323,9 @@ int prepare_attend(const void* q, const void* kv, const int32_t* block_table,
                    size_t workspace_bytes, void* out, int B, int Q, int Hq, int Hkv, int S,
                    int64_t num_blocks, float sm_scale, float k_scale, float v_scale,
                    int num_splits, int dense_span, float q_scale, const int32_t* cu_q, int T,
-                   AttendLaunch* L, bool* empty) {
+                   const float* kv_scales, AttendLaunch* L, bool* empty) {
   *empty = true;
-  if (!(q_scale == 0.f || finite_pos(q_scale))) return MSA_EINVAL;
+  if (!(q_scale == 0.f || finite_pos(q_scale)) || !aligned(kv_scales, 8)) return MSA_EINVAL;
   if (cu_q) {
     // the token count takes the place of B * Q in every size below
     if (dense_span != 0 || !aligned(cu_q, 4) || T < 0 || T > INT_MAX / 4 || (B == 0) != (T == 0))
@@ -391,6 +397,7 @@ int prepare_attend(const void* q, const void* kv, const int32_t* block_table,
   p.cu_q = cu_q;
   p.T = cu_q ? T : 0;
   p.union_tile = union_tile ? 1 : 0;
+  p.kv_scales = kv_scales;
   L->rows = rows;
   *empty = false;
   return MSA_OK;
@@ -400,7 +407,9 @@ int prepare_attend(const void* q, const void* kv, const int32_t* block_table,
 // (the merge always follows it with programmatic serialization).
 int enqueue_attend(const AttendLaunch& L, cudaStream_t s, bool pdl) {
   int st;
-  if ((st = from_cuda(msa::launch_attend(L.map, L.p, s, pdl))) != MSA_OK) return st;
+  if ((st = from_cuda(L.p.kv_scales ? msa::launch_attend_scaled(L.map, L.p, s, pdl)
+                                    : msa::launch_attend(L.map, L.p, s, pdl))) != MSA_OK)
+    return st;
   if (L.p.splits > 1)
     return from_cuda(
         msa::launch_combine(L.p.part_o, L.p.part_ml, L.p.out, L.rows, L.p.splits, s, true));
@@ -413,13 +422,13 @@ int sparse_decode(const void* q, const void* kv, const int32_t* block_table,
                   size_t workspace_bytes, void* out, int B, int Q, int Hq, int Hkv, int S,
                   int64_t num_blocks, float sm_scale, float k_scale, float v_scale,
                   int num_splits, msa_stream_t stream, int dense_span = 0, float q_scale = 0.f,
-                  const int32_t* cu_q = nullptr, int T = 0) {
+                  const int32_t* cu_q = nullptr, int T = 0, const float* kv_scales = nullptr) {
   AttendLaunch L;
   bool empty;
   const int st = prepare_attend(q, kv, block_table, seq_lens, scores, stride_h, stride_t, stride_n,
                                 topk, workspace, workspace_bytes, out, B, Q, Hq, Hkv, S,
                                 num_blocks, sm_scale, k_scale, v_scale, num_splits, dense_span,
-                                q_scale, cu_q, T, &L, &empty);
+                                q_scale, cu_q, T, kv_scales, &L, &empty);
   if (st != MSA_OK || empty) return st;
   return enqueue_attend(L, reinterpret_cast<cudaStream_t>(stream), input_overlap());
 }
@@ -561,18 +570,22 @@ int msa_sparse_prefill_select_q8(const void* q8, float q_scale, const void* kv,
                        k_scale, v_scale, num_splits, stream, 0, q_scale, cu_seqlens_q, T);
 }
 
+}  // extern "C"
+
+namespace {
+
 // One decode step: the scorer, then the selection and the attend.  Rows of at
 // most kFusedMaxBlocks candidate blocks are selected inside the attend kernel
 // (msa_sparse_decode_select); longer rows by the selector kernel, whose
 // register paths hold up to 2048 candidates, then msa_sparse_decode.  The
 // first kernel follows the input-overlap setting; the others follow a library
 // kernel and may overlap it.
-int msa_decode_step(const void* q, float q_scale, const void* kv, const void* index_k,
-                    float index_k_scale, const int32_t* block_table, const int32_t* seq_lens,
-                    float* scores, int32_t* topk, void* workspace, size_t workspace_bytes,
-                    void* out, int B, int Q, int Hq, int Hkv, int S, int64_t num_blocks,
-                    float sm_scale, float k_scale, float v_scale, int num_splits,
-                    msa_stream_t stream) {
+int decode_step(const void* q, float q_scale, const void* kv, const float* kv_scales,
+                const void* index_k, float index_k_scale, const float* index_scales,
+                const int32_t* block_table, const int32_t* seq_lens, float* scores,
+                int32_t* topk, void* workspace, size_t workspace_bytes, void* out, int B, int Q,
+                int Hq, int Hkv, int S, int64_t num_blocks, float sm_scale, float k_scale,
+                float v_scale, int num_splits, msa_stream_t stream) {
   constexpr int kFusedMaxBlocks = 512;
   if (!(q_scale == 0.f || finite_pos(q_scale))) return MSA_EINVAL;
   if (index_k && !finite_pos(index_k_scale)) return MSA_EINVAL;
@@ -581,7 +594,7 @@ int msa_decode_step(const void* q, float q_scale, const void* kv, const void* in
   CUtensorMap smap;
   int st = prepare_score(q, q_scale, index_k ? index_k : kv, block_table, seq_lens, scores, B, Q,
                          Hq, Hkv, S, num_blocks, sm_scale, index_k ? index_k_scale : k_scale,
-                         index_k != nullptr, &sp, &smap);
+                         index_k != nullptr, index_k ? index_scales : kv_scales, &sp, &smap);
   if (st != MSA_OK) return st;
   const bool fused = S <= kFusedMaxBlocks;
   const int64_t T = static_cast<int64_t>(B) * Q;
@@ -590,10 +603,10 @@ int msa_decode_step(const void* q, float q_scale, const void* kv, const void* in
   // the scores buffer [Hkv, T, S], block dim contiguous
   st = prepare_attend(q, kv, block_table, seq_lens, fused ? scores : nullptr, T * S, S, 1, topk,
                       workspace, workspace_bytes, out, B, Q, Hq, Hkv, S, num_blocks, sm_scale,
-                      k_scale, v_scale, num_splits, 0, q_scale, nullptr, 0, &L, &empty);
+                      k_scale, v_scale, num_splits, 0, q_scale, nullptr, 0, kv_scales, &L, &empty);
   if (st != MSA_OK || empty || B == 0) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if ((st = from_cuda(msa::launch_score(smap, sp, s, input_overlap()))) != MSA_OK) return st;
+  if ((st = enqueue_score(smap, sp, s, input_overlap())) != MSA_OK) return st;
   if (!fused) {
     msa::TopkParams tp{};
     tp.scores = scores;
@@ -610,6 +623,212 @@ int msa_decode_step(const void* q, float q_scale, const void* kv, const void* in
     if ((st = from_cuda(msa::launch_topk(tp, s, true))) != MSA_OK) return st;
   }
   return enqueue_attend(L, s, true);
+}
+
+}  // namespace
+
+extern "C" {
+
+int msa_decode_step(const void* q, float q_scale, const void* kv, const void* index_k,
+                    float index_k_scale, const int32_t* block_table, const int32_t* seq_lens,
+                    float* scores, int32_t* topk, void* workspace, size_t workspace_bytes,
+                    void* out, int B, int Q, int Hq, int Hkv, int S, int64_t num_blocks,
+                    float sm_scale, float k_scale, float v_scale, int num_splits,
+                    msa_stream_t stream) {
+  return decode_step(q, q_scale, kv, nullptr, index_k, index_k_scale, nullptr, block_table,
+                     seq_lens, scores, topk, workspace, workspace_bytes, out, B, Q, Hq, Hkv, S,
+                     num_blocks, sm_scale, k_scale, v_scale, num_splits, stream);
+}
+
+// The forms on a cache with page scales.
+
+int msa_decode_step_scaled(const void* q, float q_scale, const void* kv, const float* kv_scales,
+                           const void* index_k, float index_k_scale, const float* index_scales,
+                           const int32_t* block_table, const int32_t* seq_lens, float* scores,
+                           int32_t* topk, void* workspace, size_t workspace_bytes, void* out,
+                           int B, int Q, int Hq, int Hkv, int S, int64_t num_blocks,
+                           float sm_scale, float k_scale, float v_scale, int num_splits,
+                           msa_stream_t stream) {
+  if (!kv_scales) return MSA_EINVAL;
+  return decode_step(q, q_scale, kv, kv_scales, index_k, index_k_scale, index_scales, block_table,
+                     seq_lens, scores, topk, workspace, workspace_bytes, out, B, Q, Hq, Hkv, S,
+                     num_blocks, sm_scale, k_scale, v_scale, num_splits, stream);
+}
+
+int msa_score_scaled(const void* q, float q_scale, const void* kv, const float* kv_scales,
+                     int k_only, const int32_t* block_table, const int32_t* seq_lens,
+                     float* scores, int B, int Q, int Hq, int Hkv, int S, int64_t num_blocks,
+                     float sm_scale, float k_scale, msa_stream_t stream) {
+  if (!kv_scales) return MSA_EINVAL;
+  return score(q, q_scale, kv, block_table, seq_lens, scores, B, Q, Hq, Hkv, S, num_blocks,
+               sm_scale, k_scale, stream, k_only != 0, kv_scales);
+}
+
+int msa_sparse_decode_scaled(const void* q, float q_scale, const void* kv, const float* kv_scales,
+                             const int32_t* block_table, const int32_t* seq_lens,
+                             const int32_t* topk, void* workspace, size_t workspace_bytes,
+                             void* out, int B, int Q, int Hq, int Hkv, int S, int64_t num_blocks,
+                             float sm_scale, float k_scale, float v_scale, int num_splits,
+                             msa_stream_t stream) {
+  if (!kv_scales) return MSA_EINVAL;
+  return sparse_decode(q, kv, block_table, seq_lens, nullptr, 0, 0, 0, const_cast<int32_t*>(topk),
+                       workspace, workspace_bytes, out, B, Q, Hq, Hkv, S, num_blocks, sm_scale,
+                       k_scale, v_scale, num_splits, stream, 0, q_scale, nullptr, 0, kv_scales);
+}
+
+int msa_sparse_decode_select_scaled(const void* q, float q_scale, const void* kv,
+                                    const float* kv_scales, const int32_t* block_table,
+                                    const int32_t* seq_lens, const float* scores,
+                                    int64_t stride_h, int64_t stride_t, int64_t stride_n,
+                                    int32_t* topk, void* workspace, size_t workspace_bytes,
+                                    void* out, int B, int Q, int Hq, int Hkv, int S,
+                                    int64_t num_blocks, float sm_scale, float k_scale,
+                                    float v_scale, int num_splits, msa_stream_t stream) {
+  if (!kv_scales || !scores) return MSA_EINVAL;
+  return sparse_decode(q, kv, block_table, seq_lens, scores, stride_h, stride_t, stride_n, topk,
+                       workspace, workspace_bytes, out, B, Q, Hq, Hkv, S, num_blocks, sm_scale,
+                       k_scale, v_scale, num_splits, stream, 0, q_scale, nullptr, 0, kv_scales);
+}
+
+int msa_dense_decode_scaled(const void* q, float q_scale, const void* kv, const float* kv_scales,
+                            const int32_t* block_table, const int32_t* seq_lens, void* workspace,
+                            size_t workspace_bytes, void* out, int B, int Q, int Hq, int Hkv,
+                            int S, int64_t num_blocks, float sm_scale, float k_scale,
+                            float v_scale, msa_stream_t stream) {
+  if (!kv_scales || msa_dense_splits(S) == 0) return MSA_EINVAL;
+  int nsplit, span;
+  dense_split(S, &nsplit, &span);
+  return sparse_decode(q, kv, block_table, seq_lens, nullptr, 0, 0, 0, nullptr, workspace,
+                       workspace_bytes, out, B, Q, Hq, Hkv, S, num_blocks, sm_scale, k_scale,
+                       v_scale, nsplit, stream, span, q_scale, nullptr, 0, kv_scales);
+}
+
+int msa_sparse_prefill_scaled(const void* q, float q_scale, const void* kv,
+                              const float* kv_scales, const int32_t* block_table,
+                              const int32_t* seq_lens, const int32_t* cu_seqlens_q,
+                              const int32_t* topk, void* workspace, size_t workspace_bytes,
+                              void* out, int B, int T, int Hq, int Hkv, int S, int64_t num_blocks,
+                              float sm_scale, float k_scale, float v_scale, int num_splits,
+                              msa_stream_t stream) {
+  if (!kv_scales || !cu_seqlens_q) return MSA_EINVAL;
+  return sparse_decode(q, kv, block_table, seq_lens, nullptr, 0, 0, 0, const_cast<int32_t*>(topk),
+                       workspace, workspace_bytes, out, B, 1, Hq, Hkv, S, num_blocks, sm_scale,
+                       k_scale, v_scale, num_splits, stream, 0, q_scale, cu_seqlens_q, T,
+                       kv_scales);
+}
+
+int msa_sparse_prefill_select_scaled(const void* q, float q_scale, const void* kv,
+                                     const float* kv_scales, const int32_t* block_table,
+                                     const int32_t* seq_lens, const int32_t* cu_seqlens_q,
+                                     const float* scores, int64_t stride_h, int64_t stride_t,
+                                     int64_t stride_n, int32_t* topk, void* workspace,
+                                     size_t workspace_bytes, void* out, int B, int T, int Hq,
+                                     int Hkv, int S, int64_t num_blocks, float sm_scale,
+                                     float k_scale, float v_scale, int num_splits,
+                                     msa_stream_t stream) {
+  if (!kv_scales || !cu_seqlens_q || !scores) return MSA_EINVAL;
+  return sparse_decode(q, kv, block_table, seq_lens, scores, stride_h, stride_t, stride_n, topk,
+                       workspace, workspace_bytes, out, B, 1, Hq, Hkv, S, num_blocks, sm_scale,
+                       k_scale, v_scale, num_splits, stream, 0, q_scale, cu_seqlens_q, T,
+                       kv_scales);
+}
+
+}  // extern "C"
+
+namespace {
+
+// Checks and launch of msa_append_kv (cu_q null: T = B * Q tokens) and
+// msa_append_kv_prefill.
+int append_kv(const void* k, int64_t k_stride, const void* v, int64_t v_stride, const void* q,
+              int64_t q_stride, const float* cos_sin, int max_pos, int rot_dim, int interleaved,
+              void* kv, float* kv_scales, void* q_out, float q_scale, const int32_t* block_table,
+              const int32_t* seq_lens, const int32_t* cu_q, int B, int Q, int T, int Hq, int Hkv,
+              int S, int64_t num_blocks, float k_scale, float v_scale, msa_stream_t stream) {
+  // sizes as the other entry points; k stands in for the query pointer
+  int st = check_common(k, kv, block_table, seq_lens, B, Q, Hq, Hkv, S, num_blocks);
+  if (st != MSA_OK) return st;
+  const auto bad_rows = [](const void* p, int64_t stride, int heads) {
+    return !aligned(p, 16) || stride % 8 != 0 ||
+           stride < static_cast<int64_t>(heads) * MSA_HEAD_DIM;
+  };
+  if (bad_rows(k, k_stride, Hkv) || (v && bad_rows(v, v_stride, Hkv)) ||
+      (q && (bad_rows(q, q_stride, Hq) || !q_out || !aligned(q_out, 16))))
+    return MSA_EINVAL;
+  if (q && q_out == q && (q_scale != 0.f || q_stride != static_cast<int64_t>(Hq) * MSA_HEAD_DIM))
+    return MSA_EINVAL;
+  if (rot_dim < 0 || rot_dim > MSA_HEAD_DIM || rot_dim % 16 != 0 ||
+      (rot_dim > 0 && (!cos_sin || !aligned(cos_sin, 16) || max_pos < 1)))
+    return MSA_EINVAL;
+  if (!finite_pos(k_scale) || !finite_pos(v_scale) || !finite_pos(1.f / k_scale) ||
+      !finite_pos(1.f / v_scale) ||
+      !(q_scale == 0.f || (finite_pos(q_scale) && finite_pos(1.f / q_scale))) ||
+      !aligned(kv_scales, v ? 8 : 4))
+    return MSA_EINVAL;
+  if (!cu_q) T = B * Q;   // in range: checked above
+  if (T == 0) return MSA_OK;
+  DeviceState* dev;
+  if ((st = device_state(&dev)) != MSA_OK) return st;
+  msa::AppendParams p{};
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.q = static_cast<const uint16_t*>(q);
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q_stride = q_stride;
+  p.cos_sin = rot_dim > 0 ? cos_sin : nullptr;
+  p.max_pos = rot_dim > 0 ? max_pos : INT_MAX;
+  p.rot_dim = rot_dim;
+  p.interleaved = interleaved != 0;
+  p.kv = static_cast<uint8_t*>(kv);
+  p.kv_scales = kv_scales;
+  p.sides = v ? 2 : 1;
+  p.q_out = q_out;
+  p.q_fp8 = q_scale > 0.f;
+  p.inv_q = q_scale > 0.f ? 1.f / q_scale : 1.f;
+  p.inv_k = 1.f / k_scale;
+  p.inv_v = 1.f / v_scale;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.cu_q = cu_q;
+  p.err = dev->err;
+  p.B = B;
+  p.Q = Q;
+  p.T = T;
+  p.Hq = q ? Hq : 0;
+  p.Hkv = Hkv;
+  p.S = S;
+  p.num_blocks = num_blocks;
+  return from_cuda(
+      msa::launch_append(p, reinterpret_cast<cudaStream_t>(stream), input_overlap()));
+}
+
+}  // namespace
+
+extern "C" {
+
+int msa_append_kv(const void* k, int64_t k_stride, const void* v, int64_t v_stride, const void* q,
+                  int64_t q_stride, const float* cos_sin, int max_pos, int rot_dim,
+                  int interleaved, void* kv, float* kv_scales, void* q_out, float q_scale,
+                  const int32_t* block_table, const int32_t* seq_lens, int B, int Q, int Hq,
+                  int Hkv, int S, int64_t num_blocks, float k_scale, float v_scale,
+                  msa_stream_t stream) {
+  return append_kv(k, k_stride, v, v_stride, q, q_stride, cos_sin, max_pos, rot_dim, interleaved,
+                   kv, kv_scales, q_out, q_scale, block_table, seq_lens, nullptr, B, Q, 0, Hq,
+                   Hkv, S, num_blocks, k_scale, v_scale, stream);
+}
+
+int msa_append_kv_prefill(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                          const void* q, int64_t q_stride, const float* cos_sin, int max_pos,
+                          int rot_dim, int interleaved, void* kv, float* kv_scales, void* q_out,
+                          float q_scale, const int32_t* block_table, const int32_t* seq_lens,
+                          const int32_t* cu_seqlens_q, int B, int T, int Hq, int Hkv, int S,
+                          int64_t num_blocks, float k_scale, float v_scale, msa_stream_t stream) {
+  if (!cu_seqlens_q || !aligned(cu_seqlens_q, 4) || T < 0 || T > INT_MAX / 4 ||
+      (B == 0) != (T == 0))
+    return MSA_EINVAL;
+  return append_kv(k, k_stride, v, v_stride, q, q_stride, cos_sin, max_pos, rot_dim, interleaved,
+                   kv, kv_scales, q_out, q_scale, block_table, seq_lens, cu_seqlens_q, B, 1, T, Hq,
+                   Hkv, S, num_blocks, k_scale, v_scale, stream);
 }
 
 int msa_test_wait_timeout(unsigned long long limit_ns, msa_stream_t stream) {

@@ -40,15 +40,27 @@
 // map each token to its request by a warp-wide search and then run as decode
 // tokens.  Dense decode, the fp8 query and prefill batches are template
 // flags, so the bf16 list-mode decode kernel carries none of their branches.
+//
+// This file is compiled twice: as it stands (one scale per tensor), and with
+// MSA_KV_SCALES set (by msa_attend_scaled.cu) for a cache whose pages carry
+// scales of their own, one per page, KV head and side.  There the K scale goes
+// into the page's logit factor and the V scale into the softmax reference (see
+// PageScale): 16 multiplies and 16 adds more per key and page, and no
+// instruction in the kernels compiled as they stand.
 #include "msa_device.cuh"
 #include "msa_launch.h"
 #include "msa_select.cuh"
 #include "msa_tcgen05.cuh"
 
+#ifndef MSA_KV_SCALES
+#define MSA_KV_SCALES 0
+#endif
+
 namespace msa {
 
 namespace {
 
+constexpr bool kScaled = MSA_KV_SCALES != 0;  // page scales (AttendParams::kv_scales)
 constexpr int kStages = 3;
 constexpr int kWarps = 7;
 constexpr int kThreads = kWarps * 32;
@@ -87,6 +99,7 @@ struct AttendTail {
   float zs;                 // logit scale (log2 units) times 2^e of the query split
   int pages[kMaxPages];
   int blocks[kMaxPages];
+  PageScale sc[kScaled ? kMaxPages : 1];
 };
 
 // shared-memory layout (offsets from a 1024-byte aligned base)
@@ -106,37 +119,6 @@ template <int N>
 __device__ __forceinline__ void fill(float (&a)[N], float v) {
 #pragma unroll
   for (int k = 0; k < N; ++k) a[k] = v;
-}
-
-// Request of query token i in a variable-length batch whose request r owns
-// tokens [cu_q[r], cu_q[r + 1]): b is the number of requests that end at or
-// before i, found by a 32-way search across the warp (each round probes 32
-// evenly spaced request ends and keeps the sub-range where the prefix of ends
-// <= i stops).  Every probe reads cu_q[1..B].  Returns false, with b = 0, when
-// token i lies in no request's range (cu_q not ascending, or i outside
-// [cu_q[0], cu_q[B])); otherwise b, the token's offset j and the request's
-// query length.  Warp-uniform arguments; all 32 lanes call it.
-__device__ __forceinline__ bool varlen_token(const int32_t* __restrict__ cu_q, int B, int i,
-                                             int lane, int& b, int& j, int& qlen) {
-  int lo = 0, hi = B;
-  while (lo < hi) {
-    const int step = (hi - lo + 31) >> 5;
-    const int r = lo + (lane + 1) * step - 1;
-    const bool before = r < hi && cu_q[r + 1] <= i;
-    const int k = __popc(__ballot_sync(0xffffffffu, before));
-    lo += k * step;
-    hi = min(hi, lo + step - 1);
-  }
-  b = 0;
-  j = 0;
-  qlen = 1;
-  if (lo >= B) return false;
-  const int start = cu_q[lo], end = cu_q[lo + 1];
-  if (i < start || i >= end) return false;
-  b = lo;
-  j = i - start;
-  qlen = end - start;
-  return true;
 }
 
 // kDense: dense decode (every visible block of the CTA's range, no list);
@@ -355,6 +337,16 @@ __global__ void __launch_bounds__(kThreads, 2)
         tma_load_2d(st + kHalfTile, &kv_map, kHeadDim, row, &tail->full[t]);
       }
     }
+    if constexpr (kScaled) {
+      // the listed pages' scales, behind the first loads: a page whose scales
+      // are out of range keeps its slot and is attended by no key
+      __syncwarp();
+      for (int t = lane; t < np; t += 32) {
+        const PageScale s = make_page_scale(load_page_scale(p.kv_scales, tail->pages[t], p.Hkv, g));
+        if (s.bad != 0.f) flag_error(p.err, MSA_ERR_SCALE);
+        tail->sc[t] = s;
+      }
+    }
   } else if (warp == 1) {
     tc::tmem_alloc(&tail->tmem_base, kTmemCols);
     tc::tmem_relinquish();
@@ -468,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // running sum; o: the running output of value dim `key`.  Both are kept
     // relative to the current m.
     float nref[kGroup], l[kGroup], o[kGroup];
-    fill(nref, INFINITY);
+    fill(nref, kScaled ? kNoRef : INFINITY);
     fill(l, 0.f);
     fill(o, 0.f);
     bool ok = true;
@@ -498,6 +490,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       tc::fence_after_thread_sync();
       float x[kGroup], pm[kGroup];
+      const PageScale sc = kScaled ? tail->sc[t] : PageScale{1.f, 0.f, 1.f, 0.f};
+      const float zt = kScaled ? zs * sc.k : zs;
       {
         uint32_t sv[32];
         tc::ld_32x32b_x32(lane_addr + kColS + 2 * kGroup * buf, sv);
@@ -505,10 +499,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         tc::fence_before_thread_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&tail->s_empty[buf]);
-        const int lim = pos - tail->blocks[t] * kPage;  // keys <= lim are visible
+        // keys <= lim are visible
+        const int lim = kScaled && sc.bad != 0.f ? -1 : pos - tail->blocks[t] * kPage;
         const bool vis = key <= lim;
         // raw dot products (hi + lo columns); the logit in log2 units is
-        // s * zs with zs > 0, so maxima can be taken on s
+        // s * zt with zt > 0, so maxima can be taken on s
 #pragma unroll
         for (int h = 0; h < kGroup; ++h)
           x[h] = vis ? __uint_as_float(sv[h]) + __uint_as_float(sv[h + kGroup]) : -INFINITY;
@@ -544,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       bool raise = false;
 #pragma unroll
       for (int h = 0; h < kGroup; ++h) {
-        pm[h] *= zs;
+        pm[h] = kScaled ? fmaf(pm[h], zt, sc.lv) : pm[h] * zt;
         raise |= pm[h] + nref[h] > kPShift + kLazy;
       }
       float al[kGroup];  // 2^(m_old - m_new) per head
@@ -561,8 +556,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
 #pragma unroll
       for (int h = 0; h < kGroup; ++h) {
-        x[h] = ex2(fmaf(x[h], zs, nref[h]));  // P = 2^(x - m + 8); 0 for an invisible key
-        l[h] = fmaf(l[h], al[h], x[h]);
+        // P = 2^(x - m + 8); 0 for an invisible key
+        x[h] = ex2(fmaf(x[h], zt, kScaled ? nref[h] + sc.lv : nref[h]));
+        l[h] = kScaled ? fmaf(x[h], sc.iv, l[h] * al[h]) : fmaf(l[h], al[h], x[h]);
       }
       uint32_t hw[4], lw[4];
 #pragma unroll
@@ -574,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         lw[q4] = l0 | (l1 << 16);
       }
       const int s = t % kStages;
-      const int lim = pos - tail->blocks[t] * kPage;
+      const int lim = kScaled && sc.bad != 0.f ? -1 : pos - tail->blocks[t] * kPage;
       if (lim < kPage - 1 && key > lim) {
         // keys past the causal limit have P = 0, but their value rows may hold
         // any bytes (an fp8 NaN times 0 is NaN): zero them for the O^T product
@@ -677,6 +673,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
+#if !MSA_KV_SCALES
 // Split merge: one warp per (token, query head) row, 4 d-values per lane.
 // A part counts only when its l > 0 and its m is a number.
 __global__ void __launch_bounds__(256)
@@ -712,12 +709,17 @@ __global__ void __launch_bounds__(256)
   const uint32_t hi = f32_to_bf16_bits(acc.z * f) | (f32_to_bf16_bits(acc.w * f) << 16);
   *reinterpret_cast<uint2*>(out + r * kHeadDim + 4 * lane) = make_uint2(lo, hi);
 }
-
+#endif
 
 }  // namespace
 
+#if MSA_KV_SCALES
+cudaError_t launch_attend_scaled(const CUtensorMap& kv_map, const AttendParams& p,
+                                 cudaStream_t stream, bool pdl) {
+#else
 cudaError_t launch_attend(const CUtensorMap& kv_map, const AttendParams& p, cudaStream_t stream,
                           bool pdl) {
+#endif
   static_assert(kSmemBytes <= 227 * 1024, "attend shared memory");
   static std::atomic<unsigned long long> attr_done{0};
   cudaError_t e = once_per_device(attr_done, [] {
@@ -738,7 +740,9 @@ cudaError_t launch_attend(const CUtensorMap& kv_map, const AttendParams& p, cuda
   });
   if (e != cudaSuccess) return e;
   // the union attend: one pass over the pages a 4-token tile shares
-  if (p.union_tile) return launch_union_attend(kv_map, p, stream, pdl);
+  if (p.union_tile)
+    return kScaled ? launch_union_attend_scaled(kv_map, p, stream, pdl)
+                   : launch_union_attend(kv_map, p, stream, pdl);
   const int T = p.cu_q ? p.T : p.B * p.Q;
   dim3 grid(T, p.Hkv, p.splits);
   const dim3 block(kThreads);
@@ -768,6 +772,7 @@ cudaError_t launch_attend(const CUtensorMap& kv_map, const AttendParams& p, cuda
                  : launch_pdl(attend_kernel<false, false>, grid, block, kSmemBytes, stream, pdl, kv_map, p);
 }
 
+#if !MSA_KV_SCALES
 cudaError_t launch_combine(const float* part_o, const float* part_ml, uint16_t* out, int64_t rows,
                            int splits, cudaStream_t stream, bool pdl) {
   const int64_t threads = rows * 32;
@@ -776,5 +781,6 @@ cudaError_t launch_combine(const float* part_o, const float* part_ml, uint16_t* 
   return launch_pdl(combine_kernel, dim3(static_cast<unsigned>(grid)), dim3(block), 0, stream, pdl,
                     part_o, part_ml, out, rows, splits);
 }
+#endif
 
 }  // namespace msa

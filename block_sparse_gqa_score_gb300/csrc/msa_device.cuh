@@ -394,4 +394,81 @@ __device__ __forceinline__ int prepare_query_e4m3(const uint16_t* __restrict__ r
   return store_query_e4m3(raw, row0, hi, lo, lane);
 }
 
+// ----------------------------------------------------------------------------
+// token -> request
+
+// Request of query token i in a variable-length batch whose request r owns
+// tokens [cu_q[r], cu_q[r + 1]): b is the number of requests that end at or
+// before i, found by a 32-way search across the warp (each round probes 32
+// evenly spaced request ends and keeps the sub-range where the prefix of ends
+// <= i stops).  Every probe reads cu_q[1..B].  Returns false, with b = 0, when
+// token i lies in no request's range (cu_q not ascending, or i outside
+// [cu_q[0], cu_q[B])); otherwise b, the token's offset j and the request's
+// query length.  Warp-uniform arguments; all 32 lanes call it.
+__device__ __forceinline__ bool varlen_token(const int32_t* __restrict__ cu_q, int B, int i,
+                                             int lane, int& b, int& j, int& qlen) {
+  int lo = 0, hi = B;
+  while (lo < hi) {
+    const int step = (hi - lo + 31) >> 5;
+    const int r = lo + (lane + 1) * step - 1;
+    const bool before = r < hi && cu_q[r + 1] <= i;
+    const int k = __popc(__ballot_sync(0xffffffffu, before));
+    lo += k * step;
+    hi = min(hi, lo + step - 1);
+  }
+  b = 0;
+  j = 0;
+  qlen = 1;
+  if (lo >= B) return false;
+  const int start = cu_q[lo], end = cu_q[lo + 1];
+  if (i < start || i >= end) return false;
+  b = lo;
+  j = i - start;
+  qlen = end - start;
+  return true;
+}
+
+// ----------------------------------------------------------------------------
+// page scales
+//
+// A page scale is an fp32 factor of one (page, KV head) and side (K or V):
+// value = code * scale (* the tensor's scale).  The append writes powers of two
+// in [2^-40, 2^40]; readers take any factor of that range.  The bounds keep
+// the products of scales and softmax weights, and the reciprocals, far inside
+// fp32's range.
+
+constexpr float kScaleMin = 9.094947017729282e-13f;  // 2^-40
+constexpr float kScaleMax = 1.099511627776e12f;      // 2^40
+
+__device__ __forceinline__ bool page_scale_ok(float s) {  // false for NaN
+  return s >= kScaleMin && s <= kScaleMax;
+}
+
+// What the attend kernels need of one listed page's scales (ks, vs).  With z
+// the logit in log2 units and u = z + log2(vs), the output is
+//   sum 2^(u - M) V8 / sum 2^(u - M) / vs,
+// so the product with V8 takes weights relative to the largest u (a page
+// counts by the size of its values, and nothing is lost to a common
+// reference), and the running sum divides each page's weights by vs again.
+constexpr float kNoRef = 1e30f;   // kPShift - m before a head's first key: finite, so that a
+                                  // page without any key (-inf logits) has weights of 0
+
+struct PageScale {
+  float k;      // ks
+  float lv;     // log2(vs)
+  float iv;     // 1 / vs
+  float bad;    // non-zero: a scale out of range; the page is skipped
+};
+
+__device__ __forceinline__ PageScale make_page_scale(float2 s) {
+  const bool ok = page_scale_ok(s.x) && page_scale_ok(s.y);
+  if (!ok) return PageScale{1.f, 0.f, 1.f, 1.f};
+  return PageScale{s.x, log2f(s.y), 1.f / s.y, 0.f};
+}
+
+__device__ __forceinline__ float2 load_page_scale(const float* __restrict__ scales, int64_t page,
+                                                  int Hkv, int g) {
+  return __ldg(reinterpret_cast<const float2*>(scales) + page * Hkv + g);
+}
+
 }  // namespace msa

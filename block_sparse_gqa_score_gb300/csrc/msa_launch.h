@@ -23,6 +23,8 @@ struct ScoreParams {
   float scale;                 // sm_scale * k_scale
   const uint8_t* q8;           // fp8 e4m3 [T, Hq, 128], value q8 * q_scale; or nullptr
   float q_scale;
+  const float* kv_scales;      // page scales [num_blocks, Hkv, scale_sides] (K's first); or nullptr
+  int scale_sides;             // 2 (K|V pages) or 1 (K-only pages)
 };
 
 struct TopkParams {
@@ -65,6 +67,7 @@ struct AttendParams {
   // 1: the union attend (msa_union.cu) over 4-token tiles of each request;
   // 0: one CTA per (token, KV head)
   int union_tile;
+  const float* kv_scales;      // page scales [num_blocks, Hkv, 2] (K, V); or nullptr
 };
 
 // Runs `set_up` once per device (e.g. raising a kernel's dynamic shared-memory
@@ -118,10 +121,41 @@ cudaError_t launch_attend(const CUtensorMap& kv_map, const AttendParams& p, cuda
 // tile's lists; grid (B * ceil(Q / 4) * Hkv, splits).
 cudaError_t launch_union_attend(const CUtensorMap& kv_map, const AttendParams& p,
                                 cudaStream_t stream, bool pdl);
+// The same on a cache with page scales (p.kv_scales set).
+cudaError_t launch_score_scaled(const CUtensorMap& kv_map, const ScoreParams& p,
+                                cudaStream_t stream, bool pdl);
+cudaError_t launch_attend_scaled(const CUtensorMap& kv_map, const AttendParams& p,
+                                 cudaStream_t stream, bool pdl);
+cudaError_t launch_union_attend_scaled(const CUtensorMap& kv_map, const AttendParams& p,
+                                       cudaStream_t stream, bool pdl);
 // Its split count for `units` (request, tile, KV head) units: as many CTAs per
 // unit as fit one CTA per SM (at most 8), 1 when the units fill the SMs.
 int union_ctas_per_unit(int units, int sm_count);
 constexpr int kUnionTile = 4;   // query tokens per union tile
+
+// The cache append (msa_append.cu).
+struct AppendParams {
+  const uint16_t *k, *v, *q;   // bf16 bits, token i at k + i * k_stride; v, q may be null
+  int64_t k_stride, v_stride, q_stride;   // elements
+  const float* cos_sin;        // [max_pos, rot_dim]; null: no rotation
+  int max_pos, rot_dim;
+  bool interleaved;
+  uint8_t* kv;                 // [num_blocks, Hkv, 128, 128 * sides]
+  float* kv_scales;            // [num_blocks, Hkv, sides]; null: one scale per tensor
+  int sides;                   // 2: K|V pages, 1: K-only
+  void* q_out;                 // [T, Hq, 128], bf16 or fp8 (q_fp8)
+  bool q_fp8;
+  float inv_q, inv_k, inv_v;   // reciprocals of the tensors' scales
+  const int32_t* block_table;  // [B, S]
+  const int32_t* seq_lens;     // [B]
+  const int32_t* cu_q;         // [B + 1]; null: every request has Q tokens
+  unsigned* err;
+  int B, Q, T;
+  int Hq;                      // 0 without a query
+  int Hkv, S;
+  int64_t num_blocks;
+};
+cudaError_t launch_append(const AppendParams& p, cudaStream_t stream, bool pdl);
 
 // The bounded-wait exit exercised on purpose (msa_waittest.cu).
 cudaError_t launch_wait_timeout(unsigned long long limit_ns, unsigned* err, cudaStream_t stream);

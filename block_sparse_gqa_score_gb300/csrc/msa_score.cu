@@ -33,13 +33,25 @@
 //    form three more sets on the same lane quarters, the four sets taking
 //    groups of two tokens in turn (20 warps: registers capped near 96);
 //  * warp 7 combines the quarters and writes the scores.
+//
+// This file is compiled twice: as it stands (one key scale per tensor), and
+// with MSA_KV_SCALES set (by msa_score_scaled.cu) for a cache whose pages carry
+// scales of their own.  A page's key scale is a positive factor of all its
+// logits, so the maxima are taken before it and warp 7 multiplies by it; it
+// reads the scales of 32 pages at once, one per lane, 32 pages ahead.
 #include "msa_device.cuh"
 #include "msa_launch.h"
 #include "msa_tcgen05.cuh"
 
+#ifndef MSA_KV_SCALES
+#define MSA_KV_SCALES 0
+#endif
+
 namespace msa {
 
 namespace {
+
+constexpr bool kScaled = MSA_KV_SCALES != 0;  // page scales (ScoreParams::kv_scales)
 
 // 8 warps, see above; 20 with the extra epilogue warp sets (ScoreGeometry::threads)
 constexpr int kMaxWarps = 20;
@@ -776,7 +788,27 @@ __global__ void __launch_bounds__(kWide ? 640 : 256, kWide ? 1 : 2)
     int k = -1, pb = -1, pg = -1, vp = 0;
     float qm = 0.f;                              // scale of token `lane` of the current unit
     bool have_qm = false;
+    // page scales: lane l holds the key scale of page 32 (t / 32) + l of the
+    // range (0: out of range, the page scores -inf), and of the 32 after them
+    float ks_now = 1.f, ks_next = 1.f;
+    auto fetch_scale = [&](const PageWalk& from, int t_from, int skip) -> float {
+      if (t_from + skip + lane >= count) return 1.f;
+      PageWalk wl = from;
+      wl.advance(p, skip + lane);
+      int page;
+      if (!page_valid(p, wl, page)) return 1.f;
+      return __ldg(p.kv_scales + (static_cast<int64_t>(page) * p.Hkv + wl.g) * p.scale_sides);
+    };
+    if (kScaled && count > 0) ks_next = fetch_scale(w, 0, 0);
     for (int t = 0; t < count; ++t, w.next(p)) {
+      if (kScaled && (t & 31) == 0) {
+        ks_now = ks_next;
+        if (!page_scale_ok(ks_now)) {
+          flag_error(p.err, MSA_ERR_SCALE);
+          ks_now = 0.f;
+        }
+        ks_next = fetch_scale(w, t, 32);
+      }
       if (w.b != pb || w.g != pg) {
         ++k;
         pb = w.b;
@@ -802,11 +834,17 @@ __global__ void __launch_bounds__(kWide ? 640 : 256, kWide ? 1 : 2)
         if (lane == 0) flag_error(p.err, MSA_ERR_TIMEOUT);
         break;
       }
+      const float ks = kScaled ? __shfl_sync(0xffffffffu, ks_now, t & 31) : 1.f;
       if (lane < Q) {
         float v = -INFINITY;
 #pragma unroll
         for (int r = 0; r < 4 * kSub; ++r) v = fmaxf(v, red[(slot * 4 * kSub + r) * Q + lane]);
-        p.scores[row0 + static_cast<int64_t>(lane) * p.S] = (v == -INFINITY) ? v : v * qm;
+        if constexpr (kScaled) {
+          p.scores[row0 + static_cast<int64_t>(lane) * p.S] =
+              (v == -INFINITY || ks == 0.f) ? -INFINITY : v * (qm * ks);
+        } else {
+          p.scores[row0 + static_cast<int64_t>(lane) * p.S] = (v == -INFINITY) ? v : v * qm;
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&tail->red_empty[slot]);
@@ -837,8 +875,13 @@ __global__ void __launch_bounds__(kWide ? 640 : 256, kWide ? 1 : 2)
   X(false, true, false, 0) X(true, true, false, 8) X(true, true, false, 16)                   \
   X(true, true, false, 32) X(true, true, false, 0)
 
+#if MSA_KV_SCALES
+cudaError_t launch_score_scaled(const CUtensorMap& kv_map, const ScoreParams& p,
+                                cudaStream_t stream, bool pdl) {
+#else
 cudaError_t launch_score(const CUtensorMap& kv_map, const ScoreParams& p, cudaStream_t stream,
                          bool pdl) {
+#endif
   if (p.ctas < 1) return cudaErrorInvalidValue;
   const ScoreGeometry G = score_geometry(p.Q, p.q8 != nullptr);
   if (G.stages < 2 || G.smem > kSmemLimit) return cudaErrorInvalidValue;

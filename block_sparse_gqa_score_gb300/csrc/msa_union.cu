@@ -48,15 +48,27 @@
 //   3      copies the request's block-table row
 //   4..19  token j = (warp - 4) / 4: softmax; warp 4+4j selects or reads the
 //          token's list, warp 5+4j prepares its query rows
+//
+// This file is compiled twice: as it stands (one scale per tensor), and with
+// MSA_KV_SCALES set (by msa_union_scaled.cu) for a cache whose pages carry
+// scales of their own (see PageScale).  With lists the prologue puts the union
+// pages' scales into shared memory; dense decode, whose ranges have up to 2048
+// pages, reads them 32 at once, one per lane, 32 pages ahead: the producer
+// together with the page numbers, each softmax warp for itself.
 #include "msa_device.cuh"
 #include "msa_launch.h"
 #include "msa_select.cuh"
 #include "msa_tcgen05.cuh"
 
+#ifndef MSA_KV_SCALES
+#define MSA_KV_SCALES 0
+#endif
+
 namespace msa {
 
 namespace {
 
+constexpr bool kScaled = MSA_KV_SCALES != 0;  // page scales (AttendParams::kv_scales)
 constexpr int kQt = kUnionTile;               // query tokens per tile
 constexpr int kStages = 5;
 constexpr int kWarps = 4 + 4 * kQt;
@@ -113,6 +125,7 @@ struct UnionTail {
   int tok_slots[kQt][kMaxUnion];  // their slots, in page order
   int dense_lo;             // dense decode: this CTA's pages are blocks dense_lo + slot
   uint32_t dense_bad[kMaxDenseBlocks / 32];  // dense decode: slots whose block-table entry is bad
+  PageScale sc[kScaled ? kMaxUnion : 1];     // listed pages' scales, by slot
 };
 
 // shared-memory layout (offsets from a 1024-byte aligned base)
@@ -422,11 +435,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (t < np) {
         const int pg = lo + t < ncopy ? table_s[lo + t] : trow[lo + t];
         bad = pg < 0 || static_cast<int64_t>(pg) >= p.num_blocks;
+        if (bad) flag_error(p.err, MSA_ERR_PAGE_RANGE);
+        if constexpr (kScaled) {   // a page scale out of range: likewise
+          if (!bad && make_page_scale(load_page_scale(p.kv_scales, pg, p.Hkv, g)).bad != 0.f) {
+            flag_error(p.err, MSA_ERR_SCALE);
+            bad = true;
+          }
+        }
       }
       const unsigned bb = __ballot_sync(0xffffffffu, bad);
       if (lane == 0 && base / 32 < kMaxDenseBlocks / 32) tail->dense_bad[base / 32] = bb;
-      if (bb && lane == 0) flag_error(p.err, MSA_ERR_PAGE_RANGE);
     }
+    if constexpr (kScaled) __syncwarp();
     if (lane == 0) {
       const int last_block = (seq_ok && L > 0) ? (L - 1) / kPage : -1;
       tail->fix_slot = (last_block >= lo && last_block < hi) ? last_block - lo : -1;
@@ -440,6 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = 0; t < np && t < kStages; ++t) {
         int pg = lo + t < ncopy ? table_s[lo + t] : trow[lo + t];
         if (pg < 0 || static_cast<int64_t>(pg) >= p.num_blocks) pg = 0;
+        if (kScaled && ((tail->dense_bad[0] >> t) & 1u)) pg = 0;
         const int row = (pg * p.Hkv + g) * kPage;
         uint8_t* st = smem + t * kStageBytes;
         mbar_arrive_expect_tx(&tail->full[t], kStageBytes);
@@ -479,6 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool keep[2];
     uint32_t mk[2];
     int pg[2];
+    PageScale scl[kScaled ? 2 : 1];
     bool long_run = false;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -507,6 +529,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (page < 0 || static_cast<int64_t>(page) >= p.num_blocks) {
           if (split == 0) flag_error(p.err, MSA_ERR_PAGE_RANGE);
           ok = false;
+        }
+      }
+      if constexpr (kScaled) {
+        if (ok) {
+          scl[r] = make_page_scale(load_page_scale(p.kv_scales, page, p.Hkv, g));
+          if (scl[r].bad != 0.f) {
+            if (split == 0) flag_error(p.err, MSA_ERR_SCALE);
+            ok = false;
+          }
         }
       }
       keep[r] = ok;
@@ -554,6 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tail->pages[slot] = pg[r];
       tail->blocks[slot] = static_cast<int>(v[r] >> 2);
       tail->masks[slot] = mk[r];
+      if constexpr (kScaled) tail->sc[slot] = scl[r];
     }
     __syncwarp();
     // each token's slots in page order, and the slot of the request's last block
@@ -618,18 +650,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       return tail->masks[t];
     }
   };
+  auto slot_bad = [&](int t) -> bool {
+    return kDense && t < kMaxDenseBlocks && ((tail->dense_bad[t >> 5] >> (t & 31)) & 1u);
+  };
   auto slot_page = [&](int t) -> int {
     if constexpr (kDense) {
       const int pg = trow[dense_lo + t];
+      if (kScaled && slot_bad(t)) return 0;
       return (pg < 0 || static_cast<int64_t>(pg) >= p.num_blocks) ? 0 : pg;
     } else {
       return tail->pages[t];
     }
   };
   auto slot_block = [&](int t) -> int { return kDense ? dense_lo + t : tail->blocks[t]; };
-  auto slot_bad = [&](int t) -> bool {
-    return kDense && t < kMaxDenseBlocks && ((tail->dense_bad[t >> 5] >> (t & 31)) & 1u);
-  };
   auto tok_slot = [&](int j, int k) -> int { return kDense ? k : tail->tok_slots[j][k]; };
 
   if (warp == 0) {
@@ -737,7 +770,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int fix_slot = tail->fix_slot;
       if constexpr (kDense) {
         // pages in order; each page's listing tokens (consecutive, all at their
-        // t-th page) share one product once all their P^T is written
+        // t-th page) share one product once all their P^T is written.  With page
+        // scales a bad slot has none (its stage holds another page, whose bytes
+        // may be fp8 NaN); its commits still release what waits on them.
+        bool fresh = true;   // no product yet: the next one sets the accumulator
         for (int t = 0; t < n_pages; ++t) {
           const uint32_t mask = slot_mask(t);
           const int j0 = __ffs(mask) - 1, j1 = 31 - __clz(mask), buf = t & 1, s = t % kStages;
@@ -754,10 +790,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t bp = bp0 + static_cast<uint64_t>((buf * kPBuf + 256 * j0) >> 4);
           const uint32_t d = tmem + kColAcc + 32 * j0;
           const uint32_t idesc_m = tc::idesc_e4m3_f32_mn(128, 32 * (j1 - j0 + 1));
+          if (!kScaled || !slot_bad(t)) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc::mma_e4m3(d, a + 256 * kk, bp + ((4 * kPBlock) >> 4) * kk, idesc_m,
-                         (t > 0 || kk > 0) ? 1u : 0u);
+            for (int kk = 0; kk < 4; ++kk)
+              tc::mma_e4m3(d, a + 256 * kk, bp + ((4 * kPBlock) >> 4) * kk, idesc_m,
+                           (kScaled ? !fresh || kk > 0 : t > 0 || kk > 0) ? 1u : 0u);
+            fresh = false;
+          }
           // one commit for the tokens (the last token's barrier, on which
           // they all wait) and one for the stage
           tc::commit(&tail->o_done[j1][buf]);
@@ -839,13 +878,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the other lanes read it by shuffle.  l: this key slot's share of each
     // head's running sum relative to m.  The output accumulates in tensor
     // memory, relative to m.
-    float nref_h = INFINITY;
+    float nref_h = kScaled ? kNoRef : INFINITY;
     float l[kGroup];
     fill(l, 0.f);
     uint32_t sv[32];   // page k's S^T row (hi | lo columns)
+    // dense decode with page scales: lane l holds those of slot 32 (k / 32) + l
+    // and, as loaded, of the slot 32 after it (a slot with a bad table entry
+    // reads page 0's; it is attended by no key)
+    float2 sc_next = make_float2(1.f, 1.f);
+    PageScale sc_now{1.f, 0.f, 1.f, 0.f};
+    auto fetch_scale = [&](int t) -> float2 {
+      return t < n_j ? load_page_scale(p.kv_scales, slot_page(t), p.Hkv, g) : make_float2(1.f, 1.f);
+    };
+    if constexpr (kScaled && kDense) sc_next = fetch_scale(lane);
     for (int k = 0; k < n_j && ok; ++k) {
       const int t = tok_slot(j, k), buf = k & 1, sb = k % kSBufs;
       const int s = t % kStages;
+      PageScale sc{1.f, 0.f, 1.f, 0.f};
+      if constexpr (kScaled && kDense) {
+        if ((k & 31) == 0) {
+          sc_now = make_page_scale(sc_next);
+          sc_next = fetch_scale(k + 32 + lane);
+        }
+        sc.k = __shfl_sync(0xffffffffu, sc_now.k, k & 31);
+        sc.lv = __shfl_sync(0xffffffffu, sc_now.lv, k & 31);
+        sc.iv = __shfl_sync(0xffffffffu, sc_now.iv, k & 31);
+      } else if constexpr (kScaled) {
+        sc = tail->sc[t];
+      }
+      const float zt = kScaled ? zs * sc.k : zs;
       if (!mbar_wait(&tail->s_full[jw][sb], (k / kSBufs) & 1)) {
         ok = false;
         break;
@@ -885,8 +946,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       float al_h = 1.f;   // 2^(m_old - m_new): 1 when m stays, 0 when the head had no key
       bool raise_h = false;
       if (lane < kGroup) {
-        const float pm = fmaxf(fmaxf(mxb[lane], mxb[kGroup + lane]),
-                               fmaxf(mxb[2 * kGroup + lane], mxb[3 * kGroup + lane])) * zs;
+        const float mx4 = fmaxf(fmaxf(mxb[lane], mxb[kGroup + lane]),
+                                fmaxf(mxb[2 * kGroup + lane], mxb[3 * kGroup + lane]));
+        const float pm = kScaled ? fmaf(mx4, zt, sc.lv) : mx4 * zt;
         raise_h = pm + nref_h > kPShift + kLazy;
         if (raise_h) {
           al_h = ex2(kPShift - nref_h - pm);
@@ -921,8 +983,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int h = 0; h < kGroup; ++h) {
         // P = 2^(x - m + 8); 0 for an invisible key
-        x[h] = ex2(fmaf(x[h], zs, __shfl_sync(0xffffffffu, nref_h, h)));
-        l[h] += x[h];
+        const float nr = __shfl_sync(0xffffffffu, nref_h, h);
+        x[h] = ex2(fmaf(x[h], zt, kScaled ? nr + sc.lv : nr));
+        l[h] = kScaled ? fmaf(x[h], sc.iv, l[h]) : l[h] + x[h];
       }
       uint32_t hw[4], lw[4];
 #pragma unroll
@@ -1020,7 +1083,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int h = 0; h < kGroup; ++h) {
           const float f = (l[h] > 0.f) ? p.v_scale / l[h] : 0.f;
-          p.out[(row0 + h) * kHeadDim + d] = static_cast<uint16_t>(f32_to_bf16_bits(o[h] * f));
+          // (a range of bad slots alone leaves the accumulator as it was: no o * 0)
+          const float r = kScaled && !(l[h] > 0.f) ? 0.f : o[h] * f;
+          p.out[(row0 + h) * kHeadDim + d] = static_cast<uint16_t>(f32_to_bf16_bits(r));
         }
       } else {
         const int64_t rows = static_cast<int64_t>(p.B) * p.Q * p.Hq;
@@ -1054,6 +1119,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
+#if MSA_KV_SCALES
+cudaError_t launch_union_attend_scaled(const CUtensorMap& kv_map, const AttendParams& p,
+                                       cudaStream_t stream, bool pdl) {
+#else
 int union_ctas_per_unit(int units, int sm_count) {
   if (units >= sm_count) return 1;
   const int z = sm_count / units;
@@ -1062,6 +1131,7 @@ int union_ctas_per_unit(int units, int sm_count) {
 
 cudaError_t launch_union_attend(const CUtensorMap& kv_map, const AttendParams& p,
                                 cudaStream_t stream, bool pdl) {
+#endif
   static std::atomic<unsigned long long> attr_done{0};
   cudaError_t e = once_per_device(attr_done, [] {
     for (auto* k : {union_attend_kernel<false, false>, union_attend_kernel<true, false>,

@@ -17,6 +17,9 @@
  *   msa_score_kcache   stage 1 on a separate K-only (index-K) cache
  *   msa_*_q8           the same with an fp8 query and a per-tensor q_scale
  *   msa_decode_step    stages 1-4 of one step in one call
+ *   msa_append_kv(_prefill)  a step's keys and values into the cache, with the
+ *                      rotation of their positions (and of the query's)
+ *   msa_*_scaled       the same on a cache whose pages carry scales of their own
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -87,6 +90,8 @@ typedef struct CUstream_st *msa_stream_t;
 #define MSA_ERR_SEQ_RANGE 0x08u   /* seq_lens[b] < 0 or ceil(seq_lens[b]/128) > S     */
 #define MSA_ERR_SCORE_NAN 0x10u   /* msa_topk read a NaN score (ranked as -inf)       */
 #define MSA_ERR_TIMEOUT 0x20u     /* a bounded wait for an async copy expired         */
+#define MSA_ERR_POS_RANGE 0x40u   /* msa_append_kv: position past the rotation table  */
+#define MSA_ERR_SCALE 0x80u       /* page scale outside [2^-40, 2^40] (or NaN)        */
 
 /* ---- fixed geometry ----------------------------------------------------- */
 #define MSA_HEAD_DIM 128
@@ -446,6 +451,151 @@ int msa_decode_step(const void *q, float q_scale, const void *kv, const void *in
                     msa_stream_t stream);
 
 /*
+ * msa_append_kv -- the step before stage 1: the T = B * Q new tokens' keys and
+ * values are rotated by their positions, quantised and written to their places
+ * in the paged cache, and their queries are rotated in the same launch.
+ *
+ * Token j of request b sits at pos = seq_lens[b] - Q + j (seq_lens counts the
+ * new tokens, as everywhere) and goes to row pos % 128 of page
+ * block_table[b, pos / 128].  Padding rows (pos < 0) write nothing to the cache.
+ *
+ *   k, v, q       bf16, token i's heads contiguous at k + i * k_stride (elements;
+ *                 a multiple of 8, at least 128 times the heads), so they may be
+ *                 slices of one projection's output [T, (Hq + 2 Hkv) * 128].
+ *                 v NULL: a K-only cache [num_blocks, Hkv, 128, 128].  q NULL:
+ *                 no query (q_out unused).
+ *   cos_sin       fp32 [max_pos, rot_dim], row pos: rot_dim / 2 cosines, then
+ *                 the sines; NULL with rot_dim 0: no rotation.  The first
+ *                 rot_dim dims of every k and q head are rotated (v never is):
+ *                 pair (d, d + rot_dim / 2), or (2 d, 2 d + 1) with interleaved
+ *                 non-zero: (a, b) -> (a cos - b sin, b cos + a sin), in fp32.
+ *                 rot_dim: a multiple of 16 up to 128.
+ *   q_out         [T, Hq, 128], written whole (padding rows as 0): bf16, or with
+ *                 q_scale > 0 fp8 e4m3 codes of q / q_scale (what the _q8 entry
+ *                 points take).  May be q itself (bf16, q_stride = Hq * 128).
+ *   kv            the cache; only the new tokens' rows are written (and see
+ *                 kv_scales)
+ *   kv_scales     NULL: code = e4m3(x / k_scale), e4m3(x / v_scale), rounded to
+ *                 nearest even, saturating at 448.  Else page scales, fp32
+ *                 [num_blocks, Hkv, 2] (K's, V's; [.., 1] for a K-only cache),
+ *                 updated here: value = code * scale * k_scale (v_scale).  The
+ *                 scale of a page, KV head and side is the smallest power of two
+ *                 s >= 2^-40 with |x| <= 448 s (at most 2^40) for all finite
+ *                 x = value / k_scale written to the page so far, where a token
+ *                 written to row 0 starts the page anew and a token written
+ *                 further on keeps the rows before it: the scale then only
+ *                 grows, and when it does, those rows are requantised
+ *                 (code' = e4m3(code * old / new)).
+ *
+ * Two requests that append to one page in one call, or calls that overlap on
+ * the GPU and append to one page, race: pages that requests share are full ones.
+ * Numerics: fp32 from the bf16 inputs to the one rounding at the end; division by
+ * a scale is a multiplication by its fp32 reciprocal.  NaN is stored as NaN,
+ * infinities as +-448 codes.
+ * Errors: MSA_EINVAL for Q outside 1..32, sizes as msa_score (Hq = 16 * Hkv
+ * also without a query), null k, kv, block_table or seq_lens, null q_out with q,
+ * strides and rot_dim as above, rot_dim > 0 without cos_sin or max_pos < 1,
+ * scales not finite or <= 0 (q_scale 0 allowed), k, v, q, kv, q_out, cos_sin not
+ * 16-byte aligned, kv_scales not 8-byte aligned.  Device: MSA_ERR_PAGE_RANGE
+ * (the tokens of that page are not written), MSA_ERR_SEQ_RANGE (request treated
+ * as empty), MSA_ERR_POS_RANGE (pos >= max_pos: the token is not written, its
+ * q_out row is 0), MSA_ERR_SCALE (page begun earlier whose scale is out of
+ * range: not written).
+ */
+int msa_append_kv(const void *k, int64_t k_stride, const void *v, int64_t v_stride, const void *q,
+                  int64_t q_stride, const float *cos_sin, int max_pos, int rot_dim,
+                  int interleaved, void *kv, float *kv_scales, void *q_out, float q_scale,
+                  const int32_t *block_table, const int32_t *seq_lens, int B, int Q, int Hq,
+                  int Hkv, int S, int64_t num_blocks, float k_scale, float v_scale,
+                  msa_stream_t stream);
+
+/*
+ * msa_append_kv_prefill -- msa_append_kv for prefill and chunked prefill: B
+ * requests with one query length each, tokens and positions as
+ * msa_sparse_prefill (cu_seqlens_q [B + 1] on the device, T tokens).  Errors as
+ * msa_append_kv and, for cu_seqlens_q, B and T, as msa_sparse_prefill.  Device:
+ * a token in no request's range, or a request with q_len_b > seq_lens[b], sets
+ * MSA_ERR_SEQ_RANGE; its tokens are not written and their q_out rows are 0.
+ */
+int msa_append_kv_prefill(const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                          const void *q, int64_t q_stride, const float *cos_sin, int max_pos,
+                          int rot_dim, int interleaved, void *kv, float *kv_scales, void *q_out,
+                          float q_scale, const int32_t *block_table, const int32_t *seq_lens,
+                          const int32_t *cu_seqlens_q, int B, int T, int Hq, int Hkv, int S,
+                          int64_t num_blocks, float k_scale, float v_scale, msa_stream_t stream);
+
+/*
+ * msa_*_scaled -- the scorer, the attends and the step on a cache whose pages
+ * carry scales of their own: kv_scales fp32 [num_blocks, Hkv, 2], a page's K
+ * and V scale per KV head, so that
+ *
+ *   K = K8 * k_scale * kv_scales[page, g, 0],  V = V8 * v_scale * kv_scales[page, g, 1]
+ *
+ * take the places of K8 * k_scale and V8 * v_scale in the entry point without
+ * the suffix; everything else is that entry point's.  q_scale 0: q is bf16;
+ * > 0: fp8 e4m3 of value q * q_scale.  Scales are any numbers in [2^-40, 2^40]
+ * (msa_append_kv writes powers of two).  Numerics: the K scale multiplies the
+ * page's logits in fp32; the V scale enters the softmax reference, so that the
+ * fp8 probabilities of a page are relative to its values' size (about 8
+ * significant bits of P for every page whose P * V scale is within 2^-17 of the
+ * largest).  Errors: as without the suffix, plus null or not 8-byte aligned
+ * kv_scales (4-byte for a K-only cache) (MSA_EINVAL).  Device: MSA_ERR_SCALE (a
+ * listed or visible page with a scale out of range, either side for the
+ * attends, K's for the scorer: the page is skipped, its score is -inf).
+ * Workspaces and split counts: as without the suffix.
+ */
+/* k_only non-zero: kv is a K-only cache (msa_score_kcache), kv_scales
+ * [num_blocks, Hkv, 1]. */
+int msa_score_scaled(const void *q, float q_scale, const void *kv, const float *kv_scales,
+                     int k_only, const int32_t *block_table, const int32_t *seq_lens,
+                     float *scores, int B, int Q, int Hq, int Hkv, int S, int64_t num_blocks,
+                     float sm_scale, float k_scale, msa_stream_t stream);
+int msa_sparse_decode_scaled(const void *q, float q_scale, const void *kv, const float *kv_scales,
+                             const int32_t *block_table, const int32_t *seq_lens,
+                             const int32_t *topk, void *workspace, size_t workspace_bytes,
+                             void *out, int B, int Q, int Hq, int Hkv, int S, int64_t num_blocks,
+                             float sm_scale, float k_scale, float v_scale, int num_splits,
+                             msa_stream_t stream);
+int msa_sparse_decode_select_scaled(const void *q, float q_scale, const void *kv,
+                                    const float *kv_scales, const int32_t *block_table,
+                                    const int32_t *seq_lens, const float *scores,
+                                    int64_t stride_h, int64_t stride_t, int64_t stride_n,
+                                    int32_t *topk, void *workspace, size_t workspace_bytes,
+                                    void *out, int B, int Q, int Hq, int Hkv, int S,
+                                    int64_t num_blocks, float sm_scale, float k_scale,
+                                    float v_scale, int num_splits, msa_stream_t stream);
+int msa_dense_decode_scaled(const void *q, float q_scale, const void *kv, const float *kv_scales,
+                            const int32_t *block_table, const int32_t *seq_lens, void *workspace,
+                            size_t workspace_bytes, void *out, int B, int Q, int Hq, int Hkv,
+                            int S, int64_t num_blocks, float sm_scale, float k_scale,
+                            float v_scale, msa_stream_t stream);
+int msa_sparse_prefill_scaled(const void *q, float q_scale, const void *kv,
+                              const float *kv_scales, const int32_t *block_table,
+                              const int32_t *seq_lens, const int32_t *cu_seqlens_q,
+                              const int32_t *topk, void *workspace, size_t workspace_bytes,
+                              void *out, int B, int T, int Hq, int Hkv, int S, int64_t num_blocks,
+                              float sm_scale, float k_scale, float v_scale, int num_splits,
+                              msa_stream_t stream);
+int msa_sparse_prefill_select_scaled(const void *q, float q_scale, const void *kv,
+                                     const float *kv_scales, const int32_t *block_table,
+                                     const int32_t *seq_lens, const int32_t *cu_seqlens_q,
+                                     const float *scores, int64_t stride_h, int64_t stride_t,
+                                     int64_t stride_n, int32_t *topk, void *workspace,
+                                     size_t workspace_bytes, void *out, int B, int T, int Hq,
+                                     int Hkv, int S, int64_t num_blocks, float sm_scale,
+                                     float k_scale, float v_scale, int num_splits,
+                                     msa_stream_t stream);
+/* index_k (NULL: none) is a K-only cache with its own index_scales
+ * [num_blocks, Hkv, 1] (NULL: index_k_scale alone). */
+int msa_decode_step_scaled(const void *q, float q_scale, const void *kv, const float *kv_scales,
+                           const void *index_k, float index_k_scale, const float *index_scales,
+                           const int32_t *block_table, const int32_t *seq_lens, float *scores,
+                           int32_t *topk, void *workspace, size_t workspace_bytes, void *out,
+                           int B, int Q, int Hq, int Hkv, int S, int64_t num_blocks,
+                           float sm_scale, float k_scale, float v_scale, int num_splits,
+                           msa_stream_t stream);
+
+/*
  * msa_set_union_tile -- how msa_sparse_decode(_select) (and msa_decode_step,
  * msa_sparse_decode_static) attend decode steps of Q >= 2 tokens per request.
  * Off (0, the default): one CTA per (token, KV head), each loading its own
@@ -475,6 +625,8 @@ int msa_set_union_tile(int enable);
  * that call's inputs: a kernel that wrote them could otherwise be read
  * before its writes are visible.  Outputs are always ordered: no library
  * kernel writes a buffer before the previous kernel has finished.
+ * msa_append_kv(_prefill), whose outputs are the other calls' inputs, reads
+ * nothing early and has finished before a kernel enqueued after it starts.
  * Process-wide; returns the previous setting (0 or 1).
  */
 int msa_set_input_overlap(int enable);
