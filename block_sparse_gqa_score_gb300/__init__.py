@@ -130,6 +130,21 @@ def _page_scales(kv_scales, name: str, dev, num_blocks: int, num_kv_heads: int, 
     return kv_scales.data_ptr()
 
 
+def _parts(num_splits: int, kv_scales, batch: int, qlen: int, num_q_heads: int, num_kv_heads: int,
+           workspace, dev):
+    """(split count, workspace, its address and bytes) of an attend on lists: with
+    page scales the library cuts a row by itself and needs no workspace."""
+    if num_splits <= 0 and kv_scales is not None:
+        return 0, None, None, 0
+    splits = num_splits if num_splits > 0 else choose_splits(batch, qlen, num_kv_heads)
+    need = workspace_bytes(batch, qlen, num_q_heads, splits)
+    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if workspace is None:
+        return splits, None, None, 0
+    return splits, workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def score(q, kv, block_table, seq_lens, qlen: int, sm_scale: float, k_scale: float = 1.0,
           scores: torch.Tensor | None = None, stream=None, q_scale: float = 1.0,
           kv_scales: torch.Tensor | None = None) -> torch.Tensor:
@@ -197,12 +212,8 @@ def sparse_decode(q, kv, block_table, seq_lens, topk_idx, qlen: int, sm_scale: f
     if out is None:
         out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
     _need(out, "out", (torch.bfloat16,), dev)
-    splits = num_splits if num_splits > 0 else choose_splits(B, qlen, Hkv)
-    need = workspace_bytes(B, qlen, Hq, splits)
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    ws_ptr = workspace.data_ptr() if workspace is not None else None
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    splits, workspace, ws_ptr, ws_bytes = _parts(num_splits, kv_scales, B, qlen, Hq, Hkv,
+                                                 workspace, dev)
     args = (kv.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), topk_idx.data_ptr(), ws_ptr,
             ws_bytes, out.data_ptr(), B, qlen, Hq, Hkv, S, NB, float(sm_scale), float(k_scale),
             float(v_scale), splits, _stream(dev, stream))
@@ -294,12 +305,8 @@ def sparse_decode_select(q, kv, block_table, seq_lens, scores, qlen: int, sm_sca
     if out is None:
         out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
     _need(out, "out", (torch.bfloat16,), dev)
-    splits = num_splits if num_splits > 0 else choose_splits(B, qlen, Hkv)
-    need = workspace_bytes(B, qlen, Hq, splits)
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    ws_ptr = workspace.data_ptr() if workspace is not None else None
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    splits, workspace, ws_ptr, ws_bytes = _parts(num_splits, kv_scales, B, qlen, Hq, Hkv,
+                                                 workspace, dev)
     sh, st, sn = scores.stride()
     args = (kv.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), scores.data_ptr(), sh, st,
             sn, topk_out.data_ptr(), ws_ptr, ws_bytes, out.data_ptr(), B, qlen, Hq, Hkv, S, NB,
@@ -326,17 +333,6 @@ def _prefill_geometry(q, kv, block_table, seq_lens, cu_seqlens_q):
     return dev, B, int(q.shape[0]), S, Hq, Hkv, NB
 
 
-def _prefill_splits(T: int, Hq: int, Hkv: int, num_splits: int, workspace, dev):
-    # one CTA per token: the single-token rule, choose_splits(T, 1, ...)
-    splits = num_splits if num_splits > 0 else choose_splits(max(T, 1), 1, Hkv)
-    need = workspace_bytes(max(T, 1), 1, Hq, splits)
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    ws_ptr = workspace.data_ptr() if workspace is not None else None
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    return splits, ws_ptr, ws_bytes
-
-
 def sparse_prefill(q, kv, block_table, seq_lens, cu_seqlens_q, topk_idx, sm_scale: float,
                    k_scale: float = 1.0, v_scale: float = 1.0, out: torch.Tensor | None = None,
                    num_splits: int = 0, workspace: torch.Tensor | None = None, stream=None,
@@ -354,7 +350,9 @@ def sparse_prefill(q, kv, block_table, seq_lens, cu_seqlens_q, topk_idx, sm_scal
     if out is None:
         out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
     _need(out, "out", (torch.bfloat16,), dev)
-    splits, ws_ptr, ws_bytes = _prefill_splits(T, Hq, Hkv, num_splits, workspace, dev)
+    # one CTA per token: the single-token rule, choose_splits(T, 1, ...)
+    splits, workspace, ws_ptr, ws_bytes = _parts(num_splits, kv_scales, max(T, 1), 1, Hq, Hkv,
+                                                 workspace, dev)
     args = (kv.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), cu_seqlens_q.data_ptr(),
             topk_idx.data_ptr(), ws_ptr, ws_bytes, out.data_ptr(), B, T, Hq, Hkv, S, NB,
             float(sm_scale), float(k_scale), float(v_scale), splits, _stream(dev, stream))
@@ -393,7 +391,9 @@ def sparse_prefill_select(q, kv, block_table, seq_lens, cu_seqlens_q, scores, sm
     if out is None:
         out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
     _need(out, "out", (torch.bfloat16,), dev)
-    splits, ws_ptr, ws_bytes = _prefill_splits(T, Hq, Hkv, num_splits, workspace, dev)
+    # one CTA per token: the single-token rule, choose_splits(T, 1, ...)
+    splits, workspace, ws_ptr, ws_bytes = _parts(num_splits, kv_scales, max(T, 1), 1, Hq, Hkv,
+                                                 workspace, dev)
     sh, st, sn = scores.stride()
     args = (kv.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), cu_seqlens_q.data_ptr(),
             scores.data_ptr(), sh, st, sn, topk_out.data_ptr(), ws_ptr, ws_bytes, out.data_ptr(),
@@ -499,7 +499,8 @@ def decode_step(q, kv, block_table, seq_lens, qlen: int, sm_scale: float, k_scal
         *head, *index,
         block_table.data_ptr(), seq_lens.data_ptr(), bf.scores.data_ptr(), bf.topk.data_ptr(),
         ws_ptr, ws_bytes, bf.out.data_ptr(), B, qlen, Hq, Hkv, S, NB, float(sm_scale),
-        float(k_scale), float(v_scale), bf.num_splits, _stream(dev, stream))
+        float(k_scale), float(v_scale), bf.num_splits if kv_scales is None else 0,
+        _stream(dev, stream))
     _native.check(st, "msa_decode_step")
     return bf.scores, bf.topk, bf.out
 

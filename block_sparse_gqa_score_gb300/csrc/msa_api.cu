@@ -362,6 +362,12 @@ int prepare_attend(const void* q, const void* kv, const int32_t* block_table,
     const int64_t units = static_cast<int64_t>(B) * ((Q + msa::kUnionTile - 1) / msa::kUnionTile) * Hkv;
     if (units >= dev->sm_count) splits = 1;
   }
+  if (kv_scales) {
+    // page scales: lists are cut over a cluster's CTAs unless the caller asks
+    // for parts; dense decode of single tokens fills two CTAs an SM, as above
+    if (dense_span == 0 && num_splits == 0) splits = 1;
+    if (dense_span > 0 && Q == 1 && static_cast<int64_t>(B) * Hkv >= 2 * dev->sm_count) splits = 1;
+  }
   const size_t need = msa_workspace_bytes(tb, tq, Hq, splits);
   if (splits > 1 && (!workspace || !aligned(workspace, 16) || workspace_bytes < need))
     return MSA_ENOSPC;

@@ -40,27 +40,15 @@
 // map each token to its request by a warp-wide search and then run as decode
 // tokens.  Dense decode, the fp8 query and prefill batches are template
 // flags, so the bf16 list-mode decode kernel carries none of their branches.
-//
-// This file is compiled twice: as it stands (one scale per tensor), and with
-// MSA_KV_SCALES set (by msa_attend_scaled.cu) for a cache whose pages carry
-// scales of their own, one per page, KV head and side.  There the K scale goes
-// into the page's logit factor and the V scale into the softmax reference (see
-// PageScale): 16 multiplies and 16 adds more per key and page, and no
-// instruction in the kernels compiled as they stand.
 #include "msa_device.cuh"
 #include "msa_launch.h"
 #include "msa_select.cuh"
 #include "msa_tcgen05.cuh"
 
-#ifndef MSA_KV_SCALES
-#define MSA_KV_SCALES 0
-#endif
-
 namespace msa {
 
 namespace {
 
-constexpr bool kScaled = MSA_KV_SCALES != 0;  // page scales (AttendParams::kv_scales)
 constexpr int kStages = 3;
 constexpr int kWarps = 7;
 constexpr int kThreads = kWarps * 32;
@@ -99,7 +87,6 @@ struct AttendTail {
   float zs;                 // logit scale (log2 units) times 2^e of the query split
   int pages[kMaxPages];
   int blocks[kMaxPages];
-  PageScale sc[kScaled ? kMaxPages : 1];
 };
 
 // shared-memory layout (offsets from a 1024-byte aligned base)
@@ -337,16 +324,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         tma_load_2d(st + kHalfTile, &kv_map, kHeadDim, row, &tail->full[t]);
       }
     }
-    if constexpr (kScaled) {
-      // the listed pages' scales, behind the first loads: a page whose scales
-      // are out of range keeps its slot and is attended by no key
-      __syncwarp();
-      for (int t = lane; t < np; t += 32) {
-        const PageScale s = make_page_scale(load_page_scale(p.kv_scales, tail->pages[t], p.Hkv, g));
-        if (s.bad != 0.f) flag_error(p.err, MSA_ERR_SCALE);
-        tail->sc[t] = s;
-      }
-    }
   } else if (warp == 1) {
     tc::tmem_alloc(&tail->tmem_base, kTmemCols);
     tc::tmem_relinquish();
@@ -460,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // running sum; o: the running output of value dim `key`.  Both are kept
     // relative to the current m.
     float nref[kGroup], l[kGroup], o[kGroup];
-    fill(nref, kScaled ? kNoRef : INFINITY);
+    fill(nref, INFINITY);
     fill(l, 0.f);
     fill(o, 0.f);
     bool ok = true;
@@ -490,8 +467,6 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       tc::fence_after_thread_sync();
       float x[kGroup], pm[kGroup];
-      const PageScale sc = kScaled ? tail->sc[t] : PageScale{1.f, 0.f, 1.f, 0.f};
-      const float zt = kScaled ? zs * sc.k : zs;
       {
         uint32_t sv[32];
         tc::ld_32x32b_x32(lane_addr + kColS + 2 * kGroup * buf, sv);
@@ -499,11 +474,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         tc::fence_before_thread_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&tail->s_empty[buf]);
-        // keys <= lim are visible
-        const int lim = kScaled && sc.bad != 0.f ? -1 : pos - tail->blocks[t] * kPage;
+        const int lim = pos - tail->blocks[t] * kPage;  // keys <= lim are visible
         const bool vis = key <= lim;
         // raw dot products (hi + lo columns); the logit in log2 units is
-        // s * zt with zt > 0, so maxima can be taken on s
+        // s * zs with zs > 0, so maxima can be taken on s
 #pragma unroll
         for (int h = 0; h < kGroup; ++h)
           x[h] = vis ? __uint_as_float(sv[h]) + __uint_as_float(sv[h + kGroup]) : -INFINITY;
@@ -539,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       bool raise = false;
 #pragma unroll
       for (int h = 0; h < kGroup; ++h) {
-        pm[h] = kScaled ? fmaf(pm[h], zt, sc.lv) : pm[h] * zt;
+        pm[h] *= zs;
         raise |= pm[h] + nref[h] > kPShift + kLazy;
       }
       float al[kGroup];  // 2^(m_old - m_new) per head
@@ -556,9 +530,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
 #pragma unroll
       for (int h = 0; h < kGroup; ++h) {
-        // P = 2^(x - m + 8); 0 for an invisible key
-        x[h] = ex2(fmaf(x[h], zt, kScaled ? nref[h] + sc.lv : nref[h]));
-        l[h] = kScaled ? fmaf(x[h], sc.iv, l[h] * al[h]) : fmaf(l[h], al[h], x[h]);
+        x[h] = ex2(fmaf(x[h], zs, nref[h]));  // P = 2^(x - m + 8); 0 for an invisible key
+        l[h] = fmaf(l[h], al[h], x[h]);
       }
       uint32_t hw[4], lw[4];
 #pragma unroll
@@ -570,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         lw[q4] = l0 | (l1 << 16);
       }
       const int s = t % kStages;
-      const int lim = kScaled && sc.bad != 0.f ? -1 : pos - tail->blocks[t] * kPage;
+      const int lim = pos - tail->blocks[t] * kPage;
       if (lim < kPage - 1 && key > lim) {
         // keys past the causal limit have P = 0, but their value rows may hold
         // any bytes (an fp8 NaN times 0 is NaN): zero them for the O^T product
@@ -673,7 +646,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-#if !MSA_KV_SCALES
 // Split merge: one warp per (token, query head) row, 4 d-values per lane.
 // A part counts only when its l > 0 and its m is a number.
 __global__ void __launch_bounds__(256)
@@ -709,17 +681,12 @@ __global__ void __launch_bounds__(256)
   const uint32_t hi = f32_to_bf16_bits(acc.z * f) | (f32_to_bf16_bits(acc.w * f) << 16);
   *reinterpret_cast<uint2*>(out + r * kHeadDim + 4 * lane) = make_uint2(lo, hi);
 }
-#endif
+
 
 }  // namespace
 
-#if MSA_KV_SCALES
-cudaError_t launch_attend_scaled(const CUtensorMap& kv_map, const AttendParams& p,
-                                 cudaStream_t stream, bool pdl) {
-#else
 cudaError_t launch_attend(const CUtensorMap& kv_map, const AttendParams& p, cudaStream_t stream,
                           bool pdl) {
-#endif
   static_assert(kSmemBytes <= 227 * 1024, "attend shared memory");
   static std::atomic<unsigned long long> attr_done{0};
   cudaError_t e = once_per_device(attr_done, [] {
@@ -740,9 +707,7 @@ cudaError_t launch_attend(const CUtensorMap& kv_map, const AttendParams& p, cuda
   });
   if (e != cudaSuccess) return e;
   // the union attend: one pass over the pages a 4-token tile shares
-  if (p.union_tile)
-    return kScaled ? launch_union_attend_scaled(kv_map, p, stream, pdl)
-                   : launch_union_attend(kv_map, p, stream, pdl);
+  if (p.union_tile) return launch_union_attend(kv_map, p, stream, pdl);
   const int T = p.cu_q ? p.T : p.B * p.Q;
   dim3 grid(T, p.Hkv, p.splits);
   const dim3 block(kThreads);
@@ -772,7 +737,6 @@ cudaError_t launch_attend(const CUtensorMap& kv_map, const AttendParams& p, cuda
                  : launch_pdl(attend_kernel<false, false>, grid, block, kSmemBytes, stream, pdl, kv_map, p);
 }
 
-#if !MSA_KV_SCALES
 cudaError_t launch_combine(const float* part_o, const float* part_ml, uint16_t* out, int64_t rows,
                            int splits, cudaStream_t stream, bool pdl) {
   const int64_t threads = rows * 32;
@@ -781,6 +745,5 @@ cudaError_t launch_combine(const float* part_o, const float* part_ml, uint16_t* 
   return launch_pdl(combine_kernel, dim3(static_cast<unsigned>(grid)), dim3(block), 0, stream, pdl,
                     part_o, part_ml, out, rows, splits);
 }
-#endif
 
 }  // namespace msa

@@ -1,4 +1,888 @@
-// msa_attend_scaled.cu -- the attend kernels for a cache with page scales
-// (launch_attend_scaled).
-#define MSA_KV_SCALES 1
-#include "msa_attend.cu"
+// msa_attend_scaled.cu -- the attend on a cache with page scales: sparse decode
+// and prefill on lists (given, or selected in the prologue), and dense decode.
+//
+// Operation (msa_*_scaled in include/msa.h): for each query row the keys of its
+// listed (dense decode: all) pages up to its position, with K = K8 ks[page] and
+// V = V8 vs[page] per KV head; an empty key set gives 0.
+//
+// Mathematics.  With z the logit in log2 units and u = z + log2(vs[page]),
+//
+//   out = sum_t 2^(u_t - M) V8_t / sum_t 2^(u_t - M) / vs[page(t)],
+//
+// so the fp8 product takes weights P = 2^(u - M) that are relative to what a
+// page contributes, and the running sum divides each page's by vs again.  u is
+// one FFMA from the raw dot product: factor ks * sm_scale * log2(e) * 2^e (2^e
+// of the query split), addend log2(vs) - M.  M is a running reference, not the
+// running maximum: P = 2^(kPShift) at the largest u when M is set, and M stays
+// until some P would pass 2^kPTop (e4m3 holds 448).  Whether it does is one vote
+// a page: the largest of a thread's 16 u against the bound, or-ed over the
+// token's four warps by one barrier; only then are the exact maxima of the 16
+// heads formed and exchanged and the sums and the accumulator rescaled.  (With
+// exact maxima on every page a warp issued about 650 instructions a page; the
+// vote leaves about 200.)  With kPShift two binades below the top, P >= 2^-2 of
+// every term within 2^-8.5 of the largest is carried to 8 significant bits by
+// its two e4m3 parts, smaller ones to 2^-10 absolutely.
+//
+// Layout: as the attend for one scale per tensor.  One CTA per (tile of kNT
+// tokens of one request, KV head, part); the tile's 16 kNT query rows are the N
+// of two transposed tensor-core products per page, S^T = K Q^T (the bf16 query
+// as exact fp8 hi and lo parts, N = 32 per token; an fp8 query as it is, N = 16)
+// and O^T += V^T P^T (P's hi and lo parts, N = 32 per token), so that the page's
+// 128 keys, then its 128 value dims, fill M, and fp8 pages are operands as
+// stored.  O^T stays in tensor memory over all pages.  kNT = 1 (lists, and dense
+// decode of single tokens): two CTAs an SM with 3-stage rings of 32 KiB pages;
+// kNT = 4 (dense decode of two or more tokens a request): one CTA an SM, five
+// stages, each page loaded once for four tokens.
+//   warp 0       page lists, scales, TMA
+//   warp 1       S^T products (and owns tensor memory)
+//   warp 2       O^T products
+//   warps 3..    four per token: softmax, output.  A thread owns one key.
+//
+// What bounds it: bytes from HBM in decode, from L2 in prefill; the pages of a
+// short call are cut over the CTAs of a cluster (kNT = 1), which merge their
+// parts through distributed shared memory, so that a small batch needs neither
+// a workspace nor a second kernel.
+#include <cstddef>
+
+#include "msa_dense_slot.cuh"
+#include "msa_device.cuh"
+#include "msa_launch.h"
+#include "msa_select.cuh"
+#include "msa_tcgen05.cuh"
+
+namespace msa {
+
+namespace {
+
+constexpr int kStageBytes = 2 * kHalfTile;    // K tile then V tile
+constexpr float kPShift = 6.5f;               // P = 2^kPShift at the largest u when M is set
+constexpr float kPTop = 8.5f;                 // M moves when some P would pass 2^kPTop
+constexpr int kChunk = 32;                    // dense decode: pages looked up at once, one a lane
+constexpr int kSelectCap = 8000;              // selector keys in stage 1, then its slots
+constexpr int kMaxCluster = 8;
+
+enum Mode { kLists, kSelect, kDense };
+
+struct alignas(16) PageInfo {
+  float k, lv, iv;   // as PageScale
+  int block;         // logical block, -1: no key of this page is attended
+};
+
+template <int kNT>
+struct Tail {
+  static constexpr int kStages = kNT == 1 ? 3 : 5;
+  uint64_t full[kStages];   // TMA -> S^T
+  uint64_t empty[kStages];  // O^T (a stage's last reader) -> TMA
+  uint64_t s_full[2];       // S^T ready -> softmax
+  uint64_t s_empty[2];      // softmax has read S^T
+  uint64_t p_full[2];       // P^T written -> O^T
+  uint64_t o_done[2];       // O^T of a page complete (its P^T buffer free)
+  uint64_t finish;          // every role done and every product complete
+  uint32_t tmem_base;
+  int n_pages;
+  int ok;                   // 0: some softmax warp gave up on a wait
+  int pos[kNT];             // token positions, -1: none
+  float zs[kNT];            // logit scale (log2 units) times 2^e of each token's query split
+  int pages[kChunk];        // list modes: this CTA's pages
+  PageInfo info[2 * kChunk];
+  alignas(16) float mx[kNT][kGroup][4];     // page maxima by quarter
+  alignas(16) float lsum[kNT][4][kGroup];   // running sums by quarter
+  float ml[kGroup][2];          // cluster merge: (m, l) of this CTA's part
+};
+// read and written as float4
+static_assert(alignof(Tail<1>) == 16 && offsetof(Tail<1>, mx) % 16 == 0 &&
+              offsetof(Tail<1>, lsum) % 16 == 0 && offsetof(Tail<1>, info) % 16 == 0, "float4 access");
+static_assert(alignof(Tail<4>) == 16 && offsetof(Tail<4>, mx) % 16 == 0 &&
+              offsetof(Tail<4>, lsum) % 16 == 0 && offsetof(Tail<4>, info) % 16 == 0, "float4 access");
+
+template <int kNT>
+struct Smem {
+  static constexpr int kStages = Tail<kNT>::kStages;
+  static constexpr int kPBlock = 8 * 32 * kNT;   // P^T: 8 keys x (hi, lo) of each token
+  static constexpr int kPBuf = kPage * 32 * kNT;
+  static constexpr int kQ = kStages * kStageBytes;
+  static constexpr int kP = kQ + 32 * kNT * 128;
+  static constexpr int kTail = kP + 2 * kPBuf;
+  static constexpr int kBytes = kTail + static_cast<int>((sizeof(Tail<kNT>) + 15) / 16 * 16) + 1024;
+  static_assert(kQ % 1024 == 0 && kP % 1024 == 0 && kTail % 16 == 0,
+                "operand tiles need 1024-byte alignment");
+};
+static_assert(4 * kSelectCap + 4 * kTopK <= kStageBytes, "selector scratch fits stage 1");
+static_assert(2 * (Smem<1>::kBytes + 1024) <= 228 * 1024, "two CTAs an SM");
+static_assert(Smem<4>::kBytes <= 227 * 1024, "one CTA an SM");
+static_assert(kGroup * kHeadDim * 4 <= kStageBytes, "a CTA's part fits a stage");
+
+// The barrier of one token's four warps, with the or of a predicate.
+__device__ __forceinline__ bool barrier_or(int id, bool pred) {
+  unsigned r;
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "barrier.cta.red.or.aligned.pred p, %2, 128, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(pred ? 1u : 0u), "r"(id)
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// A 32-bit load from the same place in the shared memory of cluster CTA `rank`.
+__device__ __forceinline__ float ld_peer(const float* own, uint32_t rank) {
+  float v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\t"
+      "mapa.shared::cluster.u32 a, %1, %2;\n\t"
+      "ld.shared::cluster.f32 %0, [a];\n\t}"
+      : "=f"(v)
+      : "r"(smem_u32(own)), "r"(rank)
+      : "memory");
+  return v;
+}
+
+__device__ __forceinline__ PageInfo page_info(const AttendParams& p, float2 scales, int block) {
+  const PageScale s = make_page_scale(scales);
+  if (s.bad != 0.f) flag_error(p.err, MSA_ERR_SCALE);
+  return PageInfo{s.k, s.lv, s.iv, s.bad != 0.f ? -1 : block};
+}
+
+// kNT tokens a tile; kCluster: the pages of a part are cut over a cluster's CTAs.
+template <int kNT, Mode kMode, bool kFp8Q, bool kVarlen, bool kCluster>
+__global__ void __launch_bounds__(32 * (3 + 4 * kNT), kNT == 1 ? 2 : 1)
+    scaled_attend_kernel(const __grid_constant__ CUtensorMap kv_map, const AttendParams p) {
+  using Sm = Smem<kNT>;
+  constexpr int kStages = Sm::kStages;
+  constexpr int kQRows = kFp8Q ? kGroup : 2 * kGroup;      // query tile rows of one token
+  constexpr int kSN = kQRows * kNT;                        // columns of one S^T buffer
+  constexpr uint32_t kColAcc = 2 * 2 * kGroup * kNT;       // O^T behind two S^T buffers
+  constexpr int kTmemCols = kNT == 1 ? 128 : 512;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  Tail<kNT>* tail = reinterpret_cast<Tail<kNT>*>(smem + Sm::kTail);
+  uint8_t* qtile = smem + Sm::kQ;
+  uint8_t* pbuf = smem + Sm::kP;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // ---- this CTA's work: token tile, KV head, part of nparts, cluster rank ----------
+  uint32_t cs = 1, rank = 0;
+  if constexpr (kCluster) {
+    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cs));
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  }
+  const int cx = kCluster ? static_cast<int>(blockIdx.x / cs) : static_cast<int>(blockIdx.x);
+  const int ntiles = kMode == kDense ? (p.Q + kNT - 1) / kNT : 1;
+  int b = 0, tok0 = 0, qlen = p.Q, g, split, nsplit;   // tok0: first token of the tile
+  int64_t row_tok = 0;                                 // its row among the batch's tokens
+  bool tok_ok = true;
+  if constexpr (kMode == kDense) {
+    const DenseSlot ds = dense_slot<kNT>(p, ntiles, static_cast<int>(kCluster ? gridDim.x / cs : gridDim.x),
+                                         cx, lane);
+    if (ds.unit < 0) return;   // the whole cluster: no unit left for it
+    g = ds.unit % p.Hkv;
+    tok0 = kNT * ((ds.unit / p.Hkv) % ntiles);
+    b = ds.unit / (p.Hkv * ntiles);
+    split = ds.part;
+    nsplit = ds.nparts;
+    row_tok = static_cast<int64_t>(b) * p.Q + tok0;
+  } else {
+    g = static_cast<int>(blockIdx.y);
+    split = static_cast<int>(blockIdx.z);
+    nsplit = p.splits;
+    row_tok = cx;
+    if constexpr (kVarlen) {
+      tok_ok = varlen_token(p.cu_q, p.B, cx, lane, b, tok0, qlen);
+    } else {
+      b = cx / p.Q;
+      tok0 = cx - b * p.Q;
+    }
+  }
+  const int32_t* trow = p.block_table + static_cast<int64_t>(b) * p.S;
+  const int L = p.seq_lens[b];
+  // a prefill request's tokens are the last qlen of its sequence
+  const bool seq_ok = tok_ok && L >= 0 && (L == 0 || (L - 1) / kPage < p.S) &&
+                      (!kVarlen || L >= qlen);
+  auto token_pos = [&](int j) -> int {
+    return seq_ok && tok0 + j < qlen ? L - qlen + tok0 + j : -1;
+  };
+  int last_pos = -1, valid_toks = 0, last_tok = 0;   // last_tok: the largest position's
+#pragma unroll
+  for (int j = 0; j < kNT; ++j) {
+    const int q = token_pos(j);
+    if (q >= 0) {
+      last_pos = q;
+      last_tok = j;
+      ++valid_toks;
+    }
+  }
+  // dense decode: this CTA's blocks [lo, hi)
+  int lo = 0, hi = 0;
+  if constexpr (kMode == kDense) {
+    const int nblk = last_pos >= 0 ? last_pos / kPage + 1 : 0;
+    const int64_t of = static_cast<int64_t>(nsplit) * cs, at = static_cast<int64_t>(split) * cs + rank;
+    lo = static_cast<int>(nblk * at / of);
+    hi = static_cast<int>(nblk * (at + 1) / of);
+  }
+
+  // ---- prologue ----------------------------------------------------------------------
+  // dense decode, warp 0: the lane's page of the next chunk, its block (-1: none) and scales
+  int pg_next = 0, blk_next = -1;
+  float2 sc_next = make_float2(1.f, 1.f);
+  auto load_page = [&](int t, int page) {   // one lane: page `page` into stage t % kStages
+    const int s = t % kStages;
+    uint8_t* st = smem + s * kStageBytes;
+    const int row = (page * p.Hkv + g) * kPage;
+    mbar_arrive_expect_tx(&tail->full[s], kStageBytes);
+    tma_load_2d(st, &kv_map, 0, row, &tail->full[s]);
+    tma_load_2d(st + kHalfTile, &kv_map, kHeadDim, row, &tail->full[s]);
+  };
+  // dense decode: the lane's page of slot t (a bad table entry: page 0 instead,
+  // attended by no key), then its scales
+  auto look_up = [&](int t) {
+    pg_next = 0;
+    blk_next = -1;
+    if (lo + t < hi) {
+      const int pg = trow[lo + t];
+      if (pg >= 0 && static_cast<int64_t>(pg) < p.num_blocks) {
+        pg_next = pg;
+        blk_next = lo + t;
+      } else {
+        flag_error(p.err, MSA_ERR_PAGE_RANGE);
+      }
+    }
+  };
+  auto look_up_scales = [&] {
+    sc_next = load_page_scale(p.kv_scales, pg_next, p.Hkv, g);
+  };
+  auto next_info = [&]() -> PageInfo {
+    return blk_next >= 0 ? page_info(p, sc_next, blk_next) : PageInfo{1.f, 0.f, 1.f, -1};
+  };
+  if (warp == 0) {
+    if (!seq_ok && lane == 0 && split == 0 && rank == 0) flag_error(p.err, MSA_ERR_SEQ_RANGE);
+    const int cur = last_pos >= 0 ? last_pos / kPage : -1;
+    const int part = split * static_cast<int>(cs) + static_cast<int>(rank);
+    const int nparts = nsplit * static_cast<int>(cs);
+    if (kMode != kDense && 32 * lane < p.S)   // the table row's lines, for the look-ups below
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(trow + 32 * lane));
+    int pre_page = -1;   // select mode: the current block's page, always listed, first
+    if (kMode == kSelect && cur >= 0 && part == 0) {
+      const int pg = trow[cur];
+      if (pg >= 0 && static_cast<int64_t>(pg) < p.num_blocks) pre_page = pg;
+    }
+    if (lane == 0) {
+      const unsigned warps = 4u * static_cast<unsigned>(max(valid_toks, 1));
+      for (int s = 0; s < kStages; ++s) {
+        mbar_init(&tail->full[s], 1);
+        mbar_init(&tail->empty[s], 1);
+      }
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(&tail->s_full[s], 1);
+        mbar_init(&tail->s_empty[s], warps);
+        mbar_init(&tail->p_full[s], warps);
+        mbar_init(&tail->o_done[s], 1);
+      }
+      mbar_init(&tail->finish, 3 + 4 * kNT);
+      fence_barrier_init();
+      prefetch_tensormap(&kv_map);
+      tail->ok = 1;
+      for (int j = 0; j < kNT; ++j) tail->pos[j] = token_pos(j);
+      if (pre_page >= 0) load_page(0, pre_page);
+    }
+    __syncwarp();
+    int np = 0;
+    if constexpr (kMode == kDense) {
+      np = hi - lo;
+      look_up(lane);
+      look_up_scales();
+      for (int t = 0; t < np && t < kStages; ++t) {
+        const int pg = __shfl_sync(0xffffffffu, pg_next, t);
+        if (lane == 0) load_page(t, pg);
+      }
+      tail->info[lane] = next_info();
+    } else {
+      pdl_wait();   // the lists, or the scores they come from, are the previous kernel's
+      const int64_t list = (row_tok * p.Hkv + g) * kTopK;
+      int n;
+      if constexpr (kMode == kSelect) {
+        bool nan = false;
+        uint8_t* scratch = smem + kStageBytes;   // stage 1, not yet loaded
+        n = last_pos >= 0
+                ? select::select_row<16>(p.scores + g * p.s_stride_h + row_tok * p.s_stride_t,
+                                         p.s_stride_n, last_pos, lane,
+                                         reinterpret_cast<uint32_t*>(scratch), kSelectCap,
+                                         reinterpret_cast<int*>(scratch + 4 * kSelectCap), nan)
+                : -1;
+        if (lane < kTopK && part == 0) p.topk_out[list + lane] = n;
+        if (__any_sync(0xffffffffu, nan) && lane == 0) flag_error(p.err, MSA_ERR_SCORE_NAN);
+        tc::fence_proxy_async_smem();            // scratch writes before TMA loads into it
+        __syncwarp();
+      } else {
+        n = lane < kTopK ? p.topk[list + lane] : -1;
+      }
+      bool valid = lane < kTopK && last_pos >= 0 && n != -1;
+      if (valid && (n < 0 || n > cur)) {
+        flag_error(p.err, MSA_ERR_TOPK_RANGE);
+        valid = false;
+      }
+      if constexpr (kMode == kLists) {   // a block listed again at a later slot is dropped
+        const unsigned same = __match_any_sync(0xffffffffu, valid ? n : -2 - lane);
+        if (valid && (same & ((1u << lane) - 1u))) {
+          flag_error(p.err, MSA_ERR_TOPK_DUP);
+          valid = false;
+        }
+      }
+      int page = -1;
+      if (valid) {
+        page = trow[n];
+        if (page < 0 || static_cast<int64_t>(page) >= p.num_blocks) {
+          flag_error(p.err, MSA_ERR_PAGE_RANGE);
+          valid = false;
+        }
+      }
+      // page order: the current block first, then the others by slot
+      const unsigned vm = __ballot_sync(0xffffffffu, valid);
+      const bool front = valid && n == cur;
+      const unsigned fm = __ballot_sync(0xffffffffu, front);
+      const int idx = front ? 0 : __popc(vm & ~fm & ((1u << lane) - 1u)) + (fm ? 1 : 0);
+      const bool mine = valid && idx % nparts == part;
+      const int k = idx / nparts;
+      np = __popc(__ballot_sync(0xffffffffu, mine));
+      if (mine) {
+        tail->pages[k] = page;
+        if (k < kStages && !(k == 0 && pre_page >= 0)) load_page(k, page);
+        tail->info[k] = page_info(p, load_page_scale(p.kv_scales, page, p.Hkv, g), n);
+      }
+    }
+    if (lane == 0) tail->n_pages = np;
+  } else if (warp == 1) {
+    tc::tmem_alloc(&tail->tmem_base, kTmemCols);
+    tc::tmem_relinquish();
+  } else if (warp >= 3 && (warp & 3) == 3) {
+    // token j's query rows (hi, then lo; an fp8 query's as they are)
+    const int j = (warp - 3) >> 2;
+    if (tok0 + j < qlen || kNT == 1) {
+      const int64_t row = (row_tok + j) * p.Hq + g * kGroup;
+      if constexpr (kFp8Q) {
+        store_query_rows_fp8(p.q8 + row * kHeadDim, kQRows * j, qtile, lane);
+        if (lane == 0) tail->zs[j] = p.logit_scale * p.q_scale;
+      } else {
+        const int e = prepare_query_e4m3(p.q + row * kHeadDim, kQRows * j, qtile,
+                                         qtile + kGroup * 128, lane);
+        if (lane == 0) tail->zs[j] = p.logit_scale * exp2i(e);
+      }
+    } else {
+      zero_query_rows(kQRows * j, qtile, lane);
+      if (!kFp8Q) zero_query_rows(kQRows * j + kGroup, qtile, lane);
+      if (lane == 0) tail->zs[j] = 0.f;
+    }
+    tc::fence_proxy_async_smem();   // the tile is read by the tensor core
+  }
+  if (kNT > 1 && warp >= 3) {
+    // a token that is not there has P = 0: written once, read on every page
+    const int j = (warp - 3) >> 2;
+    if (token_pos(j) < 0) {
+      const int key = 32 * (warp & 3) + lane;
+#pragma unroll
+      for (int buf = 0; buf < 2; ++buf) {
+        uint8_t* pk = pbuf + buf * Sm::kPBuf + 256 * j + (key >> 3) * Sm::kPBlock + (key & 7) * 16;
+        *reinterpret_cast<uint4*>(pk) = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(pk + 128) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      tc::fence_proxy_async_smem();
+    }
+  }
+  tc::fence_before_thread_sync();
+  __syncthreads();
+  tc::fence_after_thread_sync();
+  const int n_pages = tail->n_pages;
+  const uint32_t tmem = tail->tmem_base;
+
+  if (warp == 0) {
+    // ---- TMA producer ------------------------------------------------------------------
+    int issued = min(n_pages, kStages);
+    bool ok = true;
+    if constexpr (kMode == kDense) {
+      // chunk by chunk: a chunk's pages are looked up when the one before it
+      // begins and their scales when it is half through
+      int pg = pg_next;
+      if (kChunk < n_pages) look_up(kChunk + lane);
+      for (int t = kStages; t < n_pages && ok; ++t) {
+        if (t % kChunk == kChunk / 2) look_up_scales();
+        if (t % kChunk == 0) {
+          pg = pg_next;
+          // its slots were last read two chunks ago: those pages' stages have
+          // been released since
+          tail->info[t % (2 * kChunk) + lane] = next_info();
+          __syncwarp();
+          if (t + kChunk < n_pages) look_up(t + kChunk + lane);
+        }
+        if (!mbar_wait(&tail->empty[t % kStages], ((t / kStages) - 1) & 1)) ok = false;
+        ok = __all_sync(0xffffffffu, ok);
+        const int page = __shfl_sync(0xffffffffu, pg, t % kChunk);
+        if (ok) {
+          if (lane == 0) load_page(t, page);
+          issued = t + 1;
+        }
+      }
+    } else {
+      for (int t = kStages; t < n_pages && ok; ++t) {
+        if (!mbar_wait(&tail->empty[t % kStages], ((t / kStages) - 1) & 1)) ok = false;
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+          if (lane == 0) load_page(t, tail->pages[t]);
+          issued = t + 1;
+        }
+      }
+    }
+    if (lane == 0) {
+      if (!ok) flag_error(p.err, MSA_ERR_TIMEOUT);
+      // the loads still in flight land before shared memory can be released
+      for (int t = max(0, issued - kStages); t < issued; ++t)
+        (void)mbar_wait(&tail->full[t % kStages], (t / kStages) & 1);
+      pdl_trigger();
+      mbar_arrive(&tail->finish);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---- S^T = K Q^T ---------------------------------------------------------------------
+    if (lane == 0) {
+      const uint64_t a0 = tc::sw128_kmajor_desc(smem_u32(smem));
+      const uint64_t bq = tc::sw128_kmajor_desc(smem_u32(qtile));
+      constexpr uint32_t idesc = tc::idesc_e4m3_f32(128, kSN);
+      for (int t = 0; t < n_pages; ++t) {
+        const int s = t % kStages, buf = t & 1;
+        if (!mbar_wait(&tail->full[s], (t / kStages) & 1) ||
+            (t >= 2 && !mbar_wait(&tail->s_empty[buf], ((t >> 1) - 1) & 1))) {
+          flag_error(p.err, MSA_ERR_TIMEOUT);
+          break;
+        }
+        tc::fence_after_thread_sync();
+        const uint64_t a = a0 + static_cast<uint64_t>(s) * (kStageBytes >> 4);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          tc::mma_e4m3(tmem + kSN * buf, a + 2 * ks, bq + 2 * ks, idesc, ks > 0);
+        tc::commit(&tail->s_full[buf]);
+      }
+      tc::commit(&tail->finish);
+    }
+    __syncwarp();
+    // free tensor memory once every role is done with it
+    (void)mbar_wait(&tail->finish, 0);
+    tc::fence_after_thread_sync();
+    tc::tmem_dealloc(tmem, kTmemCols);
+  } else if (warp == 2) {
+    // ---- O^T += V^T P^T --------------------------------------------------------------------
+    if (lane == 0) {
+      const uint64_t a0 = tc::sw128_mnmajor_desc(smem_u32(smem + kHalfTile));
+      // B: each token's 16 hi heads, then its 16 lo ones 128 bytes further; 8-key
+      // blocks kPBlock apart
+      const uint64_t b0 = tc::interleave_mnmajor_desc(smem_u32(pbuf), Sm::kPBlock, 128);
+      constexpr uint32_t idesc = tc::idesc_e4m3_f32_mn(128, 32 * kNT);
+      for (int t = 0; t < n_pages; ++t) {
+        const int s = t % kStages, buf = t & 1;
+        if (!mbar_wait(&tail->p_full[buf], (t >> 1) & 1)) {
+          flag_error(p.err, MSA_ERR_TIMEOUT);
+          break;
+        }
+        tc::fence_after_thread_sync();
+        const uint64_t a = a0 + static_cast<uint64_t>(s) * (kStageBytes >> 4);
+        const uint64_t bp = b0 + static_cast<uint64_t>((buf * Sm::kPBuf) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          tc::mma_e4m3(tmem + kColAcc, a + 256 * kk, bp + ((4 * Sm::kPBlock) >> 4) * kk, idesc,
+                       (t > 0 || kk > 0) ? 1u : 0u);
+        tc::commit(&tail->o_done[buf]);
+        tc::commit(&tail->empty[s]);
+      }
+      tc::commit(&tail->finish);
+    }
+    __syncwarp();
+  } else {
+    // ---- token j: softmax ------------------------------------------------------------------
+    const int j = (warp - 3) >> 2;
+    const int quarter = warp & 3;
+    const int key = 32 * quarter + lane;   // key of the page; value dim at the end
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
+    const uint32_t s_addr = lane_addr + kQRows * j, acc_addr = lane_addr + kColAcc + 32 * j;
+    const int bar = kNT == 1 ? 1 : 1 + j;
+    const float zs = tail->zs[j];
+    const int pos = tail->pos[j];
+    uint8_t* pj = pbuf + 256 * j + (key >> 3) * Sm::kPBlock + (key & 7) * 16;
+    // nl: log2(vs) - M per head, the addend of u - M (0 until the token has seen a
+    // key); lv: the log2(vs) in it.  l: this key slot's share of the running sums.
+    float nl[kGroup], l[kGroup];
+    float lv = 0.f;
+    bool unset = true;
+#pragma unroll
+    for (int h = 0; h < kGroup; ++h) nl[h] = l[h] = 0.f;
+    bool ok = true;
+
+    // Once a wait has run out the warp waits for nothing any more but still takes
+    // part in the token's barriers, so that its other warps get past them.
+    for (int k = 0; k < n_pages && pos >= 0; ++k) {
+      const int buf = k & 1, s = k % kStages;
+      float t[kGroup];
+      // the page's scales and block, written before the page was loaded
+      if (kMode == kDense && ok) ok = mbar_wait(&tail->full[s], (k / kStages) & 1);
+      if (ok) ok = mbar_wait(&tail->s_full[buf], (k >> 1) & 1);
+      tc::fence_after_thread_sync();
+      const PageInfo in = tail->info[k % (2 * kChunk)];
+      const float zt = zs * in.k;
+      if (in.lv != lv) {   // the same in every thread
+        const float d = in.lv - lv;
+#pragma unroll
+        for (int h = 0; h < kGroup; ++h) nl[h] += d;
+        lv = in.lv;
+      }
+      const int lim = in.block < 0 ? -1 : pos - in.block * kPage;   // keys <= lim are visible
+      // u - M + kPShift: the raw dot products (hi and lo columns) times zt, plus nl
+      if constexpr (kFp8Q || kNT > 1) {
+        uint32_t sv[kGroup];
+        tc::ld_32x32b_x16(s_addr + kSN * buf, sv);
+        tc::wait_ld();
+#pragma unroll
+        for (int h = 0; h < kGroup; ++h) t[h] = fmaf(__uint_as_float(sv[h]), zt, nl[h]);
+        if constexpr (!kFp8Q) {   // one half at a time: 96 registers a thread
+          tc::ld_32x32b_x16(s_addr + kSN * buf + kGroup, sv);
+          tc::wait_ld();
+#pragma unroll
+          for (int h = 0; h < kGroup; ++h) t[h] = fmaf(__uint_as_float(sv[h]), zt, t[h]);
+        }
+      } else {
+        uint32_t sv[2 * kGroup];
+        tc::ld_32x32b_x32(s_addr + kSN * buf, sv);
+        tc::wait_ld();
+#pragma unroll
+        for (int h = 0; h < kGroup; ++h)
+          t[h] = fmaf(__uint_as_float(sv[h]) + __uint_as_float(sv[h + kGroup]), zt, nl[h]);
+      }
+      tc::fence_before_thread_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tail->s_empty[buf]);
+      if (lim < kPage - 1 && key > lim) {
+#pragma unroll
+        for (int h = 0; h < kGroup; ++h) t[h] = -INFINITY;
+      }
+      float top = fmaxf(fmax3f(fmax3f(t[0], t[1], t[2]), fmax3f(t[3], t[4], t[5]),
+                               fmax3f(t[6], t[7], t[8])),
+                        fmax3f(fmax3f(t[9], t[10], t[11]), fmax3f(t[12], t[13], t[14]), t[15]));
+      bool stored = false;
+      if (barrier_or(bar, unset ? top > -INFINITY : top > kPTop)) {
+        // set or move the references: the 16 heads' maxima over the page's keys
+#pragma unroll
+        for (int h = 0; h < kGroup; ++h) {
+          const float m = warp_max_f32(t[h]);
+          if (lane == h) tail->mx[j][h][quarter] = m;
+        }
+        __syncwarp();
+        named_barrier(bar, 128);
+        // lane h (and h + 16): kPShift - the maximum where head h's reference moves, else 0
+        float d_h, al_h;
+        {
+          const float4 m4 = *reinterpret_cast<const float4*>(tail->mx[j][lane & 15]);
+          const float m = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
+          d_h = (unset || m > kPTop) && fabsf(m) < INFINITY ? kPShift - m : 0.f;
+          al_h = ex2(d_h);
+        }
+#pragma unroll
+        for (int h = 0; h < kGroup; ++h) {
+          const float d = __shfl_sync(0xffffffffu, d_h, h);
+          nl[h] += d;
+          t[h] += d;
+        }
+        if (!unset) {
+#pragma unroll
+          for (int h = 0; h < kGroup; ++h) l[h] *= __shfl_sync(0xffffffffu, al_h, h);
+          // the earlier products are relative to the old references (a token that
+          // has seen no key has only zeros there)
+          // page k - 1's product, and with it all earlier ones, complete; page
+          // k's waits for this page's P
+          if (ok) ok = mbar_wait(&tail->o_done[(k - 1) & 1], ((k - 1) >> 1) & 1);
+          tc::fence_after_thread_sync();
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {   // the hi columns, then the lo ones
+            uint32_t av[kGroup];
+            tc::ld_32x32b_x16(acc_addr + kGroup * part, av);
+            tc::wait_ld();
+#pragma unroll
+            for (int h = 0; h < kGroup; ++h)
+              av[h] = __float_as_uint(__uint_as_float(av[h]) * __shfl_sync(0xffffffffu, al_h, h));
+            tc::st_32x32b_x16(acc_addr + kGroup * part, av);
+          }
+          tc::wait_st();
+          stored = true;
+        }
+        unset = false;
+      }
+      uint32_t hw[4], lw[4];
+#pragma unroll
+      for (int q4 = 0; q4 < 4; ++q4) {
+#pragma unroll
+        for (int e = 4 * q4; e < 4 * q4 + 4; ++e) {
+          t[e] = ex2(t[e]);             // P; 0 for an invisible key
+          l[e] = fmaf(t[e], in.iv, l[e]);
+        }
+        uint32_t h0, l0, h1, l1;
+        split_e4m3x2(t[4 * q4], t[4 * q4 + 1], h0, l0);
+        split_e4m3x2(t[4 * q4 + 2], t[4 * q4 + 3], h1, l1);
+        hw[q4] = h0 | (h1 << 16);
+        lw[q4] = l0 | (l1 << 16);
+      }
+      if (j == last_tok && lim < kPage - 1) {
+        // value rows that no token of the tile sees have P = 0, but their bytes
+        // may be anything (an fp8 NaN times 0 is NaN)
+        if (ok) ok = mbar_wait(&tail->full[s], (k / kStages) & 1);
+        if (key > lim) {
+          uint4* vrow = reinterpret_cast<uint4*>(smem + s * kStageBytes + kHalfTile + key * 128);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) vrow[c] = make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+      // P^T buffer `buf` was last read by page k - 2's product
+      if (ok && k >= 2) ok = mbar_wait(&tail->o_done[buf], ((k >> 1) - 1) & 1);
+      uint8_t* pk = pj + buf * Sm::kPBuf;
+      *reinterpret_cast<uint4*>(pk) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+      *reinterpret_cast<uint4*>(pk + 128) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+      tc::fence_proxy_async_smem();
+      if (stored) tc::fence_before_thread_sync();   // the rescale before O^T
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tail->p_full[buf]);
+    }
+
+    // ---- output: this thread's value dim of each head ---------------------------------------
+    float o[kGroup];
+#pragma unroll
+    for (int h = 0; h < kGroup; ++h) o[h] = 0.f;
+    if (n_pages > 0 && pos >= 0) {
+      if (ok) ok = mbar_wait(&tail->o_done[(n_pages - 1) & 1], ((n_pages - 1) >> 1) & 1);
+      tc::fence_after_thread_sync();
+      uint32_t av[32];
+      tc::ld_32x32b_x32(acc_addr, av);
+      tc::wait_ld();
+      tc::fence_before_thread_sync();
+#pragma unroll
+      for (int h = 0; h < kGroup; ++h)
+        o[h] = __uint_as_float(av[h]) + __uint_as_float(av[h + kGroup]);
+    }
+    if (!ok && lane == 0) {
+      flag_error(p.err, MSA_ERR_TIMEOUT);
+      tail->ok = 0;
+    }
+    // running sums: this thread's share -> all 128 key slots
+#pragma unroll
+    for (int h = 0; h < kGroup; ++h) {
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], off);
+    }
+    if (lane == 0) {
+#pragma unroll
+      for (int h4 = 0; h4 < 4; ++h4)
+        *reinterpret_cast<float4*>(&tail->lsum[j][quarter][4 * h4]) =
+            make_float4(l[4 * h4], l[4 * h4 + 1], l[4 * h4 + 2], l[4 * h4 + 3]);
+    }
+    __syncwarp();
+    named_barrier(bar, 128);
+#pragma unroll
+    for (int h = 0; h < kGroup; ++h)
+      l[h] = (tail->lsum[j][0][h] + tail->lsum[j][1][h]) + (tail->lsum[j][2][h] + tail->lsum[j][3][h]);
+    const int64_t row0 = (row_tok + j) * p.Hq + g * kGroup;
+    const int64_t rows = static_cast<int64_t>(kVarlen ? p.T : p.B * p.Q) * p.Hq;
+    const int64_t base = static_cast<int64_t>(split) * rows + row0;
+    if (kMode == kDense) pdl_wait();   // the outputs may be the previous kernel's inputs
+    if constexpr (kCluster) {
+      // this CTA's part into its stages (every load has landed and every product is
+      // complete), then each CTA merges its share of the heads
+      float* po = reinterpret_cast<float*>(smem);
+#pragma unroll
+      for (int h = 0; h < kGroup; ++h) po[h * kHeadDim + key] = l[h] > 0.f ? o[h] : 0.f;
+      if (key < kGroup) {
+#pragma unroll
+        for (int h = 0; h < kGroup; ++h)
+          if (h == key) {
+            tail->ml[h][0] = lv - nl[h];   // M
+            tail->ml[h][1] = tail->ok ? l[h] : 0.f;
+          }
+      }
+    } else if (tail->ok && (kNT == 1 || tok0 + j < qlen)) {
+      if (p.splits == 1) {
+#pragma unroll
+        for (int h = 0; h < kGroup; ++h) {
+          const float r = l[h] > 0.f ? o[h] * (p.v_scale / l[h]) : 0.f;
+          p.out[(row0 + h) * kHeadDim + key] = static_cast<uint16_t>(f32_to_bf16_bits(r));
+        }
+      } else {
+#pragma unroll
+        for (int h = 0; h < kGroup; ++h) p.part_o[(base + h) * kHeadDim + key] = o[h] * p.v_scale;
+        if (key < kGroup) {
+#pragma unroll
+          for (int h = 0; h < kGroup; ++h)
+            if (h == key) {
+              p.part_ml[(base + h) * 2] = lv - nl[h];
+              p.part_ml[(base + h) * 2 + 1] = l[h];
+            }
+        }
+      }
+    }
+    if (kMode == kDense && !kCluster && split == 0 && key < kGroup && (kNT == 1 || tok0 + j < qlen)) {
+      // a unit cut into fewer ranges than the workspace's parts marks the rest empty
+      for (int s2 = nsplit; s2 < p.splits; ++s2) {
+        p.part_ml[(static_cast<int64_t>(s2) * rows + row0 + key) * 2] = -INFINITY;
+        p.part_ml[(static_cast<int64_t>(s2) * rows + row0 + key) * 2 + 1] = 0.f;
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&tail->finish);
+    if constexpr (kCluster) {
+      cluster_sync();
+      const int per = kGroup / static_cast<int>(cs);   // heads of this CTA
+      for (int h = per * static_cast<int>(rank); h < per * (static_cast<int>(rank) + 1); ++h) {
+        float m[kMaxCluster], lr[kMaxCluster], v[kMaxCluster];
+        float M = -INFINITY;
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+          m[r] = -INFINITY;
+          lr[r] = v[r] = 0.f;
+          if (r < static_cast<int>(cs)) {
+            m[r] = ld_peer(&tail->ml[h][0], r);
+            lr[r] = ld_peer(&tail->ml[h][1], r);
+            v[r] = ld_peer(reinterpret_cast<float*>(smem) + h * kHeadDim + key, r);
+          }
+          if (lr[r] > 0.f) M = fmaxf(M, m[r]);
+        }
+        float den = 0.f, acc = 0.f;
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+          const float w = lr[r] > 0.f ? ex2(m[r] - M) : 0.f;
+          den = fmaf(w, lr[r], den);
+          acc = fmaf(w, v[r], acc);
+        }
+        if (p.splits == 1) {
+          const float rr = den > 0.f ? acc * (p.v_scale / den) : 0.f;
+          p.out[(row0 + h) * kHeadDim + key] = static_cast<uint16_t>(f32_to_bf16_bits(rr));
+        } else {
+          p.part_o[(base + h) * kHeadDim + key] = acc * p.v_scale;
+          if (key == 0) {
+            p.part_ml[(base + h) * 2] = M;
+            p.part_ml[(base + h) * 2 + 1] = den;
+          }
+          if (kMode == kDense && split == 0 && key == 0)
+            for (int s2 = nsplit; s2 < p.splits; ++s2) {
+              p.part_ml[(static_cast<int64_t>(s2) * rows + row0 + h) * 2] = -INFINITY;
+              p.part_ml[(static_cast<int64_t>(s2) * rows + row0 + h) * 2 + 1] = 0.f;
+            }
+        }
+      }
+      cluster_sync();   // no CTA ends while another reads its part
+    }
+  }
+  if constexpr (kCluster) {
+    if (warp < 3) {
+      cluster_sync();
+      cluster_sync();
+    }
+  }
+}
+
+}  // namespace
+
+namespace {
+
+template <int kNT, Mode kMode, bool kFp8Q, bool kVarlen, bool kCluster>
+cudaError_t launch(const CUtensorMap& kv_map, const AttendParams& p, dim3 grid, int cs,
+                   cudaStream_t stream, bool pdl) {
+  auto* k = scaled_attend_kernel<kNT, kMode, kFp8Q, kVarlen, kCluster>;
+  static std::atomic<unsigned long long> attr_done{0};
+  cudaError_t e = once_per_device(attr_done, [&] {
+    cudaError_t r = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         Smem<kNT>::kBytes);
+    if (r != cudaSuccess) return r;
+    // all of the unified L1 / shared storage as shared memory: two CTAs per SM
+    return cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                static_cast<int>(cudaSharedmemCarveoutMaxShared));
+  });
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(32 * (3 + 4 * kNT));
+  cfg.dynamicSmemBytes = Smem<kNT>::kBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  cfg.attrs = attr;
+  if (kCluster) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = static_cast<unsigned>(cs);
+    attr[cfg.numAttrs].val.clusterDim.y = 1;
+    attr[cfg.numAttrs++].val.clusterDim.z = 1;
+  }
+  if (pdl) {   // as launch_pdl
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  return cudaLaunchKernelEx(&cfg, k, kv_map, p);
+}
+
+template <Mode kMode, bool kFp8Q>
+cudaError_t launch_lists(const CUtensorMap& kv_map, const AttendParams& p, dim3 grid, int cs,
+                         cudaStream_t stream, bool pdl) {
+  if (p.cu_q)
+    return cs > 1 ? launch<1, kMode, kFp8Q, true, true>(kv_map, p, grid, cs, stream, pdl)
+                  : launch<1, kMode, kFp8Q, true, false>(kv_map, p, grid, cs, stream, pdl);
+  return cs > 1 ? launch<1, kMode, kFp8Q, false, true>(kv_map, p, grid, cs, stream, pdl)
+                : launch<1, kMode, kFp8Q, false, false>(kv_map, p, grid, cs, stream, pdl);
+}
+
+template <bool kFp8Q>
+cudaError_t launch_dense(const CUtensorMap& kv_map, const AttendParams& p, dim3 grid, int cs,
+                         cudaStream_t stream, bool pdl) {
+  if (p.Q > 1) return launch<4, kDense, kFp8Q, false, false>(kv_map, p, grid, cs, stream, pdl);
+  return cs > 1 ? launch<1, kDense, kFp8Q, false, true>(kv_map, p, grid, cs, stream, pdl)
+                : launch<1, kDense, kFp8Q, false, false>(kv_map, p, grid, cs, stream, pdl);
+}
+
+}  // namespace
+
+cudaError_t launch_attend_scaled(const CUtensorMap& kv_map, const AttendParams& p,
+                                 cudaStream_t stream, bool pdl) {
+  const bool dense = p.dense_span > 0;
+  if (p.union_tile && !dense) return launch_union_attend_scaled(kv_map, p, stream, pdl);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int ntile = p.Q > 1 && dense ? 4 : 1;                  // tokens a tile
+  const int64_t slots = ntile == 1 ? 2 * sms : sms;            // CTAs resident at once
+  const int tiles = (p.Q + ntile - 1) / ntile;
+  const int64_t units = dense ? static_cast<int64_t>(p.B) * tiles * p.Hkv
+                              : static_cast<int64_t>(p.cu_q ? p.T : p.B * p.Q) * p.Hkv;
+  // The CTAs of a cluster cut a unit's part while that still fits one wave and
+  // leaves each a page or more (lists: 16 pages a row).
+  const int pages = dense ? p.S : kTopK;
+  int cs = 1;
+  if (ntile == 1 && (dense || p.splits == 1))
+    while (cs < kMaxCluster && units * p.splits * cs * 2 <= slots && p.splits * cs * 2 <= pages)
+      cs *= 2;
+  dim3 grid;
+  if (!dense) {
+    grid = dim3(static_cast<unsigned>(units / p.Hkv * cs), p.Hkv, p.splits);
+    if (p.scores)
+      return p.q8 ? launch_lists<kSelect, true>(kv_map, p, grid, cs, stream, pdl)
+                  : launch_lists<kSelect, false>(kv_map, p, grid, cs, stream, pdl);
+    return p.q8 ? launch_lists<kLists, true>(kv_map, p, grid, cs, stream, pdl)
+                : launch_lists<kLists, false>(kv_map, p, grid, cs, stream, pdl);
+  }
+  // dense decode: fewer units than slots share the slots out by their blocks
+  // (dense_slot), up to `splits` parts a unit; else one part a unit
+  if (p.splits > 1 && units < slots && p.B * tiles <= kBalancedTiles)
+    grid = dim3(static_cast<unsigned>(slots / cs * cs));
+  else
+    grid = dim3(static_cast<unsigned>(units * cs), p.splits);
+  return p.q8 ? launch_dense<true>(kv_map, p, grid, cs, stream, pdl)
+              : launch_dense<false>(kv_map, p, grid, cs, stream, pdl);
+}
+
+}  // namespace msa

@@ -121,7 +121,8 @@ cudaError_t launch_attend(const CUtensorMap& kv_map, const AttendParams& p, cuda
 // tile's lists; grid (B * ceil(Q / 4) * Hkv, splits).
 cudaError_t launch_union_attend(const CUtensorMap& kv_map, const AttendParams& p,
                                 cudaStream_t stream, bool pdl);
-// The same on a cache with page scales (p.kv_scales set).
+// The same on a cache with page scales (p.kv_scales set); dense decode is
+// launch_attend_scaled's alone.
 cudaError_t launch_score_scaled(const CUtensorMap& kv_map, const ScoreParams& p,
                                 cudaStream_t stream, bool pdl);
 cudaError_t launch_attend_scaled(const CUtensorMap& kv_map, const AttendParams& p,

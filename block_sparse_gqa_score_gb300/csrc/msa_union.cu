@@ -50,11 +50,11 @@
 //          token's list, warp 5+4j prepares its query rows
 //
 // This file is compiled twice: as it stands (one scale per tensor), and with
-// MSA_KV_SCALES set (by msa_union_scaled.cu) for a cache whose pages carry
-// scales of their own (see PageScale).  With lists the prologue puts the union
-// pages' scales into shared memory; dense decode, whose ranges have up to 2048
-// pages, reads them 32 at once, one per lane, 32 pages ahead: the producer
-// together with the page numbers, each softmax warp for itself.
+// MSA_KV_SCALES set (by msa_union_scaled.cu) for lists on a cache whose pages
+// carry scales of their own (see PageScale): the prologue puts the union pages'
+// scales into shared memory.  Dense decode with page scales is
+// msa_attend_scaled.cu's.
+#include "msa_dense_slot.cuh"
 #include "msa_device.cuh"
 #include "msa_launch.h"
 #include "msa_select.cuh"
@@ -90,10 +90,6 @@ constexpr int kSBufs = 3;
 constexpr uint32_t kColAcc = kSBufs * kN;
 constexpr int kTmemCols = 512;
 constexpr int kMaxDenseBlocks = 2048;         // dense decode: blocks of one CTA's range
-// dense decode with fewer (request, tile, KV head) units than SMs and split
-// parts: one CTA per SM, shared out in the kernel among up to this many
-// (request, tile) units in proportion to their blocks
-constexpr int kBalancedTiles = 256;
 constexpr float kPShift = 8.f;                // P = 2^(x - m + kPShift)
 constexpr float kLazy = 0.5f;                 // m moves when a page exceeds it by more than this
 constexpr int kTableCopy = 512;               // block-table entries copied to shared memory
@@ -174,88 +170,6 @@ __device__ __forceinline__ void warp_sort64(uint32_t (&v)[2], int lane) {
   }
 }
 
-// Blocks a dense-decode unit (request, tile) attends: up to its last token's
-// current block (0 for a padding request or a tile of padding rows).
-__device__ __forceinline__ int dense_tile_blocks(const AttendParams& p, int tu, int ntiles) {
-  const int b = tu / ntiles, tile = tu - b * ntiles;
-  const int L = p.seq_lens[b];
-  const bool seq_ok = L >= 0 && (L == 0 || (L - 1) / kPage < p.S);
-  const int tok = min(kQt * tile + kQt - 1, p.Q - 1);
-  const int pos = seq_ok ? L - p.Q + tok : -1;
-  return pos >= 0 ? pos / kPage + 1 : 0;
-}
-
-struct DenseSlot {
-  int unit;    // (request, tile, KV head) unit, in blockIdx.x order of the plain grid; -1: none
-  int part;    // which of its equal block ranges
-  int nparts;  // how many ranges the unit is cut into
-};
-
-// Dense decode's work for this CTA.  With a grid of one CTA per unit and split
-// that is (blockIdx.x, blockIdx.y, gridDim.y).  With more CTAs than units (one
-// per SM, launch_union_attend) the units share them out by their blocks: unit u (n_u blocks)
-// takes z_u = min(ceil(n_u / T), splits) CTAs (at least one) for the smallest
-// T at which every unit's CTAs fit the grid, so that no CTA holds much more
-// than its share of the batch's pages; the CTAs go to the units in order, a
-// unit's KV heads in turn, each head's ranges in turn.  Every CTA computes the
-// same assignment from seq_lens (one warp, every lane the same result); CTAs
-// past the last unit's get none.
-__device__ DenseSlot dense_slot(const AttendParams& p, int ntiles, int lane) {
-  const int NT = p.B * ntiles, H = p.Hkv, Z = p.splits, C = static_cast<int>(gridDim.x);
-  if (C <= NT * H)
-    return DenseSlot{static_cast<int>(blockIdx.x), static_cast<int>(blockIdx.y),
-                     static_cast<int>(gridDim.y)};
-  constexpr int kPer = kBalancedTiles / 32;
-  int n[kPer];
-  int maxn = 0;
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const int tu = 32 * k + lane;
-    n[k] = tu < NT ? dense_tile_blocks(p, tu, ntiles) : 0;
-    maxn = max(maxn, n[k]);
-  }
-  maxn = __reduce_max_sync(0xffffffffu, maxn);
-  auto parts = [&](int k, int T) { return min(max((n[k] + T - 1) / T, 1), Z); };
-  auto ctas = [&](int T) {
-    int s = 0;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k)
-      if (32 * k + lane < NT) s += parts(k, T);
-    return static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(s))) * H;
-  };
-  // at T = max(n) every unit takes one CTA per head, NT * H <= C (the host's rule)
-  int lo = 1, hi = max(maxn, 1);
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (ctas(mid) <= C) hi = mid;
-    else lo = mid + 1;
-  }
-  const int c = static_cast<int>(blockIdx.x);
-  int run = 0;   // CTAs of the units before this group of 32
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const int tu = 32 * k + lane;
-    const int zc = tu < NT ? parts(k, lo) : 0;
-    int incl = zc * H;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += t;
-    }
-    const int start = run + incl - zc * H;
-    const unsigned hit = __ballot_sync(0xffffffffu, zc > 0 && c >= start && c < start + zc * H);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      const int st = __shfl_sync(0xffffffffu, start, src);
-      const int z = __shfl_sync(0xffffffffu, zc, src);
-      const int rel = c - st;
-      return DenseSlot{(32 * k + src) * H + rel / z, rel % z, z};
-    }
-    run += __shfl_sync(0xffffffffu, incl, 31);
-  }
-  return DenseSlot{-1, 0, 1};
-}
-
 // kFp8Q: an fp8 query (q8 * q_scale); kDense: dense decode (no lists);
 // each compiled separately.
 template <bool kFp8Q, bool kDense>
@@ -276,7 +190,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   int unit = static_cast<int>(blockIdx.x), split = static_cast<int>(blockIdx.y);
   int nsplit = static_cast<int>(gridDim.y);
   if constexpr (kDense) {
-    const DenseSlot ds = dense_slot(p, ntiles, lane);
+    const DenseSlot ds = dense_slot<kQt>(p, ntiles, static_cast<int>(gridDim.x),
+                                         static_cast<int>(blockIdx.x), lane);
     if (ds.unit < 0) return;   // the whole CTA: no unit left for it
     unit = ds.unit;
     split = ds.part;
@@ -435,18 +350,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (t < np) {
         const int pg = lo + t < ncopy ? table_s[lo + t] : trow[lo + t];
         bad = pg < 0 || static_cast<int64_t>(pg) >= p.num_blocks;
-        if (bad) flag_error(p.err, MSA_ERR_PAGE_RANGE);
-        if constexpr (kScaled) {   // a page scale out of range: likewise
-          if (!bad && make_page_scale(load_page_scale(p.kv_scales, pg, p.Hkv, g)).bad != 0.f) {
-            flag_error(p.err, MSA_ERR_SCALE);
-            bad = true;
-          }
-        }
       }
       const unsigned bb = __ballot_sync(0xffffffffu, bad);
       if (lane == 0 && base / 32 < kMaxDenseBlocks / 32) tail->dense_bad[base / 32] = bb;
+      if (bb && lane == 0) flag_error(p.err, MSA_ERR_PAGE_RANGE);
     }
-    if constexpr (kScaled) __syncwarp();
     if (lane == 0) {
       const int last_block = (seq_ok && L > 0) ? (L - 1) / kPage : -1;
       tail->fix_slot = (last_block >= lo && last_block < hi) ? last_block - lo : -1;
@@ -460,7 +368,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = 0; t < np && t < kStages; ++t) {
         int pg = lo + t < ncopy ? table_s[lo + t] : trow[lo + t];
         if (pg < 0 || static_cast<int64_t>(pg) >= p.num_blocks) pg = 0;
-        if (kScaled && ((tail->dense_bad[0] >> t) & 1u)) pg = 0;
         const int row = (pg * p.Hkv + g) * kPage;
         uint8_t* st = smem + t * kStageBytes;
         mbar_arrive_expect_tx(&tail->full[t], kStageBytes);
@@ -650,19 +557,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       return tail->masks[t];
     }
   };
-  auto slot_bad = [&](int t) -> bool {
-    return kDense && t < kMaxDenseBlocks && ((tail->dense_bad[t >> 5] >> (t & 31)) & 1u);
-  };
   auto slot_page = [&](int t) -> int {
     if constexpr (kDense) {
       const int pg = trow[dense_lo + t];
-      if (kScaled && slot_bad(t)) return 0;
       return (pg < 0 || static_cast<int64_t>(pg) >= p.num_blocks) ? 0 : pg;
     } else {
       return tail->pages[t];
     }
   };
   auto slot_block = [&](int t) -> int { return kDense ? dense_lo + t : tail->blocks[t]; };
+  auto slot_bad = [&](int t) -> bool {
+    return kDense && t < kMaxDenseBlocks && ((tail->dense_bad[t >> 5] >> (t & 31)) & 1u);
+  };
   auto tok_slot = [&](int j, int k) -> int { return kDense ? k : tail->tok_slots[j][k]; };
 
   if (warp == 0) {
@@ -770,10 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int fix_slot = tail->fix_slot;
       if constexpr (kDense) {
         // pages in order; each page's listing tokens (consecutive, all at their
-        // t-th page) share one product once all their P^T is written.  With page
-        // scales a bad slot has none (its stage holds another page, whose bytes
-        // may be fp8 NaN); its commits still release what waits on them.
-        bool fresh = true;   // no product yet: the next one sets the accumulator
+        // t-th page) share one product once all their P^T is written
         for (int t = 0; t < n_pages; ++t) {
           const uint32_t mask = slot_mask(t);
           const int j0 = __ffs(mask) - 1, j1 = 31 - __clz(mask), buf = t & 1, s = t % kStages;
@@ -790,13 +693,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t bp = bp0 + static_cast<uint64_t>((buf * kPBuf + 256 * j0) >> 4);
           const uint32_t d = tmem + kColAcc + 32 * j0;
           const uint32_t idesc_m = tc::idesc_e4m3_f32_mn(128, 32 * (j1 - j0 + 1));
-          if (!kScaled || !slot_bad(t)) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc::mma_e4m3(d, a + 256 * kk, bp + ((4 * kPBlock) >> 4) * kk, idesc_m,
-                           (kScaled ? !fresh || kk > 0 : t > 0 || kk > 0) ? 1u : 0u);
-            fresh = false;
-          }
+          for (int kk = 0; kk < 4; ++kk)
+            tc::mma_e4m3(d, a + 256 * kk, bp + ((4 * kPBlock) >> 4) * kk, idesc_m,
+                         (t > 0 || kk > 0) ? 1u : 0u);
           // one commit for the tokens (the last token's barrier, on which
           // they all wait) and one for the stage
           tc::commit(&tail->o_done[j1][buf]);
@@ -878,34 +778,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the other lanes read it by shuffle.  l: this key slot's share of each
     // head's running sum relative to m.  The output accumulates in tensor
     // memory, relative to m.
-    float nref_h = kScaled ? kNoRef : INFINITY;
+    float nref_h = INFINITY;
     float l[kGroup];
     fill(l, 0.f);
     uint32_t sv[32];   // page k's S^T row (hi | lo columns)
-    // dense decode with page scales: lane l holds those of slot 32 (k / 32) + l
-    // and, as loaded, of the slot 32 after it (a slot with a bad table entry
-    // reads page 0's; it is attended by no key)
-    float2 sc_next = make_float2(1.f, 1.f);
-    PageScale sc_now{1.f, 0.f, 1.f, 0.f};
-    auto fetch_scale = [&](int t) -> float2 {
-      return t < n_j ? load_page_scale(p.kv_scales, slot_page(t), p.Hkv, g) : make_float2(1.f, 1.f);
-    };
-    if constexpr (kScaled && kDense) sc_next = fetch_scale(lane);
     for (int k = 0; k < n_j && ok; ++k) {
       const int t = tok_slot(j, k), buf = k & 1, sb = k % kSBufs;
       const int s = t % kStages;
-      PageScale sc{1.f, 0.f, 1.f, 0.f};
-      if constexpr (kScaled && kDense) {
-        if ((k & 31) == 0) {
-          sc_now = make_page_scale(sc_next);
-          sc_next = fetch_scale(k + 32 + lane);
-        }
-        sc.k = __shfl_sync(0xffffffffu, sc_now.k, k & 31);
-        sc.lv = __shfl_sync(0xffffffffu, sc_now.lv, k & 31);
-        sc.iv = __shfl_sync(0xffffffffu, sc_now.iv, k & 31);
-      } else if constexpr (kScaled) {
-        sc = tail->sc[t];
-      }
+      const PageScale sc = kScaled ? tail->sc[t] : PageScale{1.f, 0.f, 1.f, 0.f};
       const float zt = kScaled ? zs * sc.k : zs;
       if (!mbar_wait(&tail->s_full[jw][sb], (k / kSBufs) & 1)) {
         ok = false;
@@ -1083,9 +963,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int h = 0; h < kGroup; ++h) {
           const float f = (l[h] > 0.f) ? p.v_scale / l[h] : 0.f;
-          // (a range of bad slots alone leaves the accumulator as it was: no o * 0)
-          const float r = kScaled && !(l[h] > 0.f) ? 0.f : o[h] * f;
-          p.out[(row0 + h) * kHeadDim + d] = static_cast<uint16_t>(f32_to_bf16_bits(r));
+          p.out[(row0 + h) * kHeadDim + d] = static_cast<uint16_t>(f32_to_bf16_bits(o[h] * f));
         }
       } else {
         const int64_t rows = static_cast<int64_t>(p.B) * p.Q * p.Hq;
@@ -1120,8 +998,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 }  // namespace
 
 #if MSA_KV_SCALES
+// Lists only.
 cudaError_t launch_union_attend_scaled(const CUtensorMap& kv_map, const AttendParams& p,
                                        cudaStream_t stream, bool pdl) {
+  static std::atomic<unsigned long long> attr_done{0};
+  cudaError_t e = once_per_device(attr_done, [] {
+    for (auto* k : {union_attend_kernel<false, false>, union_attend_kernel<true, false>}) {
+      cudaError_t r = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           kSmemBytes);
+      if (r != cudaSuccess) return r;
+      r = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               static_cast<int>(cudaSharedmemCarveoutMaxShared));
+      if (r != cudaSuccess) return r;
+    }
+    return cudaSuccess;
+  });
+  if (e != cudaSuccess) return e;
+  const dim3 grid(p.B * ((p.Q + kQt - 1) / kQt) * p.Hkv, p.splits), block(kThreads);
+  return p.q8 ? launch_pdl(union_attend_kernel<true, false>, grid, block, kSmemBytes, stream, pdl,
+                           kv_map, p)
+              : launch_pdl(union_attend_kernel<false, false>, grid, block, kSmemBytes, stream, pdl,
+                           kv_map, p);
+}
 #else
 int union_ctas_per_unit(int units, int sm_count) {
   if (units >= sm_count) return 1;
@@ -1131,7 +1029,6 @@ int union_ctas_per_unit(int units, int sm_count) {
 
 cudaError_t launch_union_attend(const CUtensorMap& kv_map, const AttendParams& p,
                                 cudaStream_t stream, bool pdl) {
-#endif
   static std::atomic<unsigned long long> attr_done{0};
   cudaError_t e = once_per_device(attr_done, [] {
     for (auto* k : {union_attend_kernel<false, false>, union_attend_kernel<true, false>,
@@ -1168,5 +1065,6 @@ cudaError_t launch_union_attend(const CUtensorMap& kv_map, const AttendParams& p
               : launch_pdl(union_attend_kernel<false, false>, grid, block, kSmemBytes, stream, pdl,
                            kv_map, p);
 }
+#endif
 
 }  // namespace msa

@@ -542,7 +542,9 @@ int msa_append_kv_prefill(const void *k, int64_t k_stride, const void *v, int64_
  * kv_scales (4-byte for a K-only cache) (MSA_EINVAL).  Device: MSA_ERR_SCALE (a
  * listed or visible page with a scale out of range, either side for the
  * attends, K's for the scorer: the page is skipped, its score is -inf).
- * Workspaces and split counts: as without the suffix.
+ * Workspaces and split counts: as without the suffix, but num_splits = 0 takes
+ * one part and no workspace (a small batch's pages are cut over clusters of CTAs
+ * that merge on chip).
  */
 /* k_only non-zero: kv is a K-only cache (msa_score_kcache), kv_scales
  * [num_blocks, Hkv, 1]. */
