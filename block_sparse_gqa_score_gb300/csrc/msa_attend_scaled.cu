@@ -36,7 +36,9 @@
 //   warp 0       page lists, scales, TMA
 //   warp 1       S^T products (and owns tensor memory)
 //   warp 2       O^T products
-//   warps 3..    four per token: softmax, output.  A thread owns one key.
+//   warps 3..    softmax and output, four a group: a thread owns one key, a group
+//                a token's 16 heads (kNT = 4) or half of them (kNT = 1: the chain of
+//                one page is half as long; 1000 cycles with all 16)
 //
 // What bounds it: bytes from HBM in decode, from L2 in prefill; the pages of a
 // short call are cut over the CTAs of a cluster (kNT = 1), which merge their
@@ -68,9 +70,19 @@ struct alignas(16) PageInfo {
   int block;         // logical block, -1: no key of this page is attended
 };
 
+// Softmax groups of four warps, each with kHeads heads of one token.
+template <int kNT>
+struct Groups {
+  static constexpr int kHeads = kNT == 1 ? 8 : 16;
+  static constexpr int kPerToken = kGroup / kHeads;
+  static constexpr int kCount = kNT * kPerToken;
+  static constexpr int kThreads = 32 * (3 + 4 * kCount);
+};
+
 template <int kNT>
 struct Tail {
   static constexpr int kStages = kNT == 1 ? 3 : 5;
+  static constexpr int kHeads = Groups<kNT>::kHeads, kCount = Groups<kNT>::kCount;
   uint64_t full[kStages];   // TMA -> S^T
   uint64_t empty[kStages];  // O^T (a stage's last reader) -> TMA
   uint64_t s_full[2];       // S^T ready -> softmax
@@ -85,8 +97,8 @@ struct Tail {
   float zs[kNT];            // logit scale (log2 units) times 2^e of each token's query split
   int pages[kChunk];        // list modes: this CTA's pages
   PageInfo info[2 * kChunk];
-  alignas(16) float mx[kNT][kGroup][4];     // page maxima by quarter
-  alignas(16) float lsum[kNT][4][kGroup];   // running sums by quarter
+  alignas(16) float mx[kCount][kHeads][4];    // page maxima by quarter
+  alignas(16) float lsum[kCount][kHeads][4];  // running sums by quarter
   float ml[kGroup][2];          // cluster merge: (m, l) of this CTA's part
 };
 // read and written as float4
@@ -112,7 +124,7 @@ static_assert(2 * (Smem<1>::kBytes + 1024) <= 228 * 1024, "two CTAs an SM");
 static_assert(Smem<4>::kBytes <= 227 * 1024, "one CTA an SM");
 static_assert(kGroup * kHeadDim * 4 <= kStageBytes, "a CTA's part fits a stage");
 
-// The barrier of one token's four warps, with the or of a predicate.
+// The barrier of one group's four warps, with the or of a predicate.
 __device__ __forceinline__ bool barrier_or(int id, bool pred) {
   unsigned r;
   __syncwarp();
@@ -151,9 +163,45 @@ __device__ __forceinline__ PageInfo page_info(const AttendParams& p, float2 scal
   return PageInfo{s.k, s.lv, s.iv, s.bad != 0.f ? -1 : block};
 }
 
+// Columns of this thread's tensor-memory lane.
+__device__ __forceinline__ void ld_cols(uint32_t a, uint32_t (&r)[8]) { tc::ld_32x32b_x8(a, r); }
+__device__ __forceinline__ void ld_cols(uint32_t a, uint32_t (&r)[16]) { tc::ld_32x32b_x16(a, r); }
+__device__ __forceinline__ void st_cols(uint32_t a, const uint32_t (&r)[8]) { tc::st_32x32b_x8(a, r); }
+__device__ __forceinline__ void st_cols(uint32_t a, const uint32_t (&r)[16]) { tc::st_32x32b_x16(a, r); }
+
+__device__ __forceinline__ void store_p(uint8_t* at, const uint32_t (&w)[2]) {
+  *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ void store_p(uint8_t* at, const uint32_t (&w)[4]) {
+  *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Four probabilities (0 <= P <= 448) -> their e4m3 parts, first in the low byte:
+// hi = P rounded, lo = the remainder of P as fp16, rounded (hi + lo carries about
+// 8 significant bits).  Converting hi from fp32 and packing in one block of PTX
+// takes 57 cycles for 16 values of a warp, pair by pair through fp16 82.
+__device__ __forceinline__ void split_p(float a, float b, float c, float d, uint32_t& hi,
+                                        uint32_t& lo) {
+  asm("{\n\t.reg .b16 p, q, r, s;\n\t.reg .b32 x, y, u, v;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 p, %3, %2;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 q, %5, %4;\n\t"
+      "mov.b32 %0, {p, q};\n\t"
+      "cvt.rn.f16x2.f32 x, %3, %2;\n\t"
+      "cvt.rn.f16x2.f32 y, %5, %4;\n\t"
+      "cvt.rn.f16x2.e4m3x2 u, p;\n\t"
+      "cvt.rn.f16x2.e4m3x2 v, q;\n\t"
+      "sub.rn.f16x2 u, x, u;\n\t"
+      "sub.rn.f16x2 v, y, v;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 r, u;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 s, v;\n\t"
+      "mov.b32 %1, {r, s};\n\t}"
+      : "=&r"(hi), "=r"(lo)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+}
+
 // kNT tokens a tile; kCluster: the pages of a part are cut over a cluster's CTAs.
 template <int kNT, Mode kMode, bool kFp8Q, bool kVarlen, bool kCluster>
-__global__ void __launch_bounds__(32 * (3 + 4 * kNT), kNT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
     scaled_attend_kernel(const __grid_constant__ CUtensorMap kv_map, const AttendParams p) {
   using Sm = Smem<kNT>;
   constexpr int kStages = Sm::kStages;
@@ -275,7 +323,7 @@ __global__ void __launch_bounds__(32 * (3 + 4 * kNT), kNT == 1 ? 2 : 1)
       if (pg >= 0 && static_cast<int64_t>(pg) < p.num_blocks) pre_page = pg;
     }
     if (lane == 0) {
-      const unsigned warps = 4u * static_cast<unsigned>(max(valid_toks, 1));
+      const unsigned warps = 4u * Groups<kNT>::kPerToken * static_cast<unsigned>(max(valid_toks, 1));
       for (int s = 0; s < kStages; ++s) {
         mbar_init(&tail->full[s], 1);
         mbar_init(&tail->empty[s], 1);
@@ -286,7 +334,7 @@ __global__ void __launch_bounds__(32 * (3 + 4 * kNT), kNT == 1 ? 2 : 1)
         mbar_init(&tail->p_full[s], warps);
         mbar_init(&tail->o_done[s], 1);
       }
-      mbar_init(&tail->finish, 3 + 4 * kNT);
+      mbar_init(&tail->finish, 3 + 4 * Groups<kNT>::kCount);
       fence_barrier_init();
       prefetch_tensormap(&kv_map);
       tail->ok = 1;
@@ -362,9 +410,9 @@ __global__ void __launch_bounds__(32 * (3 + 4 * kNT), kNT == 1 ? 2 : 1)
   } else if (warp == 1) {
     tc::tmem_alloc(&tail->tmem_base, kTmemCols);
     tc::tmem_relinquish();
-  } else if (warp >= 3 && (warp & 3) == 3) {
+  } else if (warp >= 3 && (warp - 3) % (4 * Groups<kNT>::kPerToken) == 0) {
     // token j's query rows (hi, then lo; an fp8 query's as they are)
-    const int j = (warp - 3) >> 2;
+    const int j = (warp - 3) / (4 * Groups<kNT>::kPerToken);
     if (tok0 + j < qlen || kNT == 1) {
       const int64_t row = (row_tok + j) * p.Hq + g * kGroup;
       if constexpr (kFp8Q) {
@@ -384,7 +432,7 @@ __global__ void __launch_bounds__(32 * (3 + 4 * kNT), kNT == 1 ? 2 : 1)
   }
   if (kNT > 1 && warp >= 3) {
     // a token that is not there has P = 0: written once, read on every page
-    const int j = (warp - 3) >> 2;
+    const int j = (warp - 3) / (4 * Groups<kNT>::kPerToken);
     if (token_pos(j) < 0) {
       const int key = 32 * (warp & 3) + lane;
 #pragma unroll
@@ -503,101 +551,111 @@ __global__ void __launch_bounds__(32 * (3 + 4 * kNT), kNT == 1 ? 2 : 1)
     }
     __syncwarp();
   } else {
-    // ---- token j: softmax ------------------------------------------------------------------
-    const int j = (warp - 3) >> 2;
+    // ---- group gi: kH heads of token j ------------------------------------------------------
+    constexpr int kH = Groups<kNT>::kHeads;
+    const int gi = (warp - 3) >> 2;
+    const int j = gi / Groups<kNT>::kPerToken;
+    const int h0 = kH * (gi % Groups<kNT>::kPerToken);   // the group's first head
     const int quarter = warp & 3;
     const int key = 32 * quarter + lane;   // key of the page; value dim at the end
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
-    const uint32_t s_addr = lane_addr + kQRows * j, acc_addr = lane_addr + kColAcc + 32 * j;
-    const int bar = kNT == 1 ? 1 : 1 + j;
+    const uint32_t s_addr = lane_addr + kQRows * j + h0;
+    const uint32_t acc_addr = lane_addr + kColAcc + 32 * j + h0;
+    const int bar = 1 + gi;
     const float zs = tail->zs[j];
     const int pos = tail->pos[j];
-    uint8_t* pj = pbuf + 256 * j + (key >> 3) * Sm::kPBlock + (key & 7) * 16;
+    uint8_t* pj = pbuf + 256 * j + (key >> 3) * Sm::kPBlock + (key & 7) * 16 + h0;
     // nl: log2(vs) - M per head, the addend of u - M (0 until the token has seen a
     // key); lv: the log2(vs) in it.  l: this key slot's share of the running sums.
-    float nl[kGroup], l[kGroup];
+    float nl[kH], l[kH];
     float lv = 0.f;
     bool unset = true;
 #pragma unroll
-    for (int h = 0; h < kGroup; ++h) nl[h] = l[h] = 0.f;
+    for (int h = 0; h < kH; ++h) nl[h] = l[h] = 0.f;
     bool ok = true;
 
     // Once a wait has run out the warp waits for nothing any more but still takes
-    // part in the token's barriers, so that its other warps get past them.
+    // part in the group's barriers, so that its other warps get past them.
+    int s = 0;
+    unsigned full_ph = 0;
     for (int k = 0; k < n_pages && pos >= 0; ++k) {
-      const int buf = k & 1, s = k % kStages;
-      float t[kGroup];
+      const int buf = k & 1;
+      const unsigned ph = (k >> 1) & 1;
+      float t[kH];
       // the page's scales and block, written before the page was loaded
-      if (kMode == kDense && ok) ok = mbar_wait(&tail->full[s], (k / kStages) & 1);
-      if (ok) ok = mbar_wait(&tail->s_full[buf], (k >> 1) & 1);
+      if (kMode == kDense && ok) ok = mbar_wait(&tail->full[s], full_ph);
+      if (ok) ok = mbar_wait(&tail->s_full[buf], ph);
       tc::fence_after_thread_sync();
       const PageInfo in = tail->info[k % (2 * kChunk)];
       const float zt = zs * in.k;
       if (in.lv != lv) {   // the same in every thread
         const float d = in.lv - lv;
 #pragma unroll
-        for (int h = 0; h < kGroup; ++h) nl[h] += d;
+        for (int h = 0; h < kH; ++h) nl[h] += d;
         lv = in.lv;
       }
       const int lim = in.block < 0 ? -1 : pos - in.block * kPage;   // keys <= lim are visible
       // u - M + kPShift: the raw dot products (hi and lo columns) times zt, plus nl
-      if constexpr (kFp8Q || kNT > 1) {
-        uint32_t sv[kGroup];
-        tc::ld_32x32b_x16(s_addr + kSN * buf, sv);
-        tc::wait_ld();
-#pragma unroll
-        for (int h = 0; h < kGroup; ++h) t[h] = fmaf(__uint_as_float(sv[h]), zt, nl[h]);
-        if constexpr (!kFp8Q) {   // one half at a time: 96 registers a thread
-          tc::ld_32x32b_x16(s_addr + kSN * buf + kGroup, sv);
+      {
+        uint32_t sv[kH];
+        ld_cols(s_addr + kSN * buf, sv);
+        if constexpr (!kFp8Q && kH == 8) {
+          uint32_t sl[kH];
+          ld_cols(s_addr + kSN * buf + kGroup, sl);
           tc::wait_ld();
 #pragma unroll
-          for (int h = 0; h < kGroup; ++h) t[h] = fmaf(__uint_as_float(sv[h]), zt, t[h]);
-        }
-      } else {
-        uint32_t sv[2 * kGroup];
-        tc::ld_32x32b_x32(s_addr + kSN * buf, sv);
-        tc::wait_ld();
+          for (int h = 0; h < kH; ++h)
+            t[h] = fmaf(__uint_as_float(sv[h]) + __uint_as_float(sl[h]), zt, nl[h]);
+        } else {
+          tc::wait_ld();
 #pragma unroll
-        for (int h = 0; h < kGroup; ++h)
-          t[h] = fmaf(__uint_as_float(sv[h]) + __uint_as_float(sv[h + kGroup]), zt, nl[h]);
+          for (int h = 0; h < kH; ++h) t[h] = fmaf(__uint_as_float(sv[h]), zt, nl[h]);
+          if constexpr (!kFp8Q) {   // one half at a time: 96 registers a thread
+            ld_cols(s_addr + kSN * buf + kGroup, sv);
+            tc::wait_ld();
+#pragma unroll
+            for (int h = 0; h < kH; ++h) t[h] = fmaf(__uint_as_float(sv[h]), zt, t[h]);
+          }
+        }
       }
       tc::fence_before_thread_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(&tail->s_empty[buf]);
       if (lim < kPage - 1 && key > lim) {
 #pragma unroll
-        for (int h = 0; h < kGroup; ++h) t[h] = -INFINITY;
+        for (int h = 0; h < kH; ++h) t[h] = -INFINITY;
       }
-      float top = fmaxf(fmax3f(fmax3f(t[0], t[1], t[2]), fmax3f(t[3], t[4], t[5]),
-                               fmax3f(t[6], t[7], t[8])),
-                        fmax3f(fmax3f(t[9], t[10], t[11]), fmax3f(t[12], t[13], t[14]), t[15]));
+      float top = fmax3f(t[0], t[1], t[2]);
+#pragma unroll
+      for (int h = 3; h + 1 < kH; h += 2) top = fmax3f(top, t[h], t[h + 1]);
+      top = fmaxf(top, t[kH - 1]);
       bool stored = false;
       if (barrier_or(bar, unset ? top > -INFINITY : top > kPTop)) {
-        // set or move the references: the 16 heads' maxima over the page's keys
+        // set or move the references: the heads' maxima over the page's keys
 #pragma unroll
-        for (int h = 0; h < kGroup; ++h) {
+        for (int h = 0; h < kH; ++h) {
           const float m = warp_max_f32(t[h]);
-          if (lane == h) tail->mx[j][h][quarter] = m;
+          if (lane == h) tail->mx[gi][h][quarter] = m;
         }
         __syncwarp();
         named_barrier(bar, 128);
-        // lane h (and h + 16): kPShift - the maximum where head h's reference moves, else 0
+        // lane h (and h + kH ..): kPShift - the maximum where head h's reference moves, else 0
         float d_h, al_h;
         {
-          const float4 m4 = *reinterpret_cast<const float4*>(tail->mx[j][lane & 15]);
+          const float4 m4 = *reinterpret_cast<const float4*>(tail->mx[gi][lane & (kH - 1)]);
           const float m = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
           d_h = (unset || m > kPTop) && fabsf(m) < INFINITY ? kPShift - m : 0.f;
           al_h = ex2(d_h);
         }
 #pragma unroll
-        for (int h = 0; h < kGroup; ++h) {
+        for (int h = 0; h < kH; ++h) {
           const float d = __shfl_sync(0xffffffffu, d_h, h);
           nl[h] += d;
           t[h] += d;
         }
         if (!unset) {
 #pragma unroll
-          for (int h = 0; h < kGroup; ++h) l[h] *= __shfl_sync(0xffffffffu, al_h, h);
+          for (int h = 0; h < kH; ++h) l[h] *= __shfl_sync(0xffffffffu, al_h, h);
           // the earlier products are relative to the old references (a token that
           // has seen no key has only zeros there)
           // page k - 1's product, and with it all earlier ones, complete; page
@@ -606,37 +664,33 @@ __global__ void __launch_bounds__(32 * (3 + 4 * kNT), kNT == 1 ? 2 : 1)
           tc::fence_after_thread_sync();
 #pragma unroll
           for (int part = 0; part < 2; ++part) {   // the hi columns, then the lo ones
-            uint32_t av[kGroup];
-            tc::ld_32x32b_x16(acc_addr + kGroup * part, av);
+            uint32_t av[kH];
+            ld_cols(acc_addr + kGroup * part, av);
             tc::wait_ld();
 #pragma unroll
-            for (int h = 0; h < kGroup; ++h)
+            for (int h = 0; h < kH; ++h)
               av[h] = __float_as_uint(__uint_as_float(av[h]) * __shfl_sync(0xffffffffu, al_h, h));
-            tc::st_32x32b_x16(acc_addr + kGroup * part, av);
+            st_cols(acc_addr + kGroup * part, av);
           }
           tc::wait_st();
           stored = true;
         }
         unset = false;
       }
-      uint32_t hw[4], lw[4];
+      uint32_t hw[kH / 4], lw[kH / 4];
 #pragma unroll
-      for (int q4 = 0; q4 < 4; ++q4) {
+      for (int q4 = 0; q4 < kH / 4; ++q4) {
 #pragma unroll
         for (int e = 4 * q4; e < 4 * q4 + 4; ++e) {
           t[e] = ex2(t[e]);             // P; 0 for an invisible key
           l[e] = fmaf(t[e], in.iv, l[e]);
         }
-        uint32_t h0, l0, h1, l1;
-        split_e4m3x2(t[4 * q4], t[4 * q4 + 1], h0, l0);
-        split_e4m3x2(t[4 * q4 + 2], t[4 * q4 + 3], h1, l1);
-        hw[q4] = h0 | (h1 << 16);
-        lw[q4] = l0 | (l1 << 16);
+        split_p(t[4 * q4], t[4 * q4 + 1], t[4 * q4 + 2], t[4 * q4 + 3], hw[q4], lw[q4]);
       }
-      if (j == last_tok && lim < kPage - 1) {
+      if (j == last_tok && h0 == 0 && lim < kPage - 1) {
         // value rows that no token of the tile sees have P = 0, but their bytes
         // may be anything (an fp8 NaN times 0 is NaN)
-        if (ok) ok = mbar_wait(&tail->full[s], (k / kStages) & 1);
+        if (ok) ok = mbar_wait(&tail->full[s], full_ph);
         if (key > lim) {
           uint4* vrow = reinterpret_cast<uint4*>(smem + s * kStageBytes + kHalfTile + key * 128);
 #pragma unroll
@@ -644,52 +698,67 @@ __global__ void __launch_bounds__(32 * (3 + 4 * kNT), kNT == 1 ? 2 : 1)
         }
       }
       // P^T buffer `buf` was last read by page k - 2's product
-      if (ok && k >= 2) ok = mbar_wait(&tail->o_done[buf], ((k >> 1) - 1) & 1);
+      if (ok && k >= 2) ok = mbar_wait(&tail->o_done[buf], ph ^ 1);
       uint8_t* pk = pj + buf * Sm::kPBuf;
-      *reinterpret_cast<uint4*>(pk) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-      *reinterpret_cast<uint4*>(pk + 128) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+      store_p(pk, hw);
+      store_p(pk + 128, lw);
       tc::fence_proxy_async_smem();
       if (stored) tc::fence_before_thread_sync();   // the rescale before O^T
       __syncwarp();
       if (lane == 0) mbar_arrive(&tail->p_full[buf]);
+      if (++s == kStages) {
+        s = 0;
+        full_ph ^= 1;
+      }
     }
 
     // ---- output: this thread's value dim of each head ---------------------------------------
-    float o[kGroup];
+    // Running sums: 32 key slots a warp.  Each step halves the heads a lane keeps
+    // (those whose index agrees with the lane in the step's bit), then the lanes
+    // left with one head are summed.
+    {
+      float part[kH];
 #pragma unroll
-    for (int h = 0; h < kGroup; ++h) o[h] = 0.f;
+      for (int h = 0; h < kH; ++h) part[h] = l[h];
+#pragma unroll
+      for (int n = kH / 2; n >= 1; n >>= 1) {
+        const bool up = (lane & n) != 0;
+#pragma unroll
+        for (int h = 0; h < n; ++h) {
+          const float keep = up ? part[h + n] : part[h], give = up ? part[h] : part[h + n];
+          part[h] = keep + __shfl_xor_sync(0xffffffffu, give, n);
+        }
+      }
+#pragma unroll
+      for (int off = kH; off < 32; off <<= 1)
+        part[0] += __shfl_xor_sync(0xffffffffu, part[0], off);
+      if (lane < kH) tail->lsum[gi][lane][quarter] = part[0];
+    }
+    float o[kH];
+#pragma unroll
+    for (int h = 0; h < kH; ++h) o[h] = 0.f;
     if (n_pages > 0 && pos >= 0) {
       if (ok) ok = mbar_wait(&tail->o_done[(n_pages - 1) & 1], ((n_pages - 1) >> 1) & 1);
       tc::fence_after_thread_sync();
-      uint32_t av[32];
-      tc::ld_32x32b_x32(acc_addr, av);
+      uint32_t ah[kH], al[kH];
+      ld_cols(acc_addr, ah);
+      ld_cols(acc_addr + kGroup, al);
       tc::wait_ld();
       tc::fence_before_thread_sync();
 #pragma unroll
-      for (int h = 0; h < kGroup; ++h)
-        o[h] = __uint_as_float(av[h]) + __uint_as_float(av[h + kGroup]);
+      for (int h = 0; h < kH; ++h) o[h] = __uint_as_float(ah[h]) + __uint_as_float(al[h]);
     }
     if (!ok && lane == 0) {
       flag_error(p.err, MSA_ERR_TIMEOUT);
       tail->ok = 0;
     }
-    // running sums: this thread's share -> all 128 key slots
-#pragma unroll
-    for (int h = 0; h < kGroup; ++h) {
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], off);
-    }
-    if (lane == 0) {
-#pragma unroll
-      for (int h4 = 0; h4 < 4; ++h4)
-        *reinterpret_cast<float4*>(&tail->lsum[j][quarter][4 * h4]) =
-            make_float4(l[4 * h4], l[4 * h4 + 1], l[4 * h4 + 2], l[4 * h4 + 3]);
-    }
     __syncwarp();
     named_barrier(bar, 128);
 #pragma unroll
-    for (int h = 0; h < kGroup; ++h)
-      l[h] = (tail->lsum[j][0][h] + tail->lsum[j][1][h]) + (tail->lsum[j][2][h] + tail->lsum[j][3][h]);
+    for (int h = 0; h < kH; ++h) {
+      const float4 l4 = *reinterpret_cast<const float4*>(tail->lsum[gi][h]);
+      l[h] = (l4.x + l4.y) + (l4.z + l4.w);
+    }
     const int64_t row0 = (row_tok + j) * p.Hq + g * kGroup;
     const int64_t rows = static_cast<int64_t>(kVarlen ? p.T : p.B * p.Q) * p.Hq;
     const int64_t base = static_cast<int64_t>(split) * rows + row0;
@@ -699,48 +768,47 @@ __global__ void __launch_bounds__(32 * (3 + 4 * kNT), kNT == 1 ? 2 : 1)
       // complete), then each CTA merges its share of the heads
       float* po = reinterpret_cast<float*>(smem);
 #pragma unroll
-      for (int h = 0; h < kGroup; ++h) po[h * kHeadDim + key] = l[h] > 0.f ? o[h] : 0.f;
-      if (key < kGroup) {
+      for (int h = 0; h < kH; ++h) po[(h0 + h) * kHeadDim + key] = l[h] > 0.f ? o[h] : 0.f;
 #pragma unroll
-        for (int h = 0; h < kGroup; ++h)
-          if (h == key) {
-            tail->ml[h][0] = lv - nl[h];   // M
-            tail->ml[h][1] = tail->ok ? l[h] : 0.f;
-          }
-      }
+      for (int h = 0; h < kH; ++h)
+        if (h == key) {
+          tail->ml[h0 + h][0] = lv - nl[h];   // M
+          tail->ml[h0 + h][1] = tail->ok ? l[h] : 0.f;
+        }
     } else if (tail->ok && (kNT == 1 || tok0 + j < qlen)) {
       if (p.splits == 1) {
 #pragma unroll
-        for (int h = 0; h < kGroup; ++h) {
+        for (int h = 0; h < kH; ++h) {
           const float r = l[h] > 0.f ? o[h] * (p.v_scale / l[h]) : 0.f;
-          p.out[(row0 + h) * kHeadDim + key] = static_cast<uint16_t>(f32_to_bf16_bits(r));
+          p.out[(row0 + h0 + h) * kHeadDim + key] = static_cast<uint16_t>(f32_to_bf16_bits(r));
         }
       } else {
 #pragma unroll
-        for (int h = 0; h < kGroup; ++h) p.part_o[(base + h) * kHeadDim + key] = o[h] * p.v_scale;
-        if (key < kGroup) {
+        for (int h = 0; h < kH; ++h)
+          p.part_o[(base + h0 + h) * kHeadDim + key] = o[h] * p.v_scale;
 #pragma unroll
-          for (int h = 0; h < kGroup; ++h)
-            if (h == key) {
-              p.part_ml[(base + h) * 2] = lv - nl[h];
-              p.part_ml[(base + h) * 2 + 1] = l[h];
-            }
-        }
+        for (int h = 0; h < kH; ++h)
+          if (h == key) {
+            p.part_ml[(base + h0 + h) * 2] = lv - nl[h];
+            p.part_ml[(base + h0 + h) * 2 + 1] = l[h];
+          }
       }
     }
-    if (kMode == kDense && !kCluster && split == 0 && key < kGroup && (kNT == 1 || tok0 + j < qlen)) {
+    if (kMode == kDense && !kCluster && split == 0 && key < kH && (kNT == 1 || tok0 + j < qlen)) {
       // a unit cut into fewer ranges than the workspace's parts marks the rest empty
       for (int s2 = nsplit; s2 < p.splits; ++s2) {
-        p.part_ml[(static_cast<int64_t>(s2) * rows + row0 + key) * 2] = -INFINITY;
-        p.part_ml[(static_cast<int64_t>(s2) * rows + row0 + key) * 2 + 1] = 0.f;
+        const int64_t at = (static_cast<int64_t>(s2) * rows + row0 + h0 + key) * 2;
+        p.part_ml[at] = -INFINITY;
+        p.part_ml[at + 1] = 0.f;
       }
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&tail->finish);
     if constexpr (kCluster) {
       cluster_sync();
-      const int per = kGroup / static_cast<int>(cs);   // heads of this CTA
-      for (int h = per * static_cast<int>(rank); h < per * (static_cast<int>(rank) + 1); ++h) {
+      const int per = kGroup / static_cast<int>(cs);   // heads of this CTA, the groups in turn
+      for (int i = gi; i < per; i += Groups<kNT>::kCount) {
+        const int h = per * static_cast<int>(rank) + i;
         float m[kMaxCluster], lr[kMaxCluster], v[kMaxCluster];
         float M = -INFINITY;
 #pragma unroll
@@ -808,7 +876,7 @@ cudaError_t launch(const CUtensorMap& kv_map, const AttendParams& p, dim3 grid, 
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(32 * (3 + 4 * kNT));
+  cfg.blockDim = dim3(Groups<kNT>::kThreads);
   cfg.dynamicSmemBytes = Smem<kNT>::kBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];

@@ -117,7 +117,7 @@ def test_score_on_a_k_only_cache(Q, q8):
 
 
 @pytest.mark.parametrize("seq_lens,Q,Hkv,q8", SHAPES)
-@pytest.mark.parametrize("splits,union", [(1, False), (3, False), (2, True)])
+@pytest.mark.parametrize("splits,union", [(0, False), (1, False), (3, False), (2, True)])
 def test_sparse_decode(seq_lens, Q, Hkv, q8, splits, union):
     c = _inputs(seq_lens, [Q] * len(seq_lens), Hkv, 24, spread=2.0, q8=q8)
     out, bound, _ = _ref(c, c["lists"], 0.9, 1.3)
