@@ -15,11 +15,14 @@
 // neighbour in the lane), and the lane's table entries serve all the rows it
 // rotates.
 //
-// One scale per tensor: a warp takes eight rows of one token, four 16-byte
-// loads a lane in flight.  Page scales need the largest magnitude of all of the page's new
-// rows before the first code: the rows of one (page, KV head, side) stay in
-// registers, rotated, between the maximum and the quantisation, 16 rows a
-// warp in decode, the page's up to 128 rows over the CTA's eight warps in prefill.
+// One scale per tensor: a warp takes rows of one token, eight at a time, four
+// 16-byte loads a lane in flight (eight with more than one task a warp).  Page
+// scales need the largest magnitude of all of the page's new rows before the
+// first code: in decode the rows of one (page, KV head, side), at most 16, stay in
+// one warp's registers between the maximum and the quantisation; in prefill the
+// CTA's eight warps read the page's up to 128 rows a second time, from L1 (held
+// in registers they halved the CTAs an SM, which the query rows of the same
+// launch paid for: 313 us for 28779 tokens of 64/4 heads).
 #include "msa_device.cuh"
 #include "msa_launch.h"
 
@@ -124,32 +127,49 @@ __device__ __forceinline__ bool seq_len_ok(const AppendParams& p, int L) {
 
 // ----------------------------------------------------------------------------
 // Rows of one token by one warp: query rows, and with one scale per tensor the
-// K and V rows.  Task t of a token: its first ceil(Hq / 8) tasks are query rows
-// 8 t .. 8 t + 7, the rest K and V rows.
+// K and V rows, eight a task.  A token's first ceil(Hq / 8) tasks are query rows
+// 8 t .. 8 t + 7, the rest K and V rows.  A warp takes `per` consecutive tasks of
+// one token, the next task's loads in flight while one is rotated and written:
+// the token's position and table row, four dependent loads away in a prefill
+// batch, are then fetched once for many rows.
+
+template <bool kScaled>
+struct TokenTasks {
+  int gq, all;
+  __host__ __device__ explicit TokenTasks(const AppendParams& p) {
+    gq = (p.Hq + kTokenRows - 1) / kTokenRows;
+    all = gq + (kScaled ? 0 : (p.sides * p.Hkv + kTokenRows - 1) / kTokenRows);
+  }
+};
 
 template <bool kVarlen, bool kScaled>
-__device__ __forceinline__ void token_rows(const AppendParams& p, int64_t task, int lane) {
-  const int gq = (p.Hq + kTokenRows - 1) / kTokenRows;
-  const int gkv = kScaled ? 0 : (p.sides * p.Hkv + kTokenRows - 1) / kTokenRows;
-  const int i = static_cast<int>(task / (gq + gkv));
-  const int t = static_cast<int>(task - static_cast<int64_t>(i) * (gq + gkv));
+__device__ __forceinline__ void token_rows(const AppendParams& p, int64_t work, int per, int lane) {
+  const TokenTasks<kScaled> tasks(p);
+  const int parts = (tasks.all + per - 1) / per;
+  const int i = static_cast<int>(work / parts);
+  const int first = static_cast<int>(work - static_cast<int64_t>(i) * parts) * per;
   if (i >= p.T) return;
-  const bool is_q = t < gq;
-  const int r0 = kTokenRows * (is_q ? t : t - gq);
-  const int nrows = is_q ? p.Hq : p.sides * p.Hkv;
+  const int last = min(first + per, tasks.all);
   const int ch = lane & 15, odd = lane >> 4;
-  uint4 raw[kTokenRows / 2];
+  const int kv_rows = p.sides * p.Hkv;
+  auto load = [&](int t, uint4 (&raw)[kTokenRows / 2]) {
+    const bool is_q = t < tasks.gq;
+    const int r0 = kTokenRows * (is_q ? t : t - tasks.gq) + odd;
+    const int nrows = is_q ? p.Hq : kv_rows;
 #pragma unroll
-  for (int k = 0; k < kTokenRows / 2; ++k) {
-    const int r = r0 + 2 * k + odd;
-    raw[k] = make_uint4(0u, 0u, 0u, 0u);
-    if (r < nrows) {
-      const uint16_t* src = is_q ? p.q + i * p.q_stride + r * kHeadDim
-                            : r < p.Hkv ? p.k + i * p.k_stride + r * kHeadDim
-                                        : p.v + i * p.v_stride + (r - p.Hkv) * kHeadDim;
-      raw[k] = *reinterpret_cast<const uint4*>(src + 8 * ch);
+    for (int k = 0; k < kTokenRows / 2; ++k) {
+      const int r = r0 + 2 * k;
+      raw[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < nrows) {
+        const uint16_t* src = is_q ? p.q + i * p.q_stride + r * kHeadDim
+                              : r < p.Hkv ? p.k + i * p.k_stride + r * kHeadDim
+                                          : p.v + i * p.v_stride + (r - p.Hkv) * kHeadDim;
+        raw[k] = *reinterpret_cast<const uint4*>(src + 8 * ch);
+      }
     }
-  }
+  };
+  uint4 raw[kTokenRows / 2];
+  load(first, raw);
   int b, j, qlen;
   bool ok = true;
   if constexpr (kVarlen) {
@@ -167,55 +187,58 @@ __device__ __forceinline__ void token_rows(const AppendParams& p, int64_t task, 
     if (lane == 0) flag_error(p.err, MSA_ERR_POS_RANGE);
     pos = -1;
   }
-  if (!is_q) {
-    if (pos < 0) return;   // nothing to write; warp-uniform
-    const int page = p.block_table[static_cast<int64_t>(b) * p.S + pos / kPage];
-    if (page < 0 || static_cast<int64_t>(page) >= p.num_blocks) {
-      if (lane == 0) flag_error(p.err, MSA_ERR_PAGE_RANGE);
-      return;
-    }
-    Rotation rot;
-    rot.on = false;
-    if (p.rot_dim > 0) rot.load(p, pos, lane);
-    const int src = Rotation::source(p, lane);
-    const int row_bytes = kHeadDim * p.sides;
-    uint8_t* dst = p.kv + (static_cast<int64_t>(page) * p.Hkv * kPage + pos % kPage) * row_bytes;
-#pragma unroll
-    for (int k = 0; k < kTokenRows / 2; ++k) {
-      const int r = r0 + 2 * k + odd;
-      const bool is_k = r < p.Hkv;
-      float y[8];
-      rotate8(p, rot, src, is_k, raw[k], y);
-      if (r < nrows)
-        *reinterpret_cast<uint2*>(dst +
-                                  static_cast<int64_t>(is_k ? r : r - p.Hkv) * kPage * row_bytes +
-                                  (is_k ? 0 : kHeadDim) + 8 * ch) =
-            to_e4m3x8(y, is_k ? p.inv_k : p.inv_v);
-    }
-    return;
-  }
   Rotation rot;
   rot.on = false;
   if (p.rot_dim > 0 && pos >= 0) rot.load(p, pos, lane);
   const int src = Rotation::source(p, lane);
+  for (int t = first; t < last; ++t) {
+    uint4 next[kTokenRows / 2] = {};
+    if (t + 1 < last) load(t + 1, next);
+    if (t < tasks.gq) {
+      const int r0 = kTokenRows * t + odd;
 #pragma unroll
-  for (int k = 0; k < kTokenRows / 2; ++k) {
-    const int r = r0 + 2 * k + odd;
-    if (pos < 0) raw[k] = make_uint4(0u, 0u, 0u, 0u);
-    float y[8];
-    rotate8(p, rot, src, true, raw[k], y);
-    if (r >= nrows) continue;
-    const int64_t at = (static_cast<int64_t>(i) * p.Hq + r) * kHeadDim + 8 * ch;
-    if (p.q_fp8) {
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.q_out) + at) = to_e4m3x8(y, p.inv_q);
-    } else {
-      uint4 o;
-      o.x = f32_to_bf16_bits(y[0]) | (f32_to_bf16_bits(y[1]) << 16);
-      o.y = f32_to_bf16_bits(y[2]) | (f32_to_bf16_bits(y[3]) << 16);
-      o.z = f32_to_bf16_bits(y[4]) | (f32_to_bf16_bits(y[5]) << 16);
-      o.w = f32_to_bf16_bits(y[6]) | (f32_to_bf16_bits(y[7]) << 16);
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.q_out) + at) = o;
+      for (int k = 0; k < kTokenRows / 2; ++k) {
+        const int r = r0 + 2 * k;
+        if (pos < 0) raw[k] = make_uint4(0u, 0u, 0u, 0u);
+        float y[8];
+        rotate8(p, rot, src, true, raw[k], y);
+        if (r >= p.Hq) continue;
+        const int64_t at = (static_cast<int64_t>(i) * p.Hq + r) * kHeadDim + 8 * ch;
+        if (p.q_fp8) {
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.q_out) + at) = to_e4m3x8(y, p.inv_q);
+        } else {
+          uint4 o;
+          o.x = f32_to_bf16_bits(y[0]) | (f32_to_bf16_bits(y[1]) << 16);
+          o.y = f32_to_bf16_bits(y[2]) | (f32_to_bf16_bits(y[3]) << 16);
+          o.z = f32_to_bf16_bits(y[4]) | (f32_to_bf16_bits(y[5]) << 16);
+          o.w = f32_to_bf16_bits(y[6]) | (f32_to_bf16_bits(y[7]) << 16);
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.q_out) + at) = o;
+        }
+      }
+    } else if (!kScaled && pos >= 0) {
+      const int page = p.block_table[static_cast<int64_t>(b) * p.S + pos / kPage];
+      if (page < 0 || static_cast<int64_t>(page) >= p.num_blocks) {
+        if (lane == 0) flag_error(p.err, MSA_ERR_PAGE_RANGE);
+      } else {
+        const int row_bytes = kHeadDim * p.sides;
+        uint8_t* dst = p.kv + (static_cast<int64_t>(page) * p.Hkv * kPage + pos % kPage) * row_bytes;
+        const int r0 = kTokenRows * (t - tasks.gq) + odd;
+#pragma unroll
+        for (int k = 0; k < kTokenRows / 2; ++k) {
+          const int r = r0 + 2 * k;
+          const bool is_k = r < p.Hkv;
+          float y[8];
+          rotate8(p, rot, src, is_k, raw[k], y);
+          if (r < kv_rows)
+            *reinterpret_cast<uint2*>(dst +
+                                      static_cast<int64_t>(is_k ? r : r - p.Hkv) * kPage * row_bytes +
+                                      (is_k ? 0 : kHeadDim) + 8 * ch) =
+                to_e4m3x8(y, is_k ? p.inv_k : p.inv_v);
+        }
+      }
     }
+#pragma unroll
+    for (int k = 0; k < kTokenRows / 2; ++k) raw[k] = next[k];
   }
 }
 
@@ -307,31 +330,52 @@ __device__ __forceinline__ void page_unit(const AppendParams& p, int64_t unit, i
   const uint16_t* src_rows = side == 0 ? p.k + tok0 * p.k_stride + g * kHeadDim
                                        : p.v + tok0 * p.v_stride + g * kHeadDim;
   const int64_t stride = side == 0 ? p.k_stride : p.v_stride;
+  constexpr int kHeld = kW == 1 ? kPasses : kPasses / 4;   // passes in registers at once
   const int ch = lane & 15, odd = lane >> 4;
   const float inv = side == 0 ? p.inv_k : p.inv_v;
   const int shsrc = Rotation::source(p, lane);
-  uint4 raw[kPasses];
+  // rows 2 (kW k + w) + odd, k = k0 .. k0 + n - 1, rotated and over the tensor's scale
+  auto fetch = [&](int k0, auto& y) {
+    constexpr int n = sizeof(y) / sizeof(y[0]);
+    uint4 raw[n];
 #pragma unroll
-  for (int k = 0; k < kPasses; ++k) {
-    const int r = 2 * (kW * k + w) + odd;
-    raw[k] = make_uint4(0u, 0u, 0u, 0u);
-    if (r < rows) raw[k] = *reinterpret_cast<const uint4*>(src_rows + r * stride + 8 * ch);
-  }
-  float y[kPasses][8];
+    for (int k = 0; k < n; ++k) {
+      const int r = 2 * (kW * (k0 + k) + w) + odd;
+      raw[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < rows) raw[k] = *reinterpret_cast<const uint4*>(src_rows + r * stride + 8 * ch);
+    }
+#pragma unroll
+    for (int k = 0; k < n; ++k) {
+      const int r = 2 * (kW * (k0 + k) + w) + odd;
+      Rotation rot;
+      rot.on = false;
+      if (side == 0 && p.rot_dim > 0 && r < rows) rot.load(p, first + r, lane);
+      if (side == 0) rotate8(p, rot, shsrc, true, raw[k], y[k]);
+      else unpack8(raw[k], y[k]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[k][e] *= inv;
+    }
+  };
   float amax = 0.f;
+  auto largest = [&](const auto& y) {
+    constexpr int n = sizeof(y) / sizeof(y[0]);
 #pragma unroll
-  for (int k = 0; k < kPasses; ++k) {
-    const int r = 2 * (kW * k + w) + odd;
-    Rotation rot;
-    rot.on = false;
-    if (side == 0 && p.rot_dim > 0 && r < rows) rot.load(p, first + r, lane);
-    if (side == 0) rotate8(p, rot, shsrc, true, raw[k], y[k]);
-    else unpack8(raw[k], y[k]);
+    for (int k = 0; k < n; ++k)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      y[k][e] *= inv;
-      const float a = fabsf(y[k][e]);
-      amax = a < INFINITY ? fmaxf(amax, a) : amax;   // finite values only
+      for (int e = 0; e < 8; ++e) {
+        const float a = fabsf(y[k][e]);
+        amax = a < INFINITY ? fmaxf(amax, a) : amax;   // finite values only
+      }
+  };
+  float kept[kHeld][8];
+  if constexpr (kW == 1) {
+    fetch(0, kept);
+    largest(kept);
+  } else {
+#pragma unroll 1
+    for (int k0 = 0; k0 < kPasses; k0 += kHeld) {
+      fetch(k0, kept);
+      largest(kept);
     }
   }
   amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
@@ -352,12 +396,24 @@ __device__ __forceinline__ void page_unit(const AppendParams& p, int64_t unit, i
   const int row_bytes = kHeadDim * p.sides;
   uint8_t* dst = p.kv + (static_cast<int64_t>(page) * p.Hkv + g) * kPage * row_bytes + side * kHeadDim;
   const float f = 1.f / s;
+  auto write = [&](int k0, const auto& y) {
+    constexpr int n = sizeof(y) / sizeof(y[0]);
 #pragma unroll
-  for (int k = 0; k < kPasses; ++k) {
-    const int r = 2 * (kW * k + w) + odd;
-    if (r < rows)
-      *reinterpret_cast<uint2*>(dst + static_cast<int64_t>(r0 + r) * row_bytes + 8 * ch) =
-          to_e4m3x8(y[k], f);
+    for (int k = 0; k < n; ++k) {
+      const int r = 2 * (kW * (k0 + k) + w) + odd;
+      if (r < rows)
+        *reinterpret_cast<uint2*>(dst + static_cast<int64_t>(r0 + r) * row_bytes + 8 * ch) =
+            to_e4m3x8(y[k], f);
+    }
+  };
+  if constexpr (kW == 1) {
+    write(0, kept);
+  } else {
+#pragma unroll 1
+    for (int k0 = 0; k0 < kPasses; k0 += kHeld) {
+      fetch(k0, kept);
+      write(k0, kept);
+    }
   }
   if (r0 > 0 && s > old) {
     // the scale grew: the rows before the new ones, requantised
@@ -383,8 +439,8 @@ __device__ __forceinline__ void page_unit(const AppendParams& p, int64_t unit, i
 
 // Page-scale units in the first unit_blocks CTAs, then the tokens' rows.
 template <bool kVarlen, bool kScaled, int kW>
-__global__ void __launch_bounds__(kThreads)
-    append_kernel(const AppendParams p, int unit_blocks) {
+__global__ void __launch_bounds__(kThreads, kScaled && kW == 1 ? 2 : 3)
+    append_kernel(const AppendParams p, int unit_blocks, int per) {
   __shared__ float red[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();   // cache rows, scales and outputs may be the previous kernel's
@@ -399,7 +455,7 @@ __global__ void __launch_bounds__(kThreads)
     return;
   }
   token_rows<kVarlen, kScaled>(
-      p, (static_cast<int64_t>(blockIdx.x) - unit_blocks) * kWarps + warp, lane);
+      p, (static_cast<int64_t>(blockIdx.x) - unit_blocks) * kWarps + warp, per, lane);
 }
 
 // Nothing: stands between an append and a call that may start early (see launch_append).
@@ -418,18 +474,27 @@ cudaError_t launch_append(const AppendParams& p, cudaStream_t stream, bool pdl) 
     const int64_t units = slots * p.Hkv * p.sides;
     unit_blocks = narrow ? (units + kWarps - 1) / kWarps : units;
   }
-  const int64_t per_token = (p.Hq + kTokenRows - 1) / kTokenRows +
-                            (scaled ? 0 : (p.sides * p.Hkv + kTokenRows - 1) / kTokenRows);
-  const int64_t blocks = unit_blocks + (p.T * per_token + kWarps - 1) / kWarps;
+  // Tasks of one token a warp takes: one while that leaves the GPU's warps idle
+  // (decode: latency), all of a token's when there are four waves of them.
+  const int tasks = scaled ? TokenTasks<true>(p).all : TokenTasks<false>(p).all;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int64_t wave = static_cast<int64_t>(sms) * 24;   // three CTAs an SM
+  const int64_t fit = static_cast<int64_t>(p.T) * tasks / (4 * wave);
+  const int per = tasks == 0 ? 1 : static_cast<int>(fit < 1 ? 1 : fit > tasks ? tasks : fit);
+  const int64_t warps = static_cast<int64_t>(p.T) * ((tasks + per - 1) / per);
+  const int64_t blocks = unit_blocks + (warps + kWarps - 1) / kWarps;
+  if (blocks == 0) return cudaSuccess;
   if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(blocks)), block(kThreads);
   const int ub = static_cast<int>(unit_blocks);
-  cudaError_t e =
-      !scaled ? (varlen ? launch_pdl(append_kernel<true, false, 1>, grid, block, 0, stream, pdl, p, ub)
-                        : launch_pdl(append_kernel<false, false, 1>, grid, block, 0, stream, pdl, p, ub))
-      : varlen ? launch_pdl(append_kernel<true, true, kWarps>, grid, block, 0, stream, pdl, p, ub)
-      : narrow ? launch_pdl(append_kernel<false, true, 1>, grid, block, 0, stream, pdl, p, ub)
-               : launch_pdl(append_kernel<false, true, kWarps>, grid, block, 0, stream, pdl, p, ub);
+  e = !scaled ? (varlen ? launch_pdl(append_kernel<true, false, 1>, grid, block, 0, stream, pdl, p, ub, per)
+                        : launch_pdl(append_kernel<false, false, 1>, grid, block, 0, stream, pdl, p, ub, per))
+      : varlen ? launch_pdl(append_kernel<true, true, kWarps>, grid, block, 0, stream, pdl, p, ub, per)
+      : narrow ? launch_pdl(append_kernel<false, true, 1>, grid, block, 0, stream, pdl, p, ub, per)
+               : launch_pdl(append_kernel<false, true, kWarps>, grid, block, 0, stream, pdl, p, ub, per);
   // With input overlap on, the next call's first kernel reads the cache and
   // the query before it waits for the kernel just before it.  An empty kernel
   // that starts only after this one has finished stands between them.
