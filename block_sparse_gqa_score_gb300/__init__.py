@@ -52,15 +52,22 @@ __all__ = ["score", "topk", "sparse_decode", "sparse_decode_select", "sparse_pre
 
 
 def _lib():
-    return _native.load()
+    return _native._lib or _native.load()
 
 
-def _stream(device: torch.device, stream) -> ctypes.c_void_p:
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return ctypes.c_void_p(s.cuda_stream)
+def _stream(device: torch.device, stream) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _need(t: torch.Tensor, name: str, dtypes, device=None):
+    try:   # what every call passes; the checks below name what is wrong
+        if (t.is_cuda and t.dtype in dtypes and t.is_contiguous()
+                and (device is None or t.device == device)):
+            return
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -87,20 +94,21 @@ def _geometry(q, kv, block_table, seq_lens, qlen: int | None, k_only_ok: bool = 
     _need(kv, "kv", _KV_DTYPES, dev)
     _need(block_table, "block_table", (torch.int32,), dev)
     _need(seq_lens, "seq_lens", (torch.int32,), dev)
-    if kv.dim() != 4 or kv.shape[2] != PAGE_SIZE or not (
-            kv.shape[3] == 2 * HEAD_DIM or (k_only_ok and kv.shape[3] == HEAD_DIM)):
+    shape, rows, table = kv.shape, q.shape, block_table.shape
+    if len(shape) != 4 or shape[2] != PAGE_SIZE or not (
+            shape[3] == 2 * HEAD_DIM or (k_only_ok and shape[3] == HEAD_DIM)):
         raise ValueError("kv must be [num_blocks, Hkv, 128, 256]"
                          + (" (or a K-only [num_blocks, Hkv, 128, 128])" if k_only_ok else ""))
-    if q.dim() != 3 or q.shape[2] != HEAD_DIM:
+    if len(rows) != 3 or rows[2] != HEAD_DIM:
         raise ValueError("q must be [T, Hq, 128]")
-    if block_table.dim() != 2 or seq_lens.dim() != 1 or block_table.shape[0] != seq_lens.shape[0]:
+    if len(table) != 2 or seq_lens.shape != table[:1]:
         raise ValueError("block_table must be [B, S] and seq_lens [B]")
-    B, S = block_table.shape
-    Hkv = kv.shape[1]
-    Hq = q.shape[1]
-    if qlen is not None and q.shape[0] != B * qlen:
-        raise ValueError(f"q has {q.shape[0]} tokens, expected B*qlen = {B * qlen}")
-    return dev, int(B), int(S), int(Hq), int(Hkv), int(kv.shape[0])
+    B, S = table
+    Hkv = shape[1]
+    Hq = rows[1]
+    if qlen is not None and rows[0] != B * qlen:
+        raise ValueError(f"q has {rows[0]} tokens, expected B*qlen = {B * qlen}")
+    return dev, B, S, Hq, Hkv, shape[0]
 
 
 def workspace_bytes(batch: int, qlen: int, num_q_heads: int, num_splits: int) -> int:
@@ -125,7 +133,7 @@ def _fp8(q, q_scale: float) -> bool:
 def _page_scales(kv_scales, name: str, dev, num_blocks: int, num_kv_heads: int, sides: int):
     """Checks page scales fp32 [num_blocks, Hkv, sides] and returns their address."""
     _need(kv_scales, name, (torch.float32,), dev)
-    if tuple(kv_scales.shape) != (num_blocks, num_kv_heads, sides):
+    if kv_scales.shape != (num_blocks, num_kv_heads, sides):
         raise ValueError(f"{name} must be [num_blocks, Hkv, {sides}]")
     return kv_scales.data_ptr()
 
@@ -510,11 +518,11 @@ def _rows(t, name: str, heads: int, tokens: int, dev):
     returns the tokens' distance in elements."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
     if t.device != dev:
         raise ValueError(f"{name} must be on {dev}")
-    if t.dim() != 3 or t.shape[0] != tokens or t.shape[1] != heads or t.shape[2] != HEAD_DIM:
+    if t.shape != (tokens, heads, HEAD_DIM):
         raise ValueError(f"{name} must be [{tokens}, {heads}, 128]")
     st, sh, sd = t.stride()
     if sd != 1 or (heads > 1 and sh != HEAD_DIM):
@@ -533,13 +541,14 @@ def _append(fn, k, v, kv, block_table, seq_lens, tokens, cu, qlen, k_scale, v_sc
     _need(block_table, "block_table", (torch.int32,), dev)
     _need(seq_lens, "seq_lens", (torch.int32,), dev)
     sides = 1 if v is None else 2
-    if kv.dim() != 4 or kv.shape[2] != PAGE_SIZE or kv.shape[3] != sides * HEAD_DIM:
+    shape, table = kv.shape, block_table.shape
+    if len(shape) != 4 or shape[2] != PAGE_SIZE or shape[3] != sides * HEAD_DIM:
         raise ValueError("kv must be [num_blocks, Hkv, 128, 256], or without v a K-only "
                          "[num_blocks, Hkv, 128, 128]")
-    if block_table.dim() != 2 or seq_lens.dim() != 1 or block_table.shape[0] != seq_lens.shape[0]:
+    if len(table) != 2 or seq_lens.shape != table[:1]:
         raise ValueError("block_table must be [B, S] and seq_lens [B]")
-    B, S = block_table.shape
-    NB, Hkv = kv.shape[0], kv.shape[1]
+    B, S = table
+    NB, Hkv = shape[0], shape[1]
     Hq = GROUP * Hkv
     if tokens is None:
         tokens = B * qlen
@@ -552,7 +561,7 @@ def _append(fn, k, v, kv, block_table, seq_lens, tokens, cu, qlen, k_scale, v_sc
         if q_out is None:
             q_out = torch.empty((tokens, Hq, HEAD_DIM), dtype=torch.bfloat16, device=dev)
         _need(q_out, "q_out", (torch.bfloat16,) + ((_FP8_Q,) if _FP8_Q is not None else ()), dev)
-        if tuple(q_out.shape) != (tokens, Hq, HEAD_DIM):
+        if q_out.shape != (tokens, Hq, HEAD_DIM):
             raise ValueError("q_out must be [T, Hq, 128]")
         qo = q_out.data_ptr()
         if _fp8(q_out, q_scale):
@@ -565,20 +574,21 @@ def _append(fn, k, v, kv, block_table, seq_lens, tokens, cu, qlen, k_scale, v_sc
     tab, max_pos, rot = None, 0, 0
     if cos_sin is not None:
         _need(cos_sin, "cos_sin", (torch.float32,), dev)
-        if cos_sin.dim() != 2:
+        table = cos_sin.shape
+        if len(table) != 2:
             raise ValueError("cos_sin must be [max_pos, rot_dim]")
-        tab, (max_pos, rot) = cos_sin.data_ptr(), cos_sin.shape
+        tab, (max_pos, rot) = cos_sin.data_ptr(), table
         if rot == 0 or rot > HEAD_DIM or rot % 16:
             raise ValueError("rot_dim must be a multiple of 16 up to 128")
     if B == 0 and tokens == 0:
         return q_out        # empty tensors have no address to check
     mid = () if cu is None else (cu.data_ptr(),)
-    st = getattr(_lib(), fn)(
+    st = fn(
         k.data_ptr(), ks, v.data_ptr() if v is not None else None, vs, qp, qs or 0, tab, max_pos,
         rot, 1 if interleaved else 0, kv.data_ptr(), sc, qo, q8, block_table.data_ptr(),
         seq_lens.data_ptr(), *mid, B, tokens if cu is not None else qlen, Hq, Hkv, S, NB,
-        float(k_scale), float(v_scale), _stream(dev, stream))
-    _native.check(st, fn)
+        k_scale, v_scale, _stream(dev, stream))
+    _native.check(st, fn.__name__)
     return q_out
 
 
@@ -597,7 +607,7 @@ def append_kv(k, v, kv, block_table, seq_lens, qlen: int, k_scale: float = 1.0,
     halves or, with `interleaved`, in neighbouring pairs.  kv_scales [NB, Hkv,
     2] (or 1): page scales, updated; else codes are x / k_scale, x / v_scale.
     Returns q_out (None without q)."""
-    return _append("msa_append_kv", k, v, kv, block_table, seq_lens, None, None, qlen, k_scale,
+    return _append(_lib().msa_append_kv, k, v, kv, block_table, seq_lens, None, None, qlen, k_scale,
                    v_scale, kv_scales, cos_sin, interleaved, q, q_out, q_scale, stream)
 
 
@@ -611,7 +621,7 @@ def append_kv_prefill(k, v, kv, block_table, seq_lens, cu_seqlens_q, k_scale: fl
     _need(cu_seqlens_q, "cu_seqlens_q", (torch.int32,), seq_lens.device)
     if tuple(cu_seqlens_q.shape) != (seq_lens.shape[0] + 1,):
         raise ValueError("cu_seqlens_q must be [B + 1]")
-    return _append("msa_append_kv_prefill", k, v, kv, block_table, seq_lens, k.shape[0],
+    return _append(_lib().msa_append_kv_prefill, k, v, kv, block_table, seq_lens, k.shape[0],
                    cu_seqlens_q, None, k_scale, v_scale, kv_scales, cos_sin, interleaved, q, q_out,
                    q_scale, stream)
 

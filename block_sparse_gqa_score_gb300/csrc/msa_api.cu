@@ -404,6 +404,7 @@ int prepare_attend(const void* q, const void* kv, const int32_t* block_table,
   p.T = cu_q ? T : 0;
   p.union_tile = union_tile ? 1 : 0;
   p.kv_scales = kv_scales;
+  p.sms = dev->sm_count;
   L->rows = rows;
   *empty = false;
   return MSA_OK;
@@ -804,6 +805,7 @@ int append_kv(const void* k, int64_t k_stride, const void* v, int64_t v_stride, 
   p.Hkv = Hkv;
   p.S = S;
   p.num_blocks = num_blocks;
+  p.sms = dev->sm_count;
   return from_cuda(
       msa::launch_append(p, reinterpret_cast<cudaStream_t>(stream), input_overlap()));
 }

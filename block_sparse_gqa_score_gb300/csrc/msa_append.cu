@@ -475,22 +475,22 @@ cudaError_t launch_append(const AppendParams& p, cudaStream_t stream, bool pdl) 
     unit_blocks = narrow ? (units + kWarps - 1) / kWarps : units;
   }
   // Tasks of one token a warp takes: one while that leaves the GPU's warps idle
-  // (decode: latency), all of a token's when there are four waves of them.
+  // (decode: latency), all of a token's when there is a wave of such warps (6000
+  // tokens of 64/4 heads: 9 tasks a warp 41.1 us, 3 41.9, 1 58.4), in equal shares.
   const int tasks = scaled ? TokenTasks<true>(p).all : TokenTasks<false>(p).all;
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
-  const int64_t wave = static_cast<int64_t>(sms) * 24;   // three CTAs an SM
-  const int64_t fit = static_cast<int64_t>(p.T) * tasks / (4 * wave);
-  const int per = tasks == 0 ? 1 : static_cast<int>(fit < 1 ? 1 : fit > tasks ? tasks : fit);
+  const int64_t wave = static_cast<int64_t>(p.sms) * 24;   // three CTAs an SM
+  const int64_t fit = static_cast<int64_t>(p.T) * tasks / wave;
+  int per = tasks == 0 ? 1 : static_cast<int>(fit < 1 ? 1 : fit > tasks ? tasks : fit);
+  const int shares = (tasks + per - 1) / per;
+  if (shares > 0) per = (tasks + shares - 1) / shares;
   const int64_t warps = static_cast<int64_t>(p.T) * ((tasks + per - 1) / per);
   const int64_t blocks = unit_blocks + (warps + kWarps - 1) / kWarps;
   if (blocks == 0) return cudaSuccess;
   if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(blocks)), block(kThreads);
   const int ub = static_cast<int>(unit_blocks);
-  e = !scaled ? (varlen ? launch_pdl(append_kernel<true, false, 1>, grid, block, 0, stream, pdl, p, ub, per)
+  cudaError_t e =
+      !scaled ? (varlen ? launch_pdl(append_kernel<true, false, 1>, grid, block, 0, stream, pdl, p, ub, per)
                         : launch_pdl(append_kernel<false, false, 1>, grid, block, 0, stream, pdl, p, ub, per))
       : varlen ? launch_pdl(append_kernel<true, true, kWarps>, grid, block, 0, stream, pdl, p, ub, per)
       : narrow ? launch_pdl(append_kernel<false, true, 1>, grid, block, 0, stream, pdl, p, ub, per)

@@ -62,6 +62,8 @@ constexpr float kPTop = 8.5f;                 // M moves when some P would pass 
 constexpr int kChunk = 32;                    // dense decode: pages looked up at once, one a lane
 constexpr int kSelectCap = 8000;              // selector keys in stage 1, then its slots
 constexpr int kMaxCluster = 8;
+constexpr int kTableCopy = 512;               // block-table entries copied to shared memory
+constexpr int kTableBarrier = 15;             // warps 0 and 2 of the prologue
 
 enum Mode { kLists, kSelect, kDense };
 
@@ -123,6 +125,7 @@ static_assert(4 * kSelectCap + 4 * kTopK <= kStageBytes, "selector scratch fits 
 static_assert(2 * (Smem<1>::kBytes + 1024) <= 228 * 1024, "two CTAs an SM");
 static_assert(Smem<4>::kBytes <= 227 * 1024, "one CTA an SM");
 static_assert(kGroup * kHeadDim * 4 <= kStageBytes, "a CTA's part fits a stage");
+static_assert(4 * kTableCopy <= 2 * Smem<1>::kPBuf, "the block-table copy fits the P^T buffers");
 
 // The barrier of one group's four warps, with the or of a predicate.
 __device__ __forceinline__ bool barrier_or(int id, bool pred) {
@@ -251,6 +254,8 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
     }
   }
   const int32_t* trow = p.block_table + static_cast<int64_t>(b) * p.S;
+  const int ncopy = p.S < kTableCopy ? p.S : kTableCopy;
+  int32_t* table_s = reinterpret_cast<int32_t*>(pbuf);   // prologue only
   const int L = p.seq_lens[b];
   // a prefill request's tokens are the last qlen of its sequence
   const bool seq_ok = tok_ok && L >= 0 && (L == 0 || (L - 1) / kPage < p.S) &&
@@ -310,20 +315,35 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
   auto next_info = [&]() -> PageInfo {
     return blk_next >= 0 ? page_info(p, sc_next, blk_next) : PageInfo{1.f, 0.f, 1.f, -1};
   };
+  int n_list = -1;
+  if (kMode == kLists && warp == 0) {
+    pdl_wait();   // the lists may be the previous kernel's
+    if (lane < kTopK) n_list = p.topk[(row_tok * p.Hkv + g) * kTopK + lane];
+  }
+  if (kMode != kDense && warp == 2) {
+    // the request's block-table row (its first kTableCopy entries), all loads in
+    // flight while the list is fetched
+    int32_t v[kTableCopy / 32];
+#pragma unroll
+    for (int k = 0; k < kTableCopy / 32; ++k) v[k] = 32 * k + lane < ncopy ? trow[32 * k + lane] : 0;
+#pragma unroll
+    for (int k = 0; k < kTableCopy / 32; ++k)
+      if (32 * k + lane < ncopy) table_s[32 * k + lane] = v[k];
+    named_barrier(kTableBarrier, 64);
+  }
   if (warp == 0) {
     if (!seq_ok && lane == 0 && split == 0 && rank == 0) flag_error(p.err, MSA_ERR_SEQ_RANGE);
     const int cur = last_pos >= 0 ? last_pos / kPage : -1;
     const int part = split * static_cast<int>(cs) + static_cast<int>(rank);
     const int nparts = nsplit * static_cast<int>(cs);
-    if (kMode != kDense && 32 * lane < p.S)   // the table row's lines, for the look-ups below
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(trow + 32 * lane));
     int pre_page = -1;   // select mode: the current block's page, always listed, first
     if (kMode == kSelect && cur >= 0 && part == 0) {
       const int pg = trow[cur];
       if (pg >= 0 && static_cast<int64_t>(pg) < p.num_blocks) pre_page = pg;
     }
     if (lane == 0) {
-      const unsigned warps = 4u * Groups<kNT>::kPerToken * static_cast<unsigned>(max(valid_toks, 1));
+      const unsigned warps =
+          4u * Groups<kNT>::kPerToken * (kNT == 1 ? 1u : static_cast<unsigned>(max(valid_toks, 1)));
       for (int s = 0; s < kStages; ++s) {
         mbar_init(&tail->full[s], 1);
         mbar_init(&tail->empty[s], 1);
@@ -353,10 +373,10 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
       }
       tail->info[lane] = next_info();
     } else {
-      pdl_wait();   // the lists, or the scores they come from, are the previous kernel's
       const int64_t list = (row_tok * p.Hkv + g) * kTopK;
-      int n;
+      int n = n_list;
       if constexpr (kMode == kSelect) {
+        pdl_wait();   // the scores are the previous kernel's
         bool nan = false;
         uint8_t* scratch = smem + kStageBytes;   // stage 1, not yet loaded
         n = last_pos >= 0
@@ -369,8 +389,6 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
         if (__any_sync(0xffffffffu, nan) && lane == 0) flag_error(p.err, MSA_ERR_SCORE_NAN);
         tc::fence_proxy_async_smem();            // scratch writes before TMA loads into it
         __syncwarp();
-      } else {
-        n = lane < kTopK ? p.topk[list + lane] : -1;
       }
       bool valid = lane < kTopK && last_pos >= 0 && n != -1;
       if (valid && (n < 0 || n > cur)) {
@@ -385,8 +403,9 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
         }
       }
       int page = -1;
+      named_barrier(kTableBarrier, 64);
       if (valid) {
-        page = trow[n];
+        page = n < ncopy ? table_s[n] : trow[n];
         if (page < 0 || static_cast<int64_t>(page) >= p.num_blocks) {
           flag_error(p.err, MSA_ERR_PAGE_RANGE);
           valid = false;
@@ -779,7 +798,7 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
       if (p.splits == 1) {
 #pragma unroll
         for (int h = 0; h < kH; ++h) {
-          const float r = l[h] > 0.f ? o[h] * (p.v_scale / l[h]) : 0.f;
+          const float r = l[h] > 0.f ? o[h] * __fdividef(p.v_scale, l[h]) : 0.f;
           p.out[(row0 + h0 + h) * kHeadDim + key] = static_cast<uint16_t>(f32_to_bf16_bits(r));
         }
       } else {
@@ -918,10 +937,7 @@ cudaError_t launch_attend_scaled(const CUtensorMap& kv_map, const AttendParams& 
                                  cudaStream_t stream, bool pdl) {
   const bool dense = p.dense_span > 0;
   if (p.union_tile && !dense) return launch_union_attend_scaled(kv_map, p, stream, pdl);
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
+  const int sms = p.sms;
   const int ntile = p.Q > 1 && dense ? 4 : 1;                  // tokens a tile
   const int64_t slots = ntile == 1 ? 2 * sms : sms;            // CTAs resident at once
   const int tiles = (p.Q + ntile - 1) / ntile;

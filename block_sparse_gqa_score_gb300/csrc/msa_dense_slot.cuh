@@ -50,16 +50,25 @@ __device__ DenseSlot dense_slot(const AttendParams& p, int ntiles, int C, int c,
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     const int tu = 32 * k + lane;
-    n[k] = tu < NT ? dense_tile_blocks<kTile>(p, tu, ntiles) : 0;
-    maxn = max(maxn, n[k]);
+    n[k] = 0;
+    if (32 * k < NT) {   // the same in every lane, here and below
+      n[k] = tu < NT ? dense_tile_blocks<kTile>(p, tu, ntiles) : 0;
+      maxn = max(maxn, n[k]);
+    }
   }
   maxn = __reduce_max_sync(0xffffffffu, maxn);
-  auto parts = [&](int k, int T) { return min(max((n[k] + T - 1) / T, 1), Z); };
+  // ceil(n / T) as floor((n + T - 1/2) / T): the quotient is at least 1 / (2 T) off an
+  // integer and the float product at most (n + T) / T * 2^-22 off the quotient
+  // (n, T <= 2048)
+  auto parts = [&](int k, float rT, float Th) {
+    return min(max(__float2int_rz((static_cast<float>(n[k]) + Th) * rT), 1), Z);
+  };
   auto ctas = [&](int T) {
+    const float rT = 1.f / static_cast<float>(T), Th = static_cast<float>(T) - 0.5f;
     int s = 0;
 #pragma unroll
     for (int k = 0; k < kPer; ++k)
-      if (32 * k + lane < NT) s += parts(k, T);
+      if (32 * k < NT && 32 * k + lane < NT) s += parts(k, rT, Th);
     return static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(s))) * H;
   };
   // at T = max(n) every unit takes one CTA per head, NT * H <= C (the host's rule)
@@ -69,11 +78,13 @@ __device__ DenseSlot dense_slot(const AttendParams& p, int ntiles, int C, int c,
     if (ctas(mid) <= C) hi = mid;
     else lo = mid + 1;
   }
+  const float rT = 1.f / static_cast<float>(lo), Th = static_cast<float>(lo) - 0.5f;
   int run = 0;   // CTAs of the units before this group of 32
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
+    if (32 * k >= NT) break;
     const int tu = 32 * k + lane;
-    const int zc = tu < NT ? parts(k, lo) : 0;
+    const int zc = tu < NT ? parts(k, rT, Th) : 0;
     int incl = zc * H;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {

@@ -68,6 +68,7 @@ struct AttendParams {
   // 0: one CTA per (token, KV head)
   int union_tile;
   const float* kv_scales;      // page scales [num_blocks, Hkv, 2] (K, V); or nullptr
+  int sms;                     // SM count
 };
 
 // Runs `set_up` once per device (e.g. raising a kernel's dynamic shared-memory
@@ -155,6 +156,7 @@ struct AppendParams {
   int Hq;                      // 0 without a query
   int Hkv, S;
   int64_t num_blocks;
+  int sms;
 };
 cudaError_t launch_append(const AppendParams& p, cudaStream_t stream, bool pdl);
 
