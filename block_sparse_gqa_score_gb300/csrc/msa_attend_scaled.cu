@@ -91,6 +91,7 @@ struct Tail {
   uint64_t s_empty[2];      // softmax has read S^T
   uint64_t p_full[2];       // P^T written -> O^T
   uint64_t o_done[2];       // O^T of a page complete (its P^T buffer free)
+  uint64_t info_ready;      // the first pages' scales and blocks are in `info`
   uint64_t finish;          // every role done and every product complete
   uint32_t tmem_base;
   int n_pages;
@@ -283,8 +284,9 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
   }
 
   // ---- prologue ----------------------------------------------------------------------
-  // dense decode, warp 0: the lane's page of the next chunk, its block (-1: none) and scales
+  // warp 0: the lane's page, its block (-1: none) and scales (dense decode: of the next chunk)
   int pg_next = 0, blk_next = -1;
+  int slot = lane;   // list modes: the lane's page's place in this CTA's order
   float2 sc_next = make_float2(1.f, 1.f);
   auto load_page = [&](int t, int page) {   // one lane: page `page` into stage t % kStages
     const int s = t % kStages;
@@ -354,6 +356,7 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
         mbar_init(&tail->p_full[s], warps);
         mbar_init(&tail->o_done[s], 1);
       }
+      mbar_init(&tail->info_ready, 1);
       mbar_init(&tail->finish, 3 + 4 * Groups<kNT>::kCount);
       fence_barrier_init();
       prefetch_tensormap(&kv_map);
@@ -371,7 +374,6 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
         const int pg = __shfl_sync(0xffffffffu, pg_next, t);
         if (lane == 0) load_page(t, pg);
       }
-      tail->info[lane] = next_info();
     } else {
       const int64_t list = (row_tok * p.Hkv + g) * kTopK;
       int n = n_list;
@@ -419,10 +421,15 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
       const bool mine = valid && idx % nparts == part;
       const int k = idx / nparts;
       np = __popc(__ballot_sync(0xffffffffu, mine));
+      // the scales are asked for before the pages: behind the first pages of all
+      // CTAs they came two microseconds later
       if (mine) {
+        pg_next = page;
+        blk_next = n;
+        slot = k;
+        look_up_scales();
         tail->pages[k] = page;
         if (k < kStages && !(k == 0 && pre_page >= 0)) load_page(k, page);
-        tail->info[k] = page_info(p, load_page_scale(p.kv_scales, page, p.Hkv, g), n);
       }
     }
     if (lane == 0) tail->n_pages = np;
@@ -471,6 +478,10 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
 
   if (warp == 0) {
     // ---- TMA producer ------------------------------------------------------------------
+    // the first pages' scales, which the softmax waits for, have arrived meanwhile
+    if (kMode == kDense || blk_next >= 0) tail->info[slot] = next_info();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&tail->info_ready);
     int issued = min(n_pages, kStages);
     bool ok = true;
     if constexpr (kMode == kDense) {
@@ -601,7 +612,9 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
       const int buf = k & 1;
       const unsigned ph = (k >> 1) & 1;
       float t[kH];
-      // the page's scales and block, written before the page was loaded
+      // the page's scales and block, written before the page was loaded or, the
+      // first ones, announced
+      if (k == 0 && ok) ok = mbar_wait(&tail->info_ready, 0);
       if (kMode == kDense && ok) ok = mbar_wait(&tail->full[s], full_ph);
       if (ok) ok = mbar_wait(&tail->s_full[buf], ph);
       tc::fence_after_thread_sync();

@@ -44,47 +44,44 @@ __device__ DenseSlot dense_slot(const AttendParams& p, int ntiles, int C, int c,
   const int NT = p.B * ntiles, H = p.Hkv, Z = p.splits;
   if (C <= NT * H)
     return DenseSlot{c, static_cast<int>(blockIdx.y), static_cast<int>(gridDim.y)};
-  constexpr int kPer = kBalancedTiles / 32;
-  int n[kPer];
-  int maxn = 0;
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const int tu = 32 * k + lane;
-    n[k] = 0;
-    if (32 * k < NT) {   // the same in every lane, here and below
-      n[k] = tu < NT ? dense_tile_blocks<kTile>(p, tu, ntiles) : 0;
-      maxn = max(maxn, n[k]);
-    }
-  }
-  maxn = __reduce_max_sync(0xffffffffu, maxn);
+  // Lane l holds (request, tile) unit l; the units past the 32nd, if any, are read
+  // again where they are needed.  Loops, not unrolled: this code runs once, and its
+  // instructions cost more to fetch than to execute.
+  const int n0 = lane < NT ? dense_tile_blocks<kTile>(p, lane, ntiles) : 0;
+  auto blocks = [&](int k) {
+    return k == 0 ? n0 : k + lane < NT ? dense_tile_blocks<kTile>(p, k + lane, ntiles) : 0;
+  };
+  int total = 0;
+#pragma unroll 1
+  for (int k = 0; k < NT; k += 32)
+    total += static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(blocks(k))));
   // ceil(n / T) as floor((n + T - 1/2) / T): the quotient is at least 1 / (2 T) off an
   // integer and the float product at most (n + T) / T * 2^-22 off the quotient
-  // (n, T <= 2048)
+  // (n + T < 2^20)
   auto parts = [&](int k, float rT, float Th) {
-    return min(max(__float2int_rz((static_cast<float>(n[k]) + Th) * rT), 1), Z);
+    return k + lane < NT ? min(max(__float2int_rz((static_cast<float>(blocks(k)) + Th) * rT), 1), Z)
+                         : 0;
   };
-  auto ctas = [&](int T) {
-    const float rT = 1.f / static_cast<float>(T), Th = static_cast<float>(T) - 0.5f;
-    int s = 0;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k)
-      if (32 * k < NT && 32 * k + lane < NT) s += parts(k, rT, Th);
-    return static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(s))) * H;
-  };
-  // at T = max(n) every unit takes one CTA per head, NT * H <= C (the host's rule)
-  int lo = 1, hi = max(maxn, 1);
+  // the smallest T with sum z_u <= C / H: T = total / (C / H - NT) has it, since z_u is
+  // at most n / T + 1 (and so has T = total, one CTA a unit)
+  const int per = C / H;
+  int lo = 1, hi = (total + per - NT) / max(per - NT, 1) + 1;
+#pragma unroll 1
   while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (ctas(mid) <= C) hi = mid;
-    else lo = mid + 1;
+    const int T = (lo + hi) >> 1;
+    const float rT = 1.f / static_cast<float>(T), Th = static_cast<float>(T) - 0.5f;
+    int sum = 0;
+#pragma unroll 1
+    for (int k = 0; k < NT; k += 32)
+      sum += static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(parts(k, rT, Th))));
+    if (sum <= per) hi = T;
+    else lo = T + 1;
   }
   const float rT = 1.f / static_cast<float>(lo), Th = static_cast<float>(lo) - 0.5f;
   int run = 0;   // CTAs of the units before this group of 32
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    if (32 * k >= NT) break;
-    const int tu = 32 * k + lane;
-    const int zc = tu < NT ? parts(k, rT, Th) : 0;
+#pragma unroll 1
+  for (int k = 0; k < NT; k += 32) {
+    const int zc = parts(k, rT, Th);
     int incl = zc * H;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -98,7 +95,7 @@ __device__ DenseSlot dense_slot(const AttendParams& p, int ntiles, int C, int c,
       const int st = __shfl_sync(0xffffffffu, start, src);
       const int z = __shfl_sync(0xffffffffu, zc, src);
       const int rel = c - st;
-      return DenseSlot{(32 * k + src) * H + rel / z, rel % z, z};
+      return DenseSlot{(k + src) * H + rel / z, rel % z, z};
     }
     run += __shfl_sync(0xffffffffu, incl, 31);
   }

@@ -466,9 +466,18 @@ __device__ __forceinline__ PageScale make_page_scale(float2 s) {
   return PageScale{s.x, log2f(s.y), 1.f / s.y, 0.f};
 }
 
+// Kept in L2 before other lines (evict_last): the scales of a cache are a 4096th
+// of its bytes and read on every step, while its pages stream through.
 __device__ __forceinline__ float2 load_page_scale(const float* __restrict__ scales, int64_t page,
                                                   int Hkv, int g) {
-  return __ldg(reinterpret_cast<const float2*>(scales) + page * Hkv + g);
+  const float2* at = reinterpret_cast<const float2*>(scales) + page * Hkv + g;
+  float2 v;
+  asm volatile("{\n\t.reg .b64 p;\n\t"
+      "createpolicy.fractional.L2::evict_last.b64 p, 1.0;\n\t"
+      "ld.global.nc.L2::cache_hint.v2.f32 {%0, %1}, [%2], p;\n\t}"
+      : "=f"(v.x), "=f"(v.y)
+      : "l"(at));
+  return v;
 }
 
 }  // namespace msa
