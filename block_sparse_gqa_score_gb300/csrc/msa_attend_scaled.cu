@@ -209,10 +209,16 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
     scaled_attend_kernel(const __grid_constant__ CUtensorMap kv_map, const AttendParams p) {
   using Sm = Smem<kNT>;
   constexpr int kStages = Sm::kStages;
-  constexpr int kQRows = kFp8Q ? kGroup : 2 * kGroup;      // query tile rows of one token
-  constexpr int kSN = kQRows * kNT;                        // columns of one S^T buffer
-  constexpr uint32_t kColAcc = 2 * 2 * kGroup * kNT;       // O^T behind two S^T buffers
-  constexpr int kTmemCols = kNT == 1 ? 128 : 512;
+  // A bf16 query's tile: the hi rows of all tokens, then the lo rows.  One token: both
+  // in one product, N = 32, added by the softmax.  More: two products into the same
+  // columns, which takes the tensor core as long (N = 64 twice for 128 once) and
+  // halves what the softmax reads of tensor memory.
+  constexpr bool kFold = kNT > 1 && !kFp8Q;
+  constexpr int kSCols = kFp8Q || kFold ? kGroup : 2 * kGroup;   // S^T columns of one token
+  constexpr int kSN = kSCols * kNT;                        // columns of one S^T buffer
+  constexpr uint32_t kColAcc = 2 * kSN;                    // O^T behind two S^T buffers
+  constexpr int kTmemCols = kNT == 1 ? 128 : 256;
+  static_assert(kColAcc + 2 * kGroup * kNT <= kTmemCols, "tensor memory");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -442,16 +448,16 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
     if (tok0 + j < qlen || kNT == 1) {
       const int64_t row = (row_tok + j) * p.Hq + g * kGroup;
       if constexpr (kFp8Q) {
-        store_query_rows_fp8(p.q8 + row * kHeadDim, kQRows * j, qtile, lane);
+        store_query_rows_fp8(p.q8 + row * kHeadDim, kGroup * j, qtile, lane);
         if (lane == 0) tail->zs[j] = p.logit_scale * p.q_scale;
       } else {
-        const int e = prepare_query_e4m3(p.q + row * kHeadDim, kQRows * j, qtile,
-                                         qtile + kGroup * 128, lane);
+        const int e = prepare_query_e4m3(p.q + row * kHeadDim, kGroup * j, qtile,
+                                         qtile + kGroup * kNT * 128, lane);
         if (lane == 0) tail->zs[j] = p.logit_scale * exp2i(e);
       }
     } else {
-      zero_query_rows(kQRows * j, qtile, lane);
-      if (!kFp8Q) zero_query_rows(kQRows * j + kGroup, qtile, lane);
+      zero_query_rows(kGroup * j, qtile, lane);
+      if (!kFp8Q) zero_query_rows(kGroup * (kNT + j), qtile, lane);
       if (lane == 0) tail->zs[j] = 0.f;
     }
     tc::fence_proxy_async_smem();   // the tile is read by the tensor core
@@ -544,6 +550,12 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
           tc::mma_e4m3(tmem + kSN * buf, a + 2 * ks, bq + 2 * ks, idesc, ks > 0);
+        if constexpr (kFold) {
+          constexpr uint64_t kLo = (kGroup * kNT * 128) >> 4;   // the lo rows
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            tc::mma_e4m3(tmem + kSN * buf, a + 2 * ks, bq + kLo + 2 * ks, idesc, 1);
+        }
         tc::commit(&tail->s_full[buf]);
       }
       tc::commit(&tail->finish);
@@ -589,7 +601,7 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
     const int quarter = warp & 3;
     const int key = 32 * quarter + lane;   // key of the page; value dim at the end
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
-    const uint32_t s_addr = lane_addr + kQRows * j + h0;
+    const uint32_t s_addr = lane_addr + kSCols * j + h0;
     const uint32_t acc_addr = lane_addr + kColAcc + 32 * j + h0;
     const int bar = 1 + gi;
     const float zs = tail->zs[j];
@@ -627,11 +639,11 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
         lv = in.lv;
       }
       const int lim = in.block < 0 ? -1 : pos - in.block * kPage;   // keys <= lim are visible
-      // u - M + kPShift: the raw dot products (hi and lo columns) times zt, plus nl
+      // u - M + kPShift: the raw dot products times zt, plus nl
       {
         uint32_t sv[kH];
         ld_cols(s_addr + kSN * buf, sv);
-        if constexpr (!kFp8Q && kH == 8) {
+        if constexpr (kSCols == 2 * kGroup) {
           uint32_t sl[kH];
           ld_cols(s_addr + kSN * buf + kGroup, sl);
           tc::wait_ld();
@@ -642,12 +654,6 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
           tc::wait_ld();
 #pragma unroll
           for (int h = 0; h < kH; ++h) t[h] = fmaf(__uint_as_float(sv[h]), zt, nl[h]);
-          if constexpr (!kFp8Q) {   // one half at a time: 96 registers a thread
-            ld_cols(s_addr + kSN * buf + kGroup, sv);
-            tc::wait_ld();
-#pragma unroll
-            for (int h = 0; h < kH; ++h) t[h] = fmaf(__uint_as_float(sv[h]), zt, t[h]);
-          }
         }
       }
       tc::fence_before_thread_sync();
