@@ -26,19 +26,21 @@
 // Layout: as the attend for one scale per tensor.  One CTA per (tile of kNT
 // tokens of one request, KV head, part); the tile's 16 kNT query rows are the N
 // of two transposed tensor-core products per page, S^T = K Q^T (the bf16 query
-// as exact fp8 hi and lo parts, N = 32 per token; an fp8 query as it is, N = 16)
-// and O^T += V^T P^T (P's hi and lo parts, N = 32 per token), so that the page's
-// 128 keys, then its 128 value dims, fill M, and fp8 pages are operands as
-// stored.  O^T stays in tensor memory over all pages.  kNT = 1 (lists, and dense
-// decode of single tokens): two CTAs an SM with 3-stage rings of 32 KiB pages;
-// kNT = 4 (dense decode of two or more tokens a request): one CTA an SM, five
-// stages, each page loaded once for four tokens.
-//   warp 0       page lists, scales, TMA
+// as exact fp8 hi and lo parts; an fp8 query as it is) and O^T += V^T P^T (P's hi
+// and lo parts, N = 32 per token), so that the page's 128 keys, then its 128 value
+// dims, fill M, and fp8 pages are operands as stored.  O^T stays in tensor memory
+// over all pages.  kNT = 1 (lists, and dense decode of single tokens): two CTAs an
+// SM; kNT = 4 (dense decode of two or more tokens a request): one CTA an SM, each
+// page loaded once for four tokens.  K and V tiles have rings of their own (three
+// or five slots each): a K tile is free once its S^T is there, long before the V
+// tile's product.
+//   warp 0       page lists, scales, TMA of K tiles
 //   warp 1       S^T products (and owns tensor memory)
-//   warp 2       O^T products
-//   warps 3..    softmax and output, four a group: a thread owns one key, a group
-//                a token's 16 heads (kNT = 4) or half of them (kNT = 1: the chain of
-//                one page is half as long; 1000 cycles with all 16)
+//   warp 2       TMA of V tiles
+//   warp 3       O^T products
+//   warps 4..    softmax and output, four a group: a thread owns one key, a group
+//                a token's 16 heads (kNT = 4) or half of them (kNT = 1).  A step
+//                takes two pages.
 //
 // What bounds it: bytes from HBM in decode, from L2 in prefill; the pages of a
 // short call are cut over the CTAs of a cluster (kNT = 1), which merge their
@@ -56,11 +58,10 @@ namespace msa {
 
 namespace {
 
-constexpr int kStageBytes = 2 * kHalfTile;    // K tile then V tile
 constexpr float kPShift = 6.5f;               // P = 2^kPShift at the largest u when M is set
 constexpr float kPTop = 8.5f;                 // M moves when some P would pass 2^kPTop
 constexpr int kChunk = 32;                    // dense decode: pages looked up at once, one a lane
-constexpr int kSelectCap = 8000;              // selector keys in stage 1, then its slots
+constexpr int kSelectCap = 8000;              // selector keys in K slots 1 and 2, then its slots
 constexpr int kMaxCluster = 8;
 constexpr int kTableCopy = 512;               // block-table entries copied to shared memory
 constexpr int kTableBarrier = 15;             // warps 0 and 2 of the prologue
@@ -72,35 +73,39 @@ struct alignas(16) PageInfo {
   int block;         // logical block, -1: no key of this page is attended
 };
 
-// Softmax groups of four warps, each with kHeads heads of one token.
+// Softmax groups of four warps, each with kHeads heads of one token, behind four
+// warps of other roles.
 template <int kNT>
 struct Groups {
   static constexpr int kHeads = kNT == 1 ? 8 : 16;
   static constexpr int kPerToken = kGroup / kHeads;
   static constexpr int kCount = kNT * kPerToken;
-  static constexpr int kThreads = 32 * (3 + 4 * kCount);
+  static constexpr int kThreads = 32 * (4 + 4 * kCount);
+  static constexpr int kBatch = kNT == 1 ? 2 : 1;   // pages a group takes at once
 };
 
 template <int kNT>
 struct Tail {
-  static constexpr int kStages = kNT == 1 ? 3 : 5;
+  static constexpr int kSlots = kNT == 1 ? 3 : 5;   // of the K ring and of the V ring
   static constexpr int kHeads = Groups<kNT>::kHeads, kCount = Groups<kNT>::kCount;
-  uint64_t full[kStages];   // TMA -> S^T
-  uint64_t empty[kStages];  // O^T (a stage's last reader) -> TMA
-  uint64_t s_full[2];       // S^T ready -> softmax
-  uint64_t s_empty[2];      // softmax has read S^T
-  uint64_t p_full[2];       // P^T written -> O^T
-  uint64_t o_done[2];       // O^T of a page complete (its P^T buffer free)
-  uint64_t info_ready;      // the first pages' scales and blocks are in `info`
+  uint64_t k_full[kSlots];  // TMA -> S^T
+  uint64_t k_empty[kSlots]; // S^T -> TMA
+  uint64_t v_full[kSlots];  // TMA -> O^T
+  uint64_t v_empty[kSlots]; // O^T -> TMA
+  uint64_t s_full[2];       // a batch's S^T ready -> softmax
+  uint64_t s_empty[2];      // softmax has read a batch's S^T
+  uint64_t p_full;          // a batch's P^T written -> O^T
+  uint64_t o_done;          // a batch's O^T complete (the P^T buffer free)
+  uint64_t info_full[2];    // a chunk's scales and blocks are in its half of `info`
   uint64_t finish;          // every role done and every product complete
   uint32_t tmem_base;
   int n_pages;
   int ok;                   // 0: some softmax warp gave up on a wait
   int pos[kNT];             // token positions, -1: none
   float zs[kNT];            // logit scale (log2 units) times 2^e of each token's query split
-  int pages[kChunk];        // list modes: this CTA's pages
+  int pages[kTopK];         // list modes: this CTA's pages
   PageInfo info[2 * kChunk];
-  alignas(16) float mx[kCount][kHeads][4];    // page maxima by quarter
+  alignas(16) float mx[kCount][kHeads][4];    // batch maxima by quarter
   alignas(16) float lsum[kCount][kHeads][4];  // running sums by quarter
   float ml[kGroup][2];          // cluster merge: (m, l) of this CTA's part
 };
@@ -110,23 +115,37 @@ static_assert(alignof(Tail<1>) == 16 && offsetof(Tail<1>, mx) % 16 == 0 &&
 static_assert(alignof(Tail<4>) == 16 && offsetof(Tail<4>, mx) % 16 == 0 &&
               offsetof(Tail<4>, lsum) % 16 == 0 && offsetof(Tail<4>, info) % 16 == 0, "float4 access");
 
+// K ring, V ring, query tile, P^T of a batch, Tail.
 template <int kNT>
 struct Smem {
-  static constexpr int kStages = Tail<kNT>::kStages;
+  static constexpr int kSlots = Tail<kNT>::kSlots;
   static constexpr int kPBlock = 8 * 32 * kNT;   // P^T: 8 keys x (hi, lo) of each token
-  static constexpr int kPBuf = kPage * 32 * kNT;
-  static constexpr int kQ = kStages * kStageBytes;
+  static constexpr int kPBuf = kPage * 32 * kNT; // one page's
+  static constexpr int kV = kSlots * kHalfTile;
+  static constexpr int kQ = 2 * kV;
   static constexpr int kP = kQ + 32 * kNT * 128;
-  static constexpr int kTail = kP + 2 * kPBuf;
+  static constexpr int kTail = kP + Groups<kNT>::kBatch * kPBuf;
   static constexpr int kBytes = kTail + static_cast<int>((sizeof(Tail<kNT>) + 15) / 16 * 16) + 1024;
   static_assert(kQ % 1024 == 0 && kP % 1024 == 0 && kTail % 16 == 0,
                 "operand tiles need 1024-byte alignment");
 };
-static_assert(4 * kSelectCap + 4 * kTopK <= kStageBytes, "selector scratch fits stage 1");
+static_assert(4 * kSelectCap + 4 * kTopK <= 2 * kHalfTile && Smem<1>::kSlots >= 3,
+              "selector scratch fits K slots 1 and 2");
 static_assert(2 * (Smem<1>::kBytes + 1024) <= 228 * 1024, "two CTAs an SM");
 static_assert(Smem<4>::kBytes <= 227 * 1024, "one CTA an SM");
-static_assert(kGroup * kHeadDim * 4 <= kStageBytes, "a CTA's part fits a stage");
-static_assert(4 * kTableCopy <= 2 * Smem<1>::kPBuf, "the block-table copy fits the P^T buffers");
+static_assert(kGroup * kHeadDim * 4 <= Smem<1>::kV, "a CTA's part fits the K ring");
+static_assert(4 * kTableCopy <= Groups<1>::kBatch * Smem<1>::kPBuf, "the block-table copy fits the P^T buffer");
+static_assert(kChunk % 2 == 0, "a batch's pages are of one chunk");
+
+// mbar_wait with one try before the clock is read: most waits here find their phase
+// complete.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, unsigned parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = global_ns();
+  while (!mbar_try_wait_sleep(bar, parity, 1000000u))
+    if (global_ns() - t0 > kWaitLimitNs) return false;
+  return true;
+}
 
 // The barrier of one group's four warps, with the or of a predicate.
 __device__ __forceinline__ bool barrier_or(int id, bool pred) {
@@ -208,16 +227,17 @@ template <int kNT, Mode kMode, bool kFp8Q, bool kVarlen, bool kCluster>
 __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
     scaled_attend_kernel(const __grid_constant__ CUtensorMap kv_map, const AttendParams p) {
   using Sm = Smem<kNT>;
-  constexpr int kStages = Sm::kStages;
+  constexpr int kSlots = Sm::kSlots;
+  constexpr int kBatch = Groups<kNT>::kBatch;
   // A bf16 query's tile: the hi rows of all tokens, then the lo rows.  One token: both
   // in one product, N = 32, added by the softmax.  More: two products into the same
   // columns, which takes the tensor core as long (N = 64 twice for 128 once) and
   // halves what the softmax reads of tensor memory.
   constexpr bool kFold = kNT > 1 && !kFp8Q;
   constexpr int kSCols = kFp8Q || kFold ? kGroup : 2 * kGroup;   // S^T columns of one token
-  constexpr int kSN = kSCols * kNT;                        // columns of one S^T buffer
-  constexpr uint32_t kColAcc = 2 * kSN;                    // O^T behind two S^T buffers
-  constexpr int kTmemCols = kNT == 1 ? 128 : 256;
+  constexpr int kSN = kSCols * kNT;                        // columns of one page's S^T
+  constexpr uint32_t kColAcc = 2 * kBatch * kSN;           // O^T behind two batches of S^T
+  constexpr int kTmemCols = kNT == 1 ? 256 : 512;
   static_assert(kColAcc + 2 * kGroup * kNT <= kTmemCols, "tensor memory");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -294,13 +314,17 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
   int pg_next = 0, blk_next = -1;
   int slot = lane;   // list modes: the lane's page's place in this CTA's order
   float2 sc_next = make_float2(1.f, 1.f);
-  auto load_page = [&](int t, int page) {   // one lane: page `page` into stage t % kStages
-    const int s = t % kStages;
-    uint8_t* st = smem + s * kStageBytes;
-    const int row = (page * p.Hkv + g) * kPage;
-    mbar_arrive_expect_tx(&tail->full[s], kStageBytes);
-    tma_load_2d(st, &kv_map, 0, row, &tail->full[s]);
-    tma_load_2d(st + kHalfTile, &kv_map, kHeadDim, row, &tail->full[s]);
+  // one lane: the K or V tile of page `page`, the t-th, into its slot
+  auto load_k = [&](int t, int page) {
+    const int s = t % kSlots;
+    mbar_arrive_expect_tx(&tail->k_full[s], kHalfTile);
+    tma_load_2d(smem + s * kHalfTile, &kv_map, 0, (page * p.Hkv + g) * kPage, &tail->k_full[s]);
+  };
+  auto load_v = [&](int t, int page) {
+    const int s = t % kSlots;
+    mbar_arrive_expect_tx(&tail->v_full[s], kHalfTile);
+    tma_load_2d(smem + Sm::kV + s * kHalfTile, &kv_map, kHeadDim, (page * p.Hkv + g) * kPage,
+                &tail->v_full[s]);
   };
   // dense decode: the lane's page of slot t (a bad table entry: page 0 instead,
   // attended by no key), then its scales
@@ -352,23 +376,28 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
     if (lane == 0) {
       const unsigned warps =
           4u * Groups<kNT>::kPerToken * (kNT == 1 ? 1u : static_cast<unsigned>(max(valid_toks, 1)));
-      for (int s = 0; s < kStages; ++s) {
-        mbar_init(&tail->full[s], 1);
-        mbar_init(&tail->empty[s], 1);
+      for (int s = 0; s < kSlots; ++s) {
+        mbar_init(&tail->k_full[s], 1);
+        mbar_init(&tail->k_empty[s], 1);
+        mbar_init(&tail->v_full[s], 1);
+        mbar_init(&tail->v_empty[s], 1);
       }
       for (int s = 0; s < 2; ++s) {
         mbar_init(&tail->s_full[s], 1);
         mbar_init(&tail->s_empty[s], warps);
-        mbar_init(&tail->p_full[s], warps);
-        mbar_init(&tail->o_done[s], 1);
+        mbar_init(&tail->info_full[s], 1);
       }
-      mbar_init(&tail->info_ready, 1);
-      mbar_init(&tail->finish, 3 + 4 * Groups<kNT>::kCount);
+      mbar_init(&tail->p_full, warps);
+      mbar_init(&tail->o_done, 1);
+      mbar_init(&tail->finish, 4 + 4 * Groups<kNT>::kCount);
       fence_barrier_init();
       prefetch_tensormap(&kv_map);
       tail->ok = 1;
       for (int j = 0; j < kNT; ++j) tail->pos[j] = token_pos(j);
-      if (pre_page >= 0) load_page(0, pre_page);
+      if (pre_page >= 0) {
+        load_k(0, pre_page);
+        load_v(0, pre_page);
+      }
     }
     __syncwarp();
     int np = 0;
@@ -376,9 +405,9 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
       np = hi - lo;
       look_up(lane);
       look_up_scales();
-      for (int t = 0; t < np && t < kStages; ++t) {
-        const int pg = __shfl_sync(0xffffffffu, pg_next, t);
-        if (lane == 0) load_page(t, pg);
+      if (lane < min(np, kSlots)) {
+        load_k(lane, pg_next);
+        load_v(lane, pg_next);
       }
     } else {
       const int64_t list = (row_tok * p.Hkv + g) * kTopK;
@@ -386,7 +415,7 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
       if constexpr (kMode == kSelect) {
         pdl_wait();   // the scores are the previous kernel's
         bool nan = false;
-        uint8_t* scratch = smem + kStageBytes;   // stage 1, not yet loaded
+        uint8_t* scratch = smem + kHalfTile;     // K slots 1 and 2, not yet loaded
         n = last_pos >= 0
                 ? select::select_row<16>(p.scores + g * p.s_stride_h + row_tok * p.s_stride_t,
                                          p.s_stride_n, last_pos, lane,
@@ -435,16 +464,19 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
         slot = k;
         look_up_scales();
         tail->pages[k] = page;
-        if (k < kStages && !(k == 0 && pre_page >= 0)) load_page(k, page);
+        if (k < kSlots && !(k == 0 && pre_page >= 0)) {
+          load_k(k, page);
+          load_v(k, page);
+        }
       }
     }
     if (lane == 0) tail->n_pages = np;
   } else if (warp == 1) {
     tc::tmem_alloc(&tail->tmem_base, kTmemCols);
     tc::tmem_relinquish();
-  } else if (warp >= 3 && (warp - 3) % (4 * Groups<kNT>::kPerToken) == 0) {
+  } else if (warp >= 4 && (warp - 4) % (4 * Groups<kNT>::kPerToken) == 0) {
     // token j's query rows (hi, then lo; an fp8 query's as they are)
-    const int j = (warp - 3) / (4 * Groups<kNT>::kPerToken);
+    const int j = (warp - 4) / (4 * Groups<kNT>::kPerToken);
     if (tok0 + j < qlen || kNT == 1) {
       const int64_t row = (row_tok + j) * p.Hq + g * kGroup;
       if constexpr (kFp8Q) {
@@ -462,14 +494,15 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
     }
     tc::fence_proxy_async_smem();   // the tile is read by the tensor core
   }
-  if (kNT > 1 && warp >= 3) {
+  if (kMode == kDense && warp == 2) look_up(lane);   // the V producer's own pages
+  if (kNT > 1 && warp >= 4) {
     // a token that is not there has P = 0: written once, read on every page
-    const int j = (warp - 3) / (4 * Groups<kNT>::kPerToken);
+    const int j = (warp - 4) / (4 * Groups<kNT>::kPerToken);
     if (token_pos(j) < 0) {
       const int key = 32 * (warp & 3) + lane;
 #pragma unroll
-      for (int buf = 0; buf < 2; ++buf) {
-        uint8_t* pk = pbuf + buf * Sm::kPBuf + 256 * j + (key >> 3) * Sm::kPBlock + (key & 7) * 16;
+      for (int i = 0; i < kBatch; ++i) {
+        uint8_t* pk = pbuf + i * Sm::kPBuf + 256 * j + (key >> 3) * Sm::kPBlock + (key & 7) * 16;
         *reinterpret_cast<uint4*>(pk) = make_uint4(0u, 0u, 0u, 0u);
         *reinterpret_cast<uint4*>(pk + 128) = make_uint4(0u, 0u, 0u, 0u);
       }
@@ -482,82 +515,91 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
   const int n_pages = tail->n_pages;
   const uint32_t tmem = tail->tmem_base;
 
-  if (warp == 0) {
-    // ---- TMA producer ------------------------------------------------------------------
-    // the first pages' scales, which the softmax waits for, have arrived meanwhile
-    if (kMode == kDense || blk_next >= 0) tail->info[slot] = next_info();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&tail->info_ready);
-    int issued = min(n_pages, kStages);
+  if (warp == 0 || warp == 2) {
+    // ---- TMA producers: K tiles (warp 0, with the scales), V tiles (warp 2) ----------------
+    const bool is_k = warp == 0;
+    uint64_t* full = is_k ? tail->k_full : tail->v_full;
+    uint64_t* empty = is_k ? tail->k_empty : tail->v_empty;
+    if (is_k) {
+      // the first pages' scales, which the softmax waits for, have arrived meanwhile
+      if (kMode == kDense || blk_next >= 0) tail->info[slot] = next_info();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tail->info_full[0]);
+    }
+    int issued = min(n_pages, kSlots);
     bool ok = true;
-    if constexpr (kMode == kDense) {
-      // chunk by chunk: a chunk's pages are looked up when the one before it
-      // begins and their scales when it is half through
-      int pg = pg_next;
-      if (kChunk < n_pages) look_up(kChunk + lane);
-      for (int t = kStages; t < n_pages && ok; ++t) {
-        if (t % kChunk == kChunk / 2) look_up_scales();
+    // dense decode, chunk by chunk: a chunk's pages are looked up when the one before
+    // it begins and their scales when it is half through
+    int pg = pg_next;
+    if (kMode == kDense && kChunk < n_pages) look_up(kChunk + lane);
+    for (int t = kSlots; t < n_pages && ok; ++t) {
+      int page;
+      if constexpr (kMode == kDense) {
+        if (is_k && t % kChunk == kChunk / 2) look_up_scales();
         if (t % kChunk == 0) {
           pg = pg_next;
-          // its slots were last read two chunks ago: those pages' stages have
-          // been released since
-          tail->info[t % (2 * kChunk) + lane] = next_info();
-          __syncwarp();
+          if (is_k) {
+            // its half of `info` was last read two chunks ago: the K slots passed on
+            // since say that the softmax is past it
+            tail->info[t % (2 * kChunk) + lane] = next_info();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tail->info_full[(t / kChunk) & 1]);
+          }
           if (t + kChunk < n_pages) look_up(t + kChunk + lane);
         }
-        if (!mbar_wait(&tail->empty[t % kStages], ((t / kStages) - 1) & 1)) ok = false;
-        ok = __all_sync(0xffffffffu, ok);
-        const int page = __shfl_sync(0xffffffffu, pg, t % kChunk);
-        if (ok) {
-          if (lane == 0) load_page(t, page);
-          issued = t + 1;
-        }
+        page = __shfl_sync(0xffffffffu, pg, t % kChunk);
+      } else {
+        page = tail->pages[t];
       }
-    } else {
-      for (int t = kStages; t < n_pages && ok; ++t) {
-        if (!mbar_wait(&tail->empty[t % kStages], ((t / kStages) - 1) & 1)) ok = false;
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok) {
-          if (lane == 0) load_page(t, tail->pages[t]);
-          issued = t + 1;
+      if (!wait_for(&empty[t % kSlots], ((t / kSlots) - 1) & 1)) ok = false;
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) {
+        if (lane == 0) {
+          if (is_k) load_k(t, page);
+          else load_v(t, page);
         }
+        issued = t + 1;
       }
     }
     if (lane == 0) {
       if (!ok) flag_error(p.err, MSA_ERR_TIMEOUT);
       // the loads still in flight land before shared memory can be released
-      for (int t = max(0, issued - kStages); t < issued; ++t)
-        (void)mbar_wait(&tail->full[t % kStages], (t / kStages) & 1);
-      pdl_trigger();
+      for (int t = max(0, issued - kSlots); t < issued; ++t)
+        (void)wait_for(&full[t % kSlots], (t / kSlots) & 1);
+      if (!is_k) pdl_trigger();
       mbar_arrive(&tail->finish);
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ---- S^T = K Q^T ---------------------------------------------------------------------
+    // ---- S^T = K Q^T, a batch of pages a buffer --------------------------------------------
     if (lane == 0) {
       const uint64_t a0 = tc::sw128_kmajor_desc(smem_u32(smem));
       const uint64_t bq = tc::sw128_kmajor_desc(smem_u32(qtile));
       constexpr uint32_t idesc = tc::idesc_e4m3_f32(128, kSN);
-      for (int t = 0; t < n_pages; ++t) {
-        const int s = t % kStages, buf = t & 1;
-        if (!mbar_wait(&tail->full[s], (t / kStages) & 1) ||
-            (t >= 2 && !mbar_wait(&tail->s_empty[buf], ((t >> 1) - 1) & 1))) {
-          flag_error(p.err, MSA_ERR_TIMEOUT);
-          break;
-        }
-        tc::fence_after_thread_sync();
-        const uint64_t a = a0 + static_cast<uint64_t>(s) * (kStageBytes >> 4);
+      bool ok = true;
+      for (int t0 = 0, n = 0; t0 < n_pages && ok; t0 += kBatch, ++n) {
+        const int buf = n & 1;
+        ok = n < 2 || wait_for(&tail->s_empty[buf], ((n >> 1) - 1) & 1);
+        for (int t = t0; t < min(t0 + kBatch, n_pages) && ok; ++t) {
+          const int s = t % kSlots;
+          ok = wait_for(&tail->k_full[s], (t / kSlots) & 1);
+          if (!ok) break;
+          tc::fence_after_thread_sync();
+          const uint64_t a = a0 + static_cast<uint64_t>(s) * (kHalfTile >> 4);
+          const uint32_t d = tmem + kSN * (kBatch * buf + t - t0);
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          tc::mma_e4m3(tmem + kSN * buf, a + 2 * ks, bq + 2 * ks, idesc, ks > 0);
-        if constexpr (kFold) {
-          constexpr uint64_t kLo = (kGroup * kNT * 128) >> 4;   // the lo rows
+          for (int ks = 0; ks < 4; ++ks) tc::mma_e4m3(d, a + 2 * ks, bq + 2 * ks, idesc, ks > 0);
+          if constexpr (kFold) {
+            constexpr uint64_t kLo = (kGroup * kNT * 128) >> 4;   // the lo rows
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            tc::mma_e4m3(tmem + kSN * buf, a + 2 * ks, bq + kLo + 2 * ks, idesc, 1);
+            for (int ks = 0; ks < 4; ++ks)
+              tc::mma_e4m3(d, a + 2 * ks, bq + kLo + 2 * ks, idesc, 1);
+          }
+          tc::commit(&tail->k_empty[s]);
         }
-        tc::commit(&tail->s_full[buf]);
+        if (ok) tc::commit(&tail->s_full[buf]);
       }
+      if (!ok) flag_error(p.err, MSA_ERR_TIMEOUT);
       tc::commit(&tail->finish);
     }
     __syncwarp();
@@ -565,37 +607,40 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
     (void)mbar_wait(&tail->finish, 0);
     tc::fence_after_thread_sync();
     tc::tmem_dealloc(tmem, kTmemCols);
-  } else if (warp == 2) {
-    // ---- O^T += V^T P^T --------------------------------------------------------------------
+  } else if (warp == 3) {
+    // ---- O^T += V^T P^T ----------------------------------------------------------------------
     if (lane == 0) {
-      const uint64_t a0 = tc::sw128_mnmajor_desc(smem_u32(smem + kHalfTile));
+      const uint64_t a0 = tc::sw128_mnmajor_desc(smem_u32(smem + Sm::kV));
       // B: each token's 16 hi heads, then its 16 lo ones 128 bytes further; 8-key
       // blocks kPBlock apart
       const uint64_t b0 = tc::interleave_mnmajor_desc(smem_u32(pbuf), Sm::kPBlock, 128);
       constexpr uint32_t idesc = tc::idesc_e4m3_f32_mn(128, 32 * kNT);
-      for (int t = 0; t < n_pages; ++t) {
-        const int s = t % kStages, buf = t & 1;
-        if (!mbar_wait(&tail->p_full[buf], (t >> 1) & 1)) {
-          flag_error(p.err, MSA_ERR_TIMEOUT);
-          break;
-        }
-        tc::fence_after_thread_sync();
-        const uint64_t a = a0 + static_cast<uint64_t>(s) * (kStageBytes >> 4);
-        const uint64_t bp = b0 + static_cast<uint64_t>((buf * Sm::kPBuf) >> 4);
+      bool ok = true;
+      for (int t0 = 0, n = 0; t0 < n_pages && ok; t0 += kBatch, ++n) {
+        ok = wait_for(&tail->p_full, n & 1);
+        for (int t = t0; t < min(t0 + kBatch, n_pages) && ok; ++t) {
+          const int s = t % kSlots;
+          ok = wait_for(&tail->v_full[s], (t / kSlots) & 1);
+          if (!ok) break;
+          tc::fence_after_thread_sync();
+          const uint64_t a = a0 + static_cast<uint64_t>(s) * (kHalfTile >> 4);
+          const uint64_t bp = b0 + static_cast<uint64_t>(((t - t0) * Sm::kPBuf) >> 4);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          tc::mma_e4m3(tmem + kColAcc, a + 256 * kk, bp + ((4 * Sm::kPBlock) >> 4) * kk, idesc,
-                       (t > 0 || kk > 0) ? 1u : 0u);
-        tc::commit(&tail->o_done[buf]);
-        tc::commit(&tail->empty[s]);
+          for (int kk = 0; kk < 4; ++kk)
+            tc::mma_e4m3(tmem + kColAcc, a + 256 * kk, bp + ((4 * Sm::kPBlock) >> 4) * kk, idesc,
+                         (t > 0 || kk > 0) ? 1u : 0u);
+          tc::commit(&tail->v_empty[s]);
+        }
+        if (ok) tc::commit(&tail->o_done);
       }
+      if (!ok) flag_error(p.err, MSA_ERR_TIMEOUT);
       tc::commit(&tail->finish);
     }
     __syncwarp();
   } else {
     // ---- group gi: kH heads of token j ------------------------------------------------------
     constexpr int kH = Groups<kNT>::kHeads;
-    const int gi = (warp - 3) >> 2;
+    const int gi = (warp - 4) >> 2;
     const int j = gi / Groups<kNT>::kPerToken;
     const int h0 = kH * (gi % Groups<kNT>::kPerToken);   // the group's first head
     const int quarter = warp & 3;
@@ -616,63 +661,76 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
     for (int h = 0; h < kH; ++h) nl[h] = l[h] = 0.f;
     bool ok = true;
 
+    // Two pages a step: a page's chain of waits (S^T, vote, P^T buffer) and fences took
+    // 1600 cycles against 400 of work, whatever the number of warps.
     // Once a wait has run out the warp waits for nothing any more but still takes
     // part in the group's barriers, so that its other warps get past them.
-    int s = 0;
-    unsigned full_ph = 0;
-    for (int k = 0; k < n_pages && pos >= 0; ++k) {
-      const int buf = k & 1;
-      const unsigned ph = (k >> 1) & 1;
-      float t[kH];
-      // the page's scales and block, written before the page was loaded or, the
-      // first ones, announced
-      if (k == 0 && ok) ok = mbar_wait(&tail->info_ready, 0);
-      if (kMode == kDense && ok) ok = mbar_wait(&tail->full[s], full_ph);
-      if (ok) ok = mbar_wait(&tail->s_full[buf], ph);
+    const int n_steps = pos >= 0 ? (n_pages + kBatch - 1) / kBatch : 0;
+    for (int n = 0; n < n_steps; ++n) {
+      const int buf = n & 1, k0 = kBatch * n;
+      // the pages' scales and blocks
+      if (k0 % kChunk == 0 && ok)
+        ok = wait_for(&tail->info_full[(k0 / kChunk) & 1], (k0 / (2 * kChunk)) & 1);
+      if (ok) ok = wait_for(&tail->s_full[buf], (n >> 1) & 1);
       tc::fence_after_thread_sync();
-      const PageInfo in = tail->info[k % (2 * kChunk)];
-      const float zt = zs * in.k;
-      if (in.lv != lv) {   // the same in every thread
-        const float d = in.lv - lv;
-#pragma unroll
-        for (int h = 0; h < kH; ++h) nl[h] += d;
-        lv = in.lv;
-      }
-      const int lim = in.block < 0 ? -1 : pos - in.block * kPage;   // keys <= lim are visible
-      // u - M + kPShift: the raw dot products times zt, plus nl
+      float t[kBatch][kH], iv[kBatch];
+      int lim[kBatch];   // keys <= lim are visible
       {
-        uint32_t sv[kH];
-        ld_cols(s_addr + kSN * buf, sv);
+        uint32_t sv[kBatch][kH];
+        const uint32_t at = s_addr + kSN * kBatch * buf;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) ld_cols(at + kSN * i, sv[i]);
         if constexpr (kSCols == 2 * kGroup) {
-          uint32_t sl[kH];
-          ld_cols(s_addr + kSN * buf + kGroup, sl);
+          uint32_t sl[kBatch][kH];
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) ld_cols(at + kSN * i + kGroup, sl[i]);
           tc::wait_ld();
 #pragma unroll
-          for (int h = 0; h < kH; ++h)
-            t[h] = fmaf(__uint_as_float(sv[h]) + __uint_as_float(sl[h]), zt, nl[h]);
+          for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+            for (int h = 0; h < kH; ++h)
+              t[i][h] = __uint_as_float(sv[i][h]) + __uint_as_float(sl[i][h]);
         } else {
           tc::wait_ld();
 #pragma unroll
-          for (int h = 0; h < kH; ++h) t[h] = fmaf(__uint_as_float(sv[h]), zt, nl[h]);
+          for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+            for (int h = 0; h < kH; ++h) t[i][h] = __uint_as_float(sv[i][h]);
         }
       }
       tc::fence_before_thread_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(&tail->s_empty[buf]);
-      if (lim < kPage - 1 && key > lim) {
+      // u - M + kPShift: the raw dot products times zt, plus nl
+      float top = -INFINITY;
 #pragma unroll
-        for (int h = 0; h < kH; ++h) t[h] = -INFINITY;
+      for (int i = 0; i < kBatch; ++i) {
+        const PageInfo in = tail->info[(k0 + i) % (2 * kChunk)];
+        const bool have = k0 + i < n_pages;   // (the columns of an odd last page hold anything)
+        const float zt = zs * in.k;
+        if (have && in.lv != lv) {   // the same in every thread
+          const float d = in.lv - lv;
+#pragma unroll
+          for (int h = 0; h < kH; ++h) nl[h] += d;
+          lv = in.lv;
+        }
+        iv[i] = have ? in.iv : 0.f;
+        lim[i] = !have || in.block < 0 ? -1 : pos - in.block * kPage;
+#pragma unroll
+        for (int h = 0; h < kH; ++h) t[i][h] = fmaf(t[i][h], zt, nl[h]);
+        if (lim[i] < kPage - 1 && key > lim[i]) {
+#pragma unroll
+          for (int h = 0; h < kH; ++h) t[i][h] = -INFINITY;
+        }
+#pragma unroll
+        for (int h = 0; h < kH; h += 2) top = fmax3f(top, t[i][h], t[i][h + 1]);
       }
-      float top = fmax3f(t[0], t[1], t[2]);
-#pragma unroll
-      for (int h = 3; h + 1 < kH; h += 2) top = fmax3f(top, t[h], t[h + 1]);
-      top = fmaxf(top, t[kH - 1]);
-      bool stored = false;
+      bool stored = false, free_p = n == 0;
       if (barrier_or(bar, unset ? top > -INFINITY : top > kPTop)) {
-        // set or move the references: the heads' maxima over the page's keys
+        // set or move the references: the heads' maxima over the batch's keys
 #pragma unroll
         for (int h = 0; h < kH; ++h) {
-          const float m = warp_max_f32(t[h]);
+          const float m = warp_max_f32(fmaxf(t[0][h], t[kBatch - 1][h]));
           if (lane == h) tail->mx[gi][h][quarter] = m;
         }
         __syncwarp();
@@ -689,16 +747,17 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
         for (int h = 0; h < kH; ++h) {
           const float d = __shfl_sync(0xffffffffu, d_h, h);
           nl[h] += d;
-          t[h] += d;
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) t[i][h] += d;
         }
         if (!unset) {
 #pragma unroll
           for (int h = 0; h < kH; ++h) l[h] *= __shfl_sync(0xffffffffu, al_h, h);
           // the earlier products are relative to the old references (a token that
-          // has seen no key has only zeros there)
-          // page k - 1's product, and with it all earlier ones, complete; page
-          // k's waits for this page's P
-          if (ok) ok = mbar_wait(&tail->o_done[(k - 1) & 1], ((k - 1) >> 1) & 1);
+          // has seen no key has only zeros there): once they are complete, and
+          // before this batch's, whose P is not written yet
+          if (ok) ok = wait_for(&tail->o_done, (n - 1) & 1);
+          free_p = true;
           tc::fence_after_thread_sync();
 #pragma unroll
           for (int part = 0; part < 2; ++part) {   // the hi columns, then the lo ones
@@ -715,39 +774,45 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
         }
         unset = false;
       }
-      uint32_t hw[kH / 4], lw[kH / 4];
+      uint32_t hw[kBatch][kH / 4], lw[kBatch][kH / 4];
 #pragma unroll
-      for (int q4 = 0; q4 < kH / 4; ++q4) {
+      for (int i = 0; i < kBatch; ++i)
 #pragma unroll
-        for (int e = 4 * q4; e < 4 * q4 + 4; ++e) {
-          t[e] = ex2(t[e]);             // P; 0 for an invisible key
-          l[e] = fmaf(t[e], in.iv, l[e]);
+        for (int q4 = 0; q4 < kH / 4; ++q4) {
+          float* e = &t[i][4 * q4];
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            e[h] = ex2(e[h]);             // P; 0 for an invisible key
+            l[4 * q4 + h] = fmaf(e[h], iv[i], l[4 * q4 + h]);
+          }
+          split_p(e[0], e[1], e[2], e[3], hw[i][q4], lw[i][q4]);
         }
-        split_p(t[4 * q4], t[4 * q4 + 1], t[4 * q4 + 2], t[4 * q4 + 3], hw[q4], lw[q4]);
-      }
-      if (j == last_tok && h0 == 0 && lim < kPage - 1) {
+      if (j == last_tok && h0 == 0) {
         // value rows that no token of the tile sees have P = 0, but their bytes
         // may be anything (an fp8 NaN times 0 is NaN)
-        if (ok) ok = mbar_wait(&tail->full[s], full_ph);
-        if (key > lim) {
-          uint4* vrow = reinterpret_cast<uint4*>(smem + s * kStageBytes + kHalfTile + key * 128);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) vrow[c] = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < kBatch; ++i) {
+          if (lim[i] >= kPage - 1 || k0 + i >= n_pages) continue;
+          const int s = (k0 + i) % kSlots;
+          if (ok) ok = wait_for(&tail->v_full[s], ((k0 + i) / kSlots) & 1);
+          if (key > lim[i]) {
+            uint4* vrow = reinterpret_cast<uint4*>(smem + Sm::kV + s * kHalfTile + key * 128);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) vrow[c] = make_uint4(0u, 0u, 0u, 0u);
+          }
         }
       }
-      // P^T buffer `buf` was last read by page k - 2's product
-      if (ok && k >= 2) ok = mbar_wait(&tail->o_done[buf], ph ^ 1);
-      uint8_t* pk = pj + buf * Sm::kPBuf;
-      store_p(pk, hw);
-      store_p(pk + 128, lw);
+      // the P^T buffer was last read by the batch before
+      if (ok && !free_p) ok = wait_for(&tail->o_done, (n - 1) & 1);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        store_p(pj + i * Sm::kPBuf, hw[i]);
+        store_p(pj + i * Sm::kPBuf + 128, lw[i]);
+      }
       tc::fence_proxy_async_smem();
       if (stored) tc::fence_before_thread_sync();   // the rescale before O^T
       __syncwarp();
-      if (lane == 0) mbar_arrive(&tail->p_full[buf]);
-      if (++s == kStages) {
-        s = 0;
-        full_ph ^= 1;
-      }
+      if (lane == 0) mbar_arrive(&tail->p_full);
     }
 
     // ---- output: this thread's value dim of each head ---------------------------------------
@@ -775,8 +840,8 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
     float o[kH];
 #pragma unroll
     for (int h = 0; h < kH; ++h) o[h] = 0.f;
-    if (n_pages > 0 && pos >= 0) {
-      if (ok) ok = mbar_wait(&tail->o_done[(n_pages - 1) & 1], ((n_pages - 1) >> 1) & 1);
+    if (n_steps > 0) {
+      if (ok) ok = wait_for(&tail->o_done, (n_steps - 1) & 1);
       tc::fence_after_thread_sync();
       uint32_t ah[kH], al[kH];
       ld_cols(acc_addr, ah);
@@ -802,7 +867,7 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
     const int64_t base = static_cast<int64_t>(split) * rows + row0;
     if (kMode == kDense) pdl_wait();   // the outputs may be the previous kernel's inputs
     if constexpr (kCluster) {
-      // this CTA's part into its stages (every load has landed and every product is
+      // this CTA's part into its K ring (every load has landed and every product is
       // complete), then each CTA merges its share of the heads
       float* po = reinterpret_cast<float*>(smem);
 #pragma unroll
@@ -887,7 +952,7 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
     }
   }
   if constexpr (kCluster) {
-    if (warp < 3) {
+    if (warp < 4) {
       cluster_sync();
       cluster_sync();
     }
