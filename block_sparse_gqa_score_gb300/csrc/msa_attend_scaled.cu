@@ -5,23 +5,7 @@
 // listed (dense decode: all) pages up to its position, with K = K8 ks[page] and
 // V = V8 vs[page] per KV head; an empty key set gives 0.
 //
-// Mathematics.  With z the logit in log2 units and u = z + log2(vs[page]),
-//
-//   out = sum_t 2^(u_t - M) V8_t / sum_t 2^(u_t - M) / vs[page(t)],
-//
-// so the fp8 product takes weights P = 2^(u - M) that are relative to what a
-// page contributes, and the running sum divides each page's by vs again.  u is
-// one FFMA from the raw dot product: factor ks * sm_scale * log2(e) * 2^e (2^e
-// of the query split), addend log2(vs) - M.  M is a running reference, not the
-// running maximum: P = 2^(kPShift) at the largest u when M is set, and M stays
-// until some P would pass 2^kPTop (e4m3 holds 448).  Whether it does is one vote
-// a page: the largest of a thread's 16 u against the bound, or-ed over the
-// token's four warps by one barrier; only then are the exact maxima of the 16
-// heads formed and exchanged and the sums and the accumulator rescaled.  (With
-// exact maxima on every page a warp issued about 650 instructions a page; the
-// vote leaves about 200.)  With kPShift two binades below the top, P >= 2^-2 of
-// every term within 2^-8.5 of the largest is carried to 8 significant bits by
-// its two e4m3 parts, smaller ones to 2^-10 absolutely.
+// The mathematics is msa_page_softmax.cuh's.
 //
 // Layout: as the attend for one scale per tensor.  One CTA per (tile of kNT
 // tokens of one request, KV head, part); the tile's 16 kNT query rows are the N
@@ -51,6 +35,7 @@
 #include "msa_dense_slot.cuh"
 #include "msa_device.cuh"
 #include "msa_launch.h"
+#include "msa_page_softmax.cuh"
 #include "msa_select.cuh"
 #include "msa_tcgen05.cuh"
 
@@ -58,31 +43,14 @@ namespace msa {
 
 namespace {
 
-constexpr float kPShift = 6.5f;               // P = 2^kPShift at the largest u when M is set
-constexpr float kPTop = 8.5f;                 // M moves when some P would pass 2^kPTop
+using namespace paged;
+
 constexpr int kChunk = 32;                    // dense decode: pages looked up at once, one a lane
 constexpr int kSelectCap = 8000;              // selector keys in K slots 1 and 2, then its slots
 constexpr int kMaxCluster = 8;
 constexpr int kTableCopy = 512;               // block-table entries copied to shared memory
-constexpr int kTableBarrier = 15;             // warps 0 and 2 of the prologue
 
 enum Mode { kLists, kSelect, kDense };
-
-struct alignas(16) PageInfo {
-  float k, lv, iv;   // as PageScale
-  int block;         // logical block, -1: no key of this page is attended
-};
-
-// Softmax groups of four warps, each with kHeads heads of one token, behind four
-// warps of other roles.
-template <int kNT>
-struct Groups {
-  static constexpr int kHeads = kNT == 1 ? 8 : 16;
-  static constexpr int kPerToken = kGroup / kHeads;
-  static constexpr int kCount = kNT * kPerToken;
-  static constexpr int kThreads = 32 * (4 + 4 * kCount);
-  static constexpr int kBatch = kNT == 1 ? 2 : 1;   // pages a group takes at once
-};
 
 template <int kNT>
 struct Tail {
@@ -137,29 +105,10 @@ static_assert(kGroup * kHeadDim * 4 <= Smem<1>::kV, "a CTA's part fits the K rin
 static_assert(4 * kTableCopy <= Groups<1>::kBatch * Smem<1>::kPBuf, "the block-table copy fits the P^T buffer");
 static_assert(kChunk % 2 == 0, "a batch's pages are of one chunk");
 
-// mbar_wait with one try before the clock is read: most waits here find their phase
-// complete.
-__device__ __forceinline__ bool wait_for(uint64_t* bar, unsigned parity) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = global_ns();
-  while (!mbar_try_wait_sleep(bar, parity, 1000000u))
-    if (global_ns() - t0 > kWaitLimitNs) return false;
-  return true;
-}
-
-// The barrier of one group's four warps, with the or of a predicate.
-__device__ __forceinline__ bool barrier_or(int id, bool pred) {
-  unsigned r;
+// Warps 0 and 2 of the list modes' prologue (before the groups use their barriers).
+__device__ __forceinline__ void table_barrier() {
   __syncwarp();
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 q, %1, 0;\n\t"
-      "barrier.cta.red.or.aligned.pred p, %2, 128, q;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r)
-      : "r"(pred ? 1u : 0u), "r"(id)
-      : "memory");
-  return r != 0;
+  asm volatile("barrier.cta.sync.aligned 1, 64;" ::: "memory");
 }
 
 __device__ __forceinline__ void cluster_sync() {
@@ -178,48 +127,6 @@ __device__ __forceinline__ float ld_peer(const float* own, uint32_t rank) {
       : "r"(smem_u32(own)), "r"(rank)
       : "memory");
   return v;
-}
-
-__device__ __forceinline__ PageInfo page_info(const AttendParams& p, float2 scales, int block) {
-  const PageScale s = make_page_scale(scales);
-  if (s.bad != 0.f) flag_error(p.err, MSA_ERR_SCALE);
-  return PageInfo{s.k, s.lv, s.iv, s.bad != 0.f ? -1 : block};
-}
-
-// Columns of this thread's tensor-memory lane.
-__device__ __forceinline__ void ld_cols(uint32_t a, uint32_t (&r)[8]) { tc::ld_32x32b_x8(a, r); }
-__device__ __forceinline__ void ld_cols(uint32_t a, uint32_t (&r)[16]) { tc::ld_32x32b_x16(a, r); }
-__device__ __forceinline__ void st_cols(uint32_t a, const uint32_t (&r)[8]) { tc::st_32x32b_x8(a, r); }
-__device__ __forceinline__ void st_cols(uint32_t a, const uint32_t (&r)[16]) { tc::st_32x32b_x16(a, r); }
-
-__device__ __forceinline__ void store_p(uint8_t* at, const uint32_t (&w)[2]) {
-  *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
-}
-__device__ __forceinline__ void store_p(uint8_t* at, const uint32_t (&w)[4]) {
-  *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// Four probabilities (0 <= P <= 448) -> their e4m3 parts, first in the low byte:
-// hi = P rounded, lo = the remainder of P as fp16, rounded (hi + lo carries about
-// 8 significant bits).  Converting hi from fp32 and packing in one block of PTX
-// takes 57 cycles for 16 values of a warp, pair by pair through fp16 82.
-__device__ __forceinline__ void split_p(float a, float b, float c, float d, uint32_t& hi,
-                                        uint32_t& lo) {
-  asm("{\n\t.reg .b16 p, q, r, s;\n\t.reg .b32 x, y, u, v;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f32 p, %3, %2;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f32 q, %5, %4;\n\t"
-      "mov.b32 %0, {p, q};\n\t"
-      "cvt.rn.f16x2.f32 x, %3, %2;\n\t"
-      "cvt.rn.f16x2.f32 y, %5, %4;\n\t"
-      "cvt.rn.f16x2.e4m3x2 u, p;\n\t"
-      "cvt.rn.f16x2.e4m3x2 v, q;\n\t"
-      "sub.rn.f16x2 u, x, u;\n\t"
-      "sub.rn.f16x2 v, y, v;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 r, u;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 s, v;\n\t"
-      "mov.b32 %1, {r, s};\n\t}"
-      : "=&r"(hi), "=r"(lo)
-      : "f"(a), "f"(b), "f"(c), "f"(d));
 }
 
 // kNT tokens a tile; kCluster: the pages of a part are cut over a cluster's CTAs.
@@ -361,7 +268,7 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
 #pragma unroll
     for (int k = 0; k < kTableCopy / 32; ++k)
       if (32 * k + lane < ncopy) table_s[32 * k + lane] = v[k];
-    named_barrier(kTableBarrier, 64);
+    table_barrier();
   }
   if (warp == 0) {
     if (!seq_ok && lane == 0 && split == 0 && rank == 0) flag_error(p.err, MSA_ERR_SEQ_RANGE);
@@ -440,7 +347,7 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
         }
       }
       int page = -1;
-      named_barrier(kTableBarrier, 64);
+      table_barrier();
       if (valid) {
         page = n < ncopy ? table_s[n] : trow[n];
         if (page < 0 || static_cast<int64_t>(page) >= p.num_blocks) {
@@ -646,222 +553,48 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
     const int quarter = warp & 3;
     const int key = 32 * quarter + lane;   // key of the page; value dim at the end
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
-    const uint32_t s_addr = lane_addr + kSCols * j + h0;
-    const uint32_t acc_addr = lane_addr + kColAcc + 32 * j + h0;
-    const int bar = 1 + gi;
+    PageSoftmax<kNT, kSCols, kSN, Sm::kPBuf> sm;
+    sm.gi = gi;
+    sm.quarter = quarter;
+    sm.lane = lane;
+    sm.key = key;
+    sm.s_addr = lane_addr + kSCols * j + h0;
+    sm.acc_addr = lane_addr + kColAcc + 32 * j + h0;
+    sm.pj = pbuf + 256 * j + (key >> 3) * Sm::kPBlock + (key & 7) * 16 + h0;
+    sm.mx = tail->mx[gi];
+    sm.lsum = tail->lsum[gi];
+    sm.ok = true;
+    sm.begin();
     const float zs = tail->zs[j];
     const int pos = tail->pos[j];
-    uint8_t* pj = pbuf + 256 * j + (key >> 3) * Sm::kPBlock + (key & 7) * 16 + h0;
-    // nl: log2(vs) - M per head, the addend of u - M (0 until the token has seen a
-    // key); lv: the log2(vs) in it.  l: this key slot's share of the running sums.
-    float nl[kH], l[kH];
-    float lv = 0.f;
-    bool unset = true;
-#pragma unroll
-    for (int h = 0; h < kH; ++h) nl[h] = l[h] = 0.f;
-    bool ok = true;
-
-    // Two pages a step: a page's chain of waits (S^T, vote, P^T buffer) and fences took
-    // 1600 cycles against 400 of work, whatever the number of warps.
-    // Once a wait has run out the warp waits for nothing any more but still takes
-    // part in the group's barriers, so that its other warps get past them.
+    const bool zero_rows = j == last_tok && h0 == 0;
     const int n_steps = pos >= 0 ? (n_pages + kBatch - 1) / kBatch : 0;
     for (int n = 0; n < n_steps; ++n) {
       const int buf = n & 1, k0 = kBatch * n;
       // the pages' scales and blocks
-      if (k0 % kChunk == 0 && ok)
-        ok = wait_for(&tail->info_full[(k0 / kChunk) & 1], (k0 / (2 * kChunk)) & 1);
-      if (ok) ok = wait_for(&tail->s_full[buf], (n >> 1) & 1);
-      tc::fence_after_thread_sync();
-      float t[kBatch][kH], iv[kBatch];
-      int lim[kBatch];   // keys <= lim are visible
-      {
-        uint32_t sv[kBatch][kH];
-        const uint32_t at = s_addr + kSN * kBatch * buf;
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) ld_cols(at + kSN * i, sv[i]);
-        if constexpr (kSCols == 2 * kGroup) {
-          uint32_t sl[kBatch][kH];
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) ld_cols(at + kSN * i + kGroup, sl[i]);
-          tc::wait_ld();
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i)
-#pragma unroll
-            for (int h = 0; h < kH; ++h)
-              t[i][h] = __uint_as_float(sv[i][h]) + __uint_as_float(sl[i][h]);
-        } else {
-          tc::wait_ld();
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i)
-#pragma unroll
-            for (int h = 0; h < kH; ++h) t[i][h] = __uint_as_float(sv[i][h]);
-        }
-      }
-      tc::fence_before_thread_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&tail->s_empty[buf]);
-      // u - M + kPShift: the raw dot products times zt, plus nl
-      float top = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const PageInfo in = tail->info[(k0 + i) % (2 * kChunk)];
-        const bool have = k0 + i < n_pages;   // (the columns of an odd last page hold anything)
-        const float zt = zs * in.k;
-        if (have && in.lv != lv) {   // the same in every thread
-          const float d = in.lv - lv;
-#pragma unroll
-          for (int h = 0; h < kH; ++h) nl[h] += d;
-          lv = in.lv;
-        }
-        iv[i] = have ? in.iv : 0.f;
-        lim[i] = !have || in.block < 0 ? -1 : pos - in.block * kPage;
-#pragma unroll
-        for (int h = 0; h < kH; ++h) t[i][h] = fmaf(t[i][h], zt, nl[h]);
-        if (lim[i] < kPage - 1 && key > lim[i]) {
-#pragma unroll
-          for (int h = 0; h < kH; ++h) t[i][h] = -INFINITY;
-        }
-#pragma unroll
-        for (int h = 0; h < kH; h += 2) top = fmax3f(top, t[i][h], t[i][h + 1]);
-      }
-      bool stored = false, free_p = n == 0;
-      if (barrier_or(bar, unset ? top > -INFINITY : top > kPTop)) {
-        // set or move the references: the heads' maxima over the batch's keys
-#pragma unroll
-        for (int h = 0; h < kH; ++h) {
-          const float m = warp_max_f32(fmaxf(t[0][h], t[kBatch - 1][h]));
-          if (lane == h) tail->mx[gi][h][quarter] = m;
-        }
-        __syncwarp();
-        named_barrier(bar, 128);
-        // lane h (and h + kH ..): kPShift - the maximum where head h's reference moves, else 0
-        float d_h, al_h;
-        {
-          const float4 m4 = *reinterpret_cast<const float4*>(tail->mx[gi][lane & (kH - 1)]);
-          const float m = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
-          d_h = (unset || m > kPTop) && fabsf(m) < INFINITY ? kPShift - m : 0.f;
-          al_h = ex2(d_h);
-        }
-#pragma unroll
-        for (int h = 0; h < kH; ++h) {
-          const float d = __shfl_sync(0xffffffffu, d_h, h);
-          nl[h] += d;
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) t[i][h] += d;
-        }
-        if (!unset) {
-#pragma unroll
-          for (int h = 0; h < kH; ++h) l[h] *= __shfl_sync(0xffffffffu, al_h, h);
-          // the earlier products are relative to the old references (a token that
-          // has seen no key has only zeros there): once they are complete, and
-          // before this batch's, whose P is not written yet
-          if (ok) ok = wait_for(&tail->o_done, (n - 1) & 1);
-          free_p = true;
-          tc::fence_after_thread_sync();
-#pragma unroll
-          for (int part = 0; part < 2; ++part) {   // the hi columns, then the lo ones
-            uint32_t av[kH];
-            ld_cols(acc_addr + kGroup * part, av);
-            tc::wait_ld();
-#pragma unroll
-            for (int h = 0; h < kH; ++h)
-              av[h] = __float_as_uint(__uint_as_float(av[h]) * __shfl_sync(0xffffffffu, al_h, h));
-            st_cols(acc_addr + kGroup * part, av);
-          }
-          tc::wait_st();
-          stored = true;
-        }
-        unset = false;
-      }
-      uint32_t hw[kBatch][kH / 4], lw[kBatch][kH / 4];
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-#pragma unroll
-        for (int q4 = 0; q4 < kH / 4; ++q4) {
-          float* e = &t[i][4 * q4];
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            e[h] = ex2(e[h]);             // P; 0 for an invisible key
-            l[4 * q4 + h] = fmaf(e[h], iv[i], l[4 * q4 + h]);
-          }
-          split_p(e[0], e[1], e[2], e[3], hw[i][q4], lw[i][q4]);
-        }
-      if (j == last_tok && h0 == 0) {
-        // value rows that no token of the tile sees have P = 0, but their bytes
-        // may be anything (an fp8 NaN times 0 is NaN)
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          if (lim[i] >= kPage - 1 || k0 + i >= n_pages) continue;
-          const int s = (k0 + i) % kSlots;
-          if (ok) ok = wait_for(&tail->v_full[s], ((k0 + i) / kSlots) & 1);
-          if (key > lim[i]) {
-            uint4* vrow = reinterpret_cast<uint4*>(smem + Sm::kV + s * kHalfTile + key * 128);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) vrow[c] = make_uint4(0u, 0u, 0u, 0u);
-          }
-        }
-      }
-      // the P^T buffer was last read by the batch before
-      if (ok && !free_p) ok = wait_for(&tail->o_done, (n - 1) & 1);
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        store_p(pj + i * Sm::kPBuf, hw[i]);
-        store_p(pj + i * Sm::kPBuf + 128, lw[i]);
-      }
-      tc::fence_proxy_async_smem();
-      if (stored) tc::fence_before_thread_sync();   // the rescale before O^T
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&tail->p_full);
+      if (k0 % kChunk == 0 && sm.ok)
+        sm.ok = wait_for(&tail->info_full[(k0 / kChunk) & 1], (k0 / (2 * kChunk)) & 1);
+      sm.step(buf, &tail->s_full[buf], (n >> 1) & 1, &tail->s_empty[buf],
+              &tail->info[k0 % (2 * kChunk)], min(kBatch, n_pages - k0), zs, pos, &tail->o_done,
+              (n - 1) & 1, n == 0, &tail->p_full, [&](int i) -> uint8_t* {
+                if (!zero_rows) return nullptr;
+                const int s = (k0 + i) % kSlots;
+                if (sm.ok) sm.ok = wait_for(&tail->v_full[s], ((k0 + i) / kSlots) & 1);
+                return smem + Sm::kV + s * kHalfTile;
+              });
     }
 
     // ---- output: this thread's value dim of each head ---------------------------------------
-    // Running sums: 32 key slots a warp.  Each step halves the heads a lane keeps
-    // (those whose index agrees with the lane in the step's bit), then the lanes
-    // left with one head are summed.
-    {
-      float part[kH];
-#pragma unroll
-      for (int h = 0; h < kH; ++h) part[h] = l[h];
-#pragma unroll
-      for (int n = kH / 2; n >= 1; n >>= 1) {
-        const bool up = (lane & n) != 0;
-#pragma unroll
-        for (int h = 0; h < n; ++h) {
-          const float keep = up ? part[h + n] : part[h], give = up ? part[h] : part[h + n];
-          part[h] = keep + __shfl_xor_sync(0xffffffffu, give, n);
-        }
-      }
-#pragma unroll
-      for (int off = kH; off < 32; off <<= 1)
-        part[0] += __shfl_xor_sync(0xffffffffu, part[0], off);
-      if (lane < kH) tail->lsum[gi][lane][quarter] = part[0];
-    }
     float o[kH];
-#pragma unroll
-    for (int h = 0; h < kH; ++h) o[h] = 0.f;
-    if (n_steps > 0) {
-      if (ok) ok = wait_for(&tail->o_done, (n_steps - 1) & 1);
-      tc::fence_after_thread_sync();
-      uint32_t ah[kH], al[kH];
-      ld_cols(acc_addr, ah);
-      ld_cols(acc_addr + kGroup, al);
-      tc::wait_ld();
-      tc::fence_before_thread_sync();
-#pragma unroll
-      for (int h = 0; h < kH; ++h) o[h] = __uint_as_float(ah[h]) + __uint_as_float(al[h]);
-    }
-    if (!ok && lane == 0) {
+    sm.finish(n_steps > 0, &tail->o_done, (n_steps - 1) & 1, o);
+    const float lv = sm.lv;
+    float (&l)[kH] = sm.l;
+    float (&nl)[kH] = sm.nl;
+    if (!sm.ok && lane == 0) {
       flag_error(p.err, MSA_ERR_TIMEOUT);
       tail->ok = 0;
     }
-    __syncwarp();
-    named_barrier(bar, 128);
-#pragma unroll
-    for (int h = 0; h < kH; ++h) {
-      const float4 l4 = *reinterpret_cast<const float4*>(tail->lsum[gi][h]);
-      l[h] = (l4.x + l4.y) + (l4.z + l4.w);
-    }
+    group_sync<kNT>(gi);   // tail->ok
     const int64_t row0 = (row_tok + j) * p.Hq + g * kGroup;
     const int64_t rows = static_cast<int64_t>(kVarlen ? p.T : p.B * p.Q) * p.Hq;
     const int64_t base = static_cast<int64_t>(split) * rows + row0;
@@ -880,11 +613,7 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
         }
     } else if (tail->ok && (kNT == 1 || tok0 + j < qlen)) {
       if (p.splits == 1) {
-#pragma unroll
-        for (int h = 0; h < kH; ++h) {
-          const float r = l[h] > 0.f ? o[h] * __fdividef(p.v_scale, l[h]) : 0.f;
-          p.out[(row0 + h0 + h) * kHeadDim + key] = static_cast<uint16_t>(f32_to_bf16_bits(r));
-        }
+        sm.write(p.out, row0 + h0, p.v_scale, o);
       } else {
 #pragma unroll
         for (int h = 0; h < kH; ++h)
@@ -1027,13 +756,25 @@ cudaError_t launch_attend_scaled(const CUtensorMap& kv_map, const AttendParams& 
   const int tiles = (p.Q + ntile - 1) / ntile;
   const int64_t units = dense ? static_cast<int64_t>(p.B) * tiles * p.Hkv
                               : static_cast<int64_t>(p.cu_q ? p.T : p.B * p.Q) * p.Hkv;
-  // The CTAs of a cluster cut a unit's part while that still fits one wave and
-  // leaves each a page or more (lists: 16 pages a row).
+  // The CTAs of a cluster cut a unit's part where that puts more of one wave's slots to
+  // use and leaves each a page or more (lists: 16 pages a row).
   const int pages = dense ? p.S : kTopK;
   int cs = 1;
-  if (ntile == 1 && (dense || p.splits == 1))
-    while (cs < kMaxCluster && units * p.splits * cs * 2 <= slots && p.splits * cs * 2 <= pages)
-      cs *= 2;
+  if (ntile == 1 && (dense || p.splits == 1)) {
+    int64_t best = 0;
+    for (int c = 1; c <= kMaxCluster && c <= pages; c *= 2) {
+      const int64_t parts = slots / c / units;   // clusters a unit can have
+      const int64_t used = units * c * (parts < p.splits ? parts : p.splits);
+      if (used > best) {
+        best = used;
+        cs = c;
+      }
+    }
+  }
+  // rows for more than one wave of CTAs: CTAs that stay, each row's start and end hidden
+  // behind others' pages
+  if (!dense && !p.scores && p.splits == 1 && units > slots)
+    return launch_attend_stream(kv_map, p, stream, pdl);
   dim3 grid;
   if (!dense) {
     grid = dim3(static_cast<unsigned>(units / p.Hkv * cs), p.Hkv, p.splits);

@@ -128,6 +128,10 @@ cudaError_t launch_score_scaled(const CUtensorMap& kv_map, const ScoreParams& p,
                                 cudaStream_t stream, bool pdl);
 cudaError_t launch_attend_scaled(const CUtensorMap& kv_map, const AttendParams& p,
                                  cudaStream_t stream, bool pdl);
+// Lists, more rows than CTAs, one part a row (splits == 1): launch_attend_scaled's
+// choice.
+cudaError_t launch_attend_stream(const CUtensorMap& kv_map, const AttendParams& p,
+                                 cudaStream_t stream, bool pdl);
 cudaError_t launch_union_attend_scaled(const CUtensorMap& kv_map, const AttendParams& p,
                                        cudaStream_t stream, bool pdl);
 // Its split count for `units` (request, tile, KV head) units: as many CTAs per

@@ -184,6 +184,50 @@ def test_sparse_prefill(seq_lens, q_lens, q8):
     assert msa.get_error() == 0
 
 
+@pytest.mark.parametrize("q8", [False, True])
+def test_more_rows_than_ctas(q8):
+    """Rows for several waves: CTAs that take row after row (330 to 1100 rows), with
+    rows of no page, of one page, of an odd number of pages and of 16 between them."""
+    gen = torch.Generator().manual_seed(5)
+    q_lens = [120, 1, 0, 90, 60, 3]
+    lens = [2300, 1, 0, 90, 700, 5000]
+    c = _inputs(lens, q_lens, 4, 41, spread=2.0, q8=q8)
+    holes = torch.rand(c["lists"].shape, generator=gen).to(DEV)
+    c["lists"] = torch.where(holes < 0.3, -1, c["lists"])
+    c["lists"][5:9] = -1
+    cu = torch.tensor([0] + list(torch.tensor(q_lens).cumsum(0)), dtype=torch.int32, device=DEV)
+    out, bound, _ = _ref(c, c["lists"], 0.9, 1.3)
+    args = (c["q"], c["kv"], c["bt"], c["lens"], cu, c["lists"], SM, 0.9, 1.3)
+    got = msa.sparse_prefill(*args, kv_scales=c["sc"], q_scale=c["qs"])
+    check_attend(got, out, bound)
+    assert (got[5:9] == 0).all()
+    for _ in range(5):   # whatever the roles' timing: the same bits
+        assert torch.equal(got, msa.sparse_prefill(*args, kv_scales=c["sc"], q_scale=c["qs"]))
+    assert msa.get_error() == 0
+    # tokens past the last request, a bad scale and a bad page in the middle
+    cu[-1] = 270
+    page = int(c["bt"][0, 3])
+    c["sc"][page, 1, 0] = float("nan")
+    c["kv"][page, 1] = 0x7F
+    got2 = msa.sparse_prefill(*args, kv_scales=c["sc"], q_scale=c["qs"])
+    assert msa.get_error() == _native.ERR_SEQ_RANGE | _native.ERR_SCALE
+    assert (got2[270:] == 0).all() and torch.isfinite(got2.float()).all()
+    same = ~(c["lists"][:120, 1] == 3).any(dim=1)
+    assert torch.equal(got2[:120, :16], got[:120, :16]) and torch.equal(got2[120:270], got[120:270])
+    assert torch.equal(got2[:120][same], got[:120][same])
+
+
+def test_a_decode_batch_of_more_rows_than_ctas():
+    lens = [(k * 37) % 1500 if k % 10 else 0 for k in range(128)]
+    c = _inputs(lens, [1] * 128, 4, 42)
+    out, bound, _ = _ref(c, c["lists"])
+    got = msa.sparse_decode(c["q"], c["kv"], c["bt"], c["lens"], c["lists"], 1, SM,
+                            kv_scales=c["sc"])
+    check_attend(got, out, bound)
+    assert (got[torch.tensor(lens) == 0] == 0).all()
+    assert msa.get_error() == 0
+
+
 @pytest.mark.parametrize("spread_pages", [[-40, 0, -20, 30], [40, -40, 40, -40], [3, 2, 1, 0]])
 @pytest.mark.parametrize("kind", ["sparse", "union", "dense"])
 def test_scales_over_their_whole_range(spread_pages, kind):
