@@ -59,6 +59,8 @@ struct Tail {
   uint64_t k_full[kSlots];  // TMA -> S^T
   uint64_t k_empty[kSlots]; // S^T -> TMA
   uint64_t v_full[kSlots];  // TMA -> O^T
+  uint64_t v_land[2];       // TMA -> warp 2: a V tile with rows that not every token sees
+  uint64_t v_edges;         // warp 2 is through with those
   uint64_t v_empty[kSlots]; // O^T -> TMA
   uint64_t s_full[2];       // a batch's S^T ready -> softmax
   uint64_t s_empty[2];      // softmax has read a batch's S^T
@@ -68,10 +70,12 @@ struct Tail {
   uint64_t finish;          // every role done and every product complete
   uint32_t tmem_base;
   int n_pages;
+  int edge;                 // list modes: page 0's V tile lands on v_land
   int ok;                   // 0: some softmax warp gave up on a wait
   int pos[kNT];             // token positions, -1: none
   float zs[kNT];            // logit scale (log2 units) times 2^e of each token's query split
   int pages[kTopK];         // list modes: this CTA's pages
+  uint32_t nan[kNT][4];     // kNT > 1: value dims with a NaN that the token sees (nan_values)
   PageInfo info[2 * kChunk];
   alignas(16) float mx[kCount][kHeads][4];    // batch maxima by quarter
   alignas(16) float lsum[kCount][kHeads][4];  // running sums by quarter
@@ -127,6 +131,31 @@ __device__ __forceinline__ float ld_peer(const float* own, uint32_t rank) {
       : "r"(smem_u32(own)), "r"(rank)
       : "memory");
   return v;
+}
+
+// A warp: the value rows first_lim < r <= lim of block `blk`, which the tile's later
+// tokens see and the earlier ones do not.  A NaN there would reach the others' columns
+// of the product too: it is set to 0, and its dim goes into `nan` of the tokens that see
+// the row.  At most three rows; a row's 16-byte chunk c lies at c ^ (row & 7).
+template <int kNT>
+__device__ __forceinline__ void nan_values(uint8_t* tile, int first_lim, int lim, int blk,
+                                           Tail<kNT>* tail, int lane) {
+  static_assert(kNT <= 5, "eight lanes a row");
+  const int r = first_lim + 1 + (lane >> 3), c = lane & 7;
+  if (r < 0 || r > min(lim, kPage - 1)) return;
+  uint32_t* w = reinterpret_cast<uint32_t*>(tile + r * 128 + 16 * c);
+  uint32_t dims = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t x = w[e], m = __vcmpeq4(x & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    w[e] = x & ~m;
+    dims |= (((m & 0x08040201u) * 0x01010101u) >> 24) << (4 * e);   // a bit a byte
+  }
+  if (dims == 0) return;
+  const int at = c ^ (r & 7);
+#pragma unroll
+  for (int j = 0; j < kNT; ++j)
+    if (tail->pos[j] >= blk * kPage + r) atomicOr(&tail->nan[j][at >> 1], dims << (16 * (at & 1)));
 }
 
 // kNT tokens a tile; kCluster: the pages of a part are cut over a cluster's CTAs.
@@ -197,13 +226,12 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
   auto token_pos = [&](int j) -> int {
     return seq_ok && tok0 + j < qlen ? L - qlen + tok0 + j : -1;
   };
-  int last_pos = -1, valid_toks = 0, last_tok = 0;   // last_tok: the largest position's
+  int last_pos = -1, valid_toks = 0;
 #pragma unroll
   for (int j = 0; j < kNT; ++j) {
     const int q = token_pos(j);
     if (q >= 0) {
       last_pos = q;
-      last_tok = j;
       ++valid_toks;
     }
   }
@@ -216,6 +244,13 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
     hi = static_cast<int>(nblk * (at + 1) / of);
   }
 
+  const int first_pos = last_pos - max(valid_toks - 1, 0);
+  // 0 or 1, the number of v_land: block `blk` (at most the last token's) has rows that
+  // not every token sees; -1: none
+  auto edge_of = [&](int blk) {
+    return blk * kPage + kPage - 1 > first_pos ? blk - first_pos / kPage : -1;
+  };
+
   // ---- prologue ----------------------------------------------------------------------
   // warp 0: the lane's page, its block (-1: none) and scales (dense decode: of the next chunk)
   int pg_next = 0, blk_next = -1;
@@ -227,11 +262,11 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
     mbar_arrive_expect_tx(&tail->k_full[s], kHalfTile);
     tma_load_2d(smem + s * kHalfTile, &kv_map, 0, (page * p.Hkv + g) * kPage, &tail->k_full[s]);
   };
-  auto load_v = [&](int t, int page) {
+  auto load_v = [&](int t, int page, int e) {   // e: edge_of the page's block
     const int s = t % kSlots;
-    mbar_arrive_expect_tx(&tail->v_full[s], kHalfTile);
-    tma_load_2d(smem + Sm::kV + s * kHalfTile, &kv_map, kHeadDim, (page * p.Hkv + g) * kPage,
-                &tail->v_full[s]);
+    uint64_t* full = e < 0 ? &tail->v_full[s] : &tail->v_land[e];
+    mbar_arrive_expect_tx(full, kHalfTile);
+    tma_load_2d(smem + Sm::kV + s * kHalfTile, &kv_map, kHeadDim, (page * p.Hkv + g) * kPage, full);
   };
   // dense decode: the lane's page of slot t (a bad table entry: page 0 instead,
   // attended by no key), then its scales
@@ -296,14 +331,20 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
       }
       mbar_init(&tail->p_full, warps);
       mbar_init(&tail->o_done, 1);
+      mbar_init(&tail->v_land[0], 1);
+      mbar_init(&tail->v_land[1], 1);
+      mbar_init(&tail->v_edges, 1);
       mbar_init(&tail->finish, 4 + 4 * Groups<kNT>::kCount);
       fence_barrier_init();
       prefetch_tensormap(&kv_map);
       tail->ok = 1;
+      tail->edge = 0;
       for (int j = 0; j < kNT; ++j) tail->pos[j] = token_pos(j);
+      if (kNT > 1)
+        for (int e = 0; e < 4 * kNT; ++e) tail->nan[e >> 2][e & 3] = 0;
       if (pre_page >= 0) {
         load_k(0, pre_page);
-        load_v(0, pre_page);
+        load_v(0, pre_page, edge_of(cur));
       }
     }
     __syncwarp();
@@ -314,7 +355,7 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
       look_up_scales();
       if (lane < min(np, kSlots)) {
         load_k(lane, pg_next);
-        load_v(lane, pg_next);
+        load_v(lane, pg_next, edge_of(lo + lane));
       }
     } else {
       const int64_t list = (row_tok * p.Hkv + g) * kTopK;
@@ -373,8 +414,9 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
         tail->pages[k] = page;
         if (k < kSlots && !(k == 0 && pre_page >= 0)) {
           load_k(k, page);
-          load_v(k, page);
+          load_v(k, page, edge_of(n));
         }
+        if (k == 0) tail->edge = edge_of(n) >= 0;
       }
     }
     if (lane == 0) tail->n_pages = np;
@@ -422,6 +464,8 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
   const int n_pages = tail->n_pages;
   const uint32_t tmem = tail->tmem_base;
 
+  if (warp < 4) {
+  if constexpr (kNT > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
   if (warp == 0 || warp == 2) {
     // ---- TMA producers: K tiles (warp 0, with the scales), V tiles (warp 2) ----------------
     const bool is_k = warp == 0;
@@ -438,6 +482,20 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
     // dense decode, chunk by chunk: a chunk's pages are looked up when the one before
     // it begins and their scales when it is half through
     int pg = pg_next;
+    // warp 2: tile t, of block blk, has landed on v_land[e]
+    auto settle = [&](int e, int t, int blk) {
+      const bool landed = __all_sync(0xffffffffu, wait_for(&tail->v_land[e], 0));
+      ok = ok && landed;
+      if (!landed) return;
+      uint8_t* tile = smem + Sm::kV + t % kSlots * kHalfTile;
+      if constexpr (kNT > 1)
+        nan_values(tile, first_pos - blk * kPage, last_pos - blk * kPage, blk, tail, lane);
+      zero_value_rows(tile, last_pos - blk * kPage, lane);
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tail->v_full[t % kSlots]);
+    };
+    if (kMode != kDense && !is_k && tail->edge) settle(0, 0, last_pos / kPage);
     if (kMode == kDense && kChunk < n_pages) look_up(kChunk + lane);
     for (int t = kSlots; t < n_pages && ok; ++t) {
       int page;
@@ -463,12 +521,20 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
       if (ok) {
         if (lane == 0) {
           if (is_k) load_k(t, page);
-          else load_v(t, page);
+          else load_v(t, page, kMode == kDense ? edge_of(lo + t) : -1);
         }
         issued = t + 1;
       }
     }
+    if (kMode == kDense && !is_k) {
+      // the last tiles, all loads of this CTA on their way
+      for (int e = 0; e < 2; ++e) {
+        const int blk = first_pos / kPage + e, t = blk - lo;
+        if (t >= 0 && t < issued && edge_of(blk) == e) settle(e, t, blk);
+      }
+    }
     if (lane == 0) {
+      if (kNT > 1 && !is_k) mbar_arrive(&tail->v_edges);
       if (!ok) flag_error(p.err, MSA_ERR_TIMEOUT);
       // the loads still in flight land before shared memory can be released
       for (int t = max(0, issued - kSlots); t < issued; ++t)
@@ -514,7 +580,7 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
     (void)mbar_wait(&tail->finish, 0);
     tc::fence_after_thread_sync();
     tc::tmem_dealloc(tmem, kTmemCols);
-  } else if (warp == 3) {
+  } else {
     // ---- O^T += V^T P^T ----------------------------------------------------------------------
     if (lane == 0) {
       const uint64_t a0 = tc::sw128_mnmajor_desc(smem_u32(smem + Sm::kV));
@@ -523,19 +589,30 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
       const uint64_t b0 = tc::interleave_mnmajor_desc(smem_u32(pbuf), Sm::kPBlock, 128);
       constexpr uint32_t idesc = tc::idesc_e4m3_f32_mn(128, 32 * kNT);
       bool ok = true;
+      uint32_t acc = 0;   // there has been a product
       for (int t0 = 0, n = 0; t0 < n_pages && ok; t0 += kBatch, ++n) {
-        ok = wait_for(&tail->p_full, n & 1);
-        for (int t = t0; t < min(t0 + kBatch, n_pages) && ok; ++t) {
-          const int s = t % kSlots;
+        // pages of bad scales have no product (read before the wait for P)
+        if (t0 % kChunk == 0) ok = wait_for(&tail->info_full[(t0 / kChunk) & 1], (t0 / (2 * kChunk)) & 1);
+        bool bad[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) bad[i] = tail->info[(t0 + i) % (2 * kChunk)].block < 0;
+        ok = ok && wait_for(&tail->p_full, n & 1);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int t = t0 + i, s = t % kSlots;
+          if (t >= n_pages || !ok) break;
           ok = wait_for(&tail->v_full[s], (t / kSlots) & 1);
           if (!ok) break;
           tc::fence_after_thread_sync();
           const uint64_t a = a0 + static_cast<uint64_t>(s) * (kHalfTile >> 4);
           const uint64_t bp = b0 + static_cast<uint64_t>(((t - t0) * Sm::kPBuf) >> 4);
+          if (!bad[i]) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc::mma_e4m3(tmem + kColAcc, a + 256 * kk, bp + ((4 * Sm::kPBlock) >> 4) * kk, idesc,
-                         (t > 0 || kk > 0) ? 1u : 0u);
+            for (int kk = 0; kk < 4; ++kk) {
+              tc::mma_e4m3(tmem + kColAcc, a + 256 * kk, bp + ((4 * Sm::kPBlock) >> 4) * kk, idesc, acc);
+              acc = 1;
+            }
+          }
           tc::commit(&tail->v_empty[s]);
         }
         if (ok) tc::commit(&tail->o_done);
@@ -544,7 +621,9 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
       tc::commit(&tail->finish);
     }
     __syncwarp();
+  }
   } else {
+    if constexpr (kNT > 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     // ---- group gi: kH heads of token j ------------------------------------------------------
     constexpr int kH = Groups<kNT>::kHeads;
     const int gi = (warp - 4) >> 2;
@@ -567,7 +646,6 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
     sm.begin();
     const float zs = tail->zs[j];
     const int pos = tail->pos[j];
-    const bool zero_rows = j == last_tok && h0 == 0;
     const int n_steps = pos >= 0 ? (n_pages + kBatch - 1) / kBatch : 0;
     for (int n = 0; n < n_steps; ++n) {
       const int buf = n & 1, k0 = kBatch * n;
@@ -576,12 +654,7 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
         sm.ok = wait_for(&tail->info_full[(k0 / kChunk) & 1], (k0 / (2 * kChunk)) & 1);
       sm.step(buf, &tail->s_full[buf], (n >> 1) & 1, &tail->s_empty[buf],
               &tail->info[k0 % (2 * kChunk)], min(kBatch, n_pages - k0), zs, pos, &tail->o_done,
-              (n - 1) & 1, n == 0, &tail->p_full, [&](int i) -> uint8_t* {
-                if (!zero_rows) return nullptr;
-                const int s = (k0 + i) % kSlots;
-                if (sm.ok) sm.ok = wait_for(&tail->v_full[s], ((k0 + i) / kSlots) & 1);
-                return smem + Sm::kV + s * kHalfTile;
-              });
+              (n - 1) & 1, n == 0, &tail->p_full);
     }
 
     // ---- output: this thread's value dim of each head ---------------------------------------
@@ -595,6 +668,13 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
       tail->ok = 0;
     }
     group_sync<kNT>(gi);   // tail->ok
+    if constexpr (kNT > 1) {
+      if (sm.ok) sm.ok = wait_for(&tail->v_edges, 0);   // nan
+      if (tail->nan[j][key >> 5] >> lane & 1) {
+#pragma unroll
+        for (int h = 0; h < kH; ++h) o[h] = __uint_as_float(0x7FFFFFFFu);
+      }
+    }
     const int64_t row0 = (row_tok + j) * p.Hq + g * kGroup;
     const int64_t rows = static_cast<int64_t>(kVarlen ? p.T : p.B * p.Q) * p.Hq;
     const int64_t base = static_cast<int64_t>(split) * rows + row0;

@@ -52,12 +52,14 @@ struct Item {
   PageInfo info[kTopK];
   int pages[kTopK];
   int n_pages, pos;
+  int current;              // the token's own block is listed (and so the first page)
   float zs;                 // logit scale (log2 units) times 2^e of the query split
 };
 
 struct Tail {
   uint64_t k_full[kSlots], k_empty[kSlots];   // TMA <-> S^T
   uint64_t v_full[kSlots], v_empty[kSlots];   // TMA <-> O^T
+  uint64_t v_land;                  // TMA -> warp 2: a V tile with rows to be zeroed
   uint64_t s_full[2], s_empty[2];   // S^T <-> softmax, a batch a buffer
   uint64_t p_full, o_done;          // softmax <-> O^T, a batch at a time
   uint64_t q_free;                  // an item's S^T products complete
@@ -107,6 +109,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     mbar_init(&tail->p_full, 4 * kCount);
     mbar_init(&tail->o_done, 1);
+    mbar_init(&tail->v_land, 1);
     mbar_init(&tail->q_free, 1);
     mbar_init(&tail->finish, 4 + 4 * kCount);
     fence_barrier_init();
@@ -195,6 +198,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (lane == 0) {
         it->n_pages = np;
         it->pos = pos;
+        it->current = fm != 0;
         it->zs = zs;
       }
       __syncwarp();
@@ -258,23 +262,40 @@ __global__ void __launch_bounds__(kThreads, 2)
     tc::tmem_dealloc(tmem, kTmemCols);
   } else if (warp == 2) {
     // ---- V tiles -----------------------------------------------------------------------------------
-    if (lane == 0) {
-      int t = 0, i = 0;
-      for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x, ++i) {
-        const int g = static_cast<int>(u / tokens);
-        const Item* it = &tail->item[i & 1];
-        ok = wait_for(&tail->item_full[i & 1], (i >> 1) & 1);
-        const int np = ok ? it->n_pages : 0;
-        for (int x = 0; x < np && ok; ++x) {
-          const int s = t % kSlots;
-          ok = t < kSlots || wait_for(&tail->v_empty[s], ((t / kSlots) - 1) & 1);
-          if (!ok) break;
-          mbar_arrive_expect_tx(&tail->v_full[s], kHalfTile);
+    int t = 0, i = 0, edges = 0;
+    for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x, ++i) {
+      const int g = static_cast<int>(u / tokens);
+      const Item* it = &tail->item[i & 1];
+      ok = __all_sync(0xffffffffu, wait_for(&tail->item_full[i & 1], (i >> 1) & 1));
+      const int np = ok ? it->n_pages : 0;
+      // the first page is the one that may end past the token's position
+      const int lim = np > 0 ? it->pos - (it->pos / kPage) * kPage : 0;
+      const bool edge = np > 0 && it->current && lim < kPage - 1;
+      for (int x = 0; x < np && ok; ++x) {
+        const int s = t % kSlots;
+        ok = __all_sync(0xffffffffu, t < kSlots || wait_for(&tail->v_empty[s], ((t / kSlots) - 1) & 1));
+        if (!ok) break;
+        if (lane == 0) {
+          uint64_t* full = edge && x == 0 ? &tail->v_land : &tail->v_full[s];
+          mbar_arrive_expect_tx(full, kHalfTile);
           tma_load_2d(smem + kOffV + s * kHalfTile, &kv_map, kHeadDim,
-                      (it->pages[x] * p.Hkv + g) * kPage, &tail->v_full[s]);
-          ++t;
+                      (it->pages[x] * p.Hkv + g) * kPage, full);
+        }
+        ++t;
+        // (not before the next load is on its way)
+        if (edge && (x == 1 || np == 1)) {
+          const int s0 = (t - 1 - x) % kSlots;
+          ok = __all_sync(0xffffffffu, wait_for(&tail->v_land, edges & 1));
+          ++edges;
+          if (!ok) break;
+          zero_value_rows(smem + kOffV + s0 * kHalfTile, lim, lane);
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tail->v_full[s0]);
         }
       }
+    }
+    if (lane == 0) {
       if (!ok) flag_error(p.err, MSA_ERR_TIMEOUT);
       for (int x = max(0, t - kSlots); x < t; ++x)
         (void)wait_for(&tail->v_full[x % kSlots], (x / kSlots) & 1);
@@ -289,22 +310,35 @@ __global__ void __launch_bounds__(kThreads, 2)
       const uint64_t b0 = tc::interleave_mnmajor_desc(smem_u32(pbuf), kPBlock, 128);
       constexpr uint32_t idesc = tc::idesc_e4m3_f32_mn(128, 2 * kGroup);
       int t = 0, nb = 0, i = 0;
+      uint32_t acc = 0;   // the item has had a product
       for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x, ++i) {
         ok = wait_for(&tail->item_full[i & 1], (i >> 1) & 1);
         const int np = ok ? tail->item[i & 1].n_pages : 0;
         for (int x = 0; x < np && ok; x += kBatch, ++nb) {
+          // (read before the wait: behind it, the load cost 7 us of 290)
+          bool bad[kBatch];
+#pragma unroll
+          for (int y = 0; y < kBatch; ++y) bad[y] = tail->item[i & 1].info[(x + y) % kTopK].block < 0;
           ok = wait_for(&tail->p_full, nb & 1);
-          for (int y = x; y < min(x + kBatch, np) && ok; ++y, ++t) {
+          if (x == 0) acc = 0;
+#pragma unroll
+          for (int y1 = 0; y1 < kBatch; ++y1) {
+            const int y = x + y1;
+            if (y >= np || !ok) break;
             const int s = t % kSlots;
             ok = wait_for(&tail->v_full[s], (t / kSlots) & 1);
             if (!ok) break;
+            ++t;
             tc::fence_after_thread_sync();
             const uint64_t a = a0 + static_cast<uint64_t>(s) * (kHalfTile >> 4);
             const uint64_t bp = b0 + static_cast<uint64_t>(((y - x) * kPBuf) >> 4);
+            if (!bad[y1]) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc::mma_e4m3(tmem + kColAcc, a + 256 * kk, bp + ((4 * kPBlock) >> 4) * kk, idesc,
-                           (y > 0 || kk > 0) ? 1u : 0u);
+              for (int kk = 0; kk < 4; ++kk) {
+                tc::mma_e4m3(tmem + kColAcc, a + 256 * kk, bp + ((4 * kPBlock) >> 4) * kk, idesc, acc);
+                acc = 1;
+              }
+            }
             tc::commit(&tail->v_empty[s]);
           }
           if (ok) tc::commit(&tail->o_done);
@@ -332,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     sm.mx = tail->mx[gi];
     sm.lsum = tail->lsum[gi];
     sm.ok = true;
-    int t = 0, nb = 0, i = 0;
+    int nb = 0, i = 0;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x, ++i) {
       Item* it = &tail->item[i & 1];
       if (sm.ok) sm.ok = wait_for(&tail->item_full[i & 1], (i >> 1) & 1);
@@ -348,13 +382,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int x = 0; x < np; x += kBatch, ++nb) {
         const int buf = nb & 1, have = min(kBatch, np - x);
         sm.step(buf, &tail->s_full[buf], (nb >> 1) & 1, &tail->s_empty[buf], &it->info[x], have, zs,
-                pos, &tail->o_done, (nb - 1) & 1, nb == 0, &tail->p_full, [&](int y) -> uint8_t* {
-                  if (gi != 0) return nullptr;
-                  const int s = (t + y) % kSlots;
-                  if (sm.ok) sm.ok = wait_for(&tail->v_full[s], ((t + y) / kSlots) & 1);
-                  return smem + kOffV + s * kHalfTile;
-                });
-        t += have;
+                pos, &tail->o_done, (nb - 1) & 1, nb == 0, &tail->p_full);
       }
       float o[kH];
       sm.finish(np > 0, &tail->o_done, (nb - 1) & 1, o);

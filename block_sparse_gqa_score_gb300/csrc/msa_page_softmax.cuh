@@ -76,6 +76,16 @@ __device__ __forceinline__ void barrier_id() {
   asm volatile("barrier.cta.sync.aligned %0, 128;" ::"n"(kId) : "memory");
 }
 
+// Value rows that no token sees have P = 0, but their bytes may be anything (an fp8 NaN
+// times 0 is NaN).  A page whose scales are bad has no product at all; in a page that
+// ends past the (first) token's position the unseen rows are set to 0 by the warp that
+// loads the V tiles, before it hands the tile on: such a tile lands on a barrier of its
+// own.  In the softmax warps the same cost 9 us of 291 (1536 prefill tokens).
+__device__ __forceinline__ void zero_value_rows(uint8_t* tile, int lim, int lane) {
+  for (int x = 8 * max(lim + 1, 0) + lane; x < 8 * kPage; x += 32)
+    reinterpret_cast<uint4*>(tile)[x] = make_uint4(0u, 0u, 0u, 0u);
+}
+
 template <int kNT>
 __device__ __forceinline__ bool group_or(int gi, bool pred) {
   __syncwarp();
@@ -165,13 +175,10 @@ struct PageSoftmax {
   // A batch of `have` pages (1 .. kBatch): S^T in buffer s_buf, complete at s_full's
   // phase s_par; P^T, free when o_done's phase o_par is complete (at once: first), is
   // announced on p_full.  zs: the token's logit scale; pos: its position.
-  // value_tile(i): where this group has to keep unseen value rows from the product,
-  // page i's V tile once it has landed, else nullptr.
-  template <typename ValueTile>
   __device__ __forceinline__ void step(int s_buf, uint64_t* s_full, unsigned s_par,
                                        uint64_t* s_empty, const PageInfo* info, int have, float zs,
                                        int pos, uint64_t* o_done, unsigned o_par, bool first,
-                                       uint64_t* p_full, ValueTile&& value_tile) {
+                                       uint64_t* p_full) {
     if (ok) ok = wait_for(s_full, s_par);
     tc::fence_after_thread_sync();
     float t[kBatch][kH], iv[kBatch];
@@ -287,18 +294,6 @@ struct PageSoftmax {
         }
         split_p(e[0], e[1], e[2], e[3], hw[i][q4], lw[i][q4]);
       }
-    // value rows that no token of the tile sees have P = 0, but their bytes may be
-    // anything (an fp8 NaN times 0 is NaN)
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (lim[i] >= kPage - 1 || i >= have) continue;
-      uint8_t* tile = value_tile(i);
-      if (tile && key > lim[i]) {
-        uint4* vrow = reinterpret_cast<uint4*>(tile + key * 128);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) vrow[c] = make_uint4(0u, 0u, 0u, 0u);
-      }
-    }
     // the P^T buffer was last read by the batch before
     if (ok && !free_p) ok = wait_for(o_done, o_par);
 #pragma unroll
@@ -355,6 +350,10 @@ struct PageSoftmax {
     for (int h = 0; h < kH; ++h) {
       const float4 l4 = *reinterpret_cast<const float4*>(lsum[h]);
       l[h] = (l4.x + l4.y) + (l4.z + l4.w);
+      if (l[h] != l[h]) {   // a NaN logit: the whole row, whatever it is merged with
+        l[h] = 1.f;
+        o[h] = __uint_as_float(0x7FFFFFFFu);
+      }
     }
   }
 

@@ -957,6 +957,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         l[4 * h4 + 2] = t4.z;
         l[4 * h4 + 3] = t4.w;
       }
+#if MSA_KV_SCALES
+#pragma unroll
+      for (int h = 0; h < kGroup; ++h)
+        if (l[h] != l[h]) {   // a NaN logit: the whole row, whatever it is merged with
+          l[h] = 1.f;
+          o[h] = __uint_as_float(0x7FFFFFFFu);
+        }
+#endif
       const int d = key;
       const int64_t row0 = (static_cast<int64_t>(b) * p.Q + tok) * p.Hq + g * kGroup;
       if (p.splits == 1) {

@@ -308,6 +308,82 @@ def test_every_listed_page_bad_gives_zero():
     assert msa.get_error() == _native.ERR_SCALE
 
 
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("kind", ["lists1", "lists4", "parts", "union", "dense1", "dense4", "dense7",
+                                  "rows"])
+def test_a_nan_reaches_exactly_those_that_see_it(kind, q8):
+    """NaN codes of a key (all of its attenders' heads) and of single value dims (that
+    dim only), some of them seen by a tile's later tokens alone; a NaN query head."""
+    Q = {"lists1": 1, "dense1": 1, "dense7": 7, "rows": 130}.get(kind, 4)
+    lens = [900, 514, 386]     # request 1's last four tokens: 510 .. 513, across two pages
+    c = _inputs(lens, [Q] * 3, 1, 61, q8=q8)
+    bt, kv = c["bt"], c["kv"]
+    want_kw = dict(lists=None if kind.startswith("dense") else c["lists"], ks=0.9, vs=1.3)
+    clean, bound, _ = _ref(c, **want_kw)
+    kv[int(bt[0, 1]), 0, 2, 5] = 0x7F                          # a key of request 0
+    if kind != "union":        # (the union's pages are everybody's)
+        kv[int(bt[1, 512 // PAGE]), 0, 512 % PAGE, D + 77] = 0xFF
+        kv[int(bt[1, 511 // PAGE]), 0, 511 % PAGE, D + 3] = 0x7F
+        kv[int(bt[1, 511 // PAGE]), 0, 511 % PAGE, D + 124] = 0x7F
+    kv[int(bt[2, 0]), 0, 9, D + 40] = 0x7F
+    out, _, _ = _ref(c, **want_kw)
+    c["q"].view(torch.uint8 if q8 else torch.int16)[2 * Q, 6, 11] = 0x7F if q8 else 0x7FC0
+    out[2 * Q, 6] = float("nan") if (clean[2 * Q, 6] != 0).any() else 0.0
+    args = (c["q"], kv, bt, c["lens"])
+    kw = dict(kv_scales=c["sc"], q_scale=c["qs"])
+    if kind.startswith("dense"):
+        got = msa.dense_decode(*args, Q, SM, 0.9, 1.3, **kw)
+    elif kind == "rows":
+        cu = torch.arange(4, dtype=torch.int32, device=DEV) * Q
+        got = msa.sparse_prefill(*args, cu, c["lists"], SM, 0.9, 1.3, **kw)
+    else:
+        was = msa.set_union_tile(kind == "union")
+        try:
+            got = msa.sparse_decode(*args, c["lists"], Q, SM, 0.9, 1.3,
+                                    num_splits=3 if kind == "parts" else 0, **kw)
+        finally:
+            msa.set_union_tile(was)
+    nan = torch.isnan(out)
+    assert nan.any() and not nan.all()
+    assert torch.equal(torch.isnan(got), nan)
+    check_attend(torch.where(nan, 0.0, got), torch.where(nan, 0.0, out),
+                 torch.where(nan, 0.0, bound))
+    assert msa.get_error() == 0
+
+
+@pytest.mark.parametrize("Q", [2, 4])
+@pytest.mark.parametrize("S", [0, 600])
+def test_step_with_the_union_tile(Q, S):
+    """decode_step and the attends with no split count while the union tile is on."""
+    lens = [3000, 0, 5000, 1]
+    c = _inputs(lens, [Q] * 4, 2, 62)
+    bt = torch.zeros((4, max(S, c["bt"].shape[1])), dtype=torch.int32, device=DEV)
+    bt[:, :c["bt"].shape[1]] = c["bt"]
+    was = msa.set_union_tile(True)
+    try:
+        s, tk, out = msa.decode_step(c["q"], c["kv"], bt, c["lens"], Q, SM, 1.1, 0.9,
+                                     kv_scales=c["sc"])
+        out2 = msa.sparse_decode(c["q"], c["kv"], bt, c["lens"], tk, Q, SM, 1.1, 0.9,
+                                 kv_scales=c["sc"])
+    finally:
+        msa.set_union_tile(was)
+    o, bound, _ = _ref(dict(c, bt=bt), tk, 1.1, 0.9)
+    check_attend(out, o, bound)
+    check_attend(out2, o, bound)
+    assert msa.get_error() == 0
+
+
+@pytest.mark.parametrize("B,Q", [(300, 1), (270, 2), (260, 5)])
+def test_dense_decode_of_large_batches(B, Q):
+    """More requests than the shared-out assignment takes."""
+    lens = [(k * 53) % 260 if k % 7 else 0 for k in range(B)]
+    c = _inputs(lens, [Q] * B, 1, 63)
+    out, bound, _ = _ref(c)
+    got = msa.dense_decode(c["q"], c["kv"], c["bt"], c["lens"], Q, SM, kv_scales=c["sc"])
+    check_attend(got, out, bound)
+    assert (got[(out == 0).all(dim=2)] == 0).all() and msa.get_error() == 0
+
+
 @pytest.mark.parametrize("Q,S,q8,index", [(1, 1, False, False), (4, 1, True, False),
                                           (4, 600, False, False), (2, 1, False, True),
                                           (4, 600, True, True)])
