@@ -618,10 +618,12 @@ def append_kv_prefill(k, v, kv, block_table, seq_lens, cu_seqlens_q, k_scale: fl
     """append_kv of a prefill or chunked-prefill batch (msa_append_kv_prefill):
     request b's tokens are rows cu_seqlens_q[b] .. cu_seqlens_q[b + 1] - 1 of k,
     v and q, the last ones of its seq_lens[b]."""
+    _need(seq_lens, "seq_lens", (torch.int32,))
     _need(cu_seqlens_q, "cu_seqlens_q", (torch.int32,), seq_lens.device)
+    tokens = k.shape[0] if isinstance(k, torch.Tensor) and k.dim() else 0
     if tuple(cu_seqlens_q.shape) != (seq_lens.shape[0] + 1,):
         raise ValueError("cu_seqlens_q must be [B + 1]")
-    return _append(_lib().msa_append_kv_prefill, k, v, kv, block_table, seq_lens, k.shape[0],
+    return _append(_lib().msa_append_kv_prefill, k, v, kv, block_table, seq_lens, tokens,
                    cu_seqlens_q, None, k_scale, v_scale, kv_scales, cos_sin, interleaved, q, q_out,
                    q_scale, stream)
 

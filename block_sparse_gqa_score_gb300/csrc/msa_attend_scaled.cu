@@ -20,16 +20,22 @@
 // tile's product.
 //   warp 0       page lists, scales, TMA of K tiles
 //   warp 1       S^T products (and owns tensor memory)
-//   warp 2       TMA of V tiles
+//   warp 2       TMA of V tiles; sets the value rows that a token does not see to 0
 //   warp 3       O^T products
 //   warps 4..    softmax and output, four a group: a thread owns one key, a group
 //                a token's 16 heads (kNT = 4) or half of them (kNT = 1).  A step
 //                takes two pages.
 //
-// What bounds it: bytes from HBM in decode, from L2 in prefill; the pages of a
-// short call are cut over the CTAs of a cluster (kNT = 1), which merge their
-// parts through distributed shared memory, so that a small batch needs neither
+// The pages of a short call are cut over the CTAs of a cluster (kNT = 1), which merge
+// their parts through distributed shared memory, so that a small batch needs neither
 // a workspace nor a second kernel.
+//
+// What bounds it, measured (64 query heads, 4 KV heads): lists of batch 16, 4 tokens,
+// 8k-32k: 27 us, 4.1 TB/s of its pages; start, lists and pages one behind the other, a
+// call of 2 rows already takes 11 us.  Dense decode of one token over 262144: 57 us,
+// 4.7 TB/s; the first tile is asked for after 4.5 us, behind the assignment.  Dense
+// decode of batch 16, 4 tokens, 8k-32k: 99 us, 3.4 TB/s: the softmax warps' chain of
+// waits, 1.2 us a page, on the CTA with the most pages (84, the average is 67).
 #include <cstddef>
 
 #include "msa_dense_slot.cuh"
@@ -465,163 +471,165 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
   const uint32_t tmem = tail->tmem_base;
 
   if (warp < 4) {
-  if constexpr (kNT > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-  if (warp == 0 || warp == 2) {
-    // ---- TMA producers: K tiles (warp 0, with the scales), V tiles (warp 2) ----------------
-    const bool is_k = warp == 0;
-    uint64_t* full = is_k ? tail->k_full : tail->v_full;
-    uint64_t* empty = is_k ? tail->k_empty : tail->v_empty;
-    if (is_k) {
-      // the first pages' scales, which the softmax waits for, have arrived meanwhile
-      if (kMode == kDense || blk_next >= 0) tail->info[slot] = next_info();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&tail->info_full[0]);
-    }
-    int issued = min(n_pages, kSlots);
-    bool ok = true;
-    // dense decode, chunk by chunk: a chunk's pages are looked up when the one before
-    // it begins and their scales when it is half through
-    int pg = pg_next;
-    // warp 2: tile t, of block blk, has landed on v_land[e]
-    auto settle = [&](int e, int t, int blk) {
-      const bool landed = __all_sync(0xffffffffu, wait_for(&tail->v_land[e], 0));
-      ok = ok && landed;
-      if (!landed) return;
-      uint8_t* tile = smem + Sm::kV + t % kSlots * kHalfTile;
-      if constexpr (kNT > 1)
-        nan_values(tile, first_pos - blk * kPage, last_pos - blk * kPage, blk, tail, lane);
-      zero_value_rows(tile, last_pos - blk * kPage, lane);
-      tc::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&tail->v_full[t % kSlots]);
-    };
-    if (kMode != kDense && !is_k && tail->edge) settle(0, 0, last_pos / kPage);
-    if (kMode == kDense && kChunk < n_pages) look_up(kChunk + lane);
-    for (int t = kSlots; t < n_pages && ok; ++t) {
-      int page;
-      if constexpr (kMode == kDense) {
-        if (is_k && t % kChunk == kChunk / 2) look_up_scales();
-        if (t % kChunk == 0) {
-          pg = pg_next;
-          if (is_k) {
-            // its half of `info` was last read two chunks ago: the K slots passed on
-            // since say that the softmax is past it
-            tail->info[t % (2 * kChunk) + lane] = next_info();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&tail->info_full[(t / kChunk) & 1]);
-          }
-          if (t + kChunk < n_pages) look_up(t + kChunk + lane);
-        }
-        page = __shfl_sync(0xffffffffu, pg, t % kChunk);
-      } else {
-        page = tail->pages[t];
+    // kNT = 4: 32 registers a thread from these four warps to 8 of each softmax thread
+    // (96 at launch; the sum stays): 115 us -> 101 for batch 16 over 8k-32k
+    if constexpr (kNT > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == 0 || warp == 2) {
+      // ---- TMA producers: K tiles (warp 0, with the scales), V tiles (warp 2) ----------------
+      const bool is_k = warp == 0;
+      uint64_t* full = is_k ? tail->k_full : tail->v_full;
+      uint64_t* empty = is_k ? tail->k_empty : tail->v_empty;
+      if (is_k) {
+        // the first pages' scales, which the softmax waits for, have arrived meanwhile
+        if (kMode == kDense || blk_next >= 0) tail->info[slot] = next_info();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tail->info_full[0]);
       }
-      if (!wait_for(&empty[t % kSlots], ((t / kSlots) - 1) & 1)) ok = false;
-      ok = __all_sync(0xffffffffu, ok);
-      if (ok) {
-        if (lane == 0) {
-          if (is_k) load_k(t, page);
-          else load_v(t, page, kMode == kDense ? edge_of(lo + t) : -1);
-        }
-        issued = t + 1;
-      }
-    }
-    if (kMode == kDense && !is_k) {
-      // the last tiles, all loads of this CTA on their way
-      for (int e = 0; e < 2; ++e) {
-        const int blk = first_pos / kPage + e, t = blk - lo;
-        if (t >= 0 && t < issued && edge_of(blk) == e) settle(e, t, blk);
-      }
-    }
-    if (lane == 0) {
-      if (kNT > 1 && !is_k) mbar_arrive(&tail->v_edges);
-      if (!ok) flag_error(p.err, MSA_ERR_TIMEOUT);
-      // the loads still in flight land before shared memory can be released
-      for (int t = max(0, issued - kSlots); t < issued; ++t)
-        (void)wait_for(&full[t % kSlots], (t / kSlots) & 1);
-      if (!is_k) pdl_trigger();
-      mbar_arrive(&tail->finish);
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ---- S^T = K Q^T, a batch of pages a buffer --------------------------------------------
-    if (lane == 0) {
-      const uint64_t a0 = tc::sw128_kmajor_desc(smem_u32(smem));
-      const uint64_t bq = tc::sw128_kmajor_desc(smem_u32(qtile));
-      constexpr uint32_t idesc = tc::idesc_e4m3_f32(128, kSN);
+      int issued = min(n_pages, kSlots);
       bool ok = true;
-      for (int t0 = 0, n = 0; t0 < n_pages && ok; t0 += kBatch, ++n) {
-        const int buf = n & 1;
-        ok = n < 2 || wait_for(&tail->s_empty[buf], ((n >> 1) - 1) & 1);
-        for (int t = t0; t < min(t0 + kBatch, n_pages) && ok; ++t) {
-          const int s = t % kSlots;
-          ok = wait_for(&tail->k_full[s], (t / kSlots) & 1);
-          if (!ok) break;
-          tc::fence_after_thread_sync();
-          const uint64_t a = a0 + static_cast<uint64_t>(s) * (kHalfTile >> 4);
-          const uint32_t d = tmem + kSN * (kBatch * buf + t - t0);
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks) tc::mma_e4m3(d, a + 2 * ks, bq + 2 * ks, idesc, ks > 0);
-          if constexpr (kFold) {
-            constexpr uint64_t kLo = (kGroup * kNT * 128) >> 4;   // the lo rows
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              tc::mma_e4m3(d, a + 2 * ks, bq + kLo + 2 * ks, idesc, 1);
-          }
-          tc::commit(&tail->k_empty[s]);
-        }
-        if (ok) tc::commit(&tail->s_full[buf]);
-      }
-      if (!ok) flag_error(p.err, MSA_ERR_TIMEOUT);
-      tc::commit(&tail->finish);
-    }
-    __syncwarp();
-    // free tensor memory once every role is done with it
-    (void)mbar_wait(&tail->finish, 0);
-    tc::fence_after_thread_sync();
-    tc::tmem_dealloc(tmem, kTmemCols);
-  } else {
-    // ---- O^T += V^T P^T ----------------------------------------------------------------------
-    if (lane == 0) {
-      const uint64_t a0 = tc::sw128_mnmajor_desc(smem_u32(smem + Sm::kV));
-      // B: each token's 16 hi heads, then its 16 lo ones 128 bytes further; 8-key
-      // blocks kPBlock apart
-      const uint64_t b0 = tc::interleave_mnmajor_desc(smem_u32(pbuf), Sm::kPBlock, 128);
-      constexpr uint32_t idesc = tc::idesc_e4m3_f32_mn(128, 32 * kNT);
-      bool ok = true;
-      uint32_t acc = 0;   // there has been a product
-      for (int t0 = 0, n = 0; t0 < n_pages && ok; t0 += kBatch, ++n) {
-        // pages of bad scales have no product (read before the wait for P)
-        if (t0 % kChunk == 0) ok = wait_for(&tail->info_full[(t0 / kChunk) & 1], (t0 / (2 * kChunk)) & 1);
-        bool bad[kBatch];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) bad[i] = tail->info[(t0 + i) % (2 * kChunk)].block < 0;
-        ok = ok && wait_for(&tail->p_full, n & 1);
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int t = t0 + i, s = t % kSlots;
-          if (t >= n_pages || !ok) break;
-          ok = wait_for(&tail->v_full[s], (t / kSlots) & 1);
-          if (!ok) break;
-          tc::fence_after_thread_sync();
-          const uint64_t a = a0 + static_cast<uint64_t>(s) * (kHalfTile >> 4);
-          const uint64_t bp = b0 + static_cast<uint64_t>(((t - t0) * Sm::kPBuf) >> 4);
-          if (!bad[i]) {
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              tc::mma_e4m3(tmem + kColAcc, a + 256 * kk, bp + ((4 * Sm::kPBlock) >> 4) * kk, idesc, acc);
-              acc = 1;
+      // dense decode, chunk by chunk: a chunk's pages are looked up when the one before
+      // it begins and their scales when it is half through
+      int pg = pg_next;
+      // warp 2: tile t, of block blk, has landed on v_land[e]
+      auto settle = [&](int e, int t, int blk) {
+        const bool landed = __all_sync(0xffffffffu, wait_for(&tail->v_land[e], 0));
+        ok = ok && landed;
+        if (!landed) return;
+        uint8_t* tile = smem + Sm::kV + t % kSlots * kHalfTile;
+        if constexpr (kNT > 1)
+          nan_values(tile, first_pos - blk * kPage, last_pos - blk * kPage, blk, tail, lane);
+        zero_value_rows(tile, last_pos - blk * kPage, lane);
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tail->v_full[t % kSlots]);
+      };
+      if (kMode != kDense && !is_k && tail->edge) settle(0, 0, last_pos / kPage);
+      if (kMode == kDense && kChunk < n_pages) look_up(kChunk + lane);
+      for (int t = kSlots; t < n_pages && ok; ++t) {
+        int page;
+        if constexpr (kMode == kDense) {
+          if (is_k && t % kChunk == kChunk / 2) look_up_scales();
+          if (t % kChunk == 0) {
+            pg = pg_next;
+            if (is_k) {
+              // its half of `info` was last read two chunks ago: the K slots passed on
+              // since say that the softmax is past it
+              tail->info[t % (2 * kChunk) + lane] = next_info();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&tail->info_full[(t / kChunk) & 1]);
             }
+            if (t + kChunk < n_pages) look_up(t + kChunk + lane);
           }
-          tc::commit(&tail->v_empty[s]);
+          page = __shfl_sync(0xffffffffu, pg, t % kChunk);
+        } else {
+          page = tail->pages[t];
         }
-        if (ok) tc::commit(&tail->o_done);
+        if (!wait_for(&empty[t % kSlots], ((t / kSlots) - 1) & 1)) ok = false;
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+          if (lane == 0) {
+            if (is_k) load_k(t, page);
+            else load_v(t, page, kMode == kDense ? edge_of(lo + t) : -1);
+          }
+          issued = t + 1;
+        }
       }
-      if (!ok) flag_error(p.err, MSA_ERR_TIMEOUT);
-      tc::commit(&tail->finish);
+      if (kMode == kDense && !is_k) {
+        // the last tiles, all loads of this CTA on their way
+        for (int e = 0; e < 2; ++e) {
+          const int blk = first_pos / kPage + e, t = blk - lo;
+          if (t >= 0 && t < issued && edge_of(blk) == e) settle(e, t, blk);
+        }
+      }
+      if (lane == 0) {
+        if (kNT > 1 && !is_k) mbar_arrive(&tail->v_edges);
+        if (!ok) flag_error(p.err, MSA_ERR_TIMEOUT);
+        // the loads still in flight land before shared memory can be released
+        for (int t = max(0, issued - kSlots); t < issued; ++t)
+          (void)wait_for(&full[t % kSlots], (t / kSlots) & 1);
+        if (!is_k) pdl_trigger();
+        mbar_arrive(&tail->finish);
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ---- S^T = K Q^T, a batch of pages a buffer --------------------------------------------
+      if (lane == 0) {
+        const uint64_t a0 = tc::sw128_kmajor_desc(smem_u32(smem));
+        const uint64_t bq = tc::sw128_kmajor_desc(smem_u32(qtile));
+        constexpr uint32_t idesc = tc::idesc_e4m3_f32(128, kSN);
+        bool ok = true;
+        for (int t0 = 0, n = 0; t0 < n_pages && ok; t0 += kBatch, ++n) {
+          const int buf = n & 1;
+          ok = n < 2 || wait_for(&tail->s_empty[buf], ((n >> 1) - 1) & 1);
+          for (int t = t0; t < min(t0 + kBatch, n_pages) && ok; ++t) {
+            const int s = t % kSlots;
+            ok = wait_for(&tail->k_full[s], (t / kSlots) & 1);
+            if (!ok) break;
+            tc::fence_after_thread_sync();
+            const uint64_t a = a0 + static_cast<uint64_t>(s) * (kHalfTile >> 4);
+            const uint32_t d = tmem + kSN * (kBatch * buf + t - t0);
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) tc::mma_e4m3(d, a + 2 * ks, bq + 2 * ks, idesc, ks > 0);
+            if constexpr (kFold) {
+              constexpr uint64_t kLo = (kGroup * kNT * 128) >> 4;   // the lo rows
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                tc::mma_e4m3(d, a + 2 * ks, bq + kLo + 2 * ks, idesc, 1);
+            }
+            tc::commit(&tail->k_empty[s]);
+          }
+          if (ok) tc::commit(&tail->s_full[buf]);
+        }
+        if (!ok) flag_error(p.err, MSA_ERR_TIMEOUT);
+        tc::commit(&tail->finish);
+      }
+      __syncwarp();
+      // free tensor memory once every role is done with it
+      (void)mbar_wait(&tail->finish, 0);
+      tc::fence_after_thread_sync();
+      tc::tmem_dealloc(tmem, kTmemCols);
+    } else {
+      // ---- O^T += V^T P^T ----------------------------------------------------------------------
+      if (lane == 0) {
+        const uint64_t a0 = tc::sw128_mnmajor_desc(smem_u32(smem + Sm::kV));
+        // B: each token's 16 hi heads, then its 16 lo ones 128 bytes further; 8-key
+        // blocks kPBlock apart
+        const uint64_t b0 = tc::interleave_mnmajor_desc(smem_u32(pbuf), Sm::kPBlock, 128);
+        constexpr uint32_t idesc = tc::idesc_e4m3_f32_mn(128, 32 * kNT);
+        bool ok = true;
+        uint32_t acc = 0;   // there has been a product
+        for (int t0 = 0, n = 0; t0 < n_pages && ok; t0 += kBatch, ++n) {
+          // pages of bad scales have no product (read before the wait for P)
+          if (t0 % kChunk == 0) ok = wait_for(&tail->info_full[(t0 / kChunk) & 1], (t0 / (2 * kChunk)) & 1);
+          bool bad[kBatch];
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) bad[i] = tail->info[(t0 + i) % (2 * kChunk)].block < 0;
+          ok = ok && wait_for(&tail->p_full, n & 1);
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int t = t0 + i, s = t % kSlots;
+            if (t >= n_pages || !ok) break;
+            ok = wait_for(&tail->v_full[s], (t / kSlots) & 1);
+            if (!ok) break;
+            tc::fence_after_thread_sync();
+            const uint64_t a = a0 + static_cast<uint64_t>(s) * (kHalfTile >> 4);
+            const uint64_t bp = b0 + static_cast<uint64_t>(((t - t0) * Sm::kPBuf) >> 4);
+            if (!bad[i]) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) {
+                tc::mma_e4m3(tmem + kColAcc, a + 256 * kk, bp + ((4 * Sm::kPBlock) >> 4) * kk, idesc, acc);
+                acc = 1;
+              }
+            }
+            tc::commit(&tail->v_empty[s]);
+          }
+          if (ok) tc::commit(&tail->o_done);
+        }
+        if (!ok) flag_error(p.err, MSA_ERR_TIMEOUT);
+        tc::commit(&tail->finish);
+      }
+      __syncwarp();
     }
-    __syncwarp();
-  }
   } else {
     if constexpr (kNT > 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     // ---- group gi: kH heads of token j ------------------------------------------------------

@@ -538,7 +538,9 @@ int msa_append_kv_prefill(const void *k, int64_t k_stride, const void *v, int64_
  * page's logits in fp32; the V scale enters the softmax reference, so that the
  * fp8 probabilities of a page are relative to its values' size (about 8
  * significant bits of P for every page whose P * V scale is within 2^-17 of the
- * largest).  Errors: as without the suffix, plus null or not 8-byte aligned
+ * largest).  A NaN logit makes its head's output NaN and a NaN value its dim, of
+ * the tokens that see the key and of no other (with the union tile a NaN value
+ * reaches all tokens of a tile).  Errors: as without the suffix, plus null or not 8-byte aligned
  * kv_scales (4-byte for a K-only cache) (MSA_EINVAL).  Device: MSA_ERR_SCALE (a
  * listed or visible page with a scale out of range, either side for the
  * attends, K's for the scorer: the page is skipped, its score is -inf).

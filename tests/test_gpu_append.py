@@ -333,4 +333,8 @@ def test_python_refusals():
             call(**kw)
     with pytest.raises(msa.MSAError):
         call(k_scale=0.0)
+    cu = torch.tensor([0, 2, 4], dtype=torch.int32, device=DEV)
+    for k, sl in ((None, c["lens"]), (c["k"], [300, 20])):
+        with pytest.raises(TypeError):
+            msa.append_kv_prefill(k, c["v"], c["kv"], c["bt"], sl, cu, kv_scales=c["sc"])
     assert msa.get_error() == 0
