@@ -226,7 +226,7 @@ def _source_digest(*names) -> str:
 
 
 KERNEL_SOURCES = {"attend": ("msa_attend.cu", "msa_union.cu", "msa_device.cuh", "msa_tcgen05.cuh",
-                             "msa_launch.h", "msa_select.cuh"),
+                             "msa_launch.h", "msa_select.cuh", "msa_dense_slot.cuh"),
                   "score": ("msa_score.cu", "msa_device.cuh", "msa_tcgen05.cuh", "msa_launch.h"),
                   "topk": ("msa_topk.cu", "msa_device.cuh", "msa_launch.h", "msa_select.cuh")}
 
