@@ -34,7 +34,7 @@
 // 8k-32k: 27 us, 4.1 TB/s of its pages; start, lists and pages one behind the other, a
 // call of 2 rows already takes 11 us.  Dense decode of one token over 262144: 57 us,
 // 4.7 TB/s; the first tile is asked for after 4.5 us, behind the assignment.  Dense
-// decode of batch 16, 4 tokens, 8k-32k: 99 us, 3.4 TB/s: the softmax warps' chain of
+// decode of batch 16, 4 tokens, 8k-32k: 98 us, 3.5 TB/s: the softmax warps' chain of
 // waits, 1.2 us a page, on the CTA with the most pages (84, the average is 67).
 #include <cstddef>
 

@@ -145,6 +145,30 @@ __device__ __forceinline__ void split_p(float a, float b, float c, float d, uint
       : "f"(a), "f"(b), "f"(c), "f"(d));
 }
 
+// a + b and a * b + c of two neighbouring values in one instruction, each rounded as by
+// the scalar one (the warps' issue slots are 60 % taken: 278 -> 269 us for 1536 prefill
+// tokens).
+__device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%2, %3};\n\t"
+      "mov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 x, x, y;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b, float c0,
+                                     float c1) {
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%2, %3};\n\t"
+      "mov.b64 y, {%4, %4};\n\t"
+      "mov.b64 z, {%5, %6};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b), "f"(c0), "f"(c1));
+}
+
 // One thread's share of a group's softmax: key (and at the end value dim) `key` of kH
 // heads.  kSCols: S^T columns of one token, 32 where the query's hi and lo parts are
 // added here; page_cols: columns of one page's S^T, page_p: bytes of its P^T.
@@ -196,8 +220,9 @@ struct PageSoftmax {
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
 #pragma unroll
-          for (int h = 0; h < kH; ++h)
-            t[i][h] = __uint_as_float(sv[i][h]) + __uint_as_float(sl[i][h]);
+          for (int h = 0; h < kH; h += 2)
+            add2(t[i][h], t[i][h + 1], __uint_as_float(sv[i][h]), __uint_as_float(sv[i][h + 1]),
+                 __uint_as_float(sl[i][h]), __uint_as_float(sl[i][h + 1]));
       } else {
         tc::wait_ld();
 #pragma unroll
@@ -219,13 +244,14 @@ struct PageSoftmax {
       if (there && in.lv != lv) {    // the same in every thread
         const float d = in.lv - lv;
 #pragma unroll
-        for (int h = 0; h < kH; ++h) nl[h] += d;
+        for (int h = 0; h < kH; h += 2) add2(nl[h], nl[h + 1], nl[h], nl[h + 1], d, d);
         lv = in.lv;
       }
       iv[i] = there ? in.iv : 0.f;
       lim[i] = !there || in.block < 0 ? -1 : pos - in.block * kPage;
 #pragma unroll
-      for (int h = 0; h < kH; ++h) t[i][h] = fmaf(t[i][h], zt, nl[h]);
+      for (int h = 0; h < kH; h += 2)
+        fma2(t[i][h], t[i][h + 1], t[i][h], t[i][h + 1], zt, nl[h], nl[h + 1]);
       if (lim[i] < kPage - 1 && key > lim[i]) {
 #pragma unroll
         for (int h = 0; h < kH; ++h) t[i][h] = -INFINITY;
@@ -267,14 +293,15 @@ struct PageSoftmax {
         free_p = true;
         tc::fence_after_thread_sync();
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {   // the hi columns, then the lo ones
-          uint32_t av[kH];
-          ld_cols(acc_addr + kGroup * part, av);
+        for (int c = 0; c < 2 * kH; c += 8) {   // the hi columns, then the lo ones
+          const uint32_t at = acc_addr + c % kH + kGroup * (c / kH);
+          uint32_t av[8];
+          ld_cols(at, av);
           tc::wait_ld();
 #pragma unroll
-          for (int h = 0; h < kH; ++h)
-            av[h] = __float_as_uint(__uint_as_float(av[h]) * __shfl_sync(0xffffffffu, al_h, h));
-          st_cols(acc_addr + kGroup * part, av);
+          for (int h = 0; h < 8; ++h)
+            av[h] = __float_as_uint(__uint_as_float(av[h]) * __shfl_sync(0xffffffffu, al_h, c % kH + h));
+          st_cols(at, av);
         }
         tc::wait_st();
         stored = true;
@@ -288,9 +315,11 @@ struct PageSoftmax {
       for (int q4 = 0; q4 < kH / 4; ++q4) {
         float* e = &t[i][4 * q4];
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          e[h] = ex2(e[h]);             // P; 0 for an invisible key
-          l[4 * q4 + h] = fmaf(e[h], iv[i], l[4 * q4 + h]);
+        for (int h = 0; h < 4; ++h) e[h] = ex2(e[h]);   // P; 0 for an invisible key
+#pragma unroll
+        for (int h = 0; h < 4; h += 2) {
+          float* lh = &l[4 * q4 + h];
+          fma2(lh[0], lh[1], e[h], e[h + 1], iv[i], lh[0], lh[1]);
         }
         split_p(e[0], e[1], e[2], e[3], hw[i][q4], lw[i][q4]);
       }
