@@ -373,6 +373,35 @@ def test_step_with_the_union_tile(Q, S):
     assert msa.get_error() == 0
 
 
+@pytest.mark.parametrize("Q,q8", [(1, False), (3, True)])
+def test_selection_of_long_rows(Q, q8):
+    """Selecting attends over rows of 700 to 8200 blocks: the lists of topk and the
+    output of the attend on them, decode and prefill."""
+    c = _inputs([PAGE * 40, 3], [Q] * 2, 2, 64, q8=q8, nan=False)
+    lens = torch.tensor([8200 * PAGE - 5, 700 * PAGE + 1], dtype=torch.int32, device=DEV)
+    S = 8200
+    gen = torch.Generator().manual_seed(65)
+    bt = torch.randint(0, 40, (2, S), generator=gen).to(torch.int32).to(DEV)
+    s = torch.randn((2, 2 * Q, S), generator=gen).to(DEV)
+    kw = dict(kv_scales=c["sc"], q_scale=c["qs"])
+    tk = msa.topk(s, lens, Q)
+    out = msa.sparse_decode(c["q"], c["kv"], bt, lens, tk, Q, SM, 1.1, 0.9, **kw)
+    cu = torch.arange(3, dtype=torch.int32, device=DEV) * Q
+    for splits in (0, 3):
+        tk2, out2 = msa.sparse_decode_select(c["q"], c["kv"], bt, lens, s, Q, SM, 1.1, 0.9,
+                                             num_splits=splits, **kw)
+        tk3, out3 = msa.sparse_prefill_select(c["q"], c["kv"], bt, lens, cu, s, SM, 1.1, 0.9,
+                                              num_splits=splits, **kw)
+        assert torch.equal(tk, tk2) and torch.equal(tk, tk3) and torch.equal(out2, out3)
+        if splits == 0:
+            assert torch.equal(out, out2)
+    ref = dict(c, bt=bt, seq_lens=lens.tolist())
+    o, bound, _ = _ref(ref, tk, 1.1, 0.9)
+    check_attend(out, o, bound)
+    check_attend(out2, o, bound)
+    assert msa.get_error() == 0
+
+
 @pytest.mark.parametrize("B,Q", [(300, 1), (270, 2), (260, 5)])
 def test_dense_decode_of_large_batches(B, Q):
     """More requests than the shared-out assignment takes."""
