@@ -21,7 +21,7 @@
 // issued from a branch inside a loop of the whole warp, the query descriptor that
 // reached the tensor core was wrong.)
 //
-// Measured: 269 us for those 1536 tokens (334 with a CTA a row), 12.0 TB/s of pages out
+// Measured: 268 us for those 1536 tokens (334 with a CTA a row), 12.0 TB/s of pages out
 // of L2; what bounds it is the softmax warps' chain of waits, 16 of them an SM issuing
 // an instruction every two cycles, not a pipe: without the loads it takes 5 % less.
 #include <cstddef>
