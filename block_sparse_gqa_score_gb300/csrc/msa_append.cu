@@ -23,6 +23,10 @@
 // CTA's eight warps read the page's up to 128 rows a second time, from L1 (held
 // in registers they halved the CTAs an SM, which the query rows of the same
 // launch paid for: 313 us for 28779 tokens of 64/4 heads).
+//
+// Measured (64/4 heads): 28779 tokens with page scales 182 us, 5.7 TB/s, 84 % of a copy's
+// rate; 6000 tokens with one scale 41 us, 77 %; 128 single tokens 8 us, launch and four
+// dependent loads.
 #include "msa_device.cuh"
 #include "msa_launch.h"
 

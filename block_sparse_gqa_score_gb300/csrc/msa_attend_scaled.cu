@@ -24,7 +24,7 @@
 //   warp 3       O^T products
 //   warps 4..    softmax and output, four a group: a thread owns one key, a group
 //                a token's 16 heads (kNT = 4) or half of them (kNT = 1).  A step
-//                takes two pages.
+//                takes a page (kNT = 4) or two.
 //
 // The pages of a short call are cut over the CTAs of a cluster (kNT = 1), which merge
 // their parts through distributed shared memory, so that a small batch needs neither

@@ -11,7 +11,7 @@
 // over 8k-32k tokens.
 //   warp 0       lists, scales, query parts, TMA of K tiles
 //   warp 1       S^T products (and owns tensor memory)
-//   warp 2       TMA of V tiles
+//   warp 2       TMA of V tiles; sets the value rows that the token does not see to 0
 //   warp 3       O^T products
 //   warps 4..11  softmax and output, two groups of four warps, eight heads each
 // A row is an item; an item's pages and scales are in one of two places, filled by
@@ -22,8 +22,8 @@
 // reached the tensor core was wrong.)
 //
 // Measured: 268 us for those 1536 tokens (334 with a CTA a row), 12.0 TB/s of pages out
-// of L2; what bounds it is the softmax warps' chain of waits, 16 of them an SM issuing
-// an instruction every two cycles, not a pipe: without the loads it takes 5 % less.
+// of L2; what bounds it are the softmax warps, 16 of them an SM: 60 % of the issue slots,
+// the rest their chain of waits, and no pipe: without the loads it takes 5 % less.
 #include <cstddef>
 
 #include "msa_device.cuh"

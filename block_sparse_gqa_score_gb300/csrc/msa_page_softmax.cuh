@@ -11,7 +11,7 @@
 // of the query split), addend log2(vs) - M.  M is a running reference, not the
 // running maximum: P = 2^(kPShift) at the largest u when M is set, and M stays
 // until some P would pass 2^kPTop (e4m3 holds 448).  Whether it does is one vote
-// a page: the largest of a thread's 16 u against the bound, or-ed over the
+// a step: the largest of a thread's u against the bound, or-ed over the
 // token's four warps by one barrier; only then are the exact maxima of the 16
 // heads formed and exchanged and the sums and the accumulator rescaled.  (With
 // exact maxima on every page a warp issued about 650 instructions a page; the
