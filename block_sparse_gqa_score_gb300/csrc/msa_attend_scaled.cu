@@ -844,14 +844,17 @@ cudaError_t launch_attend_scaled(const CUtensorMap& kv_map, const AttendParams& 
   const int tiles = (p.Q + ntile - 1) / ntile;
   const int64_t units = dense ? static_cast<int64_t>(p.B) * tiles * p.Hkv
                               : static_cast<int64_t>(p.cu_q ? p.T : p.B * p.Q) * p.Hkv;
-  // The CTAs of a cluster cut a unit's part where that puts more of one wave's slots to
-  // use and leaves each a page or more (lists: 16 pages a row).
+  // The CTAs of a cluster cut a unit's part where that puts more CTAs to use and leaves
+  // each a page or more (lists: 16 pages a row).  Clusters count on one CTA an SM: a
+  // cluster that has to go second on its SMs starts 3.7 us later, a plain CTA 1.5 us (lists
+  // of 32 requests, 4 KV heads: 128 CTAs 20.5 us, 128 clusters of two 24.6; dense decode of
+  // 32768 tokens, 4 KV heads: 21.7 against 26.6; of 131072, one KV head: 26.4 against 26.0).
   const int pages = dense ? p.S : kTopK;
   int cs = 1;
   if (ntile == 1 && (dense || p.splits == 1)) {
     int64_t best = 0;
     for (int c = 1; c <= kMaxCluster && c <= pages; c *= 2) {
-      const int64_t parts = slots / c / units;   // clusters a unit can have
+      const int64_t parts = (c > 1 ? sms : slots) / c / units;   // clusters a unit can have
       const int64_t used = units * c * (parts < p.splits ? parts : p.splits);
       if (used > best) {
         best = used;
@@ -875,7 +878,7 @@ cudaError_t launch_attend_scaled(const CUtensorMap& kv_map, const AttendParams& 
   // dense decode: fewer units than slots share the slots out by their blocks
   // (dense_slot), up to `splits` parts a unit; else one part a unit
   if (p.splits > 1 && units < slots && p.B * tiles <= kBalancedTiles)
-    grid = dim3(static_cast<unsigned>(slots / cs * cs));
+    grid = dim3(static_cast<unsigned>((cs > 1 ? sms : slots) / cs * cs));
   else
     grid = dim3(static_cast<unsigned>(units * cs), p.splits);
   return p.q8 ? launch_dense<true>(kv_map, p, grid, cs, stream, pdl)
