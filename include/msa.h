@@ -536,9 +536,9 @@ int msa_append_kv_prefill(const void *k, int64_t k_stride, const void *v, int64_
  * > 0: fp8 e4m3 of value q * q_scale.  Scales are any numbers in [2^-40, 2^40]
  * (msa_append_kv writes powers of two).  Numerics: the K scale multiplies the
  * page's logits in fp32; the V scale enters the softmax reference, so that the
- * fp8 probabilities of a page are relative to its values' size (about 8
- * significant bits of P for every page whose P * V scale is within 2^-17 of the
- * largest).  A NaN logit makes its head's output NaN and a NaN value its dim, of
+ * fp8 probabilities of a page are relative to its values' size: P times the V
+ * scale is carried to 2^-8 of itself where it is within 2^-8.5 of the row's
+ * largest, to 2^-16.5 of that largest below.  A NaN logit makes its head's output NaN and a NaN value its dim, of
  * the tokens that see the key and of no other (with the union tile a NaN value
  * reaches all tokens of a tile).  Errors: as without the suffix, plus null or not 8-byte aligned
  * kv_scales (4-byte for a K-only cache) (MSA_EINVAL).  Device: MSA_ERR_SCALE (a

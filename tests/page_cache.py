@@ -176,10 +176,12 @@ def attend64(q, kv, scales, block_table, seq_lens, q_lens, sm, k_scale, v_scale,
     """(out, bound, scores) in 64 bits on the tensors' device: softmax attention
     of every token over its listed (or all) visible blocks with page scales, and
     the error the kernels' arithmetic allows each output element:
-      P as fp16 and two e4m3 parts: 2^-8 + 2^-11 of each term; a term below
-        2^-9.5 of the largest may have P < 2^-2 (P >= 2^7.5 at the largest: the
-        reference trails the maximum by half a binade), whose lo part is an e4m3
-        subnormal: 2^-10 of P there, 2^-17.5 of the largest term, or all of it;
+      P as fp16 and two e4m3 parts: 2^-8 + 2^-11 of each term.  hi is at most 2^-4 P
+        off, so |lo| <= 2^-4 P, and lo is off by 2^-4 |lo| <= 2^-8 P or, as an e4m3
+        subnormal (steps of 2^-9), by 2^-10, which is more only where P < 2^-2.  P is
+        2^6.5 at the row's largest term when the reference is set there and never less
+        than that at a largest seen later, so P < 2^-2 is a term below 2^-8.5 of the
+        largest and 2^-10 is 2^-16.5 of it (or all of the term);
       logits in 32 bits: |z| 2^-19 or so in the exponent;
       the bf16 query's hi + lo parts: 2^-18 of the row's largest element;
       the output's rounding to bf16: 2^-8.
@@ -226,7 +228,7 @@ def attend64(q, kv, scales, block_table, seq_lens, q_lens, sm, k_scale, v_scale,
                 # weights of the product with V8, and the largest of each row
                 w = p * vs.repeat_interleave(PAGE)
                 top = w.amax(dim=1, keepdim=True)
-                small = torch.where(w < 2.0 ** -9.5 * top, torch.minimum(2 * w, 2.0 ** -17.5 * top), 0.0)
+                small = torch.where(w < 2.0 ** -8.5 * top, torch.minimum(2 * w, 2.0 ** -16.5 * top), 0.0)
                 floor = small @ v8.flatten(0, 1).abs()
                 bound[tok, h] = ((2.0 ** -8 + 2.0 ** -11 + 2 * (zmax * 2.0 ** -19 + qerr)) * size
                                  + floor + HALF_BF16 * out[tok, h].abs())
