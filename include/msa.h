@@ -537,10 +537,12 @@ int msa_append_kv_prefill(const void *k, int64_t k_stride, const void *v, int64_
  * (msa_append_kv writes powers of two).  Numerics: the K scale multiplies the
  * page's logits in fp32; the V scale enters the softmax reference, so that the
  * fp8 probabilities of a page are relative to its values' size: P times the V
- * scale is carried to 2^-8 of itself where it is within 2^-8.5 of the row's
- * largest, to 2^-16.5 of that largest below.  A NaN logit makes its head's output NaN and a NaN value its dim, of
- * the tokens that see the key and of no other (with the union tile a NaN value
- * reaches all tokens of a tile).  Errors: as without the suffix, plus null or not 8-byte aligned
+ * scale is carried to 2^-8 of itself, or to 2^-19.5 of the row's largest where
+ * that is more, with errors that cancel over a page's keys: rows of 262144 keys
+ * beside a dominant one are within 2^-7 of sum p |v|, rounding to bf16 included.
+ * A NaN logit makes its head's output NaN and a NaN value its dim, of the tokens
+ * that see the key and of no other (with the union tile a NaN value reaches all
+ * tokens of a tile).  Errors: as without the suffix, plus null or not 8-byte aligned
  * kv_scales (4-byte for a K-only cache) (MSA_EINVAL).  Device: MSA_ERR_SCALE (a
  * listed or visible page with a scale out of range, either side for the
  * attends, K's for the scorer: the page is skipped, its score is -inf).

@@ -1,0 +1,127 @@
+"""Attention over page scales on rows where one key holds much of the weight and a long
+tail of small ones the rest, of values with a mean: what a tail loses does not average
+out.  Held to a bound that comes from what an output may be off by, not from how the
+kernels hold a probability: 2^-8 of the terms for bf16's rounding, and as much again."""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+import block_sparse_gqa_score_gb300 as msa
+from tests.page_cache import D, F8, GROUP, PAGE
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+SM = D ** -0.5
+BOUND = 2.0 ** -7
+
+
+@pytest.fixture(autouse=True)
+def _clean_error_word():
+    msa.get_error(clear=True)
+    yield
+    assert msa.get_error() == 0
+
+
+def _batch(keys, weight, spread, B, Q, Hkv, sink=0, q8=False, seed=0):
+    """B equal requests over the same pages.  The key at `sink` has about `weight` of every
+    row; the others' logits are 0 with a deviation of `spread` nats."""
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+    n = -(-keys // PAGE)
+    kv = torch.zeros((n, Hkv, PAGE, 2 * D), dtype=torch.float32, device=DEV)
+    kv[..., 1:D] = torch.randn((n, Hkv, PAGE, D - 1), generator=gen, device=DEV) * 110
+    kv[..., D:] = (1 + 0.3 * torch.randn((n, Hkv, PAGE, D), generator=gen, device=DEV)) * 100
+    kv[..., 0] = 0
+    at = torch.randperm(n, generator=gen, device=DEV).to(torch.int32)   # logical -> page
+    home = int(at[sink // PAGE])
+    kv[home, :, sink % PAGE, :D] = 0
+    kv[home, :, sink % PAGE, 0] = 256
+    sc = torch.full((n, Hkv, 2), 2.0 ** -8, device=DEV)
+    sc[..., 1] = torch.exp2(torch.randint(-9, -6, (n, Hkv), generator=gen, device=DEV).float())
+    # logits: SM * 2^-8 * q . K8
+    z = math.log(weight / (1 - weight)) + math.log(keys) + spread ** 2 / 2
+    q = torch.zeros((Q, GROUP * Hkv, D), device=DEV)
+    q[..., 1:] = torch.randn((Q, GROUP * Hkv, D - 1), generator=gen, device=DEV) * (
+        spread / (SM * 2.0 ** -8 * 110 * math.sqrt(D - 1)))
+    q[..., 0] = z / SM
+    qs = 1.0
+    if q8:
+        qs = 0.5
+        q = (q / qs).clamp(-448, 448).to(F8)
+    else:
+        q = q.to(torch.bfloat16)
+    return dict(q=q.repeat(B, 1, 1), kv=kv.clamp(-448, 448).to(F8).view(torch.uint8), sc=sc,
+                bt=at.repeat(B, 1).contiguous(), qs=qs, Q=Q, B=B, Hkv=Hkv,
+                lens=torch.full((B,), keys, dtype=torch.int32, device=DEV))
+
+
+def _want(c):
+    """(out, sum of p |v|) of the first request in 64 bits."""
+    Q, L, Hkv = c["Q"], int(c["lens"][0]), c["Hkv"]
+    out = torch.zeros((Q, GROUP * Hkv, D), dtype=torch.float64, device=DEV)
+    size = torch.zeros_like(out)
+    pages = c["bt"][0].long()
+    pos = torch.arange(L - Q, L, device=DEV)
+    for g in range(Hkv):
+        kv = c["kv"].view(F8)[pages, g].float()
+        k = (kv[..., :D].double() * c["sc"][pages, g, 0].double()[:, None, None]).flatten(0, 1)
+        v = (kv[..., D:].double() * c["sc"][pages, g, 1].double()[:, None, None]).flatten(0, 1)
+        q = c["q"][:Q, GROUP * g:GROUP * (g + 1)].double() * c["qs"]
+        z = torch.einsum("qhd,kd->qhk", q, k) * SM
+        z.masked_fill_(torch.arange(k.shape[0], device=DEV) > pos[:, None, None], -math.inf)
+        p = torch.softmax(z, dim=2)
+        out[:, GROUP * g:GROUP * (g + 1)] = p @ v
+        size[:, GROUP * g:GROUP * (g + 1)] = p @ v.abs()
+    return out, size
+
+
+def _check(got, c):
+    got = got.view(c["B"], c["Q"], *got.shape[1:])
+    assert torch.equal(got, got[:1].expand_as(got))       # equal requests
+    out, size = _want(c)
+    off = ((got[0].double() - out).abs() / size).max()
+    assert off <= BOUND, float(off)
+
+
+def _sms():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+# keys, the first key's weight, spread of the others
+TAILS = [(32768, 0.5, 1.0), (32768, 0.8, 1.0), (32768, 0.5, 0.0), (131072, 0.3, 1.0),
+         (131072, 0.5, 1.0), (131072, 0.9, 0.0), (262144, 0.5, 1.0), (262144, 0.9, 0.0)]
+
+
+@pytest.mark.parametrize("keys,weight,spread", TAILS)
+@pytest.mark.parametrize("form", ["one_cta_q1", "one_cta_q4", "one_cta_q4_fp8", "clusters", "parts"])
+def test_dense_decode(form, keys, weight, spread):
+    Hkv = 4
+    # a row a CTA once the batch fills the GPU: two rows of one token an SM, a tile of more
+    B, Q = {"one_cta_q1": (-(-2 * _sms() // Hkv), 1), "clusters": (1, 1), "parts": (2, 3)}.get(
+        form, (-(-_sms() // Hkv), 4))
+    c = _batch(keys, weight, spread, B, Q, Hkv, q8=form.endswith("fp8"))
+    _check(msa.dense_decode(c["q"], c["kv"], c["bt"], c["lens"], Q, SM, kv_scales=c["sc"],
+                            q_scale=c["qs"]), c)
+
+
+@pytest.mark.parametrize("weight,spread", [(0.5, 1.0), (0.8, 0.0), (0.97, 1.0)])
+@pytest.mark.parametrize("form", ["cluster", "parts", "rows", "select", "prefill"])
+def test_lists(form, weight, spread):
+    """16 pages a row; the dominant key in the current block, which comes first."""
+    Hkv, keys = 4, 16 * PAGE
+    B, Q = {"cluster": (2, 1), "parts": (2, 3)}.get(form, (-(-2 * _sms() // Hkv) + 5, 1))
+    c = _batch(keys, weight, spread, B, Q, Hkv, sink=keys - 100)
+    a = (c["q"], c["kv"], c["bt"], c["lens"])
+    lists = torch.arange(16, dtype=torch.int32, device=DEV).repeat(B * Q, Hkv, 1)
+    kw = dict(kv_scales=c["sc"])
+    if form == "select":
+        scores = torch.zeros((Hkv, B * Q, 16), device=DEV)
+        got = msa.sparse_decode_select(*a, scores, Q, SM, **kw)[1]
+    elif form == "prefill":
+        cu = torch.arange(B + 1, dtype=torch.int32, device=DEV)
+        got = msa.sparse_prefill(*a, cu, lists, SM, **kw)
+    else:
+        got = msa.sparse_decode(*a, lists, Q, SM, num_splits=3 if form == "parts" else 0, **kw)
+    _check(got, c)
