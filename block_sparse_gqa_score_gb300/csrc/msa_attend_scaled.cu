@@ -496,8 +496,15 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
         ok = ok && landed;
         if (!landed) return;
         uint8_t* tile = smem + Sm::kV + t % kSlots * kHalfTile;
-        if constexpr (kNT > 1)
-          nan_values(tile, first_pos - blk * kPage, last_pos - blk * kPage, blk, tail, lane);
+        if constexpr (kNT > 1) {
+          // (not of a page that is not attended, which may be any page in the place of a
+          // bad table entry's; its info is there long before its tile's turn)
+          const bool known =
+              __all_sync(0xffffffffu, wait_for(&tail->info_full[(t / kChunk) & 1], (t / (2 * kChunk)) & 1));
+          ok = ok && known;
+          if (known && tail->info[t % (2 * kChunk)].block >= 0)
+            nan_values(tile, first_pos - blk * kPage, last_pos - blk * kPage, blk, tail, lane);
+        }
         zero_value_rows(tile, last_pos - blk * kPage, lane);
         tc::fence_proxy_async_smem();
         __syncwarp();
