@@ -15,11 +15,12 @@
 //   warp 3       O^T products
 //   warps 4..11  softmax and output, two groups of four warps, eight heads each
 // A row is an item; an item's pages and scales are in one of two places, filled by
-// warp 0 and freed by the softmax.  Pages, batches of pages and items are
-// counted on across rows, each role for itself, and give every barrier's slot and
-// phase.  Two CTAs an SM.  (The products are issued by code that one lane alone runs:
-// issued from a branch inside a loop of the whole warp, the query descriptor that
-// reached the tensor core was wrong.)
+// warp 0 and freed by its readers: the softmax and warps 2 and 3 (a row without pages has
+// no product that would show them to be past it), warp 1 by the end of its products.
+// Pages, batches of pages and items are counted on across rows, each role for itself, and
+// give every barrier's slot and phase.  Two CTAs an SM.  (The products are issued by code
+// that one lane alone runs: issued from a branch inside a loop of the whole warp, the
+// query descriptor that reached the tensor core was wrong.)
 //
 // Measured: 268 us for those 1536 tokens (334 with a CTA a row), 12.0 TB/s of pages out
 // of L2; what bounds it are the softmax warps, 16 of them an SM: 60 % of the issue slots,
@@ -64,7 +65,7 @@ struct Tail {
   uint64_t p_full, o_done;          // softmax <-> O^T, a batch at a time
   uint64_t q_free;                  // an item's S^T products complete
   uint64_t item_full[2];            // pages, scales and the query's tile are there
-  uint64_t item_empty[2];           // the softmax is through with the item
+  uint64_t item_empty[2];           // the softmax and warps 2 and 3 are through with the item
   uint64_t finish;
   uint32_t tmem_base;
   alignas(16) Item item[2];
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       mbar_init(&tail->s_full[s], 1);
       mbar_init(&tail->s_empty[s], 4 * kCount);
       mbar_init(&tail->item_full[s], 1);
-      mbar_init(&tail->item_empty[s], 4 * kCount);
+      mbar_init(&tail->item_empty[s], 4 * kCount + 2);
     }
     mbar_init(&tail->p_full, 4 * kCount);
     mbar_init(&tail->o_done, 1);
@@ -294,6 +295,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (lane == 0) mbar_arrive(&tail->v_full[s0]);
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tail->item_empty[i & 1]);
     }
     if (lane == 0) {
       if (!ok) flag_error(p.err, MSA_ERR_TIMEOUT);
@@ -343,6 +346,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
           if (ok) tc::commit(&tail->o_done);
         }
+        mbar_arrive(&tail->item_empty[i & 1]);
       }
       if (!ok) flag_error(p.err, MSA_ERR_TIMEOUT);
       tc::commit(&tail->finish);

@@ -70,3 +70,46 @@ def test_a_tiles_last_page_that_is_not_attended(L, full, how):
         out, bound, _ = attend64(c["q"][:Q].double(), c["kv"], c["sc"], c["bt"][:1], [L], [Q], SM,
                                  1.0, 1.0, lists)
         check_attend(outs[1][:Q], out, bound)
+
+
+@pytest.mark.parametrize("varlen", [False, True])
+def test_long_runs_of_rows_without_pages(varlen):
+    """Two dozen rows for every CTA that takes row after row, most of them of padding
+    requests or of lists without a block: in runs of one to nine, next to rows of one page
+    and of several."""
+    wave = 2 * _sms()
+    # (visible tokens, listed) of a wave's rows; a CTA gets one row of each
+    waves = [(0, 1), (0, 1), (0, 1), (700, 1), (0, 1), (400, 0), (400, 0), (1, 1), (1, 1)]
+    waves += [(0, 1)] * 4 + [(300, 0)] * 5 + [(129, 1), (0, 1), (2000, 1), (0, 1), (0, 1)]
+    kinds = [w for w in waves for _ in range(wave)] + [(260, 1)] * 7
+    lens = [max(n, int(varlen)) for n, _ in kinds]
+    B = len(lens)
+    gen = torch.Generator().manual_seed(9)
+    bt, nb = layout([2100, 700], gen)           # the requests share their pages
+    c = dict(kv=codes((nb, 1, PAGE, 2 * D), gen).to(DEV), bt=bt[:1].repeat(B, 1).contiguous().to(DEV),
+             sc=torch.exp2(torch.randn((nb, 1, 2), generator=gen) - 8).to(DEV),
+             q=torch.randn((B, 16, D), generator=gen).to(torch.bfloat16).to(DEV),
+             lens=torch.tensor(lens, dtype=torch.int32, device=DEV))
+    lists = torch.full((B, 1, 16), -1, dtype=torch.int32)
+    for b, (n, listed) in enumerate(kinds):
+        if n and listed:
+            lists[b, 0, :(n - 1) // PAGE + 1] = torch.arange((n - 1) // PAGE + 1, dtype=torch.int32)
+    lists = lists.to(DEV)
+    a = (c["q"], c["kv"], c["bt"], c["lens"])
+    if varlen:
+        cu = torch.arange(B + 1, dtype=torch.int32, device=DEV)
+        call = lambda: msa.sparse_prefill(*a, cu, lists, SM, kv_scales=c["sc"])
+    else:
+        call = lambda: msa.sparse_decode(*a, lists, 1, SM, kv_scales=c["sc"])
+    got = call()
+    for _ in range(20):   # whatever the roles' timing: the same bits
+        assert torch.equal(got, call())
+    assert msa.get_error() == 0
+    some = [b for b in range(B) if (lists[b] >= 0).any()]
+    rest = torch.ones(B, dtype=torch.bool)
+    rest[some] = False
+    assert (got[rest.to(DEV)] == 0).all()
+    some = some[::7]
+    out, bound, _ = attend64(c["q"][some].double(), c["kv"], c["sc"], c["bt"][some],
+                             [lens[b] for b in some], [1] * len(some), SM, 1.0, 1.0, lists[some])
+    check_attend(got[some], out, bound)
