@@ -632,8 +632,8 @@ def set_union_tile(enable: bool) -> bool:
     """msa_set_union_tile: attend sparse decode steps of two or more tokens per
     request over the union of each 4-token tile's lists, loading each shared
     page once (pays off when a request's tokens list mostly the same blocks).
-    Off by default; dense decode always works this way.  Returns the previous
-    setting."""
+    Off by default; dense decode always works this way, and calls with
+    kv_scales= on lists never do.  Returns the previous setting."""
     return bool(_lib().msa_set_union_tile(1 if enable else 0))
 
 

@@ -347,9 +347,10 @@ int prepare_attend(const void* q, const void* kv, const int32_t* block_table,
   // sizes over tokens: B requests of Q, or T tokens of a prefill-style batch
   const int tb = cu_q ? 1 : B, tq = cu_q ? T : Q;
   // the union attend: dense decode, or sparse decode when the union mode is on,
-  // with two or more tokens per request
-  const bool union_tile = !cu_q && Q >= 2 &&
-                          (dense_span > 0 || g_union_tile.load(std::memory_order_relaxed) != 0);
+  // with two or more tokens per request (page scales: dense decode's tiles alone)
+  const bool union_tile =
+      !cu_q && Q >= 2 &&
+      (dense_span > 0 || (!kv_scales && g_union_tile.load(std::memory_order_relaxed) != 0));
   // prefill batches (one CTA per token): the single-token rule, msa_choose_splits(T, 1, ...)
   int splits = num_splits != 0 ? num_splits
                : cu_q ? msa_choose_splits(T, 1, Hkv, dev->sm_count)

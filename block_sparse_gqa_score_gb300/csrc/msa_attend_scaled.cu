@@ -844,7 +844,6 @@ cudaError_t launch_dense(const CUtensorMap& kv_map, const AttendParams& p, dim3 
 cudaError_t launch_attend_scaled(const CUtensorMap& kv_map, const AttendParams& p,
                                  cudaStream_t stream, bool pdl) {
   const bool dense = p.dense_span > 0;
-  if (p.union_tile && !dense) return launch_union_attend_scaled(kv_map, p, stream, pdl);
   const int sms = p.sms;
   const int ntile = p.Q > 1 && dense ? 4 : 1;                  // tokens a tile
   const int64_t slots = ntile == 1 ? 2 * sms : sms;            // CTAs resident at once

@@ -450,9 +450,6 @@ __device__ __forceinline__ bool page_scale_ok(float s) {  // false for NaN
 // so the product with V8 takes weights relative to the largest u (a page
 // counts by the size of its values, and nothing is lost to a common
 // reference), and the running sum divides each page's weights by vs again.
-constexpr float kNoRef = 1e30f;   // kPShift - m before a head's first key: finite, so that a
-                                  // page without any key (-inf logits) has weights of 0
-
 struct PageScale {
   float k;      // ks
   float lv;     // log2(vs)

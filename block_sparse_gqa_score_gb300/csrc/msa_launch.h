@@ -122,8 +122,8 @@ cudaError_t launch_attend(const CUtensorMap& kv_map, const AttendParams& p, cuda
 // tile's lists; grid (B * ceil(Q / 4) * Hkv, splits).
 cudaError_t launch_union_attend(const CUtensorMap& kv_map, const AttendParams& p,
                                 cudaStream_t stream, bool pdl);
-// The same on a cache with page scales (p.kv_scales set); dense decode is
-// launch_attend_scaled's alone.
+// The scorer and the attends (lists and dense decode) on a cache with page scales
+// (p.kv_scales set).
 cudaError_t launch_score_scaled(const CUtensorMap& kv_map, const ScoreParams& p,
                                 cudaStream_t stream, bool pdl);
 cudaError_t launch_attend_scaled(const CUtensorMap& kv_map, const AttendParams& p,
@@ -132,8 +132,6 @@ cudaError_t launch_attend_scaled(const CUtensorMap& kv_map, const AttendParams& 
 // choice.
 cudaError_t launch_attend_stream(const CUtensorMap& kv_map, const AttendParams& p,
                                  cudaStream_t stream, bool pdl);
-cudaError_t launch_union_attend_scaled(const CUtensorMap& kv_map, const AttendParams& p,
-                                       cudaStream_t stream, bool pdl);
 // Its split count for `units` (request, tile, KV head) units: as many CTAs per
 // unit as fit one CTA per SM (at most 8), 1 when the units fill the SMs.
 int union_ctas_per_unit(int units, int sm_count);

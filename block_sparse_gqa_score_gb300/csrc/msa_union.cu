@@ -48,27 +48,16 @@
 //   3      copies the request's block-table row
 //   4..19  token j = (warp - 4) / 4: softmax; warp 4+4j selects or reads the
 //          token's list, warp 5+4j prepares its query rows
-//
-// This file is compiled twice: as it stands (one scale per tensor), and with
-// MSA_KV_SCALES set (by msa_union_scaled.cu) for lists on a cache whose pages
-// carry scales of their own (see PageScale): the prologue puts the union pages'
-// scales into shared memory.  Dense decode with page scales is
-// msa_attend_scaled.cu's.
 #include "msa_dense_slot.cuh"
 #include "msa_device.cuh"
 #include "msa_launch.h"
 #include "msa_select.cuh"
 #include "msa_tcgen05.cuh"
 
-#ifndef MSA_KV_SCALES
-#define MSA_KV_SCALES 0
-#endif
-
 namespace msa {
 
 namespace {
 
-constexpr bool kScaled = MSA_KV_SCALES != 0;  // page scales (AttendParams::kv_scales)
 constexpr int kQt = kUnionTile;               // query tokens per tile
 constexpr int kStages = 5;
 constexpr int kWarps = 4 + 4 * kQt;
@@ -121,7 +110,6 @@ struct UnionTail {
   int tok_slots[kQt][kMaxUnion];  // their slots, in page order
   int dense_lo;             // dense decode: this CTA's pages are blocks dense_lo + slot
   uint32_t dense_bad[kMaxDenseBlocks / 32];  // dense decode: slots whose block-table entry is bad
-  PageScale sc[kScaled ? kMaxUnion : 1];     // listed pages' scales, by slot
 };
 
 // shared-memory layout (offsets from a 1024-byte aligned base)
@@ -407,7 +395,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool keep[2];
     uint32_t mk[2];
     int pg[2];
-    PageScale scl[kScaled ? 2 : 1];
     bool long_run = false;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -436,15 +423,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (page < 0 || static_cast<int64_t>(page) >= p.num_blocks) {
           if (split == 0) flag_error(p.err, MSA_ERR_PAGE_RANGE);
           ok = false;
-        }
-      }
-      if constexpr (kScaled) {
-        if (ok) {
-          scl[r] = make_page_scale(load_page_scale(p.kv_scales, page, p.Hkv, g));
-          if (scl[r].bad != 0.f) {
-            if (split == 0) flag_error(p.err, MSA_ERR_SCALE);
-            ok = false;
-          }
         }
       }
       keep[r] = ok;
@@ -492,7 +470,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       tail->pages[slot] = pg[r];
       tail->blocks[slot] = static_cast<int>(v[r] >> 2);
       tail->masks[slot] = mk[r];
-      if constexpr (kScaled) tail->sc[slot] = scl[r];
     }
     __syncwarp();
     // each token's slots in page order, and the slot of the request's last block
@@ -785,8 +762,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; k < n_j && ok; ++k) {
       const int t = tok_slot(j, k), buf = k & 1, sb = k % kSBufs;
       const int s = t % kStages;
-      const PageScale sc = kScaled ? tail->sc[t] : PageScale{1.f, 0.f, 1.f, 0.f};
-      const float zt = kScaled ? zs * sc.k : zs;
       if (!mbar_wait(&tail->s_full[jw][sb], (k / kSBufs) & 1)) {
         ok = false;
         break;
@@ -826,9 +801,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       float al_h = 1.f;   // 2^(m_old - m_new): 1 when m stays, 0 when the head had no key
       bool raise_h = false;
       if (lane < kGroup) {
-        const float mx4 = fmaxf(fmaxf(mxb[lane], mxb[kGroup + lane]),
-                                fmaxf(mxb[2 * kGroup + lane], mxb[3 * kGroup + lane]));
-        const float pm = kScaled ? fmaf(mx4, zt, sc.lv) : mx4 * zt;
+        const float pm = fmaxf(fmaxf(mxb[lane], mxb[kGroup + lane]),
+                               fmaxf(mxb[2 * kGroup + lane], mxb[3 * kGroup + lane])) * zs;
         raise_h = pm + nref_h > kPShift + kLazy;
         if (raise_h) {
           al_h = ex2(kPShift - nref_h - pm);
@@ -863,9 +837,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int h = 0; h < kGroup; ++h) {
         // P = 2^(x - m + 8); 0 for an invisible key
-        const float nr = __shfl_sync(0xffffffffu, nref_h, h);
-        x[h] = ex2(fmaf(x[h], zt, kScaled ? nr + sc.lv : nr));
-        l[h] = kScaled ? fmaf(x[h], sc.iv, l[h]) : l[h] + x[h];
+        x[h] = ex2(fmaf(x[h], zs, __shfl_sync(0xffffffffu, nref_h, h)));
+        l[h] += x[h];
       }
       uint32_t hw[4], lw[4];
 #pragma unroll
@@ -957,14 +930,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         l[4 * h4 + 2] = t4.z;
         l[4 * h4 + 3] = t4.w;
       }
-#if MSA_KV_SCALES
-#pragma unroll
-      for (int h = 0; h < kGroup; ++h)
-        if (l[h] != l[h]) {   // a NaN logit: the whole row, whatever it is merged with
-          l[h] = 1.f;
-          o[h] = __uint_as_float(0x7FFFFFFFu);
-        }
-#endif
       const int d = key;
       const int64_t row0 = (static_cast<int64_t>(b) * p.Q + tok) * p.Hq + g * kGroup;
       if (p.splits == 1) {
@@ -1005,30 +970,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-#if MSA_KV_SCALES
-// Lists only.
-cudaError_t launch_union_attend_scaled(const CUtensorMap& kv_map, const AttendParams& p,
-                                       cudaStream_t stream, bool pdl) {
-  static std::atomic<unsigned long long> attr_done{0};
-  cudaError_t e = once_per_device(attr_done, [] {
-    for (auto* k : {union_attend_kernel<false, false>, union_attend_kernel<true, false>}) {
-      cudaError_t r = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           kSmemBytes);
-      if (r != cudaSuccess) return r;
-      r = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout,
-                               static_cast<int>(cudaSharedmemCarveoutMaxShared));
-      if (r != cudaSuccess) return r;
-    }
-    return cudaSuccess;
-  });
-  if (e != cudaSuccess) return e;
-  const dim3 grid(p.B * ((p.Q + kQt - 1) / kQt) * p.Hkv, p.splits), block(kThreads);
-  return p.q8 ? launch_pdl(union_attend_kernel<true, false>, grid, block, kSmemBytes, stream, pdl,
-                           kv_map, p)
-              : launch_pdl(union_attend_kernel<false, false>, grid, block, kSmemBytes, stream, pdl,
-                           kv_map, p);
-}
-#else
 int union_ctas_per_unit(int units, int sm_count) {
   if (units >= sm_count) return 1;
   const int z = sm_count / units;
@@ -1073,6 +1014,5 @@ cudaError_t launch_union_attend(const CUtensorMap& kv_map, const AttendParams& p
               : launch_pdl(union_attend_kernel<false, false>, grid, block, kSmemBytes, stream, pdl,
                            kv_map, p);
 }
-#endif
 
 }  // namespace msa

@@ -541,8 +541,8 @@ int msa_append_kv_prefill(const void *k, int64_t k_stride, const void *v, int64_
  * that is more, with errors that cancel over a page's keys: rows of 262144 keys
  * beside a dominant one are within 2^-7 of sum p |v|, rounding to bf16 included.
  * A NaN logit makes its head's output NaN and a NaN value its dim, of the tokens
- * that see the key and of no other (with the union tile a NaN value reaches all
- * tokens of a tile).  Errors: as without the suffix, plus null or not 8-byte aligned
+ * that see the key and of no other.  msa_set_union_tile has no effect on them.
+ * Errors: as without the suffix, plus null or not 8-byte aligned
  * kv_scales (4-byte for a K-only cache) (MSA_EINVAL).  Device: MSA_ERR_SCALE (a
  * listed or visible page with a scale out of range, either side for the
  * attends, K's for the scorer: the page is skipped, its score is -inf).
@@ -615,7 +615,7 @@ int msa_decode_step_scaled(const void *q, float q_scale, const void *kv, const f
  * agree within the output tolerance (the accumulation order differs).  The
  * split count msa_choose_splits reports follows this setting.  Dense decode
  * (msa_dense_decode) always attends a tile's shared pages this way when
- * Q >= 2.  Process-wide; returns the previous setting (0 or 1).
+ * Q >= 2; the msa_*_scaled entry points never do on lists.  Process-wide; returns the previous setting (0 or 1).
  */
 int msa_set_union_tile(int enable);
 

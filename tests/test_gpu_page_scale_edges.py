@@ -113,3 +113,31 @@ def test_long_runs_of_rows_without_pages(varlen):
     out, bound, _ = attend64(c["q"][some].double(), c["kv"], c["sc"], c["bt"][some],
                              [lens[b] for b in some], [1] * len(some), SM, 1.0, 1.0, lists[some])
     check_attend(got[some], out, bound)
+
+
+@pytest.mark.parametrize("lens,Q", [([900, 3000, 0, 5], 4), ([2500], 32), ([700, 40], 2)])
+def test_the_union_tile_has_no_say_over_lists_on_page_scales(lens, Q):
+    """The same bits with the switch on and off, in every form, also where the caller
+    takes its split count from the switch."""
+    Hkv, B = 2, len(lens)
+    c = _inputs(lens, Q, Hkv, 11)
+    gen = torch.Generator().manual_seed(12)
+    S = c["bt"].shape[1]
+    scores = torch.randn((Hkv, B * Q, S), generator=gen).to(DEV)
+    a = (c["q"], c["kv"], c["bt"], c["lens"])
+    kw = dict(kv_scales=c["sc"])
+    lists = msa.topk(scores, c["lens"], Q)
+    outs = []
+    for on in (False, True):
+        was = msa.set_union_tile(on)
+        try:
+            buffers = msa.DecodeBuffers.allocate(B, Q, 16 * Hkv, Hkv, S, torch.device(DEV))
+            outs.append((msa.sparse_decode(*a, lists, Q, SM, **kw),
+                         msa.sparse_decode(*a, lists, Q, SM, num_splits=3, **kw),
+                         *msa.sparse_decode_select(*a, scores, Q, SM, **kw),
+                         *msa.decode_step(*a, Q, SM, buffers=buffers, **kw)))
+        finally:
+            msa.set_union_tile(was)
+    for off, on in zip(*outs):
+        assert torch.equal(off, on)
+    assert msa.get_error() == 0
