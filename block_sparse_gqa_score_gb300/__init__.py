@@ -437,12 +437,14 @@ def combine(workspace: torch.Tensor, tokens: int, num_q_heads: int, num_splits: 
 @dataclass
 class DecodeBuffers:
     """Preallocated outputs and workspace of one decode step (reusable, and
-    stable addresses for CUDA-graph capture)."""
+    stable addresses for CUDA-graph capture).  chosen: num_splits is the
+    caller's; else decode_step with kv_scales cuts rows as num_splits=0 does."""
     scores: torch.Tensor
     topk: torch.Tensor
     out: torch.Tensor
     workspace: torch.Tensor | None
     num_splits: int
+    chosen: bool = True
 
     @staticmethod
     def allocate(batch: int, qlen: int, num_q_heads: int, num_kv_heads: int, stride: int,
@@ -455,7 +457,7 @@ class DecodeBuffers:
             scores=torch.empty((num_kv_heads, T, stride), dtype=torch.float32, device=device),
             topk=torch.empty((T, num_kv_heads, TOPK), dtype=torch.int32, device=device),
             out=torch.empty((T, num_q_heads, HEAD_DIM), dtype=torch.bfloat16, device=device),
-            workspace=ws, num_splits=splits)
+            workspace=ws, num_splits=splits, chosen=num_splits > 0)
 
 
 def decode_step(q, kv, block_table, seq_lens, qlen: int, sm_scale: float, k_scale: float = 1.0,
@@ -507,7 +509,7 @@ def decode_step(q, kv, block_table, seq_lens, qlen: int, sm_scale: float, k_scal
         *head, *index,
         block_table.data_ptr(), seq_lens.data_ptr(), bf.scores.data_ptr(), bf.topk.data_ptr(),
         ws_ptr, ws_bytes, bf.out.data_ptr(), B, qlen, Hq, Hkv, S, NB, float(sm_scale),
-        float(k_scale), float(v_scale), bf.num_splits if kv_scales is None else 0,
+        float(k_scale), float(v_scale), bf.num_splits if kv_scales is None or bf.chosen else 0,
         _stream(dev, stream))
     _native.check(st, "msa_decode_step")
     return bf.scores, bf.topk, bf.out

@@ -141,3 +141,26 @@ def test_the_union_tile_has_no_say_over_lists_on_page_scales(lens, Q):
     for off, on in zip(*outs):
         assert torch.equal(off, on)
     assert msa.get_error() == 0
+
+
+@pytest.mark.parametrize("S", [0, 600])      # selection inside the attend kernel, and before it
+@pytest.mark.parametrize("scaled", [True, False])
+def test_a_step_takes_the_split_count_of_its_buffers(scaled, S):
+    """A count that the caller chose holds, with page scales as without; the one that
+    allocate chooses is for the cache with one scale per tensor."""
+    lens, Q, Hkv = [2600, 900], 2, 1
+    c = _inputs(lens, Q, Hkv, 13)
+    bt = torch.zeros((2, max(S, c["bt"].shape[1])), dtype=torch.int32, device=DEV)
+    bt[:, :c["bt"].shape[1]] = c["bt"]
+    a = (c["q"], c["kv"], bt, c["lens"])
+    kw = dict(kv_scales=c["sc"] if scaled else None)
+    for chosen in (3, 0):
+        bufs = msa.DecodeBuffers.allocate(2, Q, 16 * Hkv, Hkv, bt.shape[1], torch.device(DEV),
+                                          num_splits=chosen)
+        assert bufs.num_splits == 3 or chosen == 0
+        bufs.workspace.fill_(0xA5)
+        scores, lists, out = msa.decode_step(*a, Q, SM, buffers=bufs, **kw)
+        parts = chosen or (0 if scaled else bufs.num_splits)
+        assert bool((bufs.workspace != 0xA5).any()) == (parts > 1)
+        assert torch.equal(out, msa.sparse_decode(*a, lists, Q, SM, num_splits=parts, **kw))
+    assert msa.get_error() == 0
