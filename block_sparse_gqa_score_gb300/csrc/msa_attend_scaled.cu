@@ -492,19 +492,19 @@ __global__ void __launch_bounds__(Groups<kNT>::kThreads, kNT == 1 ? 2 : 1)
       int pg = pg_next;
       // warp 2: tile t, of block blk, has landed on v_land[e]
       auto settle = [&](int e, int t, int blk) {
-        const bool landed = __all_sync(0xffffffffu, wait_for(&tail->v_land[e], 0));
+        bool known = true, attended = true;
+        if constexpr (kNT > 1) {
+          // (a page that is not attended may be any page in the place of a bad table
+          // entry's; its info is there long before its tile's turn)
+          known = wait_for(&tail->info_full[(t / kChunk) & 1], (t / (2 * kChunk)) & 1);
+          attended = tail->info[t % (2 * kChunk)].block >= 0;
+        }
+        const bool landed = __all_sync(0xffffffffu, wait_for(&tail->v_land[e], 0) && known);
         ok = ok && landed;
         if (!landed) return;
         uint8_t* tile = smem + Sm::kV + t % kSlots * kHalfTile;
-        if constexpr (kNT > 1) {
-          // (not of a page that is not attended, which may be any page in the place of a
-          // bad table entry's; its info is there long before its tile's turn)
-          const bool known =
-              __all_sync(0xffffffffu, wait_for(&tail->info_full[(t / kChunk) & 1], (t / (2 * kChunk)) & 1));
-          ok = ok && known;
-          if (known && tail->info[t % (2 * kChunk)].block >= 0)
-            nan_values(tile, first_pos - blk * kPage, last_pos - blk * kPage, blk, tail, lane);
-        }
+        if (kNT > 1 && attended)
+          nan_values(tile, first_pos - blk * kPage, last_pos - blk * kPage, blk, tail, lane);
         zero_value_rows(tile, last_pos - blk * kPage, lane);
         tc::fence_proxy_async_smem();
         __syncwarp();
