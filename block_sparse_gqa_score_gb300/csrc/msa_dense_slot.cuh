@@ -31,14 +31,14 @@ struct DenseSlot {
 };
 
 // Dense decode's work for CTA (or cluster of CTAs) c of C along x.  With a
-// grid of one CTA per unit and split that is (c, blockIdx.y, gridDim.y).  With more CTAs than units (one
-// per SM or more) the units share them out by their blocks: unit u (n_u blocks)
-// takes z_u = min(ceil(n_u / T), splits) CTAs (at least one) for the smallest
-// T at which every unit's CTAs fit the grid, so that no CTA holds much more
-// than its share of the batch's pages; the CTAs go to the units in order, a
-// unit's KV heads in turn, each head's ranges in turn.  Every CTA computes the
-// same assignment from seq_lens (one warp, every lane the same result); CTAs
-// past the last unit's get none.
+// grid of one CTA per unit and split that is (c, blockIdx.y, gridDim.y).  With
+// more CTAs than units (one per SM or more) the units share them out by their
+// blocks: unit u (n_u blocks) takes z_u = min(ceil(n_u / T), splits) CTAs (at
+// least one) for the smallest T at which every unit's CTAs fit the grid, so that
+// no CTA holds much more than its share of the batch's pages; the CTAs go to the
+// units in order, a unit's KV heads in turn, each head's ranges in turn.  Every
+// CTA computes the same assignment from seq_lens (one warp, every lane the same
+// result); CTAs past the last unit's get none.
 template <int kTile>
 __device__ DenseSlot dense_slot(const AttendParams& p, int ntiles, int C, int c, int lane) {
   const int NT = p.B * ntiles, H = p.Hkv, Z = p.splits;

@@ -266,7 +266,12 @@ int msa_dense_splits(int S);
  * (keys 128 n + t <= pos(i)); no list is read.  Splits as msa_dense_splits;
  * with more than one the partials go to `workspace` (parts a row does not use
  * are marked empty) and the merge is enqueued on `stream`.  Numerics as
- * msa_sparse_decode.
+ * msa_sparse_decode: a key whose probability is less than 2^-18 of the row's
+ * largest is not in the output but in the sum that divides it, so a row of very
+ * many small keys beside a dominant one loses them (measured, one part a row:
+ * keys beside one of 0.9 of the weight, off by 0.19 of sum p |v| at 32768 keys
+ * and Q = 4, 0.01 at Q = 1; beside one of 0.5, 0.05 at 131072 and Q = 4).
+ * msa_dense_decode_scaled does not.
  * Errors: as msa_sparse_decode (topk and num_splits aside), plus S > 2048
  * (MSA_EINVAL).  Device: MSA_ERR_PAGE_RANGE (page skipped), MSA_ERR_SEQ_RANGE.
  */
@@ -615,7 +620,8 @@ int msa_decode_step_scaled(const void *q, float q_scale, const void *kv, const f
  * agree within the output tolerance (the accumulation order differs).  The
  * split count msa_choose_splits reports follows this setting.  Dense decode
  * (msa_dense_decode) always attends a tile's shared pages this way when
- * Q >= 2; the msa_*_scaled entry points never do on lists.  Process-wide; returns the previous setting (0 or 1).
+ * Q >= 2; the msa_*_scaled entry points never do on lists.  Process-wide;
+ * returns the previous setting (0 or 1).
  */
 int msa_set_union_tile(int enable);
 
@@ -632,7 +638,9 @@ int msa_set_union_tile(int enable);
  * before its writes are visible.  Outputs are always ordered: no library
  * kernel writes a buffer before the previous kernel has finished.
  * msa_append_kv(_prefill), whose outputs are the other calls' inputs, reads
- * nothing early and has finished before a kernel enqueued after it starts.
+ * nothing early and, enqueued with the setting on, has finished before a kernel
+ * enqueued after it starts (enqueued with it off, it is like any other kernel
+ * that wrote the inputs: turn the setting on before the append).
  * Process-wide; returns the previous setting (0 or 1).
  */
 int msa_set_input_overlap(int enable);
