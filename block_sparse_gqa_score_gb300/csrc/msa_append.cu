@@ -24,8 +24,8 @@
 // in registers they halved the CTAs an SM, which the query rows of the same
 // launch paid for: 313 us for 28779 tokens of 64/4 heads).
 //
-// Measured (64/4 heads): 28779 tokens with page scales 182 us, 5.7 TB/s, 84 % of a copy's
-// rate; 6000 tokens with one scale 41 us, 77 %; 128 single tokens 8 us, launch and four
+// Measured (64/4 heads): 28779 tokens with page scales 181 us, 5.7 TB/s, 85 % of a copy's
+// rate; 6000 tokens with one scale 39 us, 81 %; 128 single tokens 5 us, launch and four
 // dependent loads.
 #include "msa_device.cuh"
 #include "msa_launch.h"

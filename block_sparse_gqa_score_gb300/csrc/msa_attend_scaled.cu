@@ -31,10 +31,10 @@
 // a workspace nor a second kernel.
 //
 // What bounds it, measured (64 query heads, 4 KV heads): lists of batch 16, 4 tokens,
-// 8k-32k: 27 us, 4.1 TB/s of its pages; start, lists and pages one behind the other, a
-// call of 2 rows already takes 11 us.  Dense decode of one token over 262144: 57 us,
-// 4.7 TB/s; the first tile is asked for after 4.5 us, behind the assignment.  Dense
-// decode of batch 16, 4 tokens, 8k-32k: 98 us, 3.5 TB/s: the softmax warps' chain of
+// 8k-32k: 24 us, 4.6 TB/s of its pages; start, lists and pages one behind the other, a
+// call of 2 rows already takes 9 us.  Dense decode of one token over 262144: 54 us,
+// 5.0 TB/s; the first tile is asked for after 4.5 us, behind the assignment.  Dense
+// decode of batch 16, 4 tokens, 8k-32k: 97 us, 3.5 TB/s: the softmax warps' chain of
 // waits, 1.2 us a page, on the CTA with the most pages (84, the average is 67).
 #include <cstddef>
 

@@ -22,9 +22,9 @@
 // that one lane alone runs: issued from a branch inside a loop of the whole warp, the
 // query descriptor that reached the tensor core was wrong.)
 //
-// Measured: 268 us for those 1536 tokens (334 with a CTA a row), 12.0 TB/s of pages out
-// of L2; what bounds it are the softmax warps, 16 of them an SM: 60 % of the issue slots,
-// the rest their chain of waits, and no pipe: without the loads it takes 5 % less.
+// Measured: 273 us for those 1536 tokens, 11.9 TB/s of pages out of L2; what bounds it are
+// the softmax warps, 16 of them an SM: 61 % of the issue slots, the rest their chain of
+// waits, and no pipe: without the loads it takes 5 % less.
 #include <cstddef>
 
 #include "msa_device.cuh"
