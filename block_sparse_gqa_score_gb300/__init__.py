@@ -13,6 +13,10 @@ vLLM MiniMax-M3 sparse attention pages and TensorRT-LLM PR #17171 describe it:
   append_kv()      the step before: new keys and values rotated, quantised and
                    written to the paged cache, the query rotated
                    (append_kv_prefill() for prefill batches)
+  score_prefill(), topk_prefill()  the scorer and the selector for prefill batches
+  dense_prefill()  attention over every visible block for prefill batches
+  fork_pages(), compact_pages(), copy_pages()  the cache's pages: rows forked,
+                   reordered, freed and grown, pages moved together
 
 Every function here only checks and marshals torch tensors into the C ABI of
 libmsa.so (include/msa.h); all arithmetic runs in that library's CUDA kernels.
@@ -29,6 +33,7 @@ multiply k_scale and v_scale (msa_*_scaled).
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from dataclasses import dataclass
 
@@ -45,7 +50,8 @@ MAX_QLEN = 32
 
 __all__ = ["score", "topk", "sparse_decode", "sparse_decode_select", "sparse_prefill",
            "sparse_prefill_select", "dense_decode", "dense_splits",
-           "combine", "decode_step", "append_kv", "append_kv_prefill",
+           "combine", "decode_step", "append_kv", "append_kv_prefill", "score_prefill",
+           "topk_prefill", "dense_prefill", "dense_prefill_workspace_bytes", "fork_pages", "compact_pages", "copy_pages",
            "fused_selection", "FUSED_MAX_BLOCKS", "workspace_bytes",
            "choose_splits", "get_error", "set_input_overlap", "set_union_tile", "DecodeBuffers",
            "MSAError"]
@@ -331,14 +337,19 @@ def sparse_decode_select(q, kv, block_table, seq_lens, scores, qlen: int, sm_sca
     return topk_out, out
 
 
+def _cu_seqlens(cu_seqlens_q, batch: int, dev, q=None):
+    """Checks cu_seqlens_q [B + 1]; the tokens of q."""
+    _need(cu_seqlens_q, "cu_seqlens_q", (torch.int32,), dev)
+    if cu_seqlens_q.shape != (batch + 1,):
+        raise ValueError("cu_seqlens_q must be [B + 1]")
+    return int(q.shape[0]) if q is not None else None
+
+
 def _prefill_geometry(q, kv, block_table, seq_lens, cu_seqlens_q):
     """Shapes of a prefill-style batch: q holds T tokens, request b owning
     tokens cu_seqlens_q[b] .. cu_seqlens_q[b + 1] - 1."""
     dev, B, S, Hq, Hkv, NB = _geometry(q, kv, block_table, seq_lens, None)
-    _need(cu_seqlens_q, "cu_seqlens_q", (torch.int32,), dev)
-    if tuple(cu_seqlens_q.shape) != (B + 1,):
-        raise ValueError("cu_seqlens_q must be [B + 1]")
-    return dev, B, int(q.shape[0]), S, Hq, Hkv, NB
+    return dev, B, _cu_seqlens(cu_seqlens_q, B, dev, q), S, Hq, Hkv, NB
 
 
 def sparse_prefill(q, kv, block_table, seq_lens, cu_seqlens_q, topk_idx, sm_scale: float,
@@ -417,6 +428,107 @@ def sparse_prefill_select(q, kv, block_table, seq_lens, cu_seqlens_q, scores, sm
         status = _lib().msa_sparse_prefill_select(q.data_ptr(), *args)
     _native.check(status, "msa_sparse_prefill_select")
     return topk_out, out
+
+
+def score_prefill(q, kv, block_table, seq_lens, cu_seqlens_q, sm_scale: float,
+                  k_scale: float = 1.0, scores: torch.Tensor | None = None, stream=None,
+                  q_scale: float = 1.0, kv_scales: torch.Tensor | None = None) -> torch.Tensor:
+    """Block scores fp32 [Hkv, T, S] of a prefill or chunked-prefill batch
+    (msa_score_prefill): score() with one query length per request, the tokens as in
+    sparse_prefill().  `kv` may be a K-only (index-K) cache [NB, Hkv, 128, 128];
+    kv_scales: page scales [NB, Hkv, 2] ([NB, Hkv, 1] of a K-only cache)."""
+    dev, B, S, Hq, Hkv, NB = _geometry(q, kv, block_table, seq_lens, None, k_only_ok=True)
+    T = _cu_seqlens(cu_seqlens_q, B, dev, q)
+    if scores is None:
+        scores = torch.empty((Hkv, T, S), dtype=torch.float32, device=dev)
+    _need(scores, "scores", (torch.float32,), dev)
+    if scores.shape != (Hkv, T, S):
+        raise ValueError("scores must be [Hkv, T, S]")
+    k_only = kv.shape[3] == HEAD_DIM
+    sc = None
+    if kv_scales is not None:
+        sc = _page_scales(kv_scales, "kv_scales", dev, NB, Hkv, 1 if k_only else 2)
+    if T == 0 and B == 0:
+        return scores        # empty tensors have no address to check
+    st = _lib().msa_score_prefill(
+        q.data_ptr(), float(q_scale) if _fp8(q, q_scale) else 0.0, kv.data_ptr(), sc, int(k_only),
+        block_table.data_ptr(), seq_lens.data_ptr(), cu_seqlens_q.data_ptr(), scores.data_ptr(), B,
+        T, Hq, Hkv, S, NB, float(sm_scale), float(k_scale), _stream(dev, stream))
+    _native.check(st, "msa_score_prefill")
+    return scores
+
+
+def topk_prefill(scores: torch.Tensor, seq_lens: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                 k: int = TOPK, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Selected blocks int32 [T, Hkv, 16] of a prefill or chunked-prefill batch
+    (msa_topk_prefill): topk() with one query length per request.  `scores` is
+    indexed [g, i, n] and may be any strided view."""
+    if not (isinstance(scores, torch.Tensor) and scores.is_cuda and scores.dtype == torch.float32):
+        raise TypeError("scores must be a CUDA float32 tensor")
+    if scores.dim() != 3:
+        raise ValueError("scores must be [Hkv, T, S]")
+    dev = scores.device
+    _need(seq_lens, "seq_lens", (torch.int32,), dev)
+    Hkv, T, S = scores.shape
+    B = seq_lens.shape[0]
+    _cu_seqlens(cu_seqlens_q, B, dev)
+    if out is None:
+        out = torch.empty((T, Hkv, k), dtype=torch.int32, device=dev)
+    _need(out, "out", (torch.int32,), dev)
+    if out.shape != (T, Hkv, k):
+        raise ValueError("out must be [T, Hkv, 16]")
+    if T == 0 and B == 0:
+        return out
+    sh, stt, sn = scores.stride()
+    st = _lib().msa_topk_prefill(scores.data_ptr(), sh, stt, sn, seq_lens.data_ptr(),
+                                 cu_seqlens_q.data_ptr(), out.data_ptr(), B, T, Hkv, S, k,
+                                 _stream(dev, stream))
+    _native.check(st, "msa_topk_prefill")
+    return out
+
+
+@functools.lru_cache(maxsize=None)
+def _dense_prefill_bytes(index: int) -> int:
+    sms = torch.cuda.get_device_properties(index).multi_processor_count
+    return int(_lib().msa_dense_prefill_workspace_bytes(sms))
+
+
+def dense_prefill_workspace_bytes(device=None) -> int:
+    """Bytes of workspace dense_prefill uses on `device` (the current one), whatever
+    the batch."""
+    index = None if device is None else torch.device(device).index
+    return _dense_prefill_bytes(torch.cuda.current_device() if index is None else index)
+
+
+def dense_prefill(q, kv, block_table, seq_lens, cu_seqlens_q, sm_scale: float,
+                  k_scale: float = 1.0, v_scale: float = 1.0, out: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None, stream=None, q_scale: float = 1.0,
+                  kv_scales: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention over every visible key of a prefill or chunked-prefill batch, bf16
+    [T, Hq, 128] (msa_dense_prefill): the tokens as in sparse_prefill(), their keys
+    and values in the cache already.  workspace: dense_prefill_workspace_bytes();
+    kv_scales: page scales [NB, Hkv, 2]."""
+    dev, B, T, S, Hq, Hkv, NB = _prefill_geometry(q, kv, block_table, seq_lens, cu_seqlens_q)
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+    _need(out, "out", (torch.bfloat16,), dev)
+    if out.shape != q.shape:
+        raise ValueError("out must be [T, Hq, 128]")
+    sc = _page_scales(kv_scales, "kv_scales", dev, NB, Hkv, 2) if kv_scales is not None else None
+    if T == 0 and B == 0:
+        return out
+    need = dense_prefill_workspace_bytes(dev)
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev:
+        raise ValueError(f"workspace must be on {dev}")
+    st = _lib().msa_dense_prefill(
+        q.data_ptr(), float(q_scale) if _fp8(q, q_scale) else 0.0, kv.data_ptr(), sc,
+        block_table.data_ptr(), seq_lens.data_ptr(), cu_seqlens_q.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), out.data_ptr(), B, T, Hq, Hkv, S, NB,
+        float(sm_scale), float(k_scale), float(v_scale), _stream(dev, stream))
+    _native.check(st, "msa_dense_prefill")
+    return out
 
 
 def combine(workspace: torch.Tensor, tokens: int, num_q_heads: int, num_splits: int,
@@ -628,6 +740,121 @@ def append_kv_prefill(k, v, kv, block_table, seq_lens, cu_seqlens_q, k_scale: fl
     return _append(_lib().msa_append_kv_prefill, k, v, kv, block_table, seq_lens, tokens,
                    cu_seqlens_q, None, k_scale, v_scale, kv_scales, cos_sin, interleaved, q, q_out,
                    q_scale, stream)
+
+
+def _caches(caches, num_blocks, dev):
+    """msa_cache_t of each tensor [num_blocks, ...]: rows of tokens in [.., 128, bytes]
+    of 8-bit types, else whole pages."""
+    out = (_native.Cache * max(1, len(caches)))()
+    for i, c in enumerate(caches):
+        _need(c, f"caches[{i}]", _KV_DTYPES + (torch.float32,), dev)
+        if c.dim() < 2 or (num_blocks is not None and c.shape[0] != num_blocks):
+            raise ValueError(f"caches[{i}] must be [num_blocks, ...] of the pool's pages")
+        if c.dtype == torch.float32:          # page scales [NB, Hkv, sides]
+            if c.dim() != 3:
+                raise ValueError(f"caches[{i}]: page scales are [num_blocks, Hkv, sides]")
+            out[i] = _native.Cache(c.data_ptr(), c.shape[1], 1, 4 * c.shape[2])
+        else:
+            if c.dim() != 4 or c.shape[2] != PAGE_SIZE:
+                raise ValueError(f"caches[{i}] must be [num_blocks, Hkv, 128, row bytes]")
+            out[i] = _native.Cache(c.data_ptr(), c.shape[1], PAGE_SIZE, c.shape[3])
+    return out
+
+
+def _out(t, name: str, shape, dev):
+    if t is None:
+        return torch.empty(shape, dtype=torch.int32, device=dev)
+    _need(t, name, (torch.int32,), dev)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+    return t
+
+
+def _table(block_table, seq_lens, refs):
+    _need(block_table, "block_table", (torch.int32,))
+    dev = block_table.device
+    _need(seq_lens, "seq_lens", (torch.int32,), dev)
+    _need(refs, "refs", (torch.int32,), dev)
+    if block_table.dim() != 2 or seq_lens.shape != block_table.shape[:1] or refs.dim() != 1:
+        raise ValueError("block_table must be [B, S], seq_lens [B] and refs [num_blocks]")
+    return (dev, *block_table.shape, refs.shape[0])
+
+
+def _distinct(outs, ins):
+    for o in outs:
+        lo, hi = o.data_ptr(), o.data_ptr() + 4 * o.numel()
+        if any(lo < i.data_ptr() + 4 * i.numel() and i.data_ptr() < hi for i in ins):
+            raise ValueError("outputs must not overlap the inputs")
+
+
+def fork_pages(block_table, seq_lens, parents, refs, caches=(), grow=None, block_table_out=None,
+               seq_lens_out=None, refs_out=None, copies=None, stream=None):
+    """The next step's rows of a block table (msa_fork_pages): new row b continues row
+    parents[b] of block_table [B, S], seq_lens [B] (-1: a new, empty row) and has room
+    for grow[b] more tokens; rows without a child are freed.  Full pages are shared, a
+    begun page goes to the first child and is copied for the others, in every tensor
+    of `caches` (kv [NB, Hkv, 128, 256], K-only caches, page scales, of any number of
+    layers).  refs [NB]: how many rows hold each page; free pages (0) are taken in
+    ascending order.  Returns (block_table, seq_lens, refs, copies [rows, 3])."""
+    dev, B, S, NB = _table(block_table, seq_lens, refs)
+    _need(parents, "parents", (torch.int32,), dev)
+    if parents.dim() != 1:
+        raise ValueError("parents must be [rows]")
+    rows = parents.shape[0]
+    if grow is not None:
+        _need(grow, "grow", (torch.int32,), dev)
+        if grow.shape != (rows,):
+            raise ValueError("grow must be [rows]")
+    handles = _caches(caches, NB, dev)
+    block_table_out = _out(block_table_out, "block_table_out", (rows, S), dev)
+    seq_lens_out = _out(seq_lens_out, "seq_lens_out", (rows,), dev)
+    refs_out = _out(refs_out, "refs_out", (NB,), dev)
+    copies = _out(copies, "copies", (rows, 3), dev)
+    _distinct((block_table_out, seq_lens_out, refs_out, copies),
+              (block_table, seq_lens, parents, refs) + (() if grow is None else (grow,)))
+    st = _lib().msa_fork_pages(
+        block_table.data_ptr(), seq_lens.data_ptr(), parents.data_ptr(),
+        None if grow is None else grow.data_ptr(), refs.data_ptr(), block_table_out.data_ptr(),
+        seq_lens_out.data_ptr(), refs_out.data_ptr(), copies.data_ptr(), B, rows, S, NB, handles,
+        len(caches), _stream(dev, stream))
+    _native.check(st, "msa_fork_pages")
+    return block_table_out, seq_lens_out, refs_out, copies
+
+
+def compact_pages(block_table, seq_lens, refs, caches=(), block_table_out=None, refs_out=None,
+                  copies=None, stream=None):
+    """Pages in use moved to the lowest indices (msa_compact_pages), in every tensor of
+    `caches` as fork_pages() takes them.  Returns (block_table, refs, copies [NB // 2,
+    3]): copies lists the moves (from, to, 128), then (-1, -1, 0)."""
+    dev, B, S, NB = _table(block_table, seq_lens, refs)
+    handles = _caches(caches, NB, dev)
+    block_table_out = _out(block_table_out, "block_table_out", (B, S), dev)
+    refs_out = _out(refs_out, "refs_out", (NB,), dev)
+    copies = _out(copies, "copies", (NB // 2, 3), dev)
+    _distinct((block_table_out, refs_out, copies), (block_table, seq_lens, refs))
+    st = _lib().msa_compact_pages(
+        block_table.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(), block_table_out.data_ptr(),
+        refs_out.data_ptr(), copies.data_ptr(), B, S, NB, handles, len(caches),
+        _stream(dev, stream))
+    _native.check(st, "msa_compact_pages")
+    return block_table_out, refs_out, copies
+
+
+def copy_pages(copies, caches, stream=None):
+    """Copies of pages (msa_copy_pages): copies int32 [n, 3] of (source page,
+    destination page, token rows), as fork_pages() and compact_pages() return them, in
+    every tensor of `caches` (further layers' caches, say)."""
+    _need(copies, "copies", (torch.int32,))
+    dev = copies.device
+    if copies.dim() != 2 or copies.shape[1] != 3:
+        raise ValueError("copies must be [n, 3]")
+    if not caches:
+        return
+    NB = caches[0].shape[0] if isinstance(caches[0], torch.Tensor) and caches[0].dim() else None
+    handles = _caches(caches, NB, dev)
+    st = _lib().msa_copy_pages(copies.data_ptr(), copies.shape[0], NB, handles, len(caches),
+                               _stream(dev, stream))
+    _native.check(st, "msa_copy_pages")
 
 
 def set_union_tile(enable: bool) -> bool:

@@ -18,6 +18,16 @@ ERR_SCORE_NAN = 0x10
 ERR_TIMEOUT = 0x20
 ERR_POS_RANGE = 0x40
 ERR_SCALE = 0x80
+ERR_ROW_RANGE = 0x100
+ERR_NO_PAGES = 0x200
+ERR_REFS = 0x400
+
+
+class Cache(ctypes.Structure):
+    """msa_cache_t."""
+    _fields_ = [("base", ctypes.c_void_p), ("units", ctypes.c_int), ("rows", ctypes.c_int),
+                ("row_bytes", ctypes.c_int)]
+
 
 #: Every symbol include/msa.h declares.
 EXPORTS = ("msa_score", "msa_topk", "msa_workspace_bytes", "msa_choose_splits",
@@ -31,7 +41,10 @@ EXPORTS = ("msa_score", "msa_topk", "msa_workspace_bytes", "msa_choose_splits",
            "msa_append_kv", "msa_append_kv_prefill", "msa_score_scaled",
            "msa_sparse_decode_scaled", "msa_sparse_decode_select_scaled",
            "msa_dense_decode_scaled", "msa_sparse_prefill_scaled",
-           "msa_sparse_prefill_select_scaled", "msa_decode_step_scaled")
+           "msa_sparse_prefill_select_scaled", "msa_decode_step_scaled",
+           "msa_score_prefill", "msa_topk_prefill", "msa_dense_prefill",
+           "msa_dense_prefill_workspace_bytes", "msa_fork_pages", "msa_compact_pages",
+           "msa_copy_pages")
 
 _lib = None
 _lock = threading.Lock()
@@ -112,6 +125,19 @@ def load(path: str | None = None):
         sizes = [i32, i32, i32, i32, i32, i64, f32, f32, P]
         lib.msa_append_kv.argtypes = rows + sizes
         lib.msa_append_kv_prefill.argtypes = rows + [P] + sizes
+        # prefill batches over every visible page
+        lib.msa_dense_prefill.argtypes = [P, f32, P, P, P, P, P, P, sz, P, i32, i32, i32, i32, i32,
+                                          i64, f32, f32, f32, P]
+        lib.msa_dense_prefill_workspace_bytes.argtypes = [i32]
+        lib.msa_dense_prefill_workspace_bytes.restype = sz
+        lib.msa_score_prefill.argtypes = [P, f32, P, P, i32, P, P, P, P, i32, i32, i32, i32, i32,
+                                          i64, f32, f32, P]
+        lib.msa_topk_prefill.argtypes = [P, i64, i64, i64, P, P, P, i32, i32, i32, i32, i32, P]
+        # the cache's pages
+        caches = [ctypes.POINTER(Cache), i32]
+        lib.msa_fork_pages.argtypes = [P] * 9 + [i32, i32, i32, i64] + caches + [P]
+        lib.msa_compact_pages.argtypes = [P] * 6 + [i32, i32, i64] + caches + [P]
+        lib.msa_copy_pages.argtypes = [P, i32, i64] + caches + [P]
         lib.msa_set_input_overlap.argtypes = [i32]
         lib.msa_set_union_tile.argtypes = [i32]
         lib.msa_test_wait_timeout.argtypes = [ctypes.c_ulonglong, P]
@@ -129,7 +155,9 @@ def load(path: str | None = None):
                      "msa_append_kv", "msa_append_kv_prefill", "msa_score_scaled",
                      "msa_sparse_decode_scaled", "msa_sparse_decode_select_scaled",
                      "msa_dense_decode_scaled", "msa_sparse_prefill_scaled",
-                     "msa_sparse_prefill_select_scaled", "msa_decode_step_scaled"):
+                     "msa_sparse_prefill_select_scaled", "msa_decode_step_scaled",
+                     "msa_score_prefill", "msa_topk_prefill", "msa_dense_prefill",
+                     "msa_fork_pages", "msa_compact_pages", "msa_copy_pages"):
             getattr(lib, name).restype = i32
         _lib = lib
         return lib

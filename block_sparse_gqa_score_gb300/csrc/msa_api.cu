@@ -9,6 +9,7 @@
 #include <cmath>
 #include <cstdint>
 #include <atomic>
+#include <initializer_list>
 #include <mutex>
 
 #include "msa.h"
@@ -838,6 +839,237 @@ int msa_append_kv_prefill(const void* k, int64_t k_stride, const void* v, int64_
   return append_kv(k, k_stride, v, v_stride, q, q_stride, cos_sin, max_pos, rot_dim, interleaved,
                    kv, kv_scales, q_out, q_scale, block_table, seq_lens, cu_seqlens_q, B, 1, T, Hq,
                    Hkv, S, num_blocks, k_scale, v_scale, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+// Checks and parameter block that msa_dense_prefill and msa_score_prefill share: one
+// query length per request (cu_q), page scales or none.  *empty: there is no work.
+int prepare_prefill(const void* q, float q_scale, const void* kv, const float* kv_scales,
+                    bool k_only, const int32_t* block_table, const int32_t* seq_lens,
+                    const int32_t* cu_q, int B, int T, int Hq, int Hkv, int S, int64_t num_blocks,
+                    float sm_scale, float k_scale, msa::PrefillParams* p, CUtensorMap* map,
+                    bool* empty) {
+  *empty = true;
+  if (!(q_scale == 0.f || finite_pos(q_scale)) || !finite_pos(sm_scale) || !finite_pos(k_scale) ||
+      !aligned(kv_scales, k_only ? 4 : 8))
+    return MSA_EINVAL;
+  if (!cu_q || !aligned(cu_q, 4) || T < 0 || T > INT_MAX / 4 || (B == 0) != (T == 0)) return MSA_EINVAL;
+  if (T == 0) return MSA_OK;
+  int st = check_common(q, kv, block_table, seq_lens, B, 1, Hq, Hkv, S, num_blocks);
+  if (st != MSA_OK) return st;
+  DeviceState* dev;
+  if ((st = device_state(&dev)) != MSA_OK) return st;
+  if ((st = encode_kv_map(kv, Hkv, num_blocks, map, /*l2_256=*/false,
+                          k_only ? MSA_HEAD_DIM : 2 * MSA_HEAD_DIM)) != MSA_OK)
+    return st;
+  *p = msa::PrefillParams{};
+  p->q = q_scale > 0.f ? nullptr : static_cast<const uint16_t*>(q);
+  p->q8 = q_scale > 0.f ? static_cast<const uint8_t*>(q) : nullptr;
+  p->q_scale = q_scale;
+  p->kv_scales = kv_scales;
+  p->scale_sides = k_only ? 1 : 2;
+  p->block_table = block_table;
+  p->seq_lens = seq_lens;
+  p->cu_q = cu_q;
+  p->kv = static_cast<const uint8_t*>(kv);
+  p->err = dev->err;
+  p->B = B;
+  p->T = T;
+  p->Hq = Hq;
+  p->Hkv = Hkv;
+  p->S = S;
+  p->ctas = dev->sm_count;
+  p->num_blocks = num_blocks;
+  p->logit_scale = sm_scale * k_scale;
+  *empty = false;
+  return MSA_OK;
+}
+
+// The copies of a fork or a compaction, or the caller's own, over all of its caches.
+int check_caches(const msa_cache_t* caches, int num_caches) {
+  if (num_caches < 0 || (num_caches > 0 && !caches)) return MSA_EINVAL;
+  for (int c = 0; c < num_caches; ++c) {
+    const msa_cache_t& h = caches[c];
+    if (h.units < 1 || h.row_bytes < 1 || (h.rows != 1 && h.rows != MSA_PAGE_SIZE)) return MSA_EINVAL;
+    const int unit = h.rows == 1 ? 4 : 16;    // bytes that move at once
+    if (!h.base || !aligned(h.base, unit) || h.row_bytes % unit) return MSA_EINVAL;
+  }
+  return MSA_OK;
+}
+
+int enqueue_copies(const int32_t* copies, int n, const msa_cache_t* caches, int num_caches,
+                   int64_t num_blocks, const DeviceState& dev, cudaStream_t stream, bool pdl) {
+  if (n == 0) return MSA_OK;
+  for (int c0 = 0; c0 < num_caches; c0 += msa::kMaxCopyCaches) {
+    msa::CopyParams p{};
+    p.copies = copies;
+    p.n = n;
+    p.num_blocks = static_cast<int>(num_blocks);
+    p.err = dev.err;
+    p.sms = dev.sm_count;
+    p.caches = num_caches - c0 < msa::kMaxCopyCaches ? num_caches - c0 : msa::kMaxCopyCaches;
+    for (int c = 0; c < p.caches; ++c) {
+      const msa_cache_t& h = caches[c0 + c];
+      p.cache[c] = msa::CopyCache{static_cast<uint8_t*>(h.base), h.units, h.rows, h.row_bytes};
+    }
+    const int st = from_cuda(msa::launch_copy(p, stream, pdl || c0 > 0));
+    if (st != MSA_OK) return st;
+  }
+  return MSA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t msa_dense_prefill_workspace_bytes(int sm_count) {
+  return sm_count < 1 || sm_count > 4096 ? 0 : msa::dense_prefill_workspace(sm_count);
+}
+
+int msa_dense_prefill(const void* q, float q_scale, const void* kv, const float* kv_scales,
+                      const int32_t* block_table, const int32_t* seq_lens,
+                      const int32_t* cu_seqlens_q, void* workspace, size_t workspace_bytes,
+                      void* out, int B, int T, int Hq, int Hkv, int S, int64_t num_blocks,
+                      float sm_scale, float k_scale, float v_scale, msa_stream_t stream) {
+  msa::PrefillParams p;
+  CUtensorMap map;
+  bool empty;
+  if (T != 0 && (!out || !aligned(out, 16))) return MSA_EINVAL;
+  if (!std::isfinite(v_scale)) return MSA_EINVAL;
+  const int st = prepare_prefill(q, q_scale, kv, kv_scales, false, block_table, seq_lens,
+                                 cu_seqlens_q, B, T, Hq, Hkv, S, num_blocks, sm_scale, k_scale, &p,
+                                 &map, &empty);
+  if (st != MSA_OK || empty) return st;
+  if (!workspace || !aligned(workspace, 16) ||
+      workspace_bytes < msa::dense_prefill_workspace(p.ctas))
+    return MSA_ENOSPC;
+  const int64_t rows = static_cast<int64_t>(p.ctas) * 2 * 16 * MSA_GROUP;
+  p.out = static_cast<uint16_t*>(out);
+  p.part_o = static_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + rows * MSA_HEAD_DIM);
+  p.cut = reinterpret_cast<int4*>(p.part_ml + rows);
+  p.logit_scale *= 1.4426950408889634f;
+  p.v_scale = v_scale;
+  return from_cuda(msa::launch_dense_prefill(map, p, reinterpret_cast<cudaStream_t>(stream),
+                                             input_overlap()));
+}
+
+int msa_score_prefill(const void* q, float q_scale, const void* kv, const float* kv_scales,
+                      int k_only, const int32_t* block_table, const int32_t* seq_lens,
+                      const int32_t* cu_seqlens_q, float* scores, int B, int T, int Hq, int Hkv,
+                      int S, int64_t num_blocks, float sm_scale, float k_scale,
+                      msa_stream_t stream) {
+  msa::PrefillParams p;
+  CUtensorMap map;
+  bool empty;
+  if (T != 0 && (!scores || !aligned(scores, 4))) return MSA_EINVAL;
+  const int st = prepare_prefill(q, q_scale, kv, kv_scales, k_only != 0, block_table, seq_lens,
+                                 cu_seqlens_q, B, T, Hq, Hkv, S, num_blocks, sm_scale, k_scale, &p,
+                                 &map, &empty);
+  if (st != MSA_OK || empty) return st;
+  p.scores = scores;
+  return from_cuda(msa::launch_score_prefill(map, p, reinterpret_cast<cudaStream_t>(stream),
+                                             input_overlap()));
+}
+
+int msa_topk_prefill(const float* scores, int64_t stride_h, int64_t stride_t, int64_t stride_n,
+                     const int32_t* seq_lens, const int32_t* cu_seqlens_q, int32_t* topk, int B,
+                     int T, int Hkv, int S, int k, msa_stream_t stream) {
+  if (k != MSA_TOPK || B < 0 || B > 65535 || T < 0 || T > INT_MAX / 4 || Hkv < 1 || S < 1 ||
+      (B == 0) != (T == 0) || static_cast<int64_t>(T) * Hkv > INT_MAX / 2)
+    return MSA_EINVAL;
+  if (T == 0) return MSA_OK;
+  if (!scores || !seq_lens || !cu_seqlens_q || !topk || !aligned(scores, 4) || !aligned(seq_lens, 4) ||
+      !aligned(cu_seqlens_q, 4) || !aligned(topk, 4))
+    return MSA_EINVAL;
+  DeviceState* dev;
+  const int st = device_state(&dev);
+  if (st != MSA_OK) return st;
+  msa::TopkParams p{};
+  p.scores = scores;
+  p.stride_h = stride_h;
+  p.stride_t = stride_t;
+  p.stride_n = stride_n;
+  p.seq_lens = seq_lens;
+  p.cu_q = cu_seqlens_q;
+  p.topk = topk;
+  p.err = dev->err;
+  p.B = B;
+  p.T = T;
+  p.Hkv = Hkv;
+  p.S = S;
+  return from_cuda(msa::launch_topk(p, reinterpret_cast<cudaStream_t>(stream), input_overlap()));
+}
+
+int msa_fork_pages(const int32_t* block_table, const int32_t* seq_lens, const int32_t* parents,
+                   const int32_t* grow, const int32_t* refs, int32_t* block_table_out,
+                   int32_t* seq_lens_out, int32_t* refs_out, int32_t* copies, int B, int rows,
+                   int S, int64_t num_blocks, const msa_cache_t* caches, int num_caches,
+                   msa_stream_t stream) {
+  if (B < 0 || B > msa::kMaxForkRows || rows < 0 || rows > msa::kMaxForkRows || S < 1 ||
+      static_cast<int64_t>(B > rows ? B : rows) * S > INT_MAX || num_blocks < 1 || num_blocks > INT_MAX)
+    return MSA_EINVAL;
+  int st = check_caches(caches, num_caches);
+  if (st != MSA_OK) return st;
+  if (B > 0 && (!block_table || !seq_lens)) return MSA_EINVAL;
+  if (rows > 0 && (!parents || !block_table_out || !seq_lens_out || !copies)) return MSA_EINVAL;
+  if (!refs || !refs_out || refs == refs_out || (B > 0 && block_table == block_table_out) ||
+      (B > 0 && seq_lens == seq_lens_out))
+    return MSA_EINVAL;
+  for (const void* x : {static_cast<const void*>(block_table), static_cast<const void*>(seq_lens),
+                        static_cast<const void*>(parents), static_cast<const void*>(grow),
+                        static_cast<const void*>(refs), static_cast<const void*>(block_table_out),
+                        static_cast<const void*>(seq_lens_out), static_cast<const void*>(refs_out),
+                        static_cast<const void*>(copies)})
+    if (!aligned(x, 4)) return MSA_EINVAL;
+  DeviceState* dev;
+  if ((st = device_state(&dev)) != MSA_OK) return st;
+  const msa::ForkParams p{block_table,  seq_lens, parents, grow, refs, block_table_out,
+                          seq_lens_out, refs_out, copies,  dev->err, B, rows, S,
+                          static_cast<int>(num_blocks)};
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if ((st = from_cuda(msa::launch_fork(p, s, input_overlap()))) != MSA_OK) return st;
+  return enqueue_copies(copies, rows, caches, num_caches, num_blocks, *dev, s, true);
+}
+
+int msa_compact_pages(const int32_t* block_table, const int32_t* seq_lens, const int32_t* refs,
+                      int32_t* block_table_out, int32_t* refs_out, int32_t* copies, int B, int S,
+                      int64_t num_blocks, const msa_cache_t* caches, int num_caches,
+                      msa_stream_t stream) {
+  if (B < 0 || S < 1 || static_cast<int64_t>(B) * S > INT_MAX || num_blocks < 1 || num_blocks > INT_MAX)
+    return MSA_EINVAL;
+  int st = check_caches(caches, num_caches);
+  if (st != MSA_OK) return st;
+  if (B > 0 && (!block_table || !seq_lens || !block_table_out || block_table == block_table_out))
+    return MSA_EINVAL;
+  if (!refs || !refs_out || refs == refs_out || (num_blocks > 1 && !copies)) return MSA_EINVAL;
+  for (const void* x : {static_cast<const void*>(block_table), static_cast<const void*>(seq_lens),
+                        static_cast<const void*>(refs), static_cast<const void*>(block_table_out),
+                        static_cast<const void*>(refs_out), static_cast<const void*>(copies)})
+    if (!aligned(x, 4)) return MSA_EINVAL;
+  DeviceState* dev;
+  if ((st = device_state(&dev)) != MSA_OK) return st;
+  const msa::CompactParams p{block_table, seq_lens, refs, block_table_out, refs_out, copies,
+                             dev->err, B, S, static_cast<int>(num_blocks)};
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if ((st = from_cuda(msa::launch_compact(p, s, input_overlap()))) != MSA_OK) return st;
+  return enqueue_copies(copies, static_cast<int>(num_blocks / 2), caches, num_caches, num_blocks,
+                        *dev, s, true);
+}
+
+int msa_copy_pages(const int32_t* copies, int n, int64_t num_blocks, const msa_cache_t* caches,
+                   int num_caches, msa_stream_t stream) {
+  if (n < 0 || num_blocks < 1 || num_blocks > INT_MAX || !aligned(copies, 4) || (n > 0 && !copies))
+    return MSA_EINVAL;
+  int st = check_caches(caches, num_caches);
+  if (st != MSA_OK || n == 0 || num_caches == 0) return st;
+  DeviceState* dev;
+  if ((st = device_state(&dev)) != MSA_OK) return st;
+  return enqueue_copies(copies, n, caches, num_caches, num_blocks, *dev,
+                        reinterpret_cast<cudaStream_t>(stream), input_overlap());
 }
 
 int msa_test_wait_timeout(unsigned long long limit_ns, msa_stream_t stream) {

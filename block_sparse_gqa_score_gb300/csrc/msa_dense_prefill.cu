@@ -1,0 +1,702 @@
+// msa_dense_prefill.cu -- dense attention of a chunk of new tokens over the paged cache:
+// the model's dense layers in prefill and chunked prefill.
+//
+// Operation (msa_dense_prefill in include/msa.h): query token j of request b, at pos =
+// seq_lens[b] - q_len + j, attends every key t <= pos of its request:
+//   out[i, h] = sum_t softmax_t(sm_scale K_t . q[i, h]) V_t.
+// With z the logit in log2 units, vs the page's V scale and u = z + log2(vs),
+//   out = v_scale sum_t 2^(u_t - M) V8_t / sum_t 2^(u_t - M) / vs[page(t)],
+// so that the product takes weights relative to what a key contributes (without page
+// scales vs = 1).
+//
+// What bounds it: the tensor cores, 4 * 128 * 16 products a key, token and KV head
+// against a key's 256 bytes shared by the chunk's tokens.  A unit is 16 tokens x 16 heads,
+// two halves of M = 128 query rows; a step is a page of 128 keys:
+//   S = Q K^T    e4m3 x e4m3: the keys as stored; a bf16 query is two exact e4m3 parts
+//                (two products at twice the rate of a bf16 one, and no conversion of K)
+//   softmax      a query row is a tensor-memory lane and a thread: no exchange at all
+//   O += P V     fp16 x fp16 with P from tensor memory, where it takes the place of its
+//                half's S; the values are converted to fp16 (exact) by four warps, once
+//                for both halves.  (P in e4m3 parts would save the conversion and cost the
+//                softmax warps, which have more to do, two conversions for each element.)
+// While one half's softmax runs, the other half's products do: the tensor core issues
+// O(j) and S(j + 1) of one half, then of the other.  S(j + 1) may overwrite P(j) because
+// the products of a thread execute in the order they are issued.
+//
+// P = 2^(u - M + kShift) is relative to a running reference M of the row, the largest u
+// rounded up when M is set; M stays until some P would pass 2^kTop (fp16 holds 2^16), so
+// that O is rescaled in a row's first pages and then hardly ever.  So a page needs no
+// exact maximum before its first exponential: S is read 32 columns at a time, and where a
+// piece moves M, what was made of the pieces before it is rescaled, by a power of two.
+// P is rounded to fp16: 2^-11 of itself down to 2^-21 of the row's largest, and at most
+// 2^-32 of that below.  Sums are of the unrounded P, in fp32, page by page.
+//
+// A value row that a token does not see must not reach it even as NaN (0 times NaN): keys
+// past the tile's last token are 0 for all, and of those that only some of its tokens see
+// NaN codes are set to 0 and put back at the end into the rows that see them.
+//
+//   warp 0        page look-ups, TMA of K and V tiles
+//   warp 1        products (owns tensor memory)
+//   warps 2, 3    segments and query tiles, a half each
+//   warps 4..11   softmax and output, four warps a half
+//   warps 12..15  values to fp16
+// One CTA an SM, each an equal share of all pages (msa_prefill.cuh); what several CTAs
+// work on is merged by a second kernel from their parts, in the order of the pages.
+#include <cstddef>
+
+#include "msa_device.cuh"
+#include "msa_launch.h"
+#include "msa_prefill.cuh"
+#include "msa_tcgen05.cuh"
+
+namespace msa {
+
+namespace {
+
+using namespace prefill;
+
+constexpr int kThreads = 512;
+constexpr int kSlots = 3;                       // K tiles in flight
+constexpr int kVSlots = 2;                      // V tiles as stored, in flight
+constexpr int kInfo = 16;                       // pages' factors in flight
+constexpr int kExtra = 1;                       // a unit's query and output, in pages
+constexpr int kMinSteps = 3;
+constexpr int kQTile = 4 * kHalfTile;           // two halves, hi and lo parts
+constexpr int kVTile = 2 * kHalfTile;           // a page's values in fp16
+constexpr int kOffK = kQTile;
+constexpr int kOffV8 = kOffK + kSlots * kHalfTile;
+constexpr int kOffV = kOffV8 + kVSlots * kHalfTile;
+constexpr int kOffTail = kOffV + 2 * kVTile;
+constexpr int kTmemCols = 512;
+constexpr uint32_t kColS = 0, kColO = 256;      // [half] of 128 columns each
+
+constexpr float kShift = 8.f;                   // P = 2^kShift at the largest u when M is set
+constexpr float kTop = 15.f;                    // M moves when some P would pass 2^kTop
+
+struct PageInfo {
+  float k, lv, iv;      // K scale, log2 and reciprocal of the V scale
+  int block;            // logical block; -1: no key of the page is attended
+};
+
+struct Tail {
+  uint64_t k_full[kSlots], k_empty[kSlots];
+  uint64_t v8_full[kVSlots], v8_empty[kVSlots];
+  uint64_t v_full[2], v_empty[2];               // fp16 values
+  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];   // by half
+  uint64_t info_full[kInfo];
+  uint64_t seg_full[2], seg_empty[2];
+  uint64_t q_full, q_empty;
+  uint64_t finish;
+  uint32_t tmem_base;
+  int nan_seen[2];                              // by segment: NaN codes were set to 0
+  alignas(16) PageInfo info[kInfo];
+  Segment seg[2];
+  float zs[2][kTile];
+  WalkScratch scratch;
+};
+
+constexpr int kSmemBytes = kOffTail + static_cast<int>(sizeof(Tail)) + 1024;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+
+// Four e4m3 codes (a word) -> four fp16 (exact).
+__device__ __forceinline__ uint2 e4m3x4_to_f16x4(uint32_t w) {
+  uint2 r;
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(r.x), "=r"(r.y)
+      : "r"(w));
+  return r;
+}
+
+// 0x80 in each byte of w that is an e4m3 NaN (0x7F or 0xFF).
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+
+__device__ __forceinline__ void add2(float& d0, float& d1, float b0, float b1) {
+  asm("{\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%0, %1};\n\t"
+      "mov.b64 y, {%2, %3};\n\t"
+      "add.rn.f32x2 x, x, y;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(d0), "+f"(d1)
+      : "f"(b0), "f"(b1));
+}
+// (a0, a1) * b + c
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b, float c) {
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%2, %3};\n\t"
+      "mov.b64 y, {%4, %4};\n\t"
+      "mov.b64 z, {%5, %5};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    dense_prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  Tail* tail = reinterpret_cast<Tail*>(smem + kOffTail);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int parts = p.q8 ? 1 : 2;
+
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&tail->k_full[s], 1);
+      mbar_init(&tail->k_empty[s], 1);
+    }
+    for (int s = 0; s < kVSlots; ++s) {
+      mbar_init(&tail->v8_full[s], 1);
+      mbar_init(&tail->v8_empty[s], 4);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&tail->v_full[s], 4);
+      mbar_init(&tail->v_empty[s], 1);
+      mbar_init(&tail->s_full[s], 1);
+      mbar_init(&tail->p_full[s], 4);
+      mbar_init(&tail->o_full[s], 1);
+      mbar_init(&tail->o_empty[s], 4);
+      mbar_init(&tail->seg_full[s], 1);
+      mbar_init(&tail->seg_empty[s], 1 + 1 + 1 + 8 + 4);   // warps 0, 1, 3, 4..11, 12..15
+    }
+    for (int s = 0; s < kInfo; ++s) mbar_init(&tail->info_full[s], 1);
+    mbar_init(&tail->q_full, 2);
+    mbar_init(&tail->q_empty, 1);
+    mbar_init(&tail->finish, 1 + 1 + 2 + 8 + 4);
+    fence_barrier_init();
+    prefetch_tensormap(&kv_map);
+  } else if (warp == 1) {
+    tc::tmem_alloc(&tail->tmem_base, kTmemCols);
+    tc::tmem_relinquish();
+  }
+  pdl_wait();   // lengths, tables and queries may be an earlier kernel's
+  const bool bad = plan_walk<kThreads>(p, kExtra, kMinSteps, &tail->scratch);
+  tc::fence_before_thread_sync();
+  __syncthreads();
+  tc::fence_after_thread_sync();
+  const uint32_t tmem = tail->tmem_base;
+  fill_uncovered(p, bad, [&](int i) {
+    uint4* row = reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(i) * p.Hq * kHeadDim);
+    for (int x = threadIdx.x; x < p.Hq * kHeadDim / 8; x += kThreads) row[x] = make_uint4(0u, 0u, 0u, 0u);
+  });
+  bool ok = true;
+
+  if (warp < 4) {
+    if (warp == 0) {
+      // ---- K and V tiles -----------------------------------------------------------------------
+      int t = 0;    // pages so far
+      for (int i = 0; ok; ++i) {
+        ok = __all_sync(0xffffffffu, wait_for(&tail->seg_full[i & 1], (i >> 1) & 1));
+        if (!ok) break;
+        const Segment sg = tail->seg[i & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tail->seg_empty[i & 1]);
+        if (sg.ntok == 0) break;
+        const int32_t* trow = p.block_table + static_cast<int64_t>(sg.b) * p.S;
+        for (int n0 = sg.n0; n0 < sg.n1 && ok; n0 += 32) {
+          // 32 pages' entries and scales at once, a lane each
+          const int n = n0 + lane;
+          int page = 0;
+          PageInfo info{1.f, 0.f, 1.f, -1};
+          if (n < sg.n1) {
+            page = trow[n];
+            if (page < 0 || static_cast<int64_t>(page) >= p.num_blocks) {
+              flag_error(p.err, MSA_ERR_PAGE_RANGE);
+              page = 0;
+            } else {
+              info.block = n;
+              if (p.kv_scales) {
+                const PageScale sc = make_page_scale(load_page_scale(p.kv_scales, page, p.Hkv, sg.g));
+                if (sc.bad != 0.f) flag_error(p.err, MSA_ERR_SCALE);
+                info = PageInfo{sc.k, sc.lv, sc.iv, sc.bad != 0.f ? -1 : n};
+              }
+            }
+          }
+          const int have = min(32, sg.n1 - n0);
+          for (int x = 0; x < have; ++x, ++t) {
+            const int s = t % kSlots, sv = t % kVSlots;
+            ok = t < kSlots || wait_for(&tail->k_empty[s], ((t / kSlots) - 1) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const int row = (page * p.Hkv + sg.g) * kPage;
+            if (lane == x) {
+              tail->info[t % kInfo] = info;
+              mbar_arrive(&tail->info_full[t % kInfo]);
+              mbar_arrive_expect_tx(&tail->k_full[s], kHalfTile);
+              tma_load_2d(smem + kOffK + s * kHalfTile, &kv_map, 0, row, &tail->k_full[s]);
+            }
+            ok = t < kVSlots || wait_for(&tail->v8_empty[sv], ((t / kVSlots) - 1) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok && lane == x) {
+              mbar_arrive_expect_tx(&tail->v8_full[sv], kHalfTile);
+              tma_load_2d(smem + kOffV8 + sv * kHalfTile, &kv_map, kHeadDim, row, &tail->v8_full[sv]);
+            }
+            __syncwarp();
+            if (!ok) {      // this page's K tile is on its way, its V tile is not
+              if (lane == 0) (void)wait_for(&tail->k_full[s], (t / kSlots) & 1);
+              break;
+            }
+          }
+        }
+      }
+      if (lane == 0) {
+        if (!ok) flag_error(p.err, MSA_ERR_TIMEOUT);
+        // the loads still in flight land before shared memory can be released
+        for (int x = max(0, t - kSlots); x < t; ++x)
+          (void)wait_for(&tail->k_full[x % kSlots], (x / kSlots) & 1);
+        for (int x = max(0, t - kVSlots); x < t; ++x)
+          (void)wait_for(&tail->v8_full[x % kVSlots], (x / kVSlots) & 1);
+        pdl_trigger();
+        mbar_arrive(&tail->finish);
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ---- products ----------------------------------------------------------------------------
+      if (lane == 0) {
+        const uint64_t q0 = tc::sw128_kmajor_desc(smem_u32(smem));
+        const uint64_t k0 = tc::sw128_kmajor_desc(smem_u32(smem + kOffK));
+        const uint64_t v0 = tc::sw128_mnmajor16_desc(smem_u32(smem + kOffV), kHalfTile);
+        constexpr uint32_t idesc_s = tc::idesc_e4m3_f32(128, kPage);
+        constexpr uint32_t idesc_o = tc::idesc_f16_f32_bmn(128, kHeadDim);
+        int t = 0;                 // pages whose S is issued
+        int n_p[2] = {0, 0};       // pages whose O is issued, by half
+        int n_o[2] = {0, 0};       // units whose O was begun, by half
+        // S of half h against the K tile in slot s
+        auto scores = [&](int h, int s) {
+          const uint64_t bk = k0 + static_cast<uint64_t>(s) * (kHalfTile >> 4);
+          uint64_t aq = q0 + static_cast<uint64_t>(h) * (2 * kHalfTile >> 4);
+          for (int part = 0; part < parts; ++part, aq += kHalfTile >> 4) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              tc::mma_e4m3(tmem + kColS + 128 * h, aq + 2 * ks, bk + 2 * ks, idesc_s, part > 0 || ks > 0);
+          }
+          tc::commit(&tail->s_full[h]);
+        };
+        // O of half h with the values of page tv (of all pages)
+        auto output = [&](int h, int tv, bool begin) {
+          if (!wait_for(&tail->p_full[h], n_p[h] & 1)) return false;
+          if (!wait_for(&tail->v_full[tv & 1], (tv >> 1) & 1)) return false;
+          if (begin) {             // the unit before has been read out of O
+            if (n_o[h] > 0 && !wait_for(&tail->o_empty[h], (n_o[h] - 1) & 1)) return false;
+            ++n_o[h];
+          }
+          tc::fence_after_thread_sync();
+          const uint64_t bv = v0 + static_cast<uint64_t>(tv & 1) * (kVTile >> 4);
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)    // 16 keys each: 8 columns of P, two 8-row groups of V
+            tc::mma_f16_tmem(tmem + kColO + 128 * h, tmem + kColS + 128 * h + 8 * ks,
+                             bv + static_cast<uint64_t>(ks) * (2048 >> 4), idesc_o, !begin || ks > 0);
+          ++n_p[h];
+          return true;
+        };
+        for (int i = 0; ok; ++i) {
+          ok = wait_for(&tail->seg_full[i & 1], (i >> 1) & 1);
+          if (!ok) break;
+          const int ntok = tail->seg[i & 1].ntok, pages = tail->seg[i & 1].n1 - tail->seg[i & 1].n0;
+          mbar_arrive(&tail->seg_empty[i & 1]);
+          if (ntok == 0) break;
+          const int halves = ntok > kHalfTokens ? 2 : 1;
+          if (pages == 0) continue;
+          ok = wait_for(&tail->q_full, n_o[0] & 1);
+          for (int x = 0; x <= pages && ok; ++x) {
+            const int s = t % kSlots;
+            for (int h = 0; h < halves && ok; ++h) {
+              if (x > 0) {
+                ok = output(h, t - 1, x == 1);
+                if (!ok) break;
+                if (h == halves - 1) tc::commit(&tail->v_empty[(t - 1) & 1]);
+                if (x == pages) tc::commit(&tail->o_full[h]);
+              }
+              if (x < pages) {
+                if (h == 0) {
+                  ok = wait_for(&tail->k_full[s], (t / kSlots) & 1);
+                  if (!ok) break;
+                  tc::fence_after_thread_sync();
+                }
+                scores(h, s);
+              }
+            }
+            if (x < pages && ok) {
+              tc::commit(&tail->k_empty[s]);
+              if (x == pages - 1) tc::commit(&tail->q_empty);   // the query tile has been read
+              ++t;
+            }
+          }
+        }
+        if (!ok) flag_error(p.err, MSA_ERR_TIMEOUT);
+        tc::commit(&tail->finish);
+      }
+      __syncwarp();
+      (void)mbar_wait(&tail->finish, 0);
+      tc::fence_after_thread_sync();
+      tc::tmem_dealloc(tmem, kTmemCols);
+    } else {
+      // ---- segments and query tiles --------------------------------------------------------------
+      const int h = warp - 2;
+      bool any_cut = false;
+      int tiles = 0;         // query tiles so far
+      for (int i = 0;; ++i) {
+        ok = __all_sync(0xffffffffu, i < 2 || wait_for(&tail->seg_empty[i & 1], ((i >> 1) - 1) & 1));
+        if (!ok) break;
+        if (h == 0) {
+          if (lane == 0) {
+            bool cut;
+            int n;
+            const Segment next = next_segment(p, tail->scratch.walk, kExtra, cut, n);
+            tail->seg[i & 1] = next;
+            tail->nan_seen[i & 1] = 0;
+            if (cut) p.cut[blockIdx.x] = make_int4(n, next.tok0, next.ntok, next.g);
+            any_cut |= cut;
+            mbar_arrive(&tail->seg_full[i & 1]);
+          }
+          __syncwarp();
+        } else {
+          ok = __all_sync(0xffffffffu, wait_for(&tail->seg_full[i & 1], (i >> 1) & 1));
+          if (!ok) break;
+        }
+        const Segment sg = tail->seg[i & 1];
+        if (h == 0) {
+          // a part without pages (of the unit's extra steps alone) is empty
+          if (sg.ntok > 0 && sg.slot >= 0 && sg.n0 == sg.n1)
+            for (int x = lane; x < kGroup * kTile; x += 32)
+              p.part_ml[static_cast<int64_t>(sg.slot) * (kGroup * kTile) + x] = make_float2(-INFINITY, 0.f);
+        }
+        if (sg.ntok > 0 && sg.n0 < sg.n1) {
+          // (the query tile has one place; its bytes are asked for by now, in L2)
+          ok = __all_sync(0xffffffffu, tiles == 0 || wait_for(&tail->q_empty, (tiles - 1) & 1));
+          if (!ok) break;
+          ++tiles;
+          load_half_tile(p, sg.g, sg.tok0 + kHalfTokens * h, min(kHalfTokens, sg.ntok - kHalfTokens * h),
+                         smem + h * 2 * kHalfTile, tail->zs[i & 1] + kHalfTokens * h, lane);
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tail->q_full);
+        }
+        __syncwarp();
+        if (lane == 0 && h == 1) mbar_arrive(&tail->seg_empty[i & 1]);
+        if (sg.ntok == 0) break;
+      }
+      if (lane == 0) {
+        if (h == 0 && !any_cut) p.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
+        if (!ok) flag_error(p.err, MSA_ERR_TIMEOUT);
+        mbar_arrive(&tail->finish);
+      }
+      __syncwarp();
+    }
+  } else if (warp < 12) {
+    // ---- softmax of one half -------------------------------------------------------------------
+    const int h = (warp - 4) >> 2, quarter = warp & 3;
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
+    const uint32_t s_at = lane_addr + kColS + 128 * h, o_at = lane_addr + kColO + 128 * h;
+    const int row = 32 * quarter + lane;                 // of the half
+    const int j = kHalfTokens * h + row / kGroup;        // this row's token of the tile
+    int t = 0, mine = 0, units = 0;
+    for (int i = 0; ok; ++i) {
+      ok = __all_sync(0xffffffffu, wait_for(&tail->seg_full[i & 1], (i >> 1) & 1));
+      if (!ok) break;
+      const Segment sg = tail->seg[i & 1];
+      if (sg.ntok == 0) break;
+      const int pages = sg.n1 - sg.n0;
+      if (pages == 0 || (h == 1 && sg.ntok <= kHalfTokens)) {
+        t += pages;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tail->seg_empty[i & 1]);
+        continue;
+      }
+      const int pos = sg.pos0 + j;
+      float zs = 0.f;
+      float M = -INFINITY;      // the reference, -inf until the row has seen a key
+      float l = 0.f;
+      for (int n = sg.n0; n < sg.n1; ++n, ++t, ++mine) {
+        ok = wait_for(&tail->s_full[h], mine & 1) &&
+             wait_for(&tail->info_full[t % kInfo], (t / kInfo) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const PageInfo in = tail->info[t % kInfo];
+        if (n == sg.n0) zs = tail->zs[i & 1][j];
+        tc::fence_after_thread_sync();
+        const int lim = in.block < 0 ? -1 : pos - n * kPage;  // keys <= lim are visible
+        const bool edge = __any_sync(0xffffffffu, lim < kPage - 1);
+        const float zt = zs * in.k;
+        float nl = M == -INFINITY ? 0.f : in.lv - M + kShift;
+        float a0 = 0.f, a1 = 0.f, b0 = 0.f, b1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          tc::ld_32x32b_x32(s_at + 32 * c, v);
+          tc::wait_ld();
+          float s[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) s[e] = __uint_as_float(v[e]);
+          if (edge) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[e] = 32 * c + e <= lim ? s[e] : -INFINITY;
+          }
+          float top = fmaxf(s[0], s[1]), top1 = fmaxf(s[2], s[3]);
+#pragma unroll
+          for (int e = 4; e < 32; e += 4) {
+            top = fmax3f(top, s[e], s[e + 1]);
+            top1 = fmax3f(top1, s[e + 2], s[e + 3]);
+          }
+          const float u = fmaf(fmaxf(top, top1), zt, in.lv);   // -inf: no visible key
+          const bool move = u - M > kTop - kShift;             // true while the row has no reference
+          if (__any_sync(0xffffffffu, move)) {
+            const float to = move ? ceilf(u) : M;
+            const float al = move ? ex2(M - to) : 1.f;         // a power of two; 0 at the first
+            M = to;
+            nl = M == -INFINITY ? 0.f : in.lv - M + kShift;
+            l *= al;
+            a0 *= al, a1 *= al, b0 *= al, b1 *= al;
+            // this page's P so far
+            tc::wait_st();
+            for (int k = 0; k < c; ++k) {
+              uint32_t w[16];
+              tc::ld_32x32b_x16(s_at + 16 * k, w);
+              tc::wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
+                w[e] = pack_f16x2(f.x * al, f.y * al);
+              }
+              tc::st_32x32b_x16(s_at + 16 * k, w);
+            }
+            if (n > sg.n0) {
+              // the products so far are complete: S(n) was issued behind them
+              for (int k = 0; k < 128; k += 16) {
+                uint32_t w[16];
+                tc::ld_32x32b_x16(o_at + k, w);
+                tc::wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * al);
+                tc::st_32x32b_x16(o_at + k, w);
+              }
+            }
+          }
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            float x0, x1, x2, x3;
+            fma2(x0, x1, s[e], s[e + 1], zt, nl);
+            fma2(x2, x3, s[e + 2], s[e + 3], zt, nl);
+            x0 = ex2(x0), x1 = ex2(x1), x2 = ex2(x2), x3 = ex2(x3);
+            add2(a0, a1, x0, x1);
+            add2(b0, b1, x2, x3);
+            w[e / 2] = pack_f16x2(x0, x1);
+            w[e / 2 + 1] = pack_f16x2(x2, x3);
+          }
+          // over columns that have been read
+          tc::st_32x32b_x16(s_at + 16 * c, w);
+        }
+        l = fmaf((a0 + a1) + (b0 + b1), in.iv, l);
+        tc::wait_st();
+        tc::fence_before_thread_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tail->p_full[h]);
+      }
+      if (!ok) break;
+      // ---- the row's output
+      ok = __all_sync(0xffffffffu, wait_for(&tail->o_full[h], units & 1));
+      if (!ok) break;
+      ++units;
+      tc::fence_after_thread_sync();
+      const bool nan_seen = tail->nan_seen[i & 1] != 0;
+      const bool there = j < sg.ntok;
+      // (P was 2^kShift times the weights; a row with a NaN logit is NaN altogether)
+      float inv = l > 0.f ? __fdividef(p.v_scale, l) : 0.f;
+      if (l != l) inv = l;
+      const bool whole = sg.slot < 0;
+      const int64_t part = static_cast<int64_t>(sg.slot) * (kGroup * kTile) + 128 * h + row;
+      uint16_t* out = p.out + (static_cast<int64_t>(sg.tok0 + j) * p.Hq + sg.g * kGroup + row % kGroup) * kHeadDim;
+#pragma unroll
+      for (int c = 0; c < 128; c += 32) {
+        uint32_t v[32];
+        tc::ld_32x32b_x32(o_at + c, v);
+        tc::wait_ld();
+        if (nan_seen) {
+          // value rows that only some of the tile's tokens see: back to NaN for this one
+          for (int key = sg.pos0 + 1; key <= pos && there; ++key) {
+            const int n = key / kPage;
+            if (n < sg.n0 || n >= sg.n1) continue;
+            const int page = p.block_table[static_cast<int64_t>(sg.b) * p.S + n];
+            if (page < 0 || static_cast<int64_t>(page) >= p.num_blocks) continue;
+            if (p.kv_scales &&
+                make_page_scale(load_page_scale(p.kv_scales, page, p.Hkv, sg.g)).bad != 0.f)
+              continue;
+            const uint8_t* val = p.kv + ((static_cast<int64_t>(page) * p.Hkv + sg.g) * kPage + key % kPage) *
+                                 kRowBytes + kHeadDim + c;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if ((val[e] & 0x7F) == 0x7F) v[e] = 0x7FFFFFFFu;
+          }
+        }
+        if (!there) continue;
+        if (whole) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              w[x] = f32_to_bf16_bits(__uint_as_float(v[e + 2 * x]) * inv) |
+                     (f32_to_bf16_bits(__uint_as_float(v[e + 2 * x + 1]) * inv) << 16);
+            *reinterpret_cast<uint4*>(out + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<uint4*>(p.part_o + part * kHeadDim + c + e) =
+                make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        }
+      }
+      if (!whole && there) p.part_ml[part] = make_float2(M, l);
+      tc::fence_before_thread_sync();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&tail->o_empty[h]);
+        mbar_arrive(&tail->seg_empty[i & 1]);
+      }
+    }
+    if (lane == 0) {
+      if (!ok) flag_error(p.err, MSA_ERR_TIMEOUT);
+      mbar_arrive(&tail->finish);
+    }
+    __syncwarp();
+  } else {
+    // ---- values to fp16 ------------------------------------------------------------------------
+    // eight lanes take 16-byte chunks 0..3 of an even key's row and 4..7 of the next one's
+    // (then the other way round), so that neither side has bank conflicts
+    const int w4 = warp - 12;
+    int t = 0;
+    for (int i = 0; ok; ++i) {
+      ok = __all_sync(0xffffffffu, wait_for(&tail->seg_full[i & 1], (i >> 1) & 1));
+      if (!ok) break;
+      const Segment sg = tail->seg[i & 1];
+      if (sg.ntok == 0) break;
+      for (int n = sg.n0; n < sg.n1; ++n, ++t) {
+        const int sv = t % kVSlots, b = t & 1;
+        ok = wait_for(&tail->v8_full[sv], (t / kVSlots) & 1) &&
+             wait_for(&tail->info_full[t % kInfo], (t / kInfo) & 1) &&
+             (t < 2 || wait_for(&tail->v_empty[b], ((t >> 1) - 1) & 1));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const bool none = tail->info[t % kInfo].block < 0;
+        // keys <= all: seen by every token of the tile; keys > last: by none
+        const int all = none ? -1 : sg.pos0 - n * kPage;
+        const int last = none ? -1 : all + sg.ntok - 1;
+        const uint8_t* from = smem + kOffV8 + sv * kHalfTile;
+        uint8_t* to = smem + kOffV + b * kVTile;
+        bool nan = false;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const int key = 32 * w4 + 8 * (x >> 1) + 2 * (lane >> 3) + ((lane >> 2) & 1);
+          const int c = (lane & 3) + 4 * (((lane >> 2) & 1) ^ (x & 1));
+          uint4 r = *reinterpret_cast<const uint4*>(from + sw128(key, c));
+          if (key > all) {
+            if (key > last) {
+              r = make_uint4(0u, 0u, 0u, 0u);
+            } else {
+              uint32_t* q = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t m = nan_bytes(q[e]);
+                if (m) {
+                  nan = true;
+                  q[e] &= ~((m >> 7) * 0xFFu);
+                }
+              }
+            }
+          }
+          const uint2 f0 = e4m3x4_to_f16x4(r.x), f1 = e4m3x4_to_f16x4(r.y);
+          const uint2 f2 = e4m3x4_to_f16x4(r.z), f3 = e4m3x4_to_f16x4(r.w);
+          uint8_t* half = to + (c >> 2) * kHalfTile;
+          *reinterpret_cast<uint4*>(half + sw128(key, 2 * (c & 3))) = make_uint4(f0.x, f0.y, f1.x, f1.y);
+          *reinterpret_cast<uint4*>(half + sw128(key, 2 * (c & 3) + 1)) = make_uint4(f2.x, f2.y, f3.x, f3.y);
+        }
+        if (nan) tail->nan_seen[i & 1] = 1;
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&tail->v8_empty[sv]);
+          mbar_arrive(&tail->v_full[b]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tail->seg_empty[i & 1]);
+    }
+    if (lane == 0) {
+      if (!ok) flag_error(p.err, MSA_ERR_TIMEOUT);
+      mbar_arrive(&tail->finish);
+    }
+    __syncwarp();
+  }
+}
+
+// ---- merge of shared units: blockIdx.x's unit, a warp a query row ------------------------------
+constexpr int kMergeWarps = 8;
+constexpr int kRows = kGroup * kTile;
+
+__global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const PrefillParams p) {
+  pdl_trigger();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int4 cut = p.cut[blockIdx.x];    // parts, first token, tokens, KV head
+  const int row = blockIdx.y * kMergeWarps + warp;
+  if (cut.x == 0 || row >= kGroup * cut.z) return;
+  const int64_t c = blockIdx.x;
+  auto place = [&](int k) { return (k == 0 ? 2 * c + 1 : 2 * (c + k)) * kRows + row; };
+  float M = -INFINITY;
+  for (int k = lane; k < cut.x; k += 32) {
+    const float2 ml = p.part_ml[place(k)];
+    if (ml.y != 0.f) M = fmaxf(M, ml.x);
+  }
+  M = warp_max_f32(M);
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = 0; k < cut.x; ++k) {
+    const int64_t at = place(k);
+    const float2 ml = p.part_ml[at];
+    if (ml.y == 0.f) continue;            // (not for a NaN)
+    const float w = ml.x == -INFINITY ? 1.f : ex2(ml.x - M);   // no reference: the sum is NaN
+    const float4 v = *reinterpret_cast<const float4*>(p.part_o + at * kHeadDim + 4 * lane);
+    l = fmaf(w, ml.y, l);
+    o.x = fmaf(w, v.x, o.x);
+    o.y = fmaf(w, v.y, o.y);
+    o.z = fmaf(w, v.z, o.z);
+    o.w = fmaf(w, v.w, o.w);
+  }
+  float inv = l > 0.f ? __fdividef(p.v_scale, l) : 0.f;
+  if (l != l) inv = l;
+  uint2 w;
+  w.x = f32_to_bf16_bits(o.x * inv) | (f32_to_bf16_bits(o.y * inv) << 16);
+  w.y = f32_to_bf16_bits(o.z * inv) | (f32_to_bf16_bits(o.w * inv) << 16);
+  uint16_t* out = p.out + (static_cast<int64_t>(cut.y + row / kGroup) * p.Hq + cut.w * kGroup +
+                           row % kGroup) * kHeadDim;
+  *reinterpret_cast<uint2*>(out + 4 * lane) = w;
+}
+
+}  // namespace
+
+size_t dense_prefill_workspace(int ctas) {
+  return static_cast<size_t>(ctas) * (2 * kRows * (kHeadDim * sizeof(float) + sizeof(float2)) + sizeof(int4));
+}
+
+cudaError_t launch_dense_prefill(const CUtensorMap& kv_map, const PrefillParams& p,
+                                 cudaStream_t stream, bool pdl) {
+  static std::atomic<unsigned long long> attr_done{0};
+  cudaError_t e = once_per_device(attr_done, [&] {
+    return cudaFuncSetAttribute(dense_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kSmemBytes);
+  });
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(dense_prefill_kernel, dim3(static_cast<unsigned>(p.ctas)), dim3(kThreads), kSmemBytes,
+                 stream, pdl, kv_map, p);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(merge_kernel, dim3(static_cast<unsigned>(p.ctas), kRows / kMergeWarps),
+                    dim3(kMergeWarps * 32), 0, stream, true, p);
+}
+
+}  // namespace msa

@@ -34,6 +34,10 @@ struct TopkParams {
   int32_t* topk;                         // [T, Hkv, 16]
   unsigned* err;
   int B, Q, Hkv, S;
+  // prefill-style batches: request r owns tokens [cu_q[r], cu_q[r + 1]) of the T
+  // tokens (then Q is unused); nullptr: every request has Q tokens
+  const int32_t* cu_q;
+  int T;
 };
 
 struct AttendParams {
@@ -161,6 +165,83 @@ struct AppendParams {
   int sms;
 };
 cudaError_t launch_append(const AppendParams& p, cudaStream_t stream, bool pdl);
+
+// Prefill batches over every visible page: dense attention (msa_dense_prefill.cu)
+// and the block scorer (msa_score_prefill.cu).
+struct PrefillParams {
+  const uint16_t* q;           // bf16 bits [T, Hq, 128] (when q8 is null)
+  const uint8_t* q8;           // fp8 e4m3 [T, Hq, 128], value q8 * q_scale; or nullptr
+  float q_scale;
+  const float* kv_scales;      // page scales [num_blocks, Hkv, scale_sides]; or nullptr
+  int scale_sides;             // 2 (K|V pages) or 1 (K-only pages)
+  const int32_t* block_table;  // [B, S]
+  const int32_t* seq_lens;     // [B]
+  const int32_t* cu_q;         // [B + 1]
+  const uint8_t* kv;           // the cache (value rows with a NaN are looked at again)
+  uint16_t* out;               // dense: bf16 bits [T, Hq, 128]
+  float* scores;               // scorer: [Hkv, T, S]
+  float* part_o;               // dense: [2 ctas][256][128], parts of units that CTAs share
+  float2* part_ml;             // [2 ctas][256] (reference, sum)
+  int4* cut;                   // [ctas] what each CTA's shared unit is
+  unsigned* err;
+  int B, T, Hq, Hkv, S;
+  int ctas;
+  int64_t num_blocks;
+  float logit_scale;           // dense: sm_scale * k_scale * log2(e); scorer: sm_scale * k_scale
+  float v_scale;
+};
+// Bytes of the dense kernel's part_o, part_ml and cut together.
+size_t dense_prefill_workspace(int ctas);
+cudaError_t launch_dense_prefill(const CUtensorMap& kv_map, const PrefillParams& p,
+                                 cudaStream_t stream, bool pdl);
+cudaError_t launch_score_prefill(const CUtensorMap& kv_map, const PrefillParams& p,
+                                 cudaStream_t stream, bool pdl);
+
+// The cache's pages (msa_pages.cu).
+struct ForkParams {
+  const int32_t* table;        // [B, S]
+  const int32_t* lens;         // [B]
+  const int32_t* parents;      // [rows]
+  const int32_t* grow;         // [rows]; or nullptr
+  const int32_t* refs;         // [num_blocks]
+  int32_t* table_out;          // [rows, S]
+  int32_t* lens_out;           // [rows]
+  int32_t* refs_out;           // [num_blocks]
+  int32_t* copies;             // [rows, 3]
+  unsigned* err;
+  int B, rows, S;
+  int num_blocks;
+};
+struct CompactParams {
+  const int32_t* table;        // [B, S]
+  const int32_t* lens;         // [B]
+  const int32_t* refs;         // [num_blocks]
+  int32_t* table_out;
+  int32_t* refs_out;
+  int32_t* copies;             // [num_blocks / 2, 3]
+  unsigned* err;
+  int B, S;
+  int num_blocks;
+};
+// One cache of a copy: pages of `units` runs of `rows` rows of row_bytes; a copy of r
+// token rows takes the first r rows of each unit (rows 1: the whole unit).
+struct CopyCache {
+  uint8_t* base;
+  int units, rows, row_bytes;
+};
+constexpr int kMaxCopyCaches = 64;
+struct CopyParams {
+  const int32_t* copies;       // [n, 3]: source page, destination page, token rows
+  int n, num_blocks;
+  int caches;
+  unsigned* err;
+  int sms;
+  CopyCache cache[kMaxCopyCaches];
+};
+constexpr int kMaxForkRows = 8192;
+cudaError_t launch_fork(const ForkParams& p, cudaStream_t stream, bool pdl);
+cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream, bool pdl);
+cudaError_t launch_copy(const CopyParams& p, cudaStream_t stream, bool pdl);
 
 // The bounded-wait exit exercised on purpose (msa_waittest.cu).
 cudaError_t launch_wait_timeout(unsigned long long limit_ns, unsigned* err, cudaStream_t stream);

@@ -1,0 +1,276 @@
+// msa_prefill.cuh -- what the kernels over every visible page of a prefill batch share
+// (dense attention, the block scorer): how the work is cut over the CTAs, and the query
+// tiles.
+//
+// A unit is a tile of 16 query tokens of one request and one KV head, 256 query rows that
+// see the pages 0 .. pos / 128 of the tile's last token.  A unit's work is its pages (and
+// kExtra steps for its query and its output); the units of all requests, in the order
+// (request, KV head, tile), make one line of steps, and every CTA takes the same share of
+// the line, whatever the lengths are: a unit that a share's end cuts is worked on by
+// several CTAs, a range of its pages each.  A request's steps are a closed form of its
+// lengths (tiles lie 16 tokens apart and pages 128 long, so the pages of tile t are
+// floor((a + t) / 8) + 1), so a CTA finds its place by one scan over the requests and a
+// search over one request's tiles, and nothing is planned on the host.
+#pragma once
+
+#include "msa_device.cuh"
+#include "msa_launch.h"
+
+namespace msa {
+namespace prefill {
+
+constexpr int kTile = 16;               // query tokens of a unit
+constexpr int kHalfTokens = 8;          // query tokens of one 128-row half
+
+// mbar_wait with one try before the clock is read: most waits here find their phase
+// complete.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, unsigned parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = global_ns();
+  while (!mbar_try_wait_sleep(bar, parity, 1000000u))
+    if (global_ns() - t0 > kWaitLimitNs) return false;
+  return true;
+}
+
+// A request's query tokens, and whether they can be worked on.
+struct Request {
+  int start, ql, L;
+  bool bad;
+  __device__ __forceinline__ int ctx() const { return L - ql; }
+  __device__ __forceinline__ int tiles() const { return (ql + kTile - 1) / kTile; }
+};
+
+__device__ __forceinline__ Request load_request(const PrefillParams& p, int b) {
+  Request r;
+  const int c0 = p.cu_q[b], c1 = p.cu_q[b + 1];
+  r.L = p.seq_lens[b];
+  r.start = c0;
+  r.bad = c0 < 0 || c1 < c0 || c1 > p.T || r.L < 0 || (r.L > 0 && (r.L - 1) / kPage >= p.S) ||
+          r.L < c1 - c0;
+  r.ql = r.bad ? 0 : c1 - c0;
+  return r;
+}
+
+// sum over u < y of floor(u / 8)
+__device__ __forceinline__ int64_t eighths(int64_t y) {
+  const int64_t q = y >> 3;
+  return 4 * q * (q - 1) + (y & 7) * q;
+}
+
+// Pages that tile t of the request sees.
+__device__ __forceinline__ int tile_pages(const Request& r, int t) {
+  return (r.ctx() + min(kTile * (t + 1), r.ql) - 1) / kPage + 1;
+}
+
+// Steps of the request's first x tiles for one KV head.
+__device__ __forceinline__ int64_t tile_steps(const Request& r, int x, int extra) {
+  const int full = min(x, r.ql / kTile);       // tiles of 16 tokens
+  const int64_t a = (r.ctx() + kTile - 1) / kTile;
+  int64_t s = full + eighths(a + full) - eighths(a) + static_cast<int64_t>(extra) * x;
+  if (x > full) s += (r.L - 1) / kPage + 1;
+  return s;
+}
+
+// What one CTA works on next: pages n0 .. n1 - 1 of a unit.
+struct Segment {
+  int b, g;
+  int tok0, ntok;       // the tile's first token and how many it has (0: no more segments)
+  int pos0;             // position of the first token
+  int n0, n1;
+  int slot;             // where this part of a shared unit goes; -1: the unit is whole
+};
+
+// The CTA's share of the line of steps and its place in it.
+struct Walk {
+  int64_t w, w1;        // the steps [w, w1) are still to do
+  int64_t total;
+  int active;           // CTAs that have a share
+  int b, g, t;
+  int64_t s;            // steps of the current unit that lie before w
+  Request r;
+};
+
+struct WalkScratch {
+  int64_t part[32];
+  Walk walk;
+};
+
+// Sets up scratch->walk for this CTA; every thread of the block calls it, and may use
+// the scratch behind it.  min_steps: CTAs have shares of at least this many steps (fewer
+// CTAs take part in little work).  Returns whether some request's lengths are bad.
+template <int kThreads>
+__device__ __forceinline__ bool plan_walk(const PrefillParams& p, int extra, int min_steps,
+                                          WalkScratch* scratch) {
+  constexpr int kWarps = kThreads / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  bool bad = false;
+  int64_t total = 0;
+  // the line's length; a batch of at most kThreads requests is read once
+  Request r;
+  int64_t steps = 0, before = 0;
+  auto scan = [&](int b) {     // steps of request b, of those before it in the chunk; chunk total
+    r.ql = 0;
+    r.bad = false;
+    if (b < p.B) r = load_request(p, b);
+    bad |= r.bad;
+    steps = r.ql > 0 ? p.Hkv * tile_steps(r, r.tiles(), extra) : 0;
+    int64_t x = steps;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();           // the scratch of the last chunk has been read
+    if (lane == 31) scratch->part[warp] = x;
+    __syncthreads();
+    before = x - steps;
+    int64_t all = 0;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) {
+      const int64_t y = scratch->part[k];
+      if (k < warp) before += y;
+      all += y;
+    }
+    return all;
+  };
+  for (int b0 = 0; b0 < p.B; b0 += kThreads) total += scan(b0 + tid);
+  int64_t active = total / min_steps;
+  active = active < 1 ? 1 : (active < gridDim.x ? active : static_cast<int64_t>(gridDim.x));
+  const int64_t c = blockIdx.x;
+  const int64_t w0 = c < active ? total * c / active : total;
+  const int64_t w1 = c < active ? total * (c + 1) / active : total;
+  if (tid == 0) {
+    scratch->walk.w = w0;
+    scratch->walk.w1 = w1;
+    scratch->walk.total = total;
+    scratch->walk.active = static_cast<int>(active);
+  }
+  if (w0 < w1) {
+    int64_t base = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+      const int64_t all = p.B > kThreads ? scan(b0 + tid) : total;
+      const int64_t at = base + before;
+      if (steps > 0 && w0 >= at && w0 < at + steps) {
+        Walk& k = scratch->walk;
+        const int64_t per_head = steps / p.Hkv;
+        k.b = b0 + tid;
+        k.r = r;
+        k.g = static_cast<int>((w0 - at) / per_head);
+        const int64_t in = w0 - at - k.g * per_head;
+        int x = 0, y = r.tiles();        // the last tile that begins at or before `in`
+        while (y - x > 1) {
+          const int m = (x + y) >> 1;
+          if (tile_steps(r, m, extra) <= in) x = m;
+          else y = m;
+        }
+        k.t = x;
+        k.s = in - tile_steps(r, x, extra);
+      }
+      base += all;
+    }
+  }
+  return __syncthreads_or(bad);
+}
+
+// The next segment of the walk (one thread, or a warp alike); ntok 0 when the share is
+// done.  first_cut: the unit starts here and other CTAs end it; `parts` of them in all,
+// this one among them.
+__device__ __forceinline__ Segment next_segment(const PrefillParams& p, Walk& k, int extra,
+                                                bool& first_cut, int& parts) {
+  Segment s;
+  first_cut = false;
+  parts = 0;
+  s.ntok = 0;
+  if (k.w >= k.w1) return s;
+  const int np = tile_pages(k.r, k.t);
+  const int64_t steps = np + extra;
+  const int64_t s0 = k.s, s1 = min(steps, s0 + (k.w1 - k.w));
+  s.b = k.b;
+  s.g = k.g;
+  s.tok0 = k.r.start + kTile * k.t;
+  s.ntok = min(kTile, k.r.ql - kTile * k.t);
+  s.pos0 = k.r.ctx() + kTile * k.t;
+  // the extra steps come first
+  s.n0 = static_cast<int>(max(s0 - extra, static_cast<int64_t>(0)));
+  s.n1 = static_cast<int>(max(s1 - extra, static_cast<int64_t>(0)));
+  s.slot = s0 == 0 && s1 == steps ? -1 : 2 * static_cast<int>(blockIdx.x) + (s0 == 0 ? 1 : 0);
+  if (s0 == 0 && s1 < steps) {
+    first_cut = true;
+    // the CTA that has the unit's last step: the largest c with total c / active <= it
+    const int64_t last = k.w + steps - 1;
+    parts = static_cast<int>(((last + 1) * k.active - 1) / k.total) - static_cast<int>(blockIdx.x) + 1;
+  }
+  k.w += s1 - s0;
+  k.s = s1;
+  if (s1 == steps) {
+    k.s = 0;
+    if (++k.t == k.r.tiles()) {
+      k.t = 0;
+      if (++k.g == p.Hkv) {
+        k.g = 0;
+        if (k.w < k.w1)
+          do {
+            k.r = load_request(p, ++k.b);
+          } while (k.r.ql == 0 && k.b + 1 < p.B);
+      }
+    }
+  }
+  return s;
+}
+
+// Rows that no unit writes, a CTA in turn: `fill(token)` for the tokens before the first
+// and behind the last request's, and those of requests with bad lengths.  Every thread of
+// the block calls it (and fill); `bad` as plan_walk returned it.
+template <typename Fill>
+__device__ __forceinline__ void fill_uncovered(const PrefillParams& p, bool bad, Fill&& fill) {
+  const int first = p.B > 0 ? p.cu_q[0] : p.T, last = p.B > 0 ? p.cu_q[p.B] : p.T;
+  const bool ends = first > 0 || last < p.T;
+  if (!bad && !ends) return;
+  if (threadIdx.x == 0) flag_error(p.err, MSA_ERR_SEQ_RANGE);
+  for (int i = blockIdx.x; i < min(first, p.T); i += gridDim.x) fill(i);
+  for (int64_t i = static_cast<int64_t>(max(last, 0)) + blockIdx.x; i < p.T; i += gridDim.x)
+    fill(static_cast<int>(i));
+  if (!bad) return;
+  for (int b = 0; b < p.B; ++b) {
+    if (!load_request(p, b).bad) continue;
+    const int c0 = max(p.cu_q[b], 0), c1 = min(p.cu_q[b + 1], p.T);
+    for (int64_t i = static_cast<int64_t>(c0) + blockIdx.x; i < c1; i += gridDim.x)
+      fill(static_cast<int>(i));
+  }
+}
+
+// The query rows of `tokens` tokens of one half tile (128 rows of 128 bytes, swizzled):
+// fp8 rows as stored, or bf16 rows as hi and lo parts, 16 KiB each; rows of tokens that
+// are not there are 0.  zs[j]: factor of token j's dot products.  One warp.
+__device__ __forceinline__ void load_half_tile(const PrefillParams& p, int g, int tok0, int tokens,
+                                               uint8_t* tile, float* zs, int lane) {
+  const int64_t row0 = static_cast<int64_t>(tok0) * p.Hq + g * kGroup;
+  const int64_t step = p.Hq;
+  if (p.q8) {
+    for (int j = 0; j < kHalfTokens; ++j) {
+      if (j < tokens)
+        store_query_rows_fp8(p.q8 + (row0 + j * step) * kHeadDim, kGroup * j, tile, lane);
+      else
+        zero_query_rows(kGroup * j, tile, lane);
+      if (lane == 0) zs[j] = p.logit_scale * p.q_scale;
+    }
+    return;
+  }
+  uint8_t* lo = tile + kHalfTile;
+  uint4 raw[8];
+  if (tokens > 0) load_query_rows(p.q + row0 * kHeadDim, lane, raw);
+  for (int j = 0; j < kHalfTokens; ++j) {
+    if (j < tokens) {
+      const int e = store_query_e4m3(raw, kGroup * j, tile, lo, lane);
+      if (j + 1 < tokens) load_query_rows(p.q + (row0 + (j + 1) * step) * kHeadDim, lane, raw);
+      if (lane == 0) zs[j] = p.logit_scale * exp2i(e);
+    } else {
+      zero_query_rows(kGroup * j, tile, lane);
+      zero_query_rows(kGroup * j, lo, lane);
+      if (lane == 0) zs[j] = 0.f;
+    }
+  }
+}
+
+}  // namespace prefill
+}  // namespace msa

@@ -1,0 +1,344 @@
+// msa_score_prefill.cu -- the block scorer of prefill batches: for every (KV head, query
+// token, block) the largest visible scaled q.k over the head group and the block's keys.
+//
+// Operation (msa_score_prefill in include/msa.h): scores[g, i, n] = max over the 16 heads
+// of g and the keys t <= pos(i) of block n of sm_scale * k_scale * ks[page] * q.K_t;
+// -inf where the token sees no key of the block.
+//
+// What bounds it: the tensor cores, 2 * 128 * 16 products a key, token and KV head
+// against a key's 128 bytes shared by the chunk's tokens.  The product is S = Q K^T with
+// the query rows (16 tokens x 16 heads, two M = 128 halves) as A and a page of keys as B,
+// so that a thread's tensor-memory lane is one query row: the largest of its 128 columns
+// is 64 three-input maxima without an exchange, and a token's 16 heads are 16 lanes.  A
+// bf16 query is two exact e4m3 parts (two products a half, which cost what one bf16
+// product would, and the keys need no conversion), an fp8 query is one.  Two accumulators
+// a half in tensor memory: a half's next page is multiplied while its last one is
+// searched.  One CTA an SM, each an equal share of all pages (msa_prefill.cuh); the next
+// unit's query tile is prepared while the current one is worked on.
+//   warp 0       page look-ups, TMA of K tiles
+//   warp 1       products (owns tensor memory)
+//   warps 2, 3   segments and query tiles, a half each
+//   warps 4..11  maxima and scores, four warps a half
+#include <cstddef>
+
+#include "msa_device.cuh"
+#include "msa_launch.h"
+#include "msa_prefill.cuh"
+#include "msa_tcgen05.cuh"
+
+namespace msa {
+
+namespace {
+
+using namespace prefill;
+
+constexpr int kThreads = 384;
+constexpr int kSlots = 5;                       // K tiles in flight
+constexpr int kInfo = 16;                       // pages' factors in flight
+constexpr int kExtra = 0;
+constexpr int kMinSteps = 1;
+constexpr int kQTile = 4 * kHalfTile;           // two halves, hi and lo parts
+constexpr int kOffK = 2 * kQTile;
+constexpr int kOffTail = kOffK + kSlots * kHalfTile;
+constexpr int kTmemCols = 512;                  // [half][buffer] of 128 columns
+
+struct Tail {
+  uint64_t k_full[kSlots], k_empty[kSlots];
+  uint64_t s_full[2][2], s_empty[2][2];         // [half][buffer]
+  uint64_t info_full[kInfo];
+  uint64_t seg_full[2], seg_empty[2];
+  uint64_t q_full[2];
+  uint64_t finish;
+  uint32_t tmem_base;
+  float info[kInfo];                            // ks, or 0: no key of the page counts
+  Segment seg[2];
+  float zs[2][kTile];
+  WalkScratch scratch;
+};
+
+constexpr int kSmemBytes = kOffTail + static_cast<int>(sizeof(Tail)) + 1024;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+
+__global__ void __launch_bounds__(kThreads, 1)
+    score_prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  Tail* tail = reinterpret_cast<Tail*>(smem + kOffTail);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int parts = p.q8 ? 1 : 2;
+
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&tail->k_full[s], 1);
+      mbar_init(&tail->k_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&tail->s_full[h][s], 1);
+        mbar_init(&tail->s_empty[h][s], 4);
+      }
+      mbar_init(&tail->seg_full[s], 1);
+      mbar_init(&tail->seg_empty[s], 1 + 1 + 1 + 8);   // warps 0, 1, 3 and 4..11
+      mbar_init(&tail->q_full[s], 2);
+    }
+    for (int s = 0; s < kInfo; ++s) mbar_init(&tail->info_full[s], 1);
+    mbar_init(&tail->finish, 1 + 1 + 2 + 8);
+    fence_barrier_init();
+    prefetch_tensormap(&kv_map);
+  } else if (warp == 1) {
+    tc::tmem_alloc(&tail->tmem_base, kTmemCols);
+    tc::tmem_relinquish();
+  }
+  pdl_wait();   // lengths, tables and queries may be an earlier kernel's
+  const bool bad = plan_walk<kThreads>(p, kExtra, kMinSteps, &tail->scratch);
+  tc::fence_before_thread_sync();
+  __syncthreads();
+  tc::fence_after_thread_sync();
+  const uint32_t tmem = tail->tmem_base;
+  fill_uncovered(p, bad, [&](int i) {
+    for (int g = 0; g < p.Hkv; ++g)
+      for (int n = threadIdx.x; n < p.S; n += kThreads)
+        p.scores[(static_cast<int64_t>(g) * p.T + i) * p.S + n] = -INFINITY;
+  });
+  bool ok = true;
+
+  if (warp == 0) {
+    // ---- K tiles -----------------------------------------------------------------------------
+    int t = 0;    // pages so far
+    for (int i = 0; ok; ++i) {
+      ok = __all_sync(0xffffffffu, wait_for(&tail->seg_full[i & 1], (i >> 1) & 1));
+      if (!ok) break;
+      const Segment sg = tail->seg[i & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tail->seg_empty[i & 1]);
+      if (sg.ntok == 0) break;
+      const int32_t* trow = p.block_table + static_cast<int64_t>(sg.b) * p.S;
+      for (int n0 = sg.n0; n0 < sg.n1 && ok; n0 += 32) {
+        // 32 pages' entries and scales at once, a lane each
+        const int n = n0 + lane;
+        int page = 0;
+        float ks = 0.f;
+        if (n < sg.n1) {
+          page = trow[n];
+          ks = 1.f;
+          if (page < 0 || static_cast<int64_t>(page) >= p.num_blocks) {
+            flag_error(p.err, MSA_ERR_PAGE_RANGE);
+            page = 0;
+            ks = 0.f;
+          } else if (p.kv_scales) {
+            ks = p.kv_scales[(static_cast<int64_t>(page) * p.Hkv + sg.g) * p.scale_sides];
+            if (!page_scale_ok(ks)) {
+              flag_error(p.err, MSA_ERR_SCALE);
+              ks = 0.f;
+            }
+          }
+        }
+        const int have = min(32, sg.n1 - n0);
+        for (int x = 0; x < have; ++x, ++t) {
+          const int s = t % kSlots;
+          ok = t < kSlots || wait_for(&tail->k_empty[s], ((t / kSlots) - 1) & 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == x) {
+            tail->info[t % kInfo] = ks;
+            mbar_arrive(&tail->info_full[t % kInfo]);
+            mbar_arrive_expect_tx(&tail->k_full[s], kHalfTile);
+            tma_load_2d(smem + kOffK + s * kHalfTile, &kv_map, 0, (page * p.Hkv + sg.g) * kPage,
+                        &tail->k_full[s]);
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (lane == 0) {
+      if (!ok) flag_error(p.err, MSA_ERR_TIMEOUT);
+      for (int x = max(0, t - kSlots); x < t; ++x)
+        (void)wait_for(&tail->k_full[x % kSlots], (x / kSlots) & 1);
+      pdl_trigger();
+      mbar_arrive(&tail->finish);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---- S = Q K^T ---------------------------------------------------------------------------
+    if (lane == 0) {
+      const uint64_t q0 = tc::sw128_kmajor_desc(smem_u32(smem));
+      const uint64_t k0 = tc::sw128_kmajor_desc(smem_u32(smem + kOffK));
+      constexpr uint32_t idesc = tc::idesc_e4m3_f32(128, kPage);
+      int t = 0;
+      int n_s[2] = {0, 0};     // pages multiplied, by half
+      for (int i = 0; ok; ++i) {
+        ok = wait_for(&tail->seg_full[i & 1], (i >> 1) & 1);
+        if (!ok) break;
+        const int ntok = tail->seg[i & 1].ntok, n0 = tail->seg[i & 1].n0, n1 = tail->seg[i & 1].n1;
+        if (ntok == 0) break;
+        ok = wait_for(&tail->q_full[i & 1], (i >> 1) & 1);
+        const int halves = ntok > kHalfTokens ? 2 : 1;
+        for (int n = n0; n < n1 && ok; ++n, ++t) {
+          const int s = t % kSlots;
+          ok = wait_for(&tail->k_full[s], (t / kSlots) & 1);
+          if (!ok) break;
+          const uint64_t bk = k0 + static_cast<uint64_t>(s) * (kHalfTile >> 4);
+          for (int h = 0; h < halves; ++h) {
+            const int buf = n_s[h] & 1;
+            ok = n_s[h] < 2 || wait_for(&tail->s_empty[h][buf], ((n_s[h] >> 1) - 1) & 1);
+            if (!ok) break;
+            tc::fence_after_thread_sync();
+            const uint32_t d = tmem + 128 * (2 * h + buf);
+            uint64_t aq = q0 + static_cast<uint64_t>((i & 1) * kQTile + h * 2 * kHalfTile) / 16;
+            for (int part = 0; part < parts; ++part, aq += kHalfTile >> 4) {
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                tc::mma_e4m3(d, aq + 2 * ks, bk + 2 * ks, idesc, part > 0 || ks > 0);
+            }
+            tc::commit(&tail->s_full[h][buf]);
+            ++n_s[h];
+          }
+          tc::commit(&tail->k_empty[s]);
+        }
+        tc::commit(&tail->seg_empty[i & 1]);      // the query tile has been read
+      }
+      if (!ok) flag_error(p.err, MSA_ERR_TIMEOUT);
+      tc::commit(&tail->finish);
+    }
+    __syncwarp();
+    (void)mbar_wait(&tail->finish, 0);
+    tc::fence_after_thread_sync();
+    tc::tmem_dealloc(tmem, kTmemCols);
+  } else if (warp < 4) {
+    // ---- segments and query tiles ------------------------------------------------------------
+    const int h = warp - 2;
+    for (int i = 0;; ++i) {
+      ok = __all_sync(0xffffffffu, i < 2 || wait_for(&tail->seg_empty[i & 1], ((i >> 1) - 1) & 1));
+      if (!ok) break;
+      if (h == 0) {
+        if (lane == 0) {
+          bool cut;
+          int n;
+          tail->seg[i & 1] = next_segment(p, tail->scratch.walk, kExtra, cut, n);
+          mbar_arrive(&tail->seg_full[i & 1]);
+        }
+        __syncwarp();
+      } else {
+        ok = __all_sync(0xffffffffu, wait_for(&tail->seg_full[i & 1], (i >> 1) & 1));
+        if (!ok) break;
+      }
+      const Segment sg = tail->seg[i & 1];
+      if (sg.ntok > 0) {
+        const int mine = min(kHalfTokens, sg.ntok - kHalfTokens * h);
+        load_half_tile(p, sg.g, sg.tok0 + kHalfTokens * h, mine, smem + (i & 1) * kQTile + h * 2 * kHalfTile,
+                       tail->zs[i & 1] + kHalfTokens * h, lane);
+        tc::fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&tail->q_full[i & 1]);
+        if (h == 1) mbar_arrive(&tail->seg_empty[i & 1]);
+      }
+      if (sg.ntok == 0) break;
+    }
+    if (lane == 0) {
+      if (!ok) flag_error(p.err, MSA_ERR_TIMEOUT);
+      mbar_arrive(&tail->finish);
+    }
+    __syncwarp();
+  } else {
+    // ---- maxima of one half ------------------------------------------------------------------
+    const int h = (warp - 4) >> 2, quarter = warp & 3;
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + 256 * h;
+    const int j = kHalfTokens * h + 2 * quarter + (lane >> 4);   // this lane's token of the tile
+    int t = 0, mine = 0;      // pages so far, and those of this half
+    for (int i = 0; ok; ++i) {
+      ok = __all_sync(0xffffffffu, wait_for(&tail->seg_full[i & 1], (i >> 1) & 1));
+      if (!ok) break;
+      const Segment sg = tail->seg[i & 1];
+      if (sg.ntok == 0) break;
+      ok = __all_sync(0xffffffffu, wait_for(&tail->q_full[i & 1], (i >> 1) & 1));
+      if (!ok) break;
+      const float zs = tail->zs[i & 1][j];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tail->seg_empty[i & 1]);
+      const int pages = sg.n1 - sg.n0;
+      if (h == 1 && sg.ntok <= kHalfTokens) {
+        t += pages;
+        continue;
+      }
+      const int pos = sg.pos0 + j;
+      float* row = p.scores + (static_cast<int64_t>(sg.g) * p.T + sg.tok0 + j) * p.S;
+      const bool there = j < sg.ntok;
+      float keep = 0.f;                   // the score of block n with n % 16 == lane % 16
+      for (int n = sg.n0; n < sg.n1; ++n, ++t, ++mine) {
+        const int buf = mine & 1;
+        // (the products first: a half that skipped units may be many pages early, and
+        // info_full's phases come round)
+        ok = wait_for(&tail->s_full[h][buf], (mine >> 1) & 1) &&
+             wait_for(&tail->info_full[t % kInfo], (t / kInfo) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const float ks = tail->info[t % kInfo];
+        tc::fence_after_thread_sync();
+        const uint32_t at = lane_addr + 128 * buf;
+        const int lim = pos - n * kPage;  // keys <= lim are visible
+        float m = -INFINITY;
+        uint32_t v[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tc::ld_32x32b_x32(at + 32 * c, v[c]);
+        tc::wait_ld();
+        tc::fence_before_thread_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tail->s_empty[h][buf]);
+        if (__any_sync(0xffffffffu, lim < kPage - 1)) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            m = fmaxf(m, c <= lim ? __uint_as_float(v[c >> 5][c & 31]) : -INFINITY);
+        } else {
+          float a[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            a[c] = __uint_as_float(v[c][0]);
+#pragma unroll
+            for (int e = 1; e < 31; e += 2)
+              a[c] = fmax3f(a[c], __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
+            a[c] = fmaxf(a[c], __uint_as_float(v[c][31]));
+          }
+          m = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
+        }
+#pragma unroll
+        for (int o = 8; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float sc = ks > 0.f && lim >= 0 ? m * (zs * ks) : -INFINITY;
+        if ((n & 15) == (lane & 15)) keep = sc;
+        if ((n & 15) == 15 || n + 1 == sg.n1) {
+          // 16 neighbouring blocks of two tokens
+          const int at_n = (n & ~15) + (lane & 15);
+          if (there && at_n >= sg.n0 && at_n <= n) row[at_n] = keep;
+        }
+      }
+      if (!ok) break;
+      // behind the unit's last page: blocks that none of its tokens sees
+      const int last = (sg.pos0 + sg.ntok - 1) / kPage;
+      if (sg.n1 > last && there)
+        for (int n = last + 1 + (lane & 15); n < p.S; n += 16) row[n] = -INFINITY;
+    }
+    if (lane == 0) {
+      if (!ok) flag_error(p.err, MSA_ERR_TIMEOUT);
+      mbar_arrive(&tail->finish);
+    }
+    __syncwarp();
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_score_prefill(const CUtensorMap& kv_map, const PrefillParams& p,
+                                 cudaStream_t stream, bool pdl) {
+  static std::atomic<unsigned long long> attr_done{0};
+  const cudaError_t e = once_per_device(attr_done, [&] {
+    return cudaFuncSetAttribute(score_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kSmemBytes);
+  });
+  if (e != cudaSuccess) return e;
+  return launch_pdl(score_prefill_kernel, dim3(static_cast<unsigned>(p.ctas)), dim3(kThreads),
+                    kSmemBytes, stream, pdl, kv_map, p);
+}
+
+}  // namespace msa

@@ -110,6 +110,40 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64
       : "memory");
 }
 
+// Shared-memory matrix descriptor of an MN-major 16-bit operand stored with 128-byte
+// swizzling in atoms of 64 M (or N) elements: rows of 128 bytes, one per k, 8-row groups
+// along K 1024 bytes apart (stride byte offset), the next 64 elements along M or N
+// `mn_stride` bytes on (leading byte offset).
+__device__ __forceinline__ uint64_t sw128_mnmajor16_desc(uint32_t smem_addr, uint32_t mn_stride) {
+  const uint64_t start = (smem_addr & 0x3FFFFu) >> 4;
+  const uint64_t lbo = mn_stride >> 4;
+  const uint64_t sbo = 1024u >> 4;
+  return start | (lbo << 16) | (sbo << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// Instruction descriptor of kind::f16 with f16 A and B, fp32 accumulate, A K-major (in
+// tensor memory), B MN-major, shape M x N.
+__host__ __device__ constexpr uint32_t idesc_f16_f32_bmn(int M, int N) {
+  return (1u << 4)                                   // D format: f32
+         | (0u << 7)                                 // A format: f16
+         | (0u << 10)                                // B format: f16
+         | (1u << 16)                                // B MN-major
+         | (static_cast<uint32_t>(N >> 3) << 17)     // N / 8
+         | (static_cast<uint32_t>(M >> 4) << 24);    // M / 16
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]^T in fp16 with fp32 sums, issued by a single thread: A's
+// row r is lane r, two consecutive k a 32-bit column.
+__device__ __forceinline__ void mma_f16_tmem(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                             uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // Arrive once on `bar` when every tcgen05 operation this thread issued so far
 // has completed.
 __device__ __forceinline__ void commit(uint64_t* bar) {

@@ -20,6 +20,11 @@
  *   msa_append_kv(_prefill)  a step's keys and values into the cache, with the
  *                      rotation of their positions (and of the query's)
  *   msa_*_scaled       the same on a cache whose pages carry scales of their own
+ *   msa_score_prefill, msa_topk_prefill  stages 1 and 2 for prefill and
+ *                      chunked-prefill batches (then msa_sparse_prefill)
+ *   msa_dense_prefill  attention over every visible block for those batches
+ *   msa_fork_pages, msa_compact_pages, msa_copy_pages  the cache's pages: rows
+ *                      forked, reordered, freed and grown, pages moved together
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -92,6 +97,9 @@ typedef struct CUstream_st *msa_stream_t;
 #define MSA_ERR_TIMEOUT 0x20u     /* a bounded wait for an async copy expired         */
 #define MSA_ERR_POS_RANGE 0x40u   /* msa_append_kv: position past the rotation table  */
 #define MSA_ERR_SCALE 0x80u       /* page scale outside [2^-40, 2^40] (or NaN)        */
+#define MSA_ERR_ROW_RANGE 0x100u  /* msa_fork_pages: parent neither -1 nor a row      */
+#define MSA_ERR_NO_PAGES 0x200u   /* msa_fork_pages: fewer free pages than needed     */
+#define MSA_ERR_REFS 0x400u       /* a page that a row holds is counted as free       */
 
 /* ---- fixed geometry ----------------------------------------------------- */
 #define MSA_HEAD_DIM 128
@@ -607,6 +615,157 @@ int msa_decode_step_scaled(const void *q, float q_scale, const void *kv, const f
                            msa_stream_t stream);
 
 /*
+ * msa_score_prefill -- stage 1 for prefill and chunked prefill: msa_score with
+ * one query length per request.  cu_seqlens_q, B, T and the tokens' positions
+ * are msa_sparse_prefill's; scores fp32 [Hkv, T, S], the whole of it written, as
+ * msa_sparse_prefill_select and msa_topk_prefill read it.
+ *   q_scale    0: q is bf16; > 0: fp8 e4m3 of value q * q_scale
+ *   kv_scales  NULL: the keys are K8 * k_scale; else page scales [num_blocks,
+ *              Hkv, 2] as msa_score_scaled ([num_blocks, Hkv, 1] with k_only)
+ *   k_only     non-zero: kv is a K-only cache [num_blocks, Hkv, 128, 128]
+ * Numerics as msa_score: exact fp8 parts of the query, fp32 sums.
+ * Errors: as msa_score, cu_seqlens_q, B and T as msa_sparse_prefill, no bound on
+ * the query length, q_scale < 0 or not finite, misaligned kv_scales (MSA_EINVAL).
+ * Device: MSA_ERR_PAGE_RANGE, MSA_ERR_SCALE (K's: block scored -inf),
+ * MSA_ERR_SEQ_RANGE: a request with q_len_b > seq_lens[b], bad seq_lens[b] or a
+ * range of tokens outside 0 .. T, and tokens before cu_seqlens_q[0] or past
+ * cu_seqlens_q[B]: their rows are -inf.  Where cu_seqlens_q is not ascending it
+ * is set too, and rows of the batch may be unwritten or of either request.
+ */
+int msa_score_prefill(const void *q, float q_scale, const void *kv, const float *kv_scales,
+                      int k_only, const int32_t *block_table, const int32_t *seq_lens,
+                      const int32_t *cu_seqlens_q, float *scores, int B, int T, int Hq, int Hkv,
+                      int S, int64_t num_blocks, float sm_scale, float k_scale,
+                      msa_stream_t stream);
+
+/*
+ * msa_topk_prefill -- stage 2 for prefill and chunked prefill: msa_topk with one
+ * query length per request (cu_seqlens_q, B and T as msa_sparse_prefill); topk
+ * [T, Hkv, 16] is what msa_sparse_prefill takes.  The selection, the strides and
+ * the errors are msa_topk's; a token in no request's range or of a request with
+ * bad lengths gets all -1 and sets MSA_ERR_SEQ_RANGE.
+ */
+int msa_topk_prefill(const float *scores, int64_t stride_h, int64_t stride_t, int64_t stride_n,
+                     const int32_t *seq_lens, const int32_t *cu_seqlens_q, int32_t *topk, int B,
+                     int T, int Hkv, int S, int k, msa_stream_t stream);
+
+/*
+ * msa_dense_prefill -- prefill and chunked-prefill attention over every visible
+ * key: the dense layers of the model.  The operation of msa_dense_decode with one
+ * query length per request: token j of request b, at pos = seq_lens[b] - q_len_b
+ * + j, attends keys 0 .. pos (the chunk's own are in the cache: msa_append_kv_prefill
+ * comes first).  cu_seqlens_q, B and T as msa_sparse_prefill; any S.
+ *   q_scale    0: q is bf16; > 0: fp8 e4m3 of value q * q_scale
+ *   kv_scales  NULL: keys K8 * k_scale, values V8 * v_scale; else page scales
+ *              [num_blocks, Hkv, 2] that multiply them, as the msa_*_scaled calls
+ *   workspace  msa_dense_prefill_workspace_bytes(the device's SM count) bytes,
+ *              16-byte aligned, whatever the batch; nothing in it has to be set,
+ *              and calls whose work may overlap need one each
+ * Every element of out is written; a token that sees no key (a bad request, only
+ * bad pages) gets 0.
+ * Numerics: q.K exact in fp8 parts with fp32 sums (msa_score); probabilities are
+ * fp16 to 2^-11 of themselves down to 2^-21 of the row's largest (times the page's V
+ * scale) and to 2^-32 of that below; fp32 softmax sums and output sums, one rounding
+ * to bf16.  A NaN logit makes its head's output NaN and a NaN value its dim, of the
+ * tokens that see the key and of no other.
+ * Errors: as msa_score_prefill, plus null or misaligned out, v_scale not finite
+ * (MSA_EINVAL), workspace missing, misaligned or too small (MSA_ENOSPC).  Device:
+ * as msa_score_prefill (MSA_ERR_SCALE for either side; a bad page is skipped, a bad
+ * request's rows are 0).
+ */
+int msa_dense_prefill(const void *q, float q_scale, const void *kv, const float *kv_scales,
+                      const int32_t *block_table, const int32_t *seq_lens,
+                      const int32_t *cu_seqlens_q, void *workspace, size_t workspace_bytes,
+                      void *out, int B, int T, int Hq, int Hkv, int S, int64_t num_blocks,
+                      float sm_scale, float k_scale, float v_scale, msa_stream_t stream);
+size_t msa_dense_prefill_workspace_bytes(int sm_count);
+
+/*
+ * The cache's pages.  A pool is one count per page, refs int32 [num_blocks]: how
+ * many rows of block tables hold the page (and anyone else who keeps it, a prefix
+ * cache say); 0 makes it free.  Nothing else is kept, and nothing on the host:
+ * the calls read and write device memory in stream order and may be captured.
+ *
+ * A cache that the pages belong to, [num_blocks, units, rows, row_bytes]:
+ *   kv, packed         {kv, Hkv, 128, 256}     K-only  {k, Hkv, 128, 128}
+ *   page scales        {kv_scales, Hkv, 1, 8}  ([.., 1]: {.., Hkv, 1, 4})
+ * rows 128: rows of tokens, row_bytes a multiple of 16, base 16-byte aligned;
+ * rows 1: no token rows, row_bytes a multiple of 4, base 4-byte aligned.  Layers
+ * that share a block table are caches of one call.
+ */
+typedef struct msa_cache {
+  void *base;
+  int units, rows, row_bytes;
+} msa_cache_t;
+
+/*
+ * msa_copy_pages -- copies int32 [n, 3]: (source page, destination page, token
+ * rows) each: the first `token rows` rows of the page's units, and the whole of
+ * caches with rows 1, to the destination, in every cache given.  (-1, -1, x) is no
+ * copy, nor is 0 token rows.  No page may be the destination of two copies, or of one and the
+ * source of another.  Errors: MSA_EINVAL for bad sizes or caches (above).  Device:
+ * MSA_ERR_PAGE_RANGE (a page outside the pool, or rows outside 0 .. 128: skipped).
+ */
+int msa_copy_pages(const int32_t *copies, int n, int64_t num_blocks, const msa_cache_t *caches,
+                   int num_caches, msa_stream_t stream);
+
+/*
+ * msa_fork_pages -- the rows of the next step from those of this one: rows are
+ * forked (beams, parallel samples), reordered, freed and grown in one call.
+ *   block_table [B, S], seq_lens [B]   the rows as they are
+ *   parents [rows]   the row each new row continues, or -1: a new, empty row.  A
+ *                    row that is nobody's parent is freed.
+ *   grow [rows]      tokens that each new row will append next (NULL: 0)
+ *   refs             the pool's counts
+ * New row b has seq_lens_out[b] = seq_lens[parents[b]] + grow[b] tokens (the
+ * convention of msa_append_kv: the new tokens are counted) and the pages for them.
+ * Full pages are shared by all children.  A parent's last, not full page goes to
+ * its first child (the lowest b); every other child gets a page of its own and a
+ * copy of the rows that are filled.  The pages needed, in the order of the new
+ * rows and of their entries, are the free ones (refs 0) in ascending order; pages
+ * that this call frees are free from the next call on.
+ *   block_table_out [rows, S]   -1 behind a row's last page
+ *   seq_lens_out [rows], refs_out [num_blocks]   (a page nobody holds: 0)
+ *   copies [rows, 3]            row b's copy as msa_copy_pages takes it, or (-1, -1, 0)
+ * With caches the copies are made by this call too.  The inputs are only read,
+ * and outputs must not overlap them.
+ * Errors: MSA_EINVAL for B or rows outside 0 .. 8192, S < 1, sizes past 2^31 - 1,
+ * null or misaligned pointers (an input of no rows may be null), an output that is
+ * the input, bad caches.  Device: MSA_ERR_NO_PAGES (more pages needed than free:
+ * nothing is forked; every new row is empty, its table -1, its length 0, refs_out
+ * equals refs), MSA_ERR_ROW_RANGE (a parent outside -1 .. B - 1: the row is
+ * empty), MSA_ERR_SEQ_RANGE (a parent's length outside 0 .. 128 S: taken as 0;
+ * growth below 0 or past 128 S: taken as 0), MSA_ERR_PAGE_RANGE (an entry outside
+ * the pool: -1 in the new row, no copy), MSA_ERR_REFS (a page of a row whose count
+ * changes was counted as free: it may have been given away).
+ */
+int msa_fork_pages(const int32_t *block_table, const int32_t *seq_lens, const int32_t *parents,
+                   const int32_t *grow, const int32_t *refs, int32_t *block_table_out,
+                   int32_t *seq_lens_out, int32_t *refs_out, int32_t *copies, int B, int rows,
+                   int S, int64_t num_blocks, const msa_cache_t *caches, int num_caches,
+                   msa_stream_t stream);
+
+/*
+ * msa_compact_pages -- the L pages in use (refs not 0) moved to indices 0 .. L - 1:
+ * the k-th used page at or past L goes to the k-th free page below L, the others
+ * stay.  block_table_out [B, S] holds the rows with the new indices (-1 behind a
+ * row's last page), refs_out the counts, copies [num_blocks / 2, 3] the moves in
+ * order, 128 token rows each, then (-1, -1, 0): whoever else holds pages finds their
+ * new places there.  With caches the moves are made by this call too (the bytes of a
+ * page that moved away are left as they were).  The inputs are only read, and
+ * outputs must not overlap them.
+ * Errors: MSA_EINVAL for B < 0, S < 1, sizes past 2^31 - 1, null or misaligned
+ * pointers (tables of no rows may be null), an output that is the input, bad caches.
+ * Device: MSA_ERR_SEQ_RANGE (a row's length outside 0 .. 128 S: taken as 0),
+ * MSA_ERR_PAGE_RANGE, MSA_ERR_REFS (an entry outside the pool, or a page counted
+ * as free: -1 in the new table).
+ */
+int msa_compact_pages(const int32_t *block_table, const int32_t *seq_lens, const int32_t *refs,
+                      int32_t *block_table_out, int32_t *refs_out, int32_t *copies, int B, int S,
+                      int64_t num_blocks, const msa_cache_t *caches, int num_caches,
+                      msa_stream_t stream);
+
+/*
  * msa_set_union_tile -- how msa_sparse_decode(_select) (and msa_decode_step,
  * msa_sparse_decode_static) attend decode steps of Q >= 2 tokens per request.
  * Off (0, the default): one CTA per (token, KV head), each loading its own
@@ -637,6 +796,8 @@ int msa_set_union_tile(int enable);
  * that call's inputs: a kernel that wrote them could otherwise be read
  * before its writes are visible.  Outputs are always ordered: no library
  * kernel writes a buffer before the previous kernel has finished.
+ * msa_dense_prefill, msa_score_prefill, msa_topk_prefill and the calls on pages
+ * read nothing early.
  * msa_append_kv(_prefill), whose outputs are the other calls' inputs, reads
  * nothing early and, enqueued with the setting on, has finished before a kernel
  * enqueued after it starts (enqueued with it off, it is like any other kernel
