@@ -26,7 +26,7 @@
 // P = 2^(u - M + kShift) is relative to a running reference M of the row, the largest u
 // rounded up when M is set; M stays until some P would pass 2^kTop (fp16 holds 2^16), so
 // that O is rescaled in a row's first pages and then hardly ever.  So a page needs no
-// exact maximum before its first exponential: S is read 32 columns at a time, and where a
+// exact maximum before its first exponential: S is read 64 columns at a time, and where a
 // piece moves M, what was made of the pieces before it is rescaled, by a power of two.
 // P is rounded to fp16: 2^-11 of itself down to 2^-21 of the row's largest, and at most
 // 2^-32 of that below.  Sums are of the unrounded P, in fp32, page by page.
@@ -37,7 +37,7 @@
 //
 //   warp 0        page look-ups, TMA of K and V tiles
 //   warp 1        products (owns tensor memory)
-//   warps 2, 3    segments and query tiles, a half each
+//   warp 2        segments; with warp 3 and warps 12..15 query tiles, a token each in turn
 //   warps 4..11   softmax and output, four warps a half
 //   warps 12..15  values to fp16
 // One CTA an SM, each an equal share of all pages (msa_prefill.cuh); what several CTAs
@@ -67,6 +67,7 @@ constexpr int kOffK = kQTile;
 constexpr int kOffV8 = kOffK + kSlots * kHalfTile;
 constexpr int kOffV = kOffV8 + kVSlots * kHalfTile;
 constexpr int kOffTail = kOffV + 2 * kVTile;
+constexpr int kLoaders = 6;                     // warps that prepare query tiles
 constexpr int kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;      // [half] of 128 columns each
 
@@ -165,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&tail->seg_empty[s], 1 + 1 + 1 + 8 + 4);   // warps 0, 1, 3, 4..11, 12..15
     }
     for (int s = 0; s < kInfo; ++s) mbar_init(&tail->info_full[s], 1);
-    mbar_init(&tail->q_full, 2);
+    mbar_init(&tail->q_full, kLoaders);
     mbar_init(&tail->q_empty, 1);
     mbar_init(&tail->finish, 1 + 1 + 2 + 8 + 4);
     fence_barrier_init();
@@ -257,77 +258,113 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else if (warp == 1) {
       // ---- products ----------------------------------------------------------------------------
-      if (lane == 0) {
-        const uint64_t q0 = tc::sw128_kmajor_desc(smem_u32(smem));
-        const uint64_t k0 = tc::sw128_kmajor_desc(smem_u32(smem + kOffK));
-        const uint64_t v0 = tc::sw128_mnmajor16_desc(smem_u32(smem + kOffV), kHalfTile);
-        constexpr uint32_t idesc_s = tc::idesc_e4m3_f32(128, kPage);
-        constexpr uint32_t idesc_o = tc::idesc_f16_f32_bmn(128, kHeadDim);
-        int t = 0;                 // pages whose S is issued
-        int n_p[2] = {0, 0};       // pages whose O is issued, by half
-        int n_o[2] = {0, 0};       // units whose O was begun, by half
-        // S of half h against the K tile in slot s
-        auto scores = [&](int h, int s) {
+      const uint64_t q0 = tc::sw128_kmajor_desc(smem_u32(smem));
+      const uint64_t k0 = tc::sw128_kmajor_desc(smem_u32(smem + kOffK));
+      const uint64_t v0 = tc::sw128_mnmajor16_desc(smem_u32(smem + kOffV), kHalfTile);
+      constexpr uint32_t idesc_s = tc::idesc_e4m3_f32(128, kPage);
+      constexpr uint32_t idesc_o = tc::idesc_f16_f32_bmn(128, kHeadDim);
+      const bool leader = tc::elect_one();
+      // (the vote makes it the same for the compiler as well)
+      auto wait = [&](uint64_t* bar, unsigned parity) {
+        return __all_sync(0xffffffffu, wait_for(bar, parity)) != 0;
+      };
+      int t = 0, s = 0;          // pages whose S is issued; its slot
+      unsigned k_par = 0;
+      int n_p0 = 0, n_p1 = 0;    // pages whose O is issued, by half
+      int n_o0 = 0, n_o1 = 0;    // units whose O was begun, by half
+      // S of half h against the K tile in slot s
+      auto scores = [&](int h) {
+        if (leader) {
           const uint64_t bk = k0 + static_cast<uint64_t>(s) * (kHalfTile >> 4);
-          uint64_t aq = q0 + static_cast<uint64_t>(h) * (2 * kHalfTile >> 4);
-          for (int part = 0; part < parts; ++part, aq += kHalfTile >> 4) {
+          const uint64_t aq = q0 + static_cast<uint64_t>(h) * (2 * kHalfTile >> 4);
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            tc::mma_e4m3(tmem + kColS + 128 * h, aq + 2 * ks, bk + 2 * ks, idesc_s, ks > 0);
+          if (parts == 2) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              tc::mma_e4m3(tmem + kColS + 128 * h, aq + 2 * ks, bk + 2 * ks, idesc_s, part > 0 || ks > 0);
+              tc::mma_e4m3(tmem + kColS + 128 * h, aq + (kHalfTile >> 4) + 2 * ks, bk + 2 * ks, idesc_s, 1);
           }
           tc::commit(&tail->s_full[h]);
-        };
-        // O of half h with the values of page tv (of all pages)
-        auto output = [&](int h, int tv, bool begin) {
-          if (!wait_for(&tail->p_full[h], n_p[h] & 1)) return false;
-          if (!wait_for(&tail->v_full[tv & 1], (tv >> 1) & 1)) return false;
-          if (begin) {             // the unit before has been read out of O
-            if (n_o[h] > 0 && !wait_for(&tail->o_empty[h], (n_o[h] - 1) & 1)) return false;
-            ++n_o[h];
-          }
-          tc::fence_after_thread_sync();
+        }
+        __syncwarp();
+      };
+      // O of half h with the values of page tv (of all pages)
+      auto output = [&](int h, int tv, bool begin, int& n_p, int& n_o) {
+        if (!wait(&tail->p_full[h], n_p & 1)) return false;
+        if (!wait(&tail->v_full[tv & 1], (tv >> 1) & 1)) return false;
+        if (begin) {             // the unit before has been read out of O
+          if (n_o > 0 && !wait(&tail->o_empty[h], (n_o - 1) & 1)) return false;
+          ++n_o;
+        }
+        ++n_p;
+        tc::fence_after_thread_sync();
+        if (leader) {
           const uint64_t bv = v0 + static_cast<uint64_t>(tv & 1) * (kVTile >> 4);
+          // 16 keys each: 8 columns of P, two 8-row groups of V
+          tc::mma_f16_tmem(tmem + kColO + 128 * h, tmem + kColS + 128 * h, bv, idesc_o, !begin);
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)    // 16 keys each: 8 columns of P, two 8-row groups of V
+          for (int ks = 1; ks < 8; ++ks)
             tc::mma_f16_tmem(tmem + kColO + 128 * h, tmem + kColS + 128 * h + 8 * ks,
-                             bv + static_cast<uint64_t>(ks) * (2048 >> 4), idesc_o, !begin || ks > 0);
-          ++n_p[h];
-          return true;
-        };
-        for (int i = 0; ok; ++i) {
-          ok = wait_for(&tail->seg_full[i & 1], (i >> 1) & 1);
-          if (!ok) break;
-          const int ntok = tail->seg[i & 1].ntok, pages = tail->seg[i & 1].n1 - tail->seg[i & 1].n0;
-          mbar_arrive(&tail->seg_empty[i & 1]);
-          if (ntok == 0) break;
-          const int halves = ntok > kHalfTokens ? 2 : 1;
-          if (pages == 0) continue;
-          ok = wait_for(&tail->q_full, n_o[0] & 1);
-          for (int x = 0; x <= pages && ok; ++x) {
-            const int s = t % kSlots;
-            for (int h = 0; h < halves && ok; ++h) {
-              if (x > 0) {
-                ok = output(h, t - 1, x == 1);
-                if (!ok) break;
-                if (h == halves - 1) tc::commit(&tail->v_empty[(t - 1) & 1]);
-                if (x == pages) tc::commit(&tail->o_full[h]);
-              }
-              if (x < pages) {
-                if (h == 0) {
-                  ok = wait_for(&tail->k_full[s], (t / kSlots) & 1);
-                  if (!ok) break;
-                  tc::fence_after_thread_sync();
-                }
-                scores(h, s);
-              }
+                             bv + static_cast<uint64_t>(ks) * (2048 >> 4), idesc_o, 1);
+        }
+        __syncwarp();
+        return true;
+      };
+      for (int i = 0; ok; ++i) {
+        ok = wait(&tail->seg_full[i & 1], (i >> 1) & 1);
+        if (!ok) break;
+        const int ntok = __reduce_max_sync(0xffffffffu, tail->seg[i & 1].ntok);
+        const int pages = __reduce_max_sync(0xffffffffu, tail->seg[i & 1].n1 - tail->seg[i & 1].n0);
+        if (leader) mbar_arrive(&tail->seg_empty[i & 1]);
+        __syncwarp();
+        if (ntok == 0) break;
+        if (pages == 0) continue;
+        const bool both = ntok > kHalfTokens;
+        ok = wait(&tail->q_full, n_o0 & 1);
+        for (int x = 0; x <= pages && ok; ++x) {
+          if (x > 0) {
+            ok = output(0, t - 1, x == 1, n_p0, n_o0);
+            if (!ok) break;
+            if (leader) {
+              if (!both) tc::commit(&tail->v_empty[(t - 1) & 1]);
+              if (x == pages) tc::commit(&tail->o_full[0]);
             }
-            if (x < pages && ok) {
+            __syncwarp();
+          }
+          if (x < pages) {
+            ok = wait(&tail->k_full[s], k_par);
+            if (!ok) break;
+            tc::fence_after_thread_sync();
+            scores(0);
+          }
+          if (both) {
+            if (x > 0) {
+              ok = output(1, t - 1, x == 1, n_p1, n_o1);
+              if (!ok) break;
+              if (leader) {
+                tc::commit(&tail->v_empty[(t - 1) & 1]);
+                if (x == pages) tc::commit(&tail->o_full[1]);
+              }
+              __syncwarp();
+            }
+            if (x < pages) scores(1);
+          }
+          if (x < pages) {
+            if (leader) {
               tc::commit(&tail->k_empty[s]);
               if (x == pages - 1) tc::commit(&tail->q_empty);   // the query tile has been read
-              ++t;
+            }
+            __syncwarp();
+            ++t;
+            if (++s == kSlots) {
+              s = 0;
+              k_par ^= 1;
             }
           }
         }
+      }
+      if (leader) {
         if (!ok) flag_error(p.err, MSA_ERR_TIMEOUT);
         tc::commit(&tail->finish);
       }
@@ -367,14 +404,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               p.part_ml[static_cast<int64_t>(sg.slot) * (kGroup * kTile) + x] = make_float2(-INFINITY, 0.f);
         }
         if (sg.ntok > 0 && sg.n0 < sg.n1) {
-          // (the query tile has one place; its bytes are asked for by now, in L2)
-          ok = __all_sync(0xffffffffu, tiles == 0 || wait_for(&tail->q_empty, (tiles - 1) & 1));
+          ok = load_query_tile(p, sg, h, kLoaders, smem, tail->zs[i & 1], lane, [&] {
+            return __all_sync(0xffffffffu, tiles == 0 || wait_for(&tail->q_empty, (tiles - 1) & 1)) != 0;
+          });
           if (!ok) break;
           ++tiles;
-          load_half_tile(p, sg.g, sg.tok0 + kHalfTokens * h, min(kHalfTokens, sg.ntok - kHalfTokens * h),
-                         smem + h * 2 * kHalfTile, tail->zs[i & 1] + kHalfTokens * h, lane);
-          tc::fence_proxy_async_smem();
-          __syncwarp();
           if (lane == 0) mbar_arrive(&tail->q_full);
         }
         __syncwarp();
@@ -425,25 +459,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float zt = zs * in.k;
         float nl = M == -INFINITY ? 0.f : in.lv - M + kShift;
         float a0 = 0.f, a1 = 0.f, b0 = 0.f, b1 = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < kPage; c += 64) {
+          float s[64];
+          {
+            uint32_t v[2][32];
+            tc::ld_32x32b_x32(s_at + c, v[0]);
+            tc::ld_32x32b_x32(s_at + c + 32, v[1]);
+            tc::wait_ld();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[32];
-          tc::ld_32x32b_x32(s_at + 32 * c, v);
-          tc::wait_ld();
-          float s[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) s[e] = __uint_as_float(v[e]);
+            for (int e = 0; e < 64; ++e) s[e] = __uint_as_float(v[e >> 5][e & 31]);
+          }
           if (edge) {
+            const int to = lim - c;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) s[e] = 32 * c + e <= lim ? s[e] : -INFINITY;
+            for (int e = 0; e < 64; ++e) s[e] = e <= to ? s[e] : -INFINITY;
           }
-          float top = fmaxf(s[0], s[1]), top1 = fmaxf(s[2], s[3]);
+          float top[4];
 #pragma unroll
-          for (int e = 4; e < 32; e += 4) {
-            top = fmax3f(top, s[e], s[e + 1]);
-            top1 = fmax3f(top1, s[e + 2], s[e + 3]);
+          for (int k = 0; k < 4; ++k) {
+            top[k] = fmaxf(s[16 * k], s[16 * k + 1]);
+#pragma unroll
+            for (int e = 2; e < 16; e += 2) top[k] = fmax3f(top[k], s[16 * k + e], s[16 * k + e + 1]);
           }
-          const float u = fmaf(fmaxf(top, top1), zt, in.lv);   // -inf: no visible key
+          // -inf: no visible key
+          const float u = fmaf(fmaxf(fmax3f(top[0], top[1], top[2]), top[3]), zt, in.lv);
           const bool move = u - M > kTop - kShift;             // true while the row has no reference
           if (__any_sync(0xffffffffu, move)) {
             const float to = move ? ceilf(u) : M;
@@ -454,32 +494,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             a0 *= al, a1 *= al, b0 *= al, b1 *= al;
             // this page's P so far
             tc::wait_st();
-            for (int k = 0; k < c; ++k) {
-              uint32_t w[16];
-              tc::ld_32x32b_x16(s_at + 16 * k, w);
+            for (int k = 0; k < c / 2; k += 8) {
+              uint32_t w[8];
+              tc::ld_32x32b_x8(s_at + k, w);
               tc::wait_ld();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
+              for (int e = 0; e < 8; ++e) {
                 const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
                 w[e] = pack_f16x2(f.x * al, f.y * al);
               }
-              tc::st_32x32b_x16(s_at + 16 * k, w);
+              tc::st_32x32b_x8(s_at + k, w);
             }
             if (n > sg.n0) {
               // the products so far are complete: S(n) was issued behind them
-              for (int k = 0; k < 128; k += 16) {
-                uint32_t w[16];
-                tc::ld_32x32b_x16(o_at + k, w);
+              for (int k = 0; k < kHeadDim; k += 8) {
+                uint32_t w[8];
+                tc::ld_32x32b_x8(o_at + k, w);
                 tc::wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * al);
-                tc::st_32x32b_x16(o_at + k, w);
+                for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * al);
+                tc::st_32x32b_x8(o_at + k, w);
               }
             }
           }
-          uint32_t w[16];
+          uint32_t w[32];
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
+          for (int e = 0; e < 64; e += 4) {
             float x0, x1, x2, x3;
             fma2(x0, x1, s[e], s[e + 1], zt, nl);
             fma2(x2, x3, s[e + 2], s[e + 3], zt, nl);
@@ -489,8 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             w[e / 2] = pack_f16x2(x0, x1);
             w[e / 2 + 1] = pack_f16x2(x2, x3);
           }
-          // over columns that have been read
-          tc::st_32x32b_x16(s_at + 16 * c, w);
+          tc::st_32x32b_x32(s_at + c / 2, w);    // over columns that have been read
         }
         l = fmaf((a0 + a1) + (b0 + b1), in.iv, l);
         tc::wait_st();
@@ -570,12 +609,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     // eight lanes take 16-byte chunks 0..3 of an even key's row and 4..7 of the next one's
     // (then the other way round), so that neither side has bank conflicts
     const int w4 = warp - 12;
-    int t = 0;
+    int t = 0, tiles = 0;
     for (int i = 0; ok; ++i) {
       ok = __all_sync(0xffffffffu, wait_for(&tail->seg_full[i & 1], (i >> 1) & 1));
       if (!ok) break;
       const Segment sg = tail->seg[i & 1];
       if (sg.ntok == 0) break;
+      if (sg.n0 < sg.n1) {
+        ok = load_query_tile(p, sg, 2 + w4, kLoaders, smem, tail->zs[i & 1], lane, [&] {
+          return __all_sync(0xffffffffu, tiles == 0 || wait_for(&tail->q_empty, (tiles - 1) & 1)) != 0;
+        });
+        if (!ok) break;
+        ++tiles;
+        if (lane == 0) mbar_arrive(&tail->q_full);
+        __syncwarp();
+      }
       for (int n = sg.n0; n < sg.n1; ++n, ++t) {
         const int sv = t % kVSlots, b = t & 1;
         ok = wait_for(&tail->v8_full[sv], (t / kVSlots) & 1) &&

@@ -32,6 +32,11 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, unsigned parity) {
   return true;
 }
 
+// Makes generic-proxy shared-memory writes visible to the tensor core.
+__device__ __forceinline__ void fence_proxy_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 // A request's query tokens, and whether they can be worked on.
 struct Request {
   int start, ql, L;
@@ -239,37 +244,96 @@ __device__ __forceinline__ void fill_uncovered(const PrefillParams& p, bool bad,
   }
 }
 
-// The query rows of `tokens` tokens of one half tile (128 rows of 128 bytes, swizzled):
-// fp8 rows as stored, or bf16 rows as hi and lo parts, 16 KiB each; rows of tokens that
-// are not there are 0.  zs[j]: factor of token j's dot products.  One warp.
-__device__ __forceinline__ void load_half_tile(const PrefillParams& p, int g, int tok0, int tokens,
-                                               uint8_t* tile, float* zs, int lane) {
-  const int64_t row0 = static_cast<int64_t>(tok0) * p.Hq + g * kGroup;
-  const int64_t step = p.Hq;
-  if (p.q8) {
-    for (int j = 0; j < kHalfTokens; ++j) {
-      if (j < tokens)
-        store_query_rows_fp8(p.q8 + (row0 + j * step) * kHeadDim, kGroup * j, tile, lane);
-      else
-        zero_query_rows(kGroup * j, tile, lane);
-      if (lane == 0) zs[j] = p.logit_scale * p.q_scale;
-    }
-    return;
-  }
-  uint8_t* lo = tile + kHalfTile;
-  uint4 raw[8];
-  if (tokens > 0) load_query_rows(p.q + row0 * kHeadDim, lane, raw);
-  for (int j = 0; j < kHalfTokens; ++j) {
-    if (j < tokens) {
-      const int e = store_query_e4m3(raw, kGroup * j, tile, lo, lane);
-      if (j + 1 < tokens) load_query_rows(p.q + (row0 + (j + 1) * step) * kHeadDim, lane, raw);
-      if (lane == 0) zs[j] = p.logit_scale * exp2i(e);
+// One token's 16 query rows in a tile of 128-byte rows (swizzled): fp8 rows as stored, or
+// bf16 rows as hi and lo parts, the parts and the factor 2^e those of store_query_e4m3.  A
+// warp a token; a lane holds 8 elements of every other row (four of them with fp8 rows), so
+// that loads and stores are whole lines.
+struct QueryRows {
+  uint4 v[8];
+
+  __device__ __forceinline__ void load(const PrefillParams& p, int tok, int g, int lane) {
+    const int64_t row = static_cast<int64_t>(tok) * p.Hq + g * kGroup;
+    if (p.q8) {
+      const uint8_t* at = p.q8 + row * kHeadDim + 16 * lane;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = __ldg(reinterpret_cast<const uint4*>(at + 512 * k));
     } else {
-      zero_query_rows(kGroup * j, tile, lane);
-      zero_query_rows(kGroup * j, lo, lane);
+      const uint16_t* at = p.q + row * kHeadDim + 8 * lane;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = __ldg(reinterpret_cast<const uint4*>(at + 256 * k));
+    }
+  }
+
+  // Into rows row0 .. row0 + 15 of `hi` (and `lo`); returns the dot products' factor.
+  __device__ __forceinline__ float store(const PrefillParams& p, int row0, uint8_t* hi, uint8_t* lo,
+                                         int lane) const {
+    if (p.q8) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<uint4*>(hi + sw128(row0 + 4 * k + (lane >> 3), lane & 7)) = v[k];
+      return p.logit_scale * p.q_scale;
+    }
+    uint32_t m = 0;                       // the largest magnitudes as bf16 bits, two at a time
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      m = __vmaxu2(m, v[k].x & 0x7FFF7FFFu);
+      m = __vmaxu2(m, v[k].y & 0x7FFF7FFFu);
+      m = __vmaxu2(m, v[k].z & 0x7FFF7FFFu);
+      m = __vmaxu2(m, v[k].w & 0x7FFF7FFFu);
+    }
+    const unsigned top = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
+    const int biased = static_cast<int>(top >> 7);
+    int e = (biased == 0 || biased == 0xFF) ? 0 : biased - 127 - 7;   // largest in [2^7, 2^8)
+    e = e < -100 ? -100 : (e > 100 ? 100 : e);
+    const float sd = exp2i(-e);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+      uint32_t h[2], l[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float f[4] = {bf16_bits_to_f32(w[2 * x] & 0xFFFF) * sd,
+                            __uint_as_float(w[2 * x] & 0xFFFF0000u) * sd,
+                            bf16_bits_to_f32(w[2 * x + 1] & 0xFFFF) * sd,
+                            __uint_as_float(w[2 * x + 1] & 0xFFFF0000u) * sd};
+        split_e4m3x4(f, h[x], l[x]);
+      }
+      const int off = sw128(row0 + 2 * k + (lane >> 4), (lane & 15) >> 1) + 8 * (lane & 1);
+      *reinterpret_cast<uint2*>(hi + off) = make_uint2(h[0], h[1]);
+      *reinterpret_cast<uint2*>(lo + off) = make_uint2(l[0], l[1]);
+    }
+    return p.logit_scale * exp2i(e);
+  }
+};
+
+// Tokens first, first + step .. of a unit's query tile (two halves of 8 tokens, hi and lo
+// parts, kHalfTile bytes each; rows of tokens that are not there are 0) and their dot
+// products' factors zs[16].  One warp; wait() returns, false to give up, when the tile's
+// last readers are through: the first token's rows are on their way by then.
+template <typename Wait>
+__device__ __forceinline__ bool load_query_tile(const PrefillParams& p, const Segment& sg, int first,
+                                                int step, uint8_t* tile, float* zs, int lane,
+                                                Wait&& wait) {
+  QueryRows rows;
+  if (first < sg.ntok) rows.load(p, sg.tok0 + first, sg.g, lane);
+  if (!wait()) return false;
+  for (int j = first; j < kTile; j += step) {
+    uint8_t* hi = tile + (j / kHalfTokens) * (2 * kHalfTile);
+    uint8_t* lo = hi + kHalfTile;
+    const int row0 = kGroup * (j % kHalfTokens);
+    if (j < sg.ntok) {
+      const float z = rows.store(p, row0, hi, lo, lane);
+      if (j + step < sg.ntok) rows.load(p, sg.tok0 + j + step, sg.g, lane);
+      if (lane == 0) zs[j] = z;
+    } else if (j < kHalfTokens || sg.ntok > kHalfTokens) {   // (a half without tokens is not read)
+      zero_query_rows(row0, hi, lane);
+      if (!p.q8) zero_query_rows(row0, lo, lane);
       if (lane == 0) zs[j] = 0.f;
     }
   }
+  fence_proxy_async();
+  __syncwarp();
+  return true;
 }
 
 }  // namespace prefill

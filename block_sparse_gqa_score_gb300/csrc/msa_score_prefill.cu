@@ -17,7 +17,7 @@
 // unit's query tile is prepared while the current one is worked on.
 //   warp 0       page look-ups, TMA of K tiles
 //   warp 1       products (owns tensor memory)
-//   warps 2, 3   segments and query tiles, a half each
+//   warps 2, 3   segments and query tiles, a token each in turn
 //   warps 4..11  maxima and scores, four warps a half
 #include <cstddef>
 
@@ -161,43 +161,62 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ---- S = Q K^T ---------------------------------------------------------------------------
-    if (lane == 0) {
-      const uint64_t q0 = tc::sw128_kmajor_desc(smem_u32(smem));
-      const uint64_t k0 = tc::sw128_kmajor_desc(smem_u32(smem + kOffK));
-      constexpr uint32_t idesc = tc::idesc_e4m3_f32(128, kPage);
-      int t = 0;
-      int n_s[2] = {0, 0};     // pages multiplied, by half
-      for (int i = 0; ok; ++i) {
-        ok = wait_for(&tail->seg_full[i & 1], (i >> 1) & 1);
-        if (!ok) break;
-        const int ntok = tail->seg[i & 1].ntok, n0 = tail->seg[i & 1].n0, n1 = tail->seg[i & 1].n1;
-        if (ntok == 0) break;
-        ok = wait_for(&tail->q_full[i & 1], (i >> 1) & 1);
-        const int halves = ntok > kHalfTokens ? 2 : 1;
-        for (int n = n0; n < n1 && ok; ++n, ++t) {
-          const int s = t % kSlots;
-          ok = wait_for(&tail->k_full[s], (t / kSlots) & 1);
-          if (!ok) break;
-          const uint64_t bk = k0 + static_cast<uint64_t>(s) * (kHalfTile >> 4);
-          for (int h = 0; h < halves; ++h) {
-            const int buf = n_s[h] & 1;
-            ok = n_s[h] < 2 || wait_for(&tail->s_empty[h][buf], ((n_s[h] >> 1) - 1) & 1);
-            if (!ok) break;
-            tc::fence_after_thread_sync();
-            const uint32_t d = tmem + 128 * (2 * h + buf);
-            uint64_t aq = q0 + static_cast<uint64_t>((i & 1) * kQTile + h * 2 * kHalfTile) / 16;
-            for (int part = 0; part < parts; ++part, aq += kHalfTile >> 4) {
+    const uint64_t q0 = tc::sw128_kmajor_desc(smem_u32(smem));
+    const uint64_t k0 = tc::sw128_kmajor_desc(smem_u32(smem + kOffK));
+    constexpr uint32_t idesc = tc::idesc_e4m3_f32(128, kPage);
+    const bool leader = tc::elect_one();
+    // (the vote makes it the same for the compiler as well)
+    auto wait = [&](uint64_t* bar, unsigned parity) {
+      return __all_sync(0xffffffffu, wait_for(bar, parity)) != 0;
+    };
+    int s = 0;                 // slot of the next K tile
+    unsigned k_par = 0;
+    int n_0 = 0, n_1 = 0;      // pages multiplied, by half
+    auto scores = [&](int h, int qbuf, int& n) {
+      const int buf = n & 1;
+      if (n >= 2 && !wait(&tail->s_empty[h][buf], ((n >> 1) - 1) & 1)) return false;
+      tc::fence_after_thread_sync();
+      if (leader) {
+        const uint64_t bk = k0 + static_cast<uint64_t>(s) * (kHalfTile >> 4);
+        const uint64_t aq = q0 + static_cast<uint64_t>(qbuf) * (kQTile >> 4) +
+                            static_cast<uint64_t>(h) * (2 * kHalfTile >> 4);
+        const uint32_t d = tmem + 128 * (2 * h + buf);
 #pragma unroll
-              for (int ks = 0; ks < 4; ++ks)
-                tc::mma_e4m3(d, aq + 2 * ks, bk + 2 * ks, idesc, part > 0 || ks > 0);
-            }
-            tc::commit(&tail->s_full[h][buf]);
-            ++n_s[h];
-          }
-          tc::commit(&tail->k_empty[s]);
+        for (int ks = 0; ks < 4; ++ks) tc::mma_e4m3(d, aq + 2 * ks, bk + 2 * ks, idesc, ks > 0);
+        if (parts == 2) {
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            tc::mma_e4m3(d, aq + (kHalfTile >> 4) + 2 * ks, bk + 2 * ks, idesc, 1);
         }
-        tc::commit(&tail->seg_empty[i & 1]);      // the query tile has been read
+        tc::commit(&tail->s_full[h][buf]);
       }
+      __syncwarp();
+      ++n;
+      return true;
+    };
+    for (int i = 0; ok; ++i) {
+      ok = wait(&tail->seg_full[i & 1], (i >> 1) & 1);
+      if (!ok) break;
+      const int ntok = __reduce_max_sync(0xffffffffu, tail->seg[i & 1].ntok);
+      const int pages = __reduce_max_sync(0xffffffffu, tail->seg[i & 1].n1 - tail->seg[i & 1].n0);
+      if (ntok == 0) break;
+      ok = wait(&tail->q_full[i & 1], (i >> 1) & 1);
+      for (int x = 0; x < pages && ok; ++x) {
+        ok = wait(&tail->k_full[s], k_par);
+        if (!ok) break;
+        ok = scores(0, i & 1, n_0);
+        if (ok && ntok > kHalfTokens) ok = scores(1, i & 1, n_1);
+        if (leader) tc::commit(&tail->k_empty[s]);
+        __syncwarp();
+        if (++s == kSlots) {
+          s = 0;
+          k_par ^= 1;
+        }
+      }
+      if (leader) tc::commit(&tail->seg_empty[i & 1]);      // the query tile has been read
+      __syncwarp();
+    }
+    if (leader) {
       if (!ok) flag_error(p.err, MSA_ERR_TIMEOUT);
       tc::commit(&tail->finish);
     }
@@ -224,12 +243,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
       }
       const Segment sg = tail->seg[i & 1];
-      if (sg.ntok > 0) {
-        const int mine = min(kHalfTokens, sg.ntok - kHalfTokens * h);
-        load_half_tile(p, sg.g, sg.tok0 + kHalfTokens * h, mine, smem + (i & 1) * kQTile + h * 2 * kHalfTile,
-                       tail->zs[i & 1] + kHalfTokens * h, lane);
-        tc::fence_proxy_async_smem();
-      }
+      if (sg.ntok > 0)
+        (void)load_query_tile(p, sg, h, 2, smem + (i & 1) * kQTile, tail->zs[i & 1], lane, [] { return true; });
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&tail->q_full[i & 1]);

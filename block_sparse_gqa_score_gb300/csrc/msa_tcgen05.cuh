@@ -97,6 +97,19 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32_mn(int M, int N) {
   return idesc_e4m3_f32(M, N) | (1u << 15) | (1u << 16);
 }
 
+// One lane of a converged warp.  The products' operands are uniform registers: where the
+// whole warp runs the loop around them and this alone picks the lane that issues, the
+// descriptors are worked out there; in code of one lane each is moved there again.
+__device__ __forceinline__ bool elect_one() {
+  unsigned r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 // ---- MMA -----------------------------------------------------------------------
 
 // D[tmem] (+)= A[smem] * B[smem]^T, issued by a single thread.
