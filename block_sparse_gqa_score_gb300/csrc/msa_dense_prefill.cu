@@ -59,8 +59,9 @@ constexpr int kThreads = 512;
 constexpr int kSlots = 3;                       // K tiles in flight
 constexpr int kVSlots = 2;                      // V tiles as stored, in flight
 constexpr int kInfo = 16;                       // pages' factors in flight
-constexpr int kExtra = 1;                       // a unit's query and output, in pages
+constexpr int kExtra = 4;                       // a unit's query and output, in pages
 constexpr int kMinSteps = 3;
+constexpr int kRows = kGroup * kTile;           // query rows of a unit
 constexpr int kQTile = 4 * kHalfTile;           // two halves, hi and lo parts
 constexpr int kVTile = 2 * kHalfTile;           // a page's values in fp16
 constexpr int kOffK = kQTile;
@@ -135,6 +136,26 @@ __device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, f
       "mov.b64 {%0, %1}, x;\n\t}"
       : "=f"(d0), "=f"(d1)
       : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+
+// Four lanes' rows of four 16-byte pieces turned: lane k of a group of four gets piece k of
+// each of its rows, so that a store of the group is 64 bytes of one row.  (A thread's row
+// stored by itself, 16 bytes a line, took 4.5 us a unit.)
+__device__ __forceinline__ void turn4(uint4 (&v)[4], int lane) {
+  auto trade = [&](uint4& a, uint4& b, bool up, int x) {   // up: a goes, else b
+    uint4 g = up ? a : b;
+    g.x = __shfl_xor_sync(0xffffffffu, g.x, x);
+    g.y = __shfl_xor_sync(0xffffffffu, g.y, x);
+    g.z = __shfl_xor_sync(0xffffffffu, g.z, x);
+    g.w = __shfl_xor_sync(0xffffffffu, g.w, x);
+    if (up) a = g;
+    else b = g;
+  };
+  const bool b0 = lane & 1, b1 = lane & 2;
+  trade(v[0], v[1], b0, 1);
+  trade(v[2], v[3], b0, 1);
+  trade(v[0], v[2], b1, 2);
+  trade(v[1], v[3], b1, 2);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -400,11 +421,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (h == 0) {
           // a part without pages (of the unit's extra steps alone) is empty
           if (sg.ntok > 0 && sg.slot >= 0 && sg.n0 == sg.n1)
-            for (int x = lane; x < kGroup * kTile; x += 32)
-              p.part_ml[static_cast<int64_t>(sg.slot) * (kGroup * kTile) + x] = make_float2(-INFINITY, 0.f);
+            for (int x = lane; x < kRows; x += 32)
+              p.part_ml[static_cast<int64_t>(sg.slot) * kRows + x] = make_float2(-INFINITY, 0.f);
         }
         if (sg.ntok > 0 && sg.n0 < sg.n1) {
-          ok = load_query_tile(p, sg, h, kLoaders, smem, tail->zs[i & 1], lane, [&] {
+          ok = load_query_tile<(kTile + kLoaders - 1) / kLoaders>(p, sg, h, kLoaders, smem, tail->zs[i & 1], lane, [&] {
             return __all_sync(0xffffffffu, tiles == 0 || wait_for(&tail->q_empty, (tiles - 1) & 1)) != 0;
           });
           if (!ok) break;
@@ -549,10 +570,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       float inv = l > 0.f ? __fdividef(p.v_scale, l) : 0.f;
       if (l != l) inv = l;
       const bool whole = sg.slot < 0;
-      const int64_t part = static_cast<int64_t>(sg.slot) * (kGroup * kTile) + 128 * h + row;
-      uint16_t* out = p.out + (static_cast<int64_t>(sg.tok0 + j) * p.Hq + sg.g * kGroup + row % kGroup) * kHeadDim;
-#pragma unroll
-      for (int c = 0; c < 128; c += 32) {
+      // rows are written four at a time, 64 bytes of each by a group of four lanes
+      const int row4 = 128 * h + 32 * quarter + (lane & ~3), piece = lane & 3;
+#pragma unroll 1
+      for (int c = 0; c < kHeadDim; c += 32) {
         uint32_t v[32];
         tc::ld_32x32b_x32(o_at + c, v);
         tc::wait_ld();
@@ -573,25 +594,46 @@ __global__ void __launch_bounds__(kThreads, 1)
               if ((val[e] & 0x7F) == 0x7F) v[e] = 0x7FFFFFFFu;
           }
         }
-        if (!there) continue;
         if (whole) {
+          uint4 q[4];
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint32_t w[4];
+          for (int x = 0; x < 4; ++x) {
+            uint32_t o[4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-              w[x] = f32_to_bf16_bits(__uint_as_float(v[e + 2 * x]) * inv) |
-                     (f32_to_bf16_bits(__uint_as_float(v[e + 2 * x + 1]) * inv) << 16);
-            *reinterpret_cast<uint4*>(out + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int e = 0; e < 4; ++e)
+              o[e] = f32_to_bf16_bits(__uint_as_float(v[8 * x + 2 * e]) * inv) |
+                     (f32_to_bf16_bits(__uint_as_float(v[8 * x + 2 * e + 1]) * inv) << 16);
+            q[x] = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+          turn4(q, lane);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int r = row4 + x;
+            if (r / kGroup < sg.ntok)
+              *reinterpret_cast<uint4*>(
+                  p.out + (static_cast<int64_t>(sg.tok0 + r / kGroup) * p.Hq + sg.g * kGroup + r % kGroup) *
+                              kHeadDim + c + 8 * piece) = q[x];
           }
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<uint4*>(p.part_o + part * kHeadDim + c + e) =
-                make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+          for (int y = 0; y < 32; y += 16) {
+            uint4 q[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              q[x] = make_uint4(v[y + 4 * x], v[y + 4 * x + 1], v[y + 4 * x + 2], v[y + 4 * x + 3]);
+            turn4(q, lane);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int r = row4 + x;
+              if (r / kGroup < sg.ntok)
+                *reinterpret_cast<uint4*>(p.part_o + (static_cast<int64_t>(sg.slot) * kRows + r) * kHeadDim +
+                                          c + y + 4 * piece) = q[x];
+            }
+          }
         }
       }
-      if (!whole && there) p.part_ml[part] = make_float2(M, l);
+      if (!whole && there)
+        p.part_ml[static_cast<int64_t>(sg.slot) * kRows + 128 * h + row] = make_float2(M, l);
       tc::fence_before_thread_sync();
       __syncwarp();
       if (lane == 0) {
@@ -616,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Segment sg = tail->seg[i & 1];
       if (sg.ntok == 0) break;
       if (sg.n0 < sg.n1) {
-        ok = load_query_tile(p, sg, 2 + w4, kLoaders, smem, tail->zs[i & 1], lane, [&] {
+        ok = load_query_tile<(kTile + kLoaders - 1) / kLoaders>(p, sg, 2 + w4, kLoaders, smem, tail->zs[i & 1], lane, [&] {
           return __all_sync(0xffffffffu, tiles == 0 || wait_for(&tail->q_empty, (tiles - 1) & 1)) != 0;
         });
         if (!ok) break;
@@ -685,7 +727,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---- merge of shared units: blockIdx.x's unit, a warp a query row ------------------------------
 constexpr int kMergeWarps = 8;
-constexpr int kRows = kGroup * kTile;
 
 __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const PrefillParams p) {
   pdl_trigger();
@@ -704,17 +745,30 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const PrefillPa
   M = warp_max_f32(M);
   float l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k = 0; k < cut.x; ++k) {
-    const int64_t at = place(k);
-    const float2 ml = p.part_ml[at];
-    if (ml.y == 0.f) continue;            // (not for a NaN)
-    const float w = ml.x == -INFINITY ? 1.f : ex2(ml.x - M);   // no reference: the sum is NaN
-    const float4 v = *reinterpret_cast<const float4*>(p.part_o + at * kHeadDim + 4 * lane);
-    l = fmaf(w, ml.y, l);
-    o.x = fmaf(w, v.x, o.x);
-    o.y = fmaf(w, v.y, o.y);
-    o.z = fmaf(w, v.z, o.z);
-    o.w = fmaf(w, v.w, o.w);
+  for (int k0 = 0; k0 < cut.x; k0 += 32) {
+    // lane k: the weight of part k0 + k, 0 where it is empty
+    const float2 ml = k0 + lane < cut.x ? p.part_ml[place(k0 + lane)] : make_float2(0.f, 0.f);
+    const float mine = ml.y == 0.f ? 0.f : ml.x == -INFINITY ? 1.f : ex2(ml.x - M);   // (no reference: NaN)
+    const int have = min(32, cut.x - k0);
+    for (int k = 0; k < have; k += 4) {
+      float4 v[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const bool some = __shfl_sync(0xffffffffu, ml.y, (k + x) & 31) != 0.f && k + x < have;
+        v[x] = some ? *reinterpret_cast<const float4*>(p.part_o + place(k0 + k + x) * kHeadDim + 4 * lane)
+                    : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float w = k + x < have ? __shfl_sync(0xffffffffu, mine, (k + x) & 31) : 0.f;
+        if (w == 0.f) continue;
+        l = fmaf(w, __shfl_sync(0xffffffffu, ml.y, (k + x) & 31), l);
+        o.x = fmaf(w, v[x].x, o.x);
+        o.y = fmaf(w, v[x].y, o.y);
+        o.z = fmaf(w, v[x].z, o.z);
+        o.w = fmaf(w, v[x].w, o.w);
+      }
+    }
   }
   float inv = l > 0.f ? __fdividef(p.v_scale, l) : 0.f;
   if (l != l) inv = l;

@@ -76,6 +76,13 @@ __device__ __forceinline__ int64_t tile_steps(const Request& r, int x, int extra
   return s;
 }
 
+// (a b - minus) / c of numbers that are not negative, by 32-bit division where they fit.
+__device__ __forceinline__ int64_t scaled(int64_t a, int64_t b, int64_t c, int minus = 0) {
+  if (a < (1 << 22) && b < 512 && c < (1ll << 31))
+    return static_cast<uint32_t>(a * b - minus) / static_cast<uint32_t>(c);
+  return (a * b - minus) / c;
+}
+
 // What one CTA works on next: pages n0 .. n1 - 1 of a unit.
 struct Segment {
   int b, g;
@@ -142,8 +149,8 @@ __device__ __forceinline__ bool plan_walk(const PrefillParams& p, int extra, int
   int64_t active = total / min_steps;
   active = active < 1 ? 1 : (active < gridDim.x ? active : static_cast<int64_t>(gridDim.x));
   const int64_t c = blockIdx.x;
-  const int64_t w0 = c < active ? total * c / active : total;
-  const int64_t w1 = c < active ? total * (c + 1) / active : total;
+  const int64_t w0 = c < active ? scaled(total, c, active) : total;
+  const int64_t w1 = c < active ? scaled(total, c + 1, active) : total;
   if (tid == 0) {
     scratch->walk.w = w0;
     scratch->walk.w1 = w1;
@@ -157,10 +164,10 @@ __device__ __forceinline__ bool plan_walk(const PrefillParams& p, int extra, int
       const int64_t at = base + before;
       if (steps > 0 && w0 >= at && w0 < at + steps) {
         Walk& k = scratch->walk;
-        const int64_t per_head = steps / p.Hkv;
+        const int64_t per_head = tile_steps(r, r.tiles(), extra);
         k.b = b0 + tid;
         k.r = r;
-        k.g = static_cast<int>((w0 - at) / per_head);
+        k.g = static_cast<int>(scaled(w0 - at, 1, per_head));
         const int64_t in = w0 - at - k.g * per_head;
         int x = 0, y = r.tiles();        // the last tile that begins at or before `in`
         while (y - x > 1) {
@@ -203,7 +210,7 @@ __device__ __forceinline__ Segment next_segment(const PrefillParams& p, Walk& k,
     first_cut = true;
     // the CTA that has the unit's last step: the largest c with total c / active <= it
     const int64_t last = k.w + steps - 1;
-    parts = static_cast<int>(((last + 1) * k.active - 1) / k.total) - static_cast<int>(blockIdx.x) + 1;
+    parts = static_cast<int>(scaled(last + 1, k.active, k.total, 1)) - static_cast<int>(blockIdx.x) + 1;
   }
   k.w += s1 - s0;
   k.s = s1;
@@ -264,15 +271,10 @@ struct QueryRows {
     }
   }
 
-  // Into rows row0 .. row0 + 15 of `hi` (and `lo`); returns the dot products' factor.
-  __device__ __forceinline__ float store(const PrefillParams& p, int row0, uint8_t* hi, uint8_t* lo,
-                                         int lane) const {
-    if (p.q8) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        *reinterpret_cast<uint4*>(hi + sw128(row0 + 4 * k + (lane >> 3), lane & 7)) = v[k];
-      return p.logit_scale * p.q_scale;
-    }
+  // A bf16 row's values to their parts, in place: v[k].x, .y hi and .z, .w lo of the lane's eight
+  // elements.  Returns the dot products' factor.
+  __device__ __forceinline__ float split(const PrefillParams& p) {
+    if (p.q8) return p.logit_scale * p.q_scale;
     uint32_t m = 0;                       // the largest magnitudes as bf16 bits, two at a time
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -298,37 +300,69 @@ struct QueryRows {
                             __uint_as_float(w[2 * x + 1] & 0xFFFF0000u) * sd};
         split_e4m3x4(f, h[x], l[x]);
       }
-      const int off = sw128(row0 + 2 * k + (lane >> 4), (lane & 15) >> 1) + 8 * (lane & 1);
-      *reinterpret_cast<uint2*>(hi + off) = make_uint2(h[0], h[1]);
-      *reinterpret_cast<uint2*>(lo + off) = make_uint2(l[0], l[1]);
+      v[k] = make_uint4(h[0], h[1], l[0], l[1]);
     }
     return p.logit_scale * exp2i(e);
+  }
+
+  // Into rows row0 .. row0 + 15 of `hi` (and `lo`).
+  __device__ __forceinline__ void store(const PrefillParams& p, int row0, uint8_t* hi, uint8_t* lo,
+                                        int lane) const {
+    if (p.q8) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<uint4*>(hi + sw128(row0 + 4 * k + (lane >> 3), lane & 7)) = v[k];
+      return;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int off = sw128(row0 + 2 * k + (lane >> 4), (lane & 15) >> 1) + 8 * (lane & 1);
+      *reinterpret_cast<uint2*>(hi + off) = make_uint2(v[k].x, v[k].y);
+      *reinterpret_cast<uint2*>(lo + off) = make_uint2(v[k].z, v[k].w);
+    }
   }
 };
 
 // Tokens first, first + step .. of a unit's query tile (two halves of 8 tokens, hi and lo
 // parts, kHalfTile bytes each; rows of tokens that are not there are 0) and their dot
-// products' factors zs[16].  One warp; wait() returns, false to give up, when the tile's
-// last readers are through: the first token's rows are on their way by then.
-template <typename Wait>
+// products' factors zs[16].  One warp, which takes at most kMost tokens; wait() returns,
+// false to give up, when the tile's last readers are through: the rows are loaded and split
+// by then.
+template <int kMost, typename Wait>
 __device__ __forceinline__ bool load_query_tile(const PrefillParams& p, const Segment& sg, int first,
                                                 int step, uint8_t* tile, float* zs, int lane,
                                                 Wait&& wait) {
-  QueryRows rows;
-  if (first < sg.ntok) rows.load(p, sg.tok0 + first, sg.g, lane);
+  constexpr int kAhead = kMost < 2 ? kMost : 2;    // tokens in registers at a time
+  QueryRows rows[kAhead];
+  float z[kAhead];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k)
+    if (first + k * step < sg.ntok) rows[k].load(p, sg.tok0 + first + k * step, sg.g, lane);
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k)
+    if (first + k * step < sg.ntok) z[k] = rows[k].split(p);
   if (!wait()) return false;
-  for (int j = first; j < kTile; j += step) {
-    uint8_t* hi = tile + (j / kHalfTokens) * (2 * kHalfTile);
-    uint8_t* lo = hi + kHalfTile;
-    const int row0 = kGroup * (j % kHalfTokens);
-    if (j < sg.ntok) {
-      const float z = rows.store(p, row0, hi, lo, lane);
-      if (j + step < sg.ntok) rows.load(p, sg.tok0 + j + step, sg.g, lane);
-      if (lane == 0) zs[j] = z;
-    } else if (j < kHalfTokens || sg.ntok > kHalfTokens) {   // (a half without tokens is not read)
-      zero_query_rows(row0, hi, lane);
-      if (!p.q8) zero_query_rows(row0, lo, lane);
-      if (lane == 0) zs[j] = 0.f;
+#pragma unroll 1
+  for (int j0 = first; j0 < kTile; j0 += kAhead * step) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int j = j0 + k * step;
+      if (j >= kTile) break;
+      uint8_t* hi = tile + (j / kHalfTokens) * (2 * kHalfTile);
+      uint8_t* lo = hi + kHalfTile;
+      const int row0 = kGroup * (j % kHalfTokens);
+      if (j < sg.ntok) {
+        rows[k].store(p, row0, hi, lo, lane);
+        if (lane == 0) zs[j] = z[k];
+        if (kMost > kAhead && j + kAhead * step < sg.ntok) {
+          rows[k].load(p, sg.tok0 + j + kAhead * step, sg.g, lane);
+          z[k] = rows[k].split(p);
+        }
+      } else if (j < kHalfTokens || sg.ntok > kHalfTokens) {   // (a half without tokens is not read)
+        zero_query_rows(row0, hi, lane);
+        if (!p.q8) zero_query_rows(row0, lo, lane);
+        if (lane == 0) zs[j] = 0.f;
+      }
     }
   }
   fence_proxy_async();

@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const Segment sg = tail->seg[i & 1];
       if (sg.ntok > 0)
-        (void)load_query_tile(p, sg, h, 2, smem + (i & 1) * kQTile, tail->zs[i & 1], lane, [] { return true; });
+        (void)load_query_tile<kTile / 2>(p, sg, h, 2, smem + (i & 1) * kQTile, tail->zs[i & 1], lane, [] { return true; });
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&tail->q_full[i & 1]);
