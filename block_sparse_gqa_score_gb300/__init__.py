@@ -748,43 +748,61 @@ def _caches(caches, num_blocks, dev):
     out = (_native.Cache * max(1, len(caches)))()
     for i, c in enumerate(caches):
         _need(c, f"caches[{i}]", _KV_DTYPES + (torch.float32,), dev)
-        if c.dim() < 2 or (num_blocks is not None and c.shape[0] != num_blocks):
+        shape = c.shape
+        if len(shape) < 2 or shape[0] != num_blocks:
             raise ValueError(f"caches[{i}] must be [num_blocks, ...] of the pool's pages")
-        if c.dtype == torch.float32:          # page scales [NB, Hkv, sides]
-            if c.dim() != 3:
+        h = out[i]
+        h.base, h.units = c.data_ptr(), shape[1]
+        if c.dtype is torch.float32:          # page scales [NB, Hkv, sides]
+            if len(shape) != 3:
                 raise ValueError(f"caches[{i}]: page scales are [num_blocks, Hkv, sides]")
-            out[i] = _native.Cache(c.data_ptr(), c.shape[1], 1, 4 * c.shape[2])
+            h.rows, h.row_bytes = 1, 4 * shape[2]
         else:
-            if c.dim() != 4 or c.shape[2] != PAGE_SIZE:
+            if len(shape) != 4 or shape[2] != PAGE_SIZE:
                 raise ValueError(f"caches[{i}] must be [num_blocks, Hkv, 128, row bytes]")
-            out[i] = _native.Cache(c.data_ptr(), c.shape[1], PAGE_SIZE, c.shape[3])
+            h.rows, h.row_bytes = PAGE_SIZE, shape[3]
     return out
 
 
-def _out(t, name: str, shape, dev):
-    if t is None:
-        return torch.empty(shape, dtype=torch.int32, device=dev)
+def _int32(t, name: str, shape, dev):
+    """Checks int32 `t` of `shape` (None: any length of a vector) and returns its address
+    and end."""
+    try:
+        if (t.dtype is torch.int32 and t.is_cuda and t.is_contiguous() and t.device == dev
+                and (t.shape == shape or (shape is None and t.dim() == 1))):
+            at = t.data_ptr()
+            return at, at + 4 * t.numel()
+    except AttributeError:
+        pass
     _need(t, name, (torch.int32,), dev)
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}")
-    return t
+    raise ValueError(f"{name} must be " + ("a vector" if shape is None else str(list(shape))))
+
+
+def _outputs(given, inputs, dev):
+    """Tensors and addresses of the outputs [(tensor or None, name, shape)], which must
+    not overlap the inputs."""
+    out, at = [], []
+    for t, name, shape in given:
+        if t is None:
+            t = torch.empty(shape, dtype=torch.int32, device=dev)
+        lo, hi = _int32(t, name, shape, dev)
+        for i_lo, i_hi in inputs:
+            if lo < i_hi and i_lo < hi:
+                raise ValueError("outputs must not overlap the inputs")
+        out.append(t)
+        at.append(lo)
+    return out, at
 
 
 def _table(block_table, seq_lens, refs):
-    _need(block_table, "block_table", (torch.int32,))
-    dev = block_table.device
-    _need(seq_lens, "seq_lens", (torch.int32,), dev)
-    _need(refs, "refs", (torch.int32,), dev)
-    if block_table.dim() != 2 or seq_lens.shape != block_table.shape[:1] or refs.dim() != 1:
-        raise ValueError("block_table must be [B, S], seq_lens [B] and refs [num_blocks]")
-    return (dev, *block_table.shape, refs.shape[0])
-
-
-def _distinct(outs, ins):
-    for o in outs:
-        lo, hi = o.data_ptr(), o.data_ptr() + 4 * o.numel()
-        if any(lo < i.data_ptr() + 4 * i.numel() and i.data_ptr() < hi for i in ins):
-            raise ValueError("outputs must not overlap the inputs")
+    if not isinstance(block_table, torch.Tensor) or not isinstance(refs, torch.Tensor):
+        raise TypeError("block_table and refs must be torch.Tensors")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, S]")
+    dev, (B, S) = block_table.device, block_table.shape
+    return (dev, B, S, refs.shape[0] if refs.dim() else 0,
+            [_int32(block_table, "block_table", (B, S), dev), _int32(seq_lens, "seq_lens", (B,), dev),
+             _int32(refs, "refs", None, dev)])
 
 
 def fork_pages(block_table, seq_lens, parents, refs, caches=(), grow=None, block_table_out=None,
@@ -796,29 +814,20 @@ def fork_pages(block_table, seq_lens, parents, refs, caches=(), grow=None, block
     of `caches` (kv [NB, Hkv, 128, 256], K-only caches, page scales, of any number of
     layers).  refs [NB]: how many rows hold each page; free pages (0) are taken in
     ascending order.  Returns (block_table, seq_lens, refs, copies [rows, 3])."""
-    dev, B, S, NB = _table(block_table, seq_lens, refs)
-    _need(parents, "parents", (torch.int32,), dev)
-    if parents.dim() != 1:
-        raise ValueError("parents must be [rows]")
+    dev, B, S, NB, ins = _table(block_table, seq_lens, refs)
+    ins.append(_int32(parents, "parents", None, dev))
     rows = parents.shape[0]
     if grow is not None:
-        _need(grow, "grow", (torch.int32,), dev)
-        if grow.shape != (rows,):
-            raise ValueError("grow must be [rows]")
+        ins.append(_int32(grow, "grow", (rows,), dev))
     handles = _caches(caches, NB, dev)
-    block_table_out = _out(block_table_out, "block_table_out", (rows, S), dev)
-    seq_lens_out = _out(seq_lens_out, "seq_lens_out", (rows,), dev)
-    refs_out = _out(refs_out, "refs_out", (NB,), dev)
-    copies = _out(copies, "copies", (rows, 3), dev)
-    _distinct((block_table_out, seq_lens_out, refs_out, copies),
-              (block_table, seq_lens, parents, refs) + (() if grow is None else (grow,)))
+    out, at = _outputs(((block_table_out, "block_table_out", (rows, S)),
+                        (seq_lens_out, "seq_lens_out", (rows,)), (refs_out, "refs_out", (NB,)),
+                        (copies, "copies", (rows, 3))), ins, dev)
     st = _lib().msa_fork_pages(
-        block_table.data_ptr(), seq_lens.data_ptr(), parents.data_ptr(),
-        None if grow is None else grow.data_ptr(), refs.data_ptr(), block_table_out.data_ptr(),
-        seq_lens_out.data_ptr(), refs_out.data_ptr(), copies.data_ptr(), B, rows, S, NB, handles,
-        len(caches), _stream(dev, stream))
+        ins[0][0], ins[1][0], ins[3][0], None if grow is None else ins[4][0], ins[2][0], *at, B,
+        rows, S, NB, handles, len(caches), _stream(dev, stream))
     _native.check(st, "msa_fork_pages")
-    return block_table_out, seq_lens_out, refs_out, copies
+    return tuple(out)
 
 
 def compact_pages(block_table, seq_lens, refs, caches=(), block_table_out=None, refs_out=None,
@@ -826,18 +835,14 @@ def compact_pages(block_table, seq_lens, refs, caches=(), block_table_out=None, 
     """Pages in use moved to the lowest indices (msa_compact_pages), in every tensor of
     `caches` as fork_pages() takes them.  Returns (block_table, refs, copies [NB // 2,
     3]): copies lists the moves (from, to, 128), then (-1, -1, 0)."""
-    dev, B, S, NB = _table(block_table, seq_lens, refs)
+    dev, B, S, NB, ins = _table(block_table, seq_lens, refs)
     handles = _caches(caches, NB, dev)
-    block_table_out = _out(block_table_out, "block_table_out", (B, S), dev)
-    refs_out = _out(refs_out, "refs_out", (NB,), dev)
-    copies = _out(copies, "copies", (NB // 2, 3), dev)
-    _distinct((block_table_out, refs_out, copies), (block_table, seq_lens, refs))
-    st = _lib().msa_compact_pages(
-        block_table.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(), block_table_out.data_ptr(),
-        refs_out.data_ptr(), copies.data_ptr(), B, S, NB, handles, len(caches),
-        _stream(dev, stream))
+    out, at = _outputs(((block_table_out, "block_table_out", (B, S)), (refs_out, "refs_out", (NB,)),
+                        (copies, "copies", (NB // 2, 3))), ins, dev)
+    st = _lib().msa_compact_pages(ins[0][0], ins[1][0], ins[2][0], *at, B, S, NB, handles,
+                                  len(caches), _stream(dev, stream))
     _native.check(st, "msa_compact_pages")
-    return block_table_out, refs_out, copies
+    return tuple(out)
 
 
 def copy_pages(copies, caches, stream=None):
@@ -850,7 +855,7 @@ def copy_pages(copies, caches, stream=None):
         raise ValueError("copies must be [n, 3]")
     if not caches:
         return
-    NB = caches[0].shape[0] if isinstance(caches[0], torch.Tensor) and caches[0].dim() else None
+    NB = caches[0].shape[0] if isinstance(caches[0], torch.Tensor) and caches[0].dim() else 0
     handles = _caches(caches, NB, dev)
     st = _lib().msa_copy_pages(copies.data_ptr(), copies.shape[0], NB, handles, len(caches),
                                _stream(dev, stream))

@@ -88,15 +88,6 @@ struct Shared {
 // ---------------------------------------------------------------------------
 // fork
 
-// Row b of the next step, from its parent row: n tokens are taken over.
-struct ForkRow {
-  int parent;     // -1: none
-  int n, grow;
-  int held;       // entries taken over from the parent (all but a page to be copied)
-  int want;       // entries of the row
-  bool copy;      // the parent's begun page goes to another row: entry `held` is a copy
-};
-
 __device__ __forceinline__ int row_tokens(const int32_t* lens, int row, int S, bool& bad) {
   const int L = lens[row];
   if (L >= 0 && (L == 0 || (L - 1) / kPage < S)) return L;
@@ -104,29 +95,33 @@ __device__ __forceinline__ int row_tokens(const int32_t* lens, int row, int S, b
   return 0;
 }
 
-__device__ __forceinline__ ForkRow fork_row(const ForkParams& p, const int* first, int b,
-                                            unsigned& bad) {
-  ForkRow r;
-  r.parent = p.parents[b];
+// Row b of the next step: n tokens are taken over from the parent row.
+struct ForkRow {
+  int parent;     // -1: none
+  int n, grow;
+  __device__ __forceinline__ bool copied(const int* first, int b) const {
+    // the parent's begun page goes to another row: entry held() is a copy
+    return n % kPage != 0 && first[parent] != b;
+  }
+  // entries taken over from the parent (all but a page to be copied), and entries of the row
+  __device__ __forceinline__ int held(bool copy) const { return pages_of(n) - (copy ? 1 : 0); }
+  __device__ __forceinline__ int want() const { return pages_of(static_cast<int64_t>(n) + grow); }
+};
+
+__device__ __forceinline__ ForkRow load_fork_row(const ForkParams& p, int b, unsigned& bad) {
+  ForkRow r{p.parents[b], 0, p.grow ? p.grow[b] : 0};
   if (r.parent < -1 || r.parent >= p.B) {
     bad |= MSA_ERR_ROW_RANGE;
-    r.parent = -1;
-    r.n = r.grow = r.held = r.want = 0;
-    r.copy = false;
-    return r;
+    return ForkRow{-1, 0, 0};
   }
   bool seq = false;
-  r.n = r.parent >= 0 ? row_tokens(p.lens, r.parent, p.S, seq) : 0;
-  r.grow = p.grow ? p.grow[b] : 0;
+  if (r.parent >= 0) r.n = row_tokens(p.lens, r.parent, p.S, seq);
   if (r.grow < 0 || r.n + static_cast<int64_t>(r.grow) > static_cast<int64_t>(p.S) * kPage ||
       r.n > INT_MAX - r.grow) {
     seq = true;
     r.grow = 0;
   }
   if (seq) bad |= MSA_ERR_SEQ_RANGE;
-  r.copy = r.n % kPage != 0 && first[r.parent] != b;
-  r.held = pages_of(r.n) - (r.copy ? 1 : 0);
-  r.want = pages_of(static_cast<int64_t>(r.n) + r.grow);
   return r;
 }
 
@@ -137,6 +132,7 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster)
   int* first = dyn;                 // [B] the lowest row that follows this one
   int* children = first + p.B;      // [B] how many do
   int* before = children + p.B;     // [rows + 1] pages that the rows before need
+  ForkRow* facts = reinterpret_cast<ForkRow*>(before + p.rows + 1);   // [rows]
   const int tid = threadIdx.x, lane = tid & 31;
   const unsigned cta = cluster_rank();
   pdl_trigger();
@@ -158,33 +154,31 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster)
     first[b] = INT_MAX;
     children[b] = 0;
   }
+  // `each` neighbouring rows a thread
+  unsigned bad = 0;
+  const int each = (p.rows + kThreads - 1) / kThreads;
+  const int r0 = min(tid * each, p.rows), r1 = min(r0 + each, p.rows);
+  for (int b = r0; b < r1; ++b) facts[b] = load_fork_row(p, b, bad);
   int cta_free;
   const int at = block_scan(mine, sh.scan_a, cta_free);
   if (tid < kCluster) store_remote(&sh.total[cta], tid, cta_free);
-  for (int b = tid; b < p.rows; b += kThreads) {
-    const int q = p.parents[b];
-    if (q >= 0 && q < p.B) {
+  for (int b = r0; b < r1; ++b) {
+    const int q = facts[b].parent;
+    if (q >= 0) {
       atomicMin(&first[q], b);
       atomicAdd(&children[q], 1);
     }
   }
   __syncthreads();
-  // rows' needs: `each` neighbouring rows a thread
-  unsigned bad = 0;
-  const int each = (p.rows + kThreads - 1) / kThreads;
-  const int r0 = min(tid * each, p.rows), r1 = min(r0 + each, p.rows);
   int need = 0;
   for (int b = r0; b < r1; ++b) {
-    const ForkRow r = fork_row(p, first, b, bad);
-    need += r.want - r.held;
+    const ForkRow r = facts[b];
+    before[b] = need;
+    need += r.want() - r.held(r.copied(first, b));
   }
   int total_need;
-  int sum = block_scan(need, sh.scan_b, total_need);
-  for (int b = r0; b < r1; ++b) {
-    const ForkRow r = fork_row(p, first, b, bad);
-    before[b] = sum;
-    sum += r.want - r.held;
-  }
+  const int sum = block_scan(need, sh.scan_b, total_need);
+  for (int b = r0; b < r1; ++b) before[b] += sum;
   if (tid == 0) before[p.rows] = total_need;
   // the totals of all CTAs, and refs_out as a copy of refs, before the changes to it
   cluster_sync();
@@ -208,11 +202,12 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster)
         if (before[m] <= k) x = m;
         else y = m;
       }
-      const ForkRow r = fork_row(p, first, x, bad);
-      const int e = r.held + k - before[x];
+      const ForkRow r = facts[x];
+      const bool copy = r.copied(first, x);
+      const int e = r.held(copy) + k - before[x];
       p.table_out[static_cast<int64_t>(x) * p.S + e] = i;
       p.refs_out[i] = 1;
-      if (r.copy && e == r.held) {
+      if (copy && k == before[x]) {
         int src = p.table[static_cast<int64_t>(r.parent) * p.S + e], tokens = r.n % kPage, dst = i;
         if (src < 0 || src >= p.num_blocks) {
           bad |= MSA_ERR_PAGE_RANGE;
@@ -229,10 +224,11 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster)
   // the rows: what they take over, and -1 behind their last page; a warp a row
   const int warps = threads / 32, warp = static_cast<int>(cta) * (kThreads / 32) + tid / 32;
   for (int b = warp; b < p.rows; b += warps) {
-    const ForkRow r = fork_row(p, first, b, bad);
+    const ForkRow r = facts[b];
+    const bool copy = r.copied(first, b);
     int32_t* to = p.table_out + static_cast<int64_t>(b) * p.S;
     const int32_t* from = p.table + static_cast<int64_t>(max(r.parent, 0)) * p.S;
-    const int held = fits ? r.held : 0, want = fits ? r.want : 0;
+    const int held = fits ? r.held(copy) : 0, want = fits ? r.want() : 0;
     for (int e = lane; e < p.S; e += 32) {
       if (e >= held && e < want) continue;
       int page = -1;
@@ -246,7 +242,7 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster)
       to[e] = page;
     }
     if (lane == 0) p.lens_out[b] = fits ? r.n + r.grow : 0;
-    if (lane < 3 && !(fits && r.copy)) p.copies[3 * static_cast<int64_t>(b) + lane] = lane < 2 ? -1 : 0;
+    if (lane < 3 && !(fits && copy)) p.copies[3 * static_cast<int64_t>(b) + lane] = lane < 2 ? -1 : 0;
   }
   // the counts of the pages that were held: one row fewer, children[b] more
   for (int b = warp; b < p.B && fits; b += warps) {
@@ -425,11 +421,12 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
 }  // namespace
 
 cudaError_t launch_fork(const ForkParams& p, cudaStream_t stream, bool pdl) {
-  const size_t smem = (2 * static_cast<size_t>(p.B) + p.rows + 1) * sizeof(int);
+  const size_t smem = (2 * static_cast<size_t>(p.B) + p.rows + 1) * sizeof(int) + p.rows * sizeof(ForkRow);
   static std::atomic<unsigned long long> attr_done{0};
   const cudaError_t e = once_per_device(attr_done, [&] {
     return cudaFuncSetAttribute(fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (3 * kMaxForkRows + 1) * static_cast<int>(sizeof(int)));
+                                (3 * kMaxForkRows + 1) * static_cast<int>(sizeof(int)) +
+                                    kMaxForkRows * static_cast<int>(sizeof(ForkRow)));
   });
   if (e != cudaSuccess) return e;
   return launch_pdl(fork_kernel, dim3(kCluster), dim3(kThreads), smem, stream, pdl, p);
@@ -442,9 +439,11 @@ cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream, bool pdl
 cudaError_t launch_copy(const CopyParams& p, cudaStream_t stream, bool pdl) {
   int units = 0;
   for (int c = 0; c < p.caches; ++c) units += p.cache[c].rows == 1 ? 1 : p.cache[c].units;
-  const int slots = 8 * p.sms;
-  const int x = p.n < slots ? p.n : slots;
-  int y = (slots + x - 1) / x;
+  // CTAs for eight an SM; each copy in four shares at least (one share each for 2170 moves of
+  // 192 KiB left the SMs uneven: 90 us, 87 with four; a share a unit, ten: 109)
+  const int x = p.n < 4096 ? p.n : 4096;
+  const int fill = (8 * p.sms + x - 1) / x;
+  int y = fill > 4 ? fill : 4;
   y = y < units ? y : units;
   return launch_pdl(copy_kernel, dim3(static_cast<unsigned>(x), static_cast<unsigned>(y)),
                     dim3(kCopyThreads), 0, stream, pdl, p);
