@@ -6,19 +6,22 @@
 // -inf where the token sees no key of the block.
 //
 // What bounds it: the tensor cores, 2 * 128 * 16 products a key, token and KV head
-// against a key's 128 bytes shared by the chunk's tokens.  The product is S = Q K^T with
-// the query rows (16 tokens x 16 heads, two M = 128 halves) as A and a page of keys as B,
-// so that a thread's tensor-memory lane is one query row: the largest of its 128 columns
-// is 64 three-input maxima without an exchange, and a token's 16 heads are 16 lanes.  A
-// bf16 query is two exact e4m3 parts (two products a half, which cost what one bf16
-// product would, and the keys need no conversion), an fp8 query is one.  Two accumulators
-// a half in tensor memory: a half's next page is multiplied while its last one is
-// searched.  One CTA an SM, each an equal share of all pages (msa_prefill.cuh); the next
-// unit's query tile is prepared while the current one is worked on.
+// against a key's 128 bytes shared by the chunk's tokens, and the shared memory that feeds
+// them.  The product is S = Q K^T with the query rows (16 tokens x 16 heads, two M = 128
+// halves) as A and two pages of keys as B, so that a thread's tensor-memory lane is one
+// query row: the largest of a page's 128 columns is 64 three-input maxima without an
+// exchange, and a token's 16 heads are 16 lanes.  (Two pages, N = 256: A is read once for
+// both, 12 KiB of operands in 128 cycles; with a page at a time, 8 KiB in 64 cycles, shared
+// memory was the limit and there were twice the products to issue: 340 us for the listed
+// four chunks.)  A bf16 query is two exact e4m3 parts (two products a half, which cost what
+// one bf16 product would, and the keys need no conversion), an fp8 query is one.  Each half
+// has its 256 columns of tensor memory: while one is searched the other is multiplied.  One
+// CTA an SM, each an equal share of all pages (msa_prefill.cuh); the next unit's query tile
+// is prepared while the current one is worked on.
 //   warp 0       page look-ups, TMA of K tiles
 //   warp 1       products (owns tensor memory)
 //   warps 2, 3   segments and query tiles, a token each in turn
-//   warps 4..11  maxima and scores, four warps a half
+//   warps 4..19  maxima and scores, four warps a half and page
 #include <cstddef>
 
 #include "msa_device.cuh"
@@ -32,25 +35,25 @@ namespace {
 
 using namespace prefill;
 
-constexpr int kThreads = 384;
-constexpr int kSlots = 5;                       // K tiles in flight
-constexpr int kInfo = 16;                       // pages' factors in flight
+constexpr int kThreads = 640;
+constexpr int kPairs = 3;                       // pairs of K tiles in flight
+constexpr int kInfo = 8;                        // pairs' factors in flight
 constexpr int kExtra = 0;
 constexpr int kMinSteps = 1;
 constexpr int kQTile = 4 * kHalfTile;           // two halves, hi and lo parts
 constexpr int kOffK = 2 * kQTile;
-constexpr int kOffTail = kOffK + kSlots * kHalfTile;
-constexpr int kTmemCols = 512;                  // [half][buffer] of 128 columns
+constexpr int kOffTail = kOffK + kPairs * 2 * kHalfTile;
+constexpr int kTmemCols = 512;                  // [half] of 256 columns, a page 128
 
 struct Tail {
-  uint64_t k_full[kSlots], k_empty[kSlots];
-  uint64_t s_full[2][2], s_empty[2][2];         // [half][buffer]
+  uint64_t k_full[kPairs], k_empty[kPairs];
+  uint64_t s_full[2], s_empty[2];               // by half
   uint64_t info_full[kInfo];
   uint64_t seg_full[2], seg_empty[2];
   uint64_t q_full[2];
   uint64_t finish;
   uint32_t tmem_base;
-  float info[kInfo];                            // ks, or 0: no key of the page counts
+  float info[kInfo][2];                         // ks, or 0: no key of the page counts
   Segment seg[2];
   float zs[2][kTile];
   WalkScratch scratch;
@@ -69,21 +72,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int parts = p.q8 ? 1 : 2;
 
   if (warp == 0 && lane == 0) {
-    for (int s = 0; s < kSlots; ++s) {
+    for (int s = 0; s < kPairs; ++s) {
       mbar_init(&tail->k_full[s], 1);
       mbar_init(&tail->k_empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
-      for (int h = 0; h < 2; ++h) {
-        mbar_init(&tail->s_full[h][s], 1);
-        mbar_init(&tail->s_empty[h][s], 4);
-      }
+      mbar_init(&tail->s_full[s], 1);
+      mbar_init(&tail->s_empty[s], 8);
       mbar_init(&tail->seg_full[s], 1);
-      mbar_init(&tail->seg_empty[s], 1 + 1 + 1 + 8);   // warps 0, 1, 3 and 4..11
+      mbar_init(&tail->seg_empty[s], 1 + 1 + 1 + 16);   // warps 0, 1, 3 and 4..19
       mbar_init(&tail->q_full[s], 2);
     }
     for (int s = 0; s < kInfo; ++s) mbar_init(&tail->info_full[s], 1);
-    mbar_init(&tail->finish, 1 + 1 + 2 + 8);
+    mbar_init(&tail->finish, 1 + 1 + 2 + 16);
     fence_barrier_init();
     prefetch_tensormap(&kv_map);
   } else if (warp == 1) {
@@ -105,7 +106,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ---- K tiles -----------------------------------------------------------------------------
-    int t = 0;    // pages so far
+    int t = 0, s = 0;    // pairs so far; the next one's place
+    unsigned par = 0;    // its phase
     for (int i = 0; ok; ++i) {
       ok = __all_sync(0xffffffffu, wait_for(&tail->seg_full[i & 1], (i >> 1) & 1));
       if (!ok) break;
@@ -135,26 +137,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const int have = min(32, sg.n1 - n0);
-        for (int x = 0; x < have; ++x, ++t) {
-          const int s = t % kSlots;
-          ok = t < kSlots || wait_for(&tail->k_empty[s], ((t / kSlots) - 1) & 1);
+        for (int x = 0; x < have; x += 2, ++t) {
+          ok = t < kPairs || wait_for(&tail->k_empty[s], par ^ 1);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          if (lane == x) {
-            tail->info[t % kInfo] = ks;
+          const int y = lane - x;              // this lane's page of the pair
+          if ((y == 0 || y == 1) && lane < have) tail->info[t % kInfo][y] = ks;
+          __syncwarp();
+          if (y == 0) {
             mbar_arrive(&tail->info_full[t % kInfo]);
-            mbar_arrive_expect_tx(&tail->k_full[s], kHalfTile);
-            tma_load_2d(smem + kOffK + s * kHalfTile, &kv_map, 0, (page * p.Hkv + sg.g) * kPage,
-                        &tail->k_full[s]);
+            mbar_arrive_expect_tx(&tail->k_full[s], x + 1 < have ? 2 * kHalfTile : kHalfTile);
           }
           __syncwarp();
+          if ((y == 0 || y == 1) && lane < have)
+            tma_load_2d(smem + kOffK + (2 * s + y) * kHalfTile, &kv_map, 0, (page * p.Hkv + sg.g) * kPage,
+                        &tail->k_full[s]);
+          __syncwarp();
+          if (++s == kPairs) {
+            s = 0;
+            par ^= 1;
+          }
         }
       }
     }
     if (lane == 0) {
       if (!ok) flag_error(p.err, MSA_ERR_TIMEOUT);
-      for (int x = max(0, t - kSlots); x < t; ++x)
-        (void)wait_for(&tail->k_full[x % kSlots], (x / kSlots) & 1);
+      for (int x = max(0, t - kPairs); x < t; ++x)
+        (void)wait_for(&tail->k_full[x % kPairs], (x / kPairs) & 1);
       pdl_trigger();
       mbar_arrive(&tail->finish);
     }
@@ -163,24 +172,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- S = Q K^T ---------------------------------------------------------------------------
     const uint64_t q0 = tc::sw128_kmajor_desc(smem_u32(smem));
     const uint64_t k0 = tc::sw128_kmajor_desc(smem_u32(smem + kOffK));
-    constexpr uint32_t idesc = tc::idesc_e4m3_f32(128, kPage);
     const bool leader = tc::elect_one();
     // (the vote makes it the same for the compiler as well)
     auto wait = [&](uint64_t* bar, unsigned parity) {
       return __all_sync(0xffffffffu, wait_for(bar, parity)) != 0;
     };
-    int s = 0;                 // slot of the next K tile
+    int s = 0;                 // place of the next pair
     unsigned k_par = 0;
-    int n_0 = 0, n_1 = 0;      // pages multiplied, by half
-    auto scores = [&](int h, int qbuf, int& n) {
-      const int buf = n & 1;
-      if (n >= 2 && !wait(&tail->s_empty[h][buf], ((n >> 1) - 1) & 1)) return false;
+    int n_0 = 0, n_1 = 0;      // pairs multiplied, by half
+    auto scores = [&](int h, int qbuf, int& n, uint32_t idesc) {
+      if (n >= 1 && !wait(&tail->s_empty[h], (n - 1) & 1)) return false;
       tc::fence_after_thread_sync();
       if (leader) {
-        const uint64_t bk = k0 + static_cast<uint64_t>(s) * (kHalfTile >> 4);
+        const uint64_t bk = k0 + static_cast<uint64_t>(s) * (2 * kHalfTile >> 4);
         const uint64_t aq = q0 + static_cast<uint64_t>(qbuf) * (kQTile >> 4) +
                             static_cast<uint64_t>(h) * (2 * kHalfTile >> 4);
-        const uint32_t d = tmem + 128 * (2 * h + buf);
+        const uint32_t d = tmem + 256 * h;
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) tc::mma_e4m3(d, aq + 2 * ks, bk + 2 * ks, idesc, ks > 0);
         if (parts == 2) {
@@ -188,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int ks = 0; ks < 4; ++ks)
             tc::mma_e4m3(d, aq + (kHalfTile >> 4) + 2 * ks, bk + 2 * ks, idesc, 1);
         }
-        tc::commit(&tail->s_full[h][buf]);
+        tc::commit(&tail->s_full[h]);
       }
       __syncwarp();
       ++n;
@@ -201,14 +208,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int pages = __reduce_max_sync(0xffffffffu, tail->seg[i & 1].n1 - tail->seg[i & 1].n0);
       if (ntok == 0) break;
       ok = wait(&tail->q_full[i & 1], (i >> 1) & 1);
-      for (int x = 0; x < pages && ok; ++x) {
+      for (int x = 0; x < pages && ok; x += 2) {
+        const uint32_t idesc = x + 1 < pages ? tc::idesc_e4m3_f32(128, 2 * kPage) : tc::idesc_e4m3_f32(128, kPage);
         ok = wait(&tail->k_full[s], k_par);
         if (!ok) break;
-        ok = scores(0, i & 1, n_0);
-        if (ok && ntok > kHalfTokens) ok = scores(1, i & 1, n_1);
+        ok = scores(0, i & 1, n_0, idesc);
+        if (ok && ntok > kHalfTokens) ok = scores(1, i & 1, n_1, idesc);
         if (leader) tc::commit(&tail->k_empty[s]);
         __syncwarp();
-        if (++s == kSlots) {
+        if (++s == kPairs) {
           s = 0;
           k_par ^= 1;
         }
@@ -258,11 +266,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    // ---- maxima of one half ------------------------------------------------------------------
-    const int h = (warp - 4) >> 2, quarter = warp & 3;
-    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + 256 * h;
+    // ---- maxima of half h, page pg of each pair ----------------------------------------------
+    const int h = (warp - 4) >> 3, pg = ((warp - 4) >> 2) & 1, quarter = warp & 3;
+    const uint32_t at = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + 256 * h + 128 * pg;
     const int j = kHalfTokens * h + 2 * quarter + (lane >> 4);   // this lane's token of the tile
-    int t = 0, mine = 0;      // pages so far, and those of this half
+    int t = 0, mine = 0;      // pairs so far, and those of this half
     for (int i = 0; ok; ++i) {
       ok = __all_sync(0xffffffffu, wait_for(&tail->seg_full[i & 1], (i >> 1) & 1));
       if (!ok) break;
@@ -273,66 +281,68 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float zs = tail->zs[i & 1][j];
       __syncwarp();
       if (lane == 0) mbar_arrive(&tail->seg_empty[i & 1]);
-      const int pages = sg.n1 - sg.n0;
       if (h == 1 && sg.ntok <= kHalfTokens) {
-        t += pages;
+        t += (sg.n1 - sg.n0 + 1) / 2;
         continue;
       }
       const int pos = sg.pos0 + j;
       float* row = p.scores + (static_cast<int64_t>(sg.g) * p.T + sg.tok0 + j) * p.S;
       const bool there = j < sg.ntok;
       float keep = 0.f;                   // the score of block n with n % 16 == lane % 16
-      for (int n = sg.n0; n < sg.n1; ++n, ++t, ++mine) {
-        const int buf = mine & 1;
+      for (int n = sg.n0 + pg; n < sg.n1 + pg; n += 2, ++t, ++mine) {
         // (the products first: a half that skipped units may be many pages early, and
         // info_full's phases come round)
-        ok = wait_for(&tail->s_full[h][buf], (mine >> 1) & 1) &&
-             wait_for(&tail->info_full[t % kInfo], (t / kInfo) & 1);
+        ok = wait_for(&tail->s_full[h], mine & 1) && wait_for(&tail->info_full[t % kInfo], (t / kInfo) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const float ks = tail->info[t % kInfo];
+        const bool one = n >= sg.n1;      // the last pair has one page, not this warp's
+        const float ks = one ? 0.f : tail->info[t % kInfo][pg];
         tc::fence_after_thread_sync();
-        const uint32_t at = lane_addr + 128 * buf;
         const int lim = pos - n * kPage;  // keys <= lim are visible
+        const bool edge = __any_sync(0xffffffffu, lim < kPage - 1);
         float m = -INFINITY;
-        uint32_t v[4][32];
+        if (!one) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tc::ld_32x32b_x32(at + 32 * c, v[c]);
-        tc::wait_ld();
-        tc::fence_before_thread_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&tail->s_empty[h][buf]);
-        if (__any_sync(0xffffffffu, lim < kPage - 1)) {
+          for (int c = 0; c < kPage; c += 64) {
+            uint32_t v[2][32];
+            tc::ld_32x32b_x32(at + c, v[0]);
+            tc::ld_32x32b_x32(at + c + 32, v[1]);
+            tc::wait_ld();
+            if (edge) {
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            m = fmaxf(m, c <= lim ? __uint_as_float(v[c >> 5][c & 31]) : -INFINITY);
-        } else {
-          float a[4];
+              for (int e = 0; e < 64; ++e)
+                v[e >> 5][e & 31] = c + e <= lim ? v[e >> 5][e & 31] : 0xFF800000u;
+            }
+            float a[2];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            a[c] = __uint_as_float(v[c][0]);
+            for (int k = 0; k < 2; ++k) {
+              a[k] = fmaxf(__uint_as_float(v[k][0]), __uint_as_float(v[k][1]));
 #pragma unroll
-            for (int e = 1; e < 31; e += 2)
-              a[c] = fmax3f(a[c], __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
-            a[c] = fmaxf(a[c], __uint_as_float(v[c][31]));
+              for (int e = 2; e < 32; e += 2)
+                a[k] = fmax3f(a[k], __uint_as_float(v[k][e]), __uint_as_float(v[k][e + 1]));
+            }
+            m = c == 0 ? fmaxf(a[0], a[1]) : fmax3f(m, a[0], a[1]);   // (NaN only where all are)
           }
-          m = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
+          tc::fence_before_thread_sync();
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tail->s_empty[h]);
+        if (one) continue;
 #pragma unroll
         for (int o = 8; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         const float sc = ks > 0.f && lim >= 0 ? m * (zs * ks) : -INFINITY;
         if ((n & 15) == (lane & 15)) keep = sc;
-        if ((n & 15) == 15 || n + 1 == sg.n1) {
-          // 16 neighbouring blocks of two tokens
+        if ((n & 15) >= 14 || n + 2 >= sg.n1) {
+          // this warp's eight of 16 neighbouring blocks, of two tokens
           const int at_n = (n & ~15) + (lane & 15);
-          if (there && at_n >= sg.n0 && at_n <= n) row[at_n] = keep;
+          if (there && at_n >= sg.n0 && at_n <= n && ((at_n ^ n) & 1) == 0) row[at_n] = keep;
         }
       }
       if (!ok) break;
       // behind the unit's last page: blocks that none of its tokens sees
       const int last = (sg.pos0 + sg.ntok - 1) / kPage;
       if (sg.n1 > last && there)
-        for (int n = last + 1 + (lane & 15); n < p.S; n += 16) row[n] = -INFINITY;
+        for (int n = last + 1 + pg * 16 + (lane & 15); n < p.S; n += 32) row[n] = -INFINITY;
     }
     if (lane == 0) {
       if (!ok) flag_error(p.err, MSA_ERR_TIMEOUT);
