@@ -198,6 +198,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_wait();   // lengths, tables and queries may be an earlier kernel's
   const bool bad = plan_walk<kThreads>(p, kExtra, kMinSteps, &tail->scratch);
+  bool any_cut = false;          // (warp 2's first lane, which goes on with the segments)
+  if (threadIdx.x == 64) {
+    int n;
+    tail->seg[0] = next_segment(p, tail->scratch.walk, kExtra, any_cut, n);
+    tail->nan_seen[0] = 0;
+    if (any_cut) p.cut[blockIdx.x] = make_int4(n, tail->seg[0].tok0, tail->seg[0].ntok, tail->seg[0].g);
+  }
   tc::fence_before_thread_sync();
   __syncthreads();
   tc::fence_after_thread_sync();
@@ -207,6 +214,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int x = threadIdx.x; x < p.Hq * kHeadDim / 8; x += kThreads) row[x] = make_uint4(0u, 0u, 0u, 0u);
   });
   bool ok = true;
+  // The first query tile: nobody but warp 0, which loads the first pages, has anything else
+  // to do yet.
+  if (warp > 0 && tail->seg[0].ntok > 0 && tail->seg[0].n0 < tail->seg[0].n1) {
+    (void)load_query_tile<2>(p, tail->seg[0], warp - 1, 15, smem, tail->zs[0], lane, [] { return true; });
+    named_barrier(1, 32 * 15);
+  }
 
   if (warp < 4) {
     if (warp == 0) {
@@ -396,20 +409,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       // ---- segments and query tiles --------------------------------------------------------------
       const int h = warp - 2;
-      bool any_cut = false;
       int tiles = 0;         // query tiles so far
       for (int i = 0;; ++i) {
         ok = __all_sync(0xffffffffu, i < 2 || wait_for(&tail->seg_empty[i & 1], ((i >> 1) - 1) & 1));
         if (!ok) break;
         if (h == 0) {
           if (lane == 0) {
-            bool cut;
-            int n;
-            const Segment next = next_segment(p, tail->scratch.walk, kExtra, cut, n);
-            tail->seg[i & 1] = next;
-            tail->nan_seen[i & 1] = 0;
-            if (cut) p.cut[blockIdx.x] = make_int4(n, next.tok0, next.ntok, next.g);
-            any_cut |= cut;
+            if (i > 0) {
+              bool cut;
+              int n;
+              const Segment next = next_segment(p, tail->scratch.walk, kExtra, cut, n);
+              tail->seg[i & 1] = next;
+              tail->nan_seen[i & 1] = 0;
+              if (cut) p.cut[blockIdx.x] = make_int4(n, next.tok0, next.ntok, next.g);
+              any_cut |= cut;
+            }
             mbar_arrive(&tail->seg_full[i & 1]);
           }
           __syncwarp();
@@ -425,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               p.part_ml[static_cast<int64_t>(sg.slot) * kRows + x] = make_float2(-INFINITY, 0.f);
         }
         if (sg.ntok > 0 && sg.n0 < sg.n1) {
-          ok = load_query_tile<(kTile + kLoaders - 1) / kLoaders>(p, sg, h, kLoaders, smem, tail->zs[i & 1], lane, [&] {
+          if (i > 0) ok = load_query_tile<(kTile + kLoaders - 1) / kLoaders>(p, sg, h, kLoaders, smem, tail->zs[i & 1], lane, [&] {
             return __all_sync(0xffffffffu, tiles == 0 || wait_for(&tail->q_empty, (tiles - 1) & 1)) != 0;
           });
           if (!ok) break;
@@ -658,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Segment sg = tail->seg[i & 1];
       if (sg.ntok == 0) break;
       if (sg.n0 < sg.n1) {
-        ok = load_query_tile<(kTile + kLoaders - 1) / kLoaders>(p, sg, 2 + w4, kLoaders, smem, tail->zs[i & 1], lane, [&] {
+        if (i > 0) ok = load_query_tile<(kTile + kLoaders - 1) / kLoaders>(p, sg, 2 + w4, kLoaders, smem, tail->zs[i & 1], lane, [&] {
           return __all_sync(0xffffffffu, tiles == 0 || wait_for(&tail->q_empty, (tiles - 1) & 1)) != 0;
         });
         if (!ok) break;

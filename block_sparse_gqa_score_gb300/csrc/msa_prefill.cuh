@@ -354,15 +354,18 @@ __device__ __forceinline__ bool load_query_tile(const PrefillParams& p, const Se
       if (j < sg.ntok) {
         rows[k].store(p, row0, hi, lo, lane);
         if (lane == 0) zs[j] = z[k];
-        if (kMost > kAhead && j + kAhead * step < sg.ntok) {
+        if (kMost > kAhead && j + kAhead * step < sg.ntok)
           rows[k].load(p, sg.tok0 + j + kAhead * step, sg.g, lane);
-          z[k] = rows[k].split(p);
-        }
       } else if (j < kHalfTokens || sg.ntok > kHalfTokens) {   // (a half without tokens is not read)
         zero_query_rows(row0, hi, lane);
         if (!p.q8) zero_query_rows(row0, lo, lane);
         if (lane == 0) zs[j] = 0.f;
       }
+    }
+    if (kMost > kAhead) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (j0 + (kAhead + k) * step < sg.ntok) z[k] = rows[k].split(p);
     }
   }
   fence_proxy_async();

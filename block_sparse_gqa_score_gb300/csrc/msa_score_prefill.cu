@@ -20,7 +20,8 @@
 // is prepared while the current one is worked on.
 //   warp 0       page look-ups, TMA of K tiles
 //   warp 1       products (owns tensor memory)
-//   warps 2, 3   segments and query tiles, a token each in turn
+//   warps 2, 3   segments and query tiles, a token each in turn (behind a short unit: warps
+//                4..19, a token each)
 //   warps 4..19  maxima and scores, four warps a half and page
 #include <cstddef>
 
@@ -38,8 +39,9 @@ using namespace prefill;
 constexpr int kThreads = 640;
 constexpr int kPairs = 3;                       // pairs of K tiles in flight
 constexpr int kInfo = 8;                        // pairs' factors in flight
-constexpr int kExtra = 0;
+constexpr int kExtra = 3;                       // a unit's query tile, in pages
 constexpr int kMinSteps = 1;
+constexpr int kShort = 16;                      // pages of a unit too few to hide the next one's query tile
 constexpr int kQTile = 4 * kHalfTile;           // two halves, hi and lo parts
 constexpr int kOffK = 2 * kQTile;
 constexpr int kOffTail = kOffK + kPairs * 2 * kHalfTile;
@@ -51,6 +53,7 @@ struct Tail {
   uint64_t info_full[kInfo];
   uint64_t seg_full[2], seg_empty[2];
   uint64_t q_full[2];
+  uint64_t q_part;                              // warps 4..19 <-> 2, 3: their tokens of a tile
   uint64_t finish;
   uint32_t tmem_base;
   float info[kInfo][2];                         // ks, or 0: no key of the page counts
@@ -62,8 +65,15 @@ struct Tail {
 constexpr int kSmemBytes = kOffTail + static_cast<int>(sizeof(Tail)) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
+// Token x of a segment's query tile.  Not in line: its registers are not the search's.
+__device__ __noinline__ void load_token(const PrefillParams& p, const Segment* sg, int x, uint8_t* tile,
+                                        float* zs) {
+  (void)load_query_tile<1>(p, *sg, x, kTile, tile, zs, threadIdx.x & 31, [] { return true; });
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
-    score_prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p) {
+    score_prefill_kernel(const __grid_constant__ CUtensorMap kv_map,
+                         const __grid_constant__ PrefillParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -84,6 +94,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&tail->q_full[s], 2);
     }
     for (int s = 0; s < kInfo; ++s) mbar_init(&tail->info_full[s], 1);
+    mbar_init(&tail->q_part, 16);
     mbar_init(&tail->finish, 1 + 1 + 2 + 16);
     fence_barrier_init();
     prefetch_tensormap(&kv_map);
@@ -93,6 +104,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_wait();   // lengths, tables and queries may be an earlier kernel's
   const bool bad = plan_walk<kThreads>(p, kExtra, kMinSteps, &tail->scratch);
+  if (threadIdx.x == 0) {
+    bool cut;
+    int n;
+    tail->seg[0] = next_segment(p, tail->scratch.walk, kExtra, cut, n);
+  }
   tc::fence_before_thread_sync();
   __syncthreads();
   tc::fence_after_thread_sync();
@@ -235,6 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < 4) {
     // ---- segments and query tiles ------------------------------------------------------------
     const int h = warp - 2;
+    int last_pages = 0, parted = 0;   // pages of the segment before; tiles of warps 4..19
     for (int i = 0;; ++i) {
       ok = __all_sync(0xffffffffu, i < 2 || wait_for(&tail->seg_empty[i & 1], ((i >> 1) - 1) & 1));
       if (!ok) break;
@@ -242,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           bool cut;
           int n;
-          tail->seg[i & 1] = next_segment(p, tail->scratch.walk, kExtra, cut, n);
+          if (i > 0) tail->seg[i & 1] = next_segment(p, tail->scratch.walk, kExtra, cut, n);
           mbar_arrive(&tail->seg_full[i & 1]);
         }
         __syncwarp();
@@ -251,14 +268,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
       }
       const Segment sg = tail->seg[i & 1];
-      if (sg.ntok > 0)
-        (void)load_query_tile<kTile / 2>(p, sg, h, 2, smem + (i & 1) * kQTile, tail->zs[i & 1], lane, [] { return true; });
+      if (sg.ntok > 0 && last_pages < kShort) {
+        // the tile is prepared by warps 4..19
+        ok = __all_sync(0xffffffffu, wait_for(&tail->q_part, parted & 1));
+        if (!ok) break;
+        ++parted;
+      } else if (sg.ntok > 0)
+        (void)load_query_tile<kTile / 2>(p, sg, h, 2, smem + (i & 1) * kQTile, tail->zs[i & 1], lane,
+                                         [] { return true; });
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&tail->q_full[i & 1]);
         if (h == 1) mbar_arrive(&tail->seg_empty[i & 1]);
       }
       if (sg.ntok == 0) break;
+      last_pages = sg.n1 - sg.n0;
     }
     if (lane == 0) {
       if (!ok) flag_error(p.err, MSA_ERR_TIMEOUT);
@@ -271,11 +295,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t at = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + 256 * h + 128 * pg;
     const int j = kHalfTokens * h + 2 * quarter + (lane >> 4);   // this lane's token of the tile
     int t = 0, mine = 0;      // pairs so far, and those of this half
+    int last_pages = 0;       // of the segment before
     for (int i = 0; ok; ++i) {
       ok = __all_sync(0xffffffffu, wait_for(&tail->seg_full[i & 1], (i >> 1) & 1));
       if (!ok) break;
       const Segment sg = tail->seg[i & 1];
       if (sg.ntok == 0) break;
+      if (last_pages < kShort) {
+        // at the start, or behind a unit in whose time two warps could not have: a token a warp
+        load_token(p, &tail->seg[i & 1], warp - 4, smem + (i & 1) * kQTile, tail->zs[i & 1]);
+        if (lane == 0) mbar_arrive(&tail->q_part);
+        __syncwarp();
+      }
+      last_pages = sg.n1 - sg.n0;
       ok = __all_sync(0xffffffffu, wait_for(&tail->q_full[i & 1], (i >> 1) & 1));
       if (!ok) break;
       const float zs = tail->zs[i & 1][j];
@@ -303,23 +335,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         float m = -INFINITY;
         if (!one) {
 #pragma unroll
-          for (int c = 0; c < kPage; c += 64) {
-            uint32_t v[2][32];
-            tc::ld_32x32b_x32(at + c, v[0]);
-            tc::ld_32x32b_x32(at + c + 32, v[1]);
+          for (int c = 0; c < kPage; c += 32) {
+            uint32_t v[32];
+            tc::ld_32x32b_x32(at + c, v);
             tc::wait_ld();
             if (edge) {
 #pragma unroll
-              for (int e = 0; e < 64; ++e)
-                v[e >> 5][e & 31] = c + e <= lim ? v[e >> 5][e & 31] : 0xFF800000u;
+              for (int e = 0; e < 32; ++e) v[e] = c + e <= lim ? v[e] : 0xFF800000u;
             }
             float a[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              a[k] = fmaxf(__uint_as_float(v[k][0]), __uint_as_float(v[k][1]));
+              a[k] = fmaxf(__uint_as_float(v[k]), __uint_as_float(v[k + 2]));
 #pragma unroll
-              for (int e = 2; e < 32; e += 2)
-                a[k] = fmax3f(a[k], __uint_as_float(v[k][e]), __uint_as_float(v[k][e + 1]));
+              for (int e = k + 4; e < 32; e += 4)
+                a[k] = fmax3f(a[k], __uint_as_float(v[e]), __uint_as_float(v[e + 2]));
             }
             m = c == 0 ? fmaxf(a[0], a[1]) : fmax3f(m, a[0], a[1]);   // (NaN only where all are)
           }
