@@ -37,7 +37,7 @@
 //
 //   warp 0        page look-ups, TMA of K and V tiles
 //   warp 1        products (owns tensor memory)
-//   warp 2        segments; with warp 3 and warps 12..15 query tiles, a token each in turn
+//   warps 2, 3    segments (warp 2); query tiles: tokens 8..15, warps 12..15 two of the others each
 //   warps 4..11   softmax and output, four warps a half
 //   warps 12..15  values to fp16
 // One CTA an SM, each an equal share of all pages (msa_prefill.cuh); what several CTAs
@@ -59,6 +59,7 @@ constexpr int kThreads = 512;
 constexpr int kSlots = 3;                       // K tiles in flight
 constexpr int kVSlots = 2;                      // V tiles as stored, in flight
 constexpr int kInfo = 16;                       // pages' factors in flight
+constexpr int kSegs = 4;                        // segments known at a time
 constexpr int kExtra = 4;                       // a unit's query and output, in pages
 constexpr int kMinSteps = 3;
 constexpr int kRows = kGroup * kTile;           // query rows of a unit
@@ -86,14 +87,14 @@ struct Tail {
   uint64_t v_full[2], v_empty[2];               // fp16 values
   uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];   // by half
   uint64_t info_full[kInfo];
-  uint64_t seg_full[2], seg_empty[2];
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint64_t q_full, q_empty;
   uint64_t finish;
   uint32_t tmem_base;
-  int nan_seen[2];                              // by segment: NaN codes were set to 0
+  int nan_seen[kSegs];                          // by segment: NaN codes were set to 0
   alignas(16) PageInfo info[kInfo];
-  Segment seg[2];
-  float zs[2][kTile];
+  Segment seg[kSegs];
+  float zs[kSegs][kTile];
   WalkScratch scratch;
 };
 
@@ -136,6 +137,11 @@ __device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, f
       "mov.b64 {%0, %1}, x;\n\t}"
       : "=f"(d0), "=f"(d1)
       : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // Four lanes' rows of four 16-byte pieces turned: lane k of a group of four gets piece k of
@@ -183,6 +189,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&tail->p_full[s], 4);
       mbar_init(&tail->o_full[s], 1);
       mbar_init(&tail->o_empty[s], 4);
+    }
+    for (int s = 0; s < kSegs; ++s) {
       mbar_init(&tail->seg_full[s], 1);
       mbar_init(&tail->seg_empty[s], 1 + 1 + 1 + 8 + 4);   // warps 0, 1, 3, 4..11, 12..15
     }
@@ -226,11 +234,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- K and V tiles -----------------------------------------------------------------------
       int t = 0;    // pages so far
       for (int i = 0; ok; ++i) {
-        ok = __all_sync(0xffffffffu, wait_for(&tail->seg_full[i & 1], (i >> 1) & 1));
+        ok = __all_sync(0xffffffffu, wait_for(&tail->seg_full[i & 3], (i >> 2) & 1));
         if (!ok) break;
-        const Segment sg = tail->seg[i & 1];
+        const Segment sg = tail->seg[i & 3];
         __syncwarp();
-        if (lane == 0) mbar_arrive(&tail->seg_empty[i & 1]);
+        if (lane == 0) mbar_arrive(&tail->seg_empty[i & 3]);
         if (sg.ntok == 0) break;
         const int32_t* trow = p.block_table + static_cast<int64_t>(sg.b) * p.S;
         for (int n0 = sg.n0; n0 < sg.n1 && ok; n0 += 32) {
@@ -346,11 +354,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       for (int i = 0; ok; ++i) {
-        ok = wait(&tail->seg_full[i & 1], (i >> 1) & 1);
+        ok = wait(&tail->seg_full[i & 3], (i >> 2) & 1);
         if (!ok) break;
-        const int ntok = __reduce_max_sync(0xffffffffu, tail->seg[i & 1].ntok);
-        const int pages = __reduce_max_sync(0xffffffffu, tail->seg[i & 1].n1 - tail->seg[i & 1].n0);
-        if (leader) mbar_arrive(&tail->seg_empty[i & 1]);
+        const int ntok = __reduce_max_sync(0xffffffffu, tail->seg[i & 3].ntok);
+        const int pages = __reduce_max_sync(0xffffffffu, tail->seg[i & 3].n1 - tail->seg[i & 3].n0);
+        if (leader) mbar_arrive(&tail->seg_empty[i & 3]);
         __syncwarp();
         if (ntok == 0) break;
         if (pages == 0) continue;
@@ -410,28 +418,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- segments and query tiles --------------------------------------------------------------
       const int h = warp - 2;
       int tiles = 0;         // query tiles so far
+      bool more = true;      // warp 2: the last segment is not known yet
       for (int i = 0;; ++i) {
-        ok = __all_sync(0xffffffffu, i < 2 || wait_for(&tail->seg_empty[i & 1], ((i >> 1) - 1) & 1));
-        if (!ok) break;
         if (h == 0) {
-          if (lane == 0) {
-            if (i > 0) {
-              bool cut;
-              int n;
-              const Segment next = next_segment(p, tail->scratch.walk, kExtra, cut, n);
-              tail->seg[i & 1] = next;
-              tail->nan_seen[i & 1] = 0;
-              if (cut) p.cut[blockIdx.x] = make_int4(n, next.tok0, next.ntok, next.g);
-              any_cut |= cut;
+          // up to two segments ahead, so that their queries can be on their way
+          for (int a = i == 0 ? 0 : i + 2; a <= i + 2 && more; ++a) {
+            ok = __all_sync(0xffffffffu, a < kSegs || wait_for(&tail->seg_empty[a & 3], ((a >> 2) - 1) & 1));
+            if (!ok) break;
+            if (lane == 0) {
+              if (a > 0) {
+                bool cut;
+                int n;
+                const Segment next = next_segment(p, tail->scratch.walk, kExtra, cut, n);
+                tail->seg[a & 3] = next;
+                tail->nan_seen[a & 3] = 0;
+                if (cut) p.cut[blockIdx.x] = make_int4(n, next.tok0, next.ntok, next.g);
+                any_cut |= cut;
+              }
+              mbar_arrive(&tail->seg_full[a & 3]);
             }
-            mbar_arrive(&tail->seg_full[i & 1]);
+            __syncwarp();
+            more = tail->seg[a & 3].ntok > 0;
           }
-          __syncwarp();
+          if (!ok) break;
         } else {
-          ok = __all_sync(0xffffffffu, wait_for(&tail->seg_full[i & 1], (i >> 1) & 1));
+          ok = __all_sync(0xffffffffu, wait_for(&tail->seg_full[i & 3], (i >> 2) & 1));
           if (!ok) break;
         }
-        const Segment sg = tail->seg[i & 1];
+        const Segment sg = tail->seg[i & 3];
         if (h == 0) {
           // a part without pages (of the unit's extra steps alone) is empty
           if (sg.ntok > 0 && sg.slot >= 0 && sg.n0 == sg.n1)
@@ -439,15 +453,17 @@ __global__ void __launch_bounds__(kThreads, 1)
               p.part_ml[static_cast<int64_t>(sg.slot) * kRows + x] = make_float2(-INFINITY, 0.f);
         }
         if (sg.ntok > 0 && sg.n0 < sg.n1) {
-          if (i > 0) ok = load_query_tile<(kTile + kLoaders - 1) / kLoaders>(p, sg, h, kLoaders, smem, tail->zs[i & 1], lane, [&] {
-            return __all_sync(0xffffffffu, tiles == 0 || wait_for(&tail->q_empty, (tiles - 1) & 1)) != 0;
-          });
+          // tokens 8 + h, 10 + h, .. (warps 12..15 take the first eight)
+          if (i > 0)
+            ok = load_query_tile<4>(p, sg, kHalfTokens + h, 2, smem, tail->zs[i & 3], lane, [&] {
+              return __all_sync(0xffffffffu, tiles == 0 || wait_for(&tail->q_empty, (tiles - 1) & 1)) != 0;
+            });
           if (!ok) break;
           ++tiles;
           if (lane == 0) mbar_arrive(&tail->q_full);
         }
         __syncwarp();
-        if (lane == 0 && h == 1) mbar_arrive(&tail->seg_empty[i & 1]);
+        if (lane == 0 && h == 1) mbar_arrive(&tail->seg_empty[i & 3]);
         if (sg.ntok == 0) break;
       }
       if (lane == 0) {
@@ -466,15 +482,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int j = kHalfTokens * h + row / kGroup;        // this row's token of the tile
     int t = 0, mine = 0, units = 0;
     for (int i = 0; ok; ++i) {
-      ok = __all_sync(0xffffffffu, wait_for(&tail->seg_full[i & 1], (i >> 1) & 1));
+      ok = __all_sync(0xffffffffu, wait_for(&tail->seg_full[i & 3], (i >> 2) & 1));
       if (!ok) break;
-      const Segment sg = tail->seg[i & 1];
+      const Segment sg = tail->seg[i & 3];
       if (sg.ntok == 0) break;
       const int pages = sg.n1 - sg.n0;
       if (pages == 0 || (h == 1 && sg.ntok <= kHalfTokens)) {
         t += pages;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&tail->seg_empty[i & 1]);
+        if (lane == 0) mbar_arrive(&tail->seg_empty[i & 3]);
         continue;
       }
       const int pos = sg.pos0 + j;
@@ -487,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const PageInfo in = tail->info[t % kInfo];
-        if (n == sg.n0) zs = tail->zs[i & 1][j];
+        if (n == sg.n0) zs = tail->zs[i & 3][j];
         tc::fence_after_thread_sync();
         const int lim = in.block < 0 ? -1 : pos - n * kPage;  // keys <= lim are visible
         const bool edge = __any_sync(0xffffffffu, lim < kPage - 1);
@@ -578,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       ++units;
       tc::fence_after_thread_sync();
-      const bool nan_seen = tail->nan_seen[i & 1] != 0;
+      const bool nan_seen = tail->nan_seen[i & 3] != 0;
       const bool there = j < sg.ntok;
       // (P was 2^kShift times the weights; a row with a NaN logit is NaN altogether)
       float inv = l > 0.f ? __fdividef(p.v_scale, l) : 0.f;
@@ -615,8 +631,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t o[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              o[e] = f32_to_bf16_bits(__uint_as_float(v[8 * x + 2 * e]) * inv) |
-                     (f32_to_bf16_bits(__uint_as_float(v[8 * x + 2 * e + 1]) * inv) << 16);
+              o[e] = pack_bf16x2(__uint_as_float(v[8 * x + 2 * e]) * inv,
+                                 __uint_as_float(v[8 * x + 2 * e + 1]) * inv);
             q[x] = make_uint4(o[0], o[1], o[2], o[3]);
           }
           turn4(q, lane);
@@ -652,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&tail->o_empty[h]);
-        mbar_arrive(&tail->seg_empty[i & 1]);
+        mbar_arrive(&tail->seg_empty[i & 3]);
       }
     }
     if (lane == 0) {
@@ -666,20 +682,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     // (then the other way round), so that neither side has bank conflicts
     const int w4 = warp - 12;
     int t = 0, tiles = 0;
+    // tokens 2 w4 and 2 w4 + 1 of the next query tile, asked for a segment ahead
+    QueryRows rows[2];
     for (int i = 0; ok; ++i) {
-      ok = __all_sync(0xffffffffu, wait_for(&tail->seg_full[i & 1], (i >> 1) & 1));
+      ok = __all_sync(0xffffffffu, wait_for(&tail->seg_full[i & 3], (i >> 2) & 1));
       if (!ok) break;
-      const Segment sg = tail->seg[i & 1];
+      const Segment sg = tail->seg[i & 3];
       if (sg.ntok == 0) break;
       if (sg.n0 < sg.n1) {
-        if (i > 0) ok = load_query_tile<(kTile + kLoaders - 1) / kLoaders>(p, sg, 2 + w4, kLoaders, smem, tail->zs[i & 1], lane, [&] {
-          return __all_sync(0xffffffffu, tiles == 0 || wait_for(&tail->q_empty, (tiles - 1) & 1)) != 0;
-        });
-        if (!ok) break;
+        if (i > 0) {
+          float z[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (2 * w4 + k < sg.ntok) z[k] = rows[k].split(p);
+          ok = __all_sync(0xffffffffu, tiles == 0 || wait_for(&tail->q_empty, (tiles - 1) & 1));
+          if (!ok) break;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int j = 2 * w4 + k;
+            if (j < sg.ntok) {
+              rows[k].store(p, kGroup * j, smem, smem + kHalfTile, lane);
+            } else {
+              zero_query_rows(kGroup * j, smem, lane);
+              if (!p.q8) zero_query_rows(kGroup * j, smem + kHalfTile, lane);
+            }
+            if (lane == 0) tail->zs[i & 3][j] = j < sg.ntok ? z[k] : 0.f;
+          }
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+        }
         ++tiles;
         if (lane == 0) mbar_arrive(&tail->q_full);
         __syncwarp();
       }
+      ok = __all_sync(0xffffffffu, wait_for(&tail->seg_full[(i + 1) & 3], ((i + 1) >> 2) & 1));
+      if (!ok) break;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (2 * w4 + k < tail->seg[(i + 1) & 3].ntok)
+          rows[k].load(p, tail->seg[(i + 1) & 3].tok0 + 2 * w4 + k, tail->seg[(i + 1) & 3].g, lane);
       for (int n = sg.n0; n < sg.n1; ++n, ++t) {
         const int sv = t % kVSlots, b = t & 1;
         ok = wait_for(&tail->v8_full[sv], (t / kVSlots) & 1) &&
@@ -720,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<uint4*>(half + sw128(key, 2 * (c & 3))) = make_uint4(f0.x, f0.y, f1.x, f1.y);
           *reinterpret_cast<uint4*>(half + sw128(key, 2 * (c & 3) + 1)) = make_uint4(f2.x, f2.y, f3.x, f3.y);
         }
-        if (nan) tail->nan_seen[i & 1] = 1;
+        if (nan) tail->nan_seen[i & 3] = 1;
         tc::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -729,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&tail->seg_empty[i & 1]);
+      if (lane == 0) mbar_arrive(&tail->seg_empty[i & 3]);
     }
     if (lane == 0) {
       if (!ok) flag_error(p.err, MSA_ERR_TIMEOUT);
