@@ -60,8 +60,9 @@ constexpr int kSlots = 3;                       // K tiles in flight
 constexpr int kVSlots = 2;                      // V tiles as stored, in flight
 constexpr int kInfo = 16;                       // pages' factors in flight
 constexpr int kSegs = 4;                        // segments known at a time
-constexpr int kExtra = 4;                       // a unit's query and output, in pages
-constexpr int kMinSteps = 3;
+// A unit's query and output, in pages' time: an fp8 query is copied, a bf16 one split.
+__device__ __forceinline__ int extra_steps(const PrefillParams& p) { return p.q8 ? 3 : 6; }
+constexpr int kMinSteps = 2;
 constexpr int kRows = kGroup * kTile;           // query rows of a unit
 constexpr int kQTile = 4 * kHalfTile;           // two halves, hi and lo parts
 constexpr int kVTile = 2 * kHalfTile;           // a page's values in fp16
@@ -205,11 +206,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tmem_relinquish();
   }
   pdl_wait();   // lengths, tables and queries may be an earlier kernel's
-  const bool bad = plan_walk<kThreads>(p, kExtra, kMinSteps, &tail->scratch);
+  const bool bad = plan_walk<kThreads>(p, extra_steps(p), kMinSteps, &tail->scratch);
   bool any_cut = false;          // (warp 2's first lane, which goes on with the segments)
   if (threadIdx.x == 64) {
     int n;
-    tail->seg[0] = next_segment(p, tail->scratch.walk, kExtra, any_cut, n);
+    tail->seg[0] = next_segment(p, tail->scratch.walk, extra_steps(p), any_cut, n);
     tail->nan_seen[0] = 0;
     if (any_cut) p.cut[blockIdx.x] = make_int4(n, tail->seg[0].tok0, tail->seg[0].ntok, tail->seg[0].g);
   }
@@ -429,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (a > 0) {
                 bool cut;
                 int n;
-                const Segment next = next_segment(p, tail->scratch.walk, kExtra, cut, n);
+                const Segment next = next_segment(p, tail->scratch.walk, extra_steps(p), cut, n);
                 tail->seg[a & 3] = next;
                 tail->nan_seen[a & 3] = 0;
                 if (cut) p.cut[blockIdx.x] = make_int4(n, next.tok0, next.ntok, next.g);
