@@ -183,3 +183,79 @@ def test_refusals():
     with pytest.raises((ValueError, msa.MSAError)):
         msa.topk_prefill(s, x.lens, x.cu, k=8)
     assert msa.get_error() == 0
+
+
+@pytest.mark.parametrize("n,S", [(130, 200), (500, 512), (900, 1024), (2000, 2048)])
+@pytest.mark.parametrize("lanes", [1, 3, 14, 15, 31])
+def test_topk_prefill_keys_in_few_columns(n, S, lanes):
+    """The best blocks all at indices that are the same modulo 32: many keys above the
+    15th largest of the 32 columns' maxima, or none."""
+    gen = torch.Generator().manual_seed(n + lanes)
+    x = torch.randn((2, 12, S), generator=gen)
+    col = torch.arange(S) % 32 < lanes
+    x[:, :6] = torch.where(col, x[:, :6] + 100, x[:, :6])
+    x[:, 6:9] = torch.where(col, 7.0, x[:, 6:9])                        # and all alike
+    x[:, 9:] = torch.where(col, (x[:, 9:] * 2).round() + 100, x[:, 9:])  # and with ties
+    lens = torch.tensor([n * PAGE + 60], dtype=torch.int32, device="cuda")
+    got = msa.topk_prefill(x.cuda(), lens, cu([12]))
+    assert torch.equal(got.cpu(), select(x, lens.tolist(), [12]))
+    assert torch.equal(msa.topk(x.cuda(), lens, 12).cpu(), got.cpu())
+
+
+@pytest.mark.parametrize("op", ["score", "dense"])
+def test_requests_out_of_order_stay_in_bounds(op):
+    """cu_seqlens_q that does not ascend: the error is set, and tokens of a request that is
+    in order are right."""
+    x = Batch([300, 200, 100], [20, 30, 10], 1, 12)
+    x.cu = torch.tensor([0, 20, 5, 60], dtype=torch.int32, device="cuda")
+    x.lens[2] = 100                                   # tokens 5 .. 59 of 100
+    if op == "score":
+        got = score(x)
+        want, tol = every(Batch([300, 200, 100], [20, 30, 10], 1, 12), scores=True)
+        check(got[:, :5], want[:, :5], tol[:, :5])
+    else:
+        got = msa.dense_prefill(*x.args(), x.v_scale, **x.kw())
+        want, tol = every(Batch([300, 200, 100], [20, 30, 10], 1, 12))
+        check(got[:5], want[:5], tol[:5])
+    assert msa.get_error() == _native.ERR_SEQ_RANGE
+    x.cu = torch.tensor([-7, 20, 1 << 30, 60], dtype=torch.int32, device="cuda")
+    (score(x) if op == "score" else msa.dense_prefill(*x.args(), x.v_scale, **x.kw()))
+    assert msa.get_error() == _native.ERR_SEQ_RANGE
+
+
+def test_overlapped_calls_keep_their_order():
+    """With input overlap on, append, scorer, selector, sparse and dense attention back to
+    back give what they give one by one."""
+    x = Batch([1500, 700, 2600], [130, 700, 64], 2, 21, scaled=True)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    k, v = (torch.randn((x.T, 2, D), device="cuda", generator=gen).to(torch.bfloat16) for _ in range(2))
+    x.scales.copy_(torch.exp2(torch.log2(x.scales).round()))
+    kv0, sc0 = x.kv.clone(), x.scales.clone()
+
+    def run(sync):
+        x.kv.copy_(kv0)
+        x.scales.copy_(sc0)
+        torch.cuda.synchronize()
+        out = []
+        for f in (lambda: msa.append_kv_prefill(k, v, x.kv, x.bt, x.lens, x.cu, kv_scales=x.scales),
+                  lambda: out.append(score(x)),
+                  lambda: out.append(msa.topk_prefill(out[0], x.lens, x.cu)),
+                  lambda: out.append(msa.sparse_prefill(x.q, x.kv, x.bt, x.lens, x.cu, out[1], x.sm,
+                                                        kv_scales=x.scales)),
+                  lambda: out.append(msa.dense_prefill(*x.args(), **x.kw())),
+                  lambda: out.append(msa.score_prefill(*x.args(), **x.kw()))):
+            f()
+            if sync:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return out
+
+    want = run(True)
+    was = msa.set_input_overlap(True)
+    try:
+        for _ in range(3):
+            for a, b in zip(run(False), want):
+                assert torch.equal(a, b)
+    finally:
+        msa.set_input_overlap(was)
+    assert msa.get_error() == 0
