@@ -8,14 +8,14 @@
 // scorer's [head, token, block] buffer through a transposed view.  One warp
 // per row.
 //
-// What bounds it: the issue slots, some 650 instructions a row (its scores are a few hundred
+// What bounds it: the issue slots, some 600 instructions a row (its scores are a few hundred
 // floats).  The kept blocks are found from the lanes' own maxima: L, the 15th largest of
 // the 32, has at least 15 keys at or above it, and few keys are above it (some 20 of 256
 // random ones).  If fewer than 15 are, they are kept with the first keys equal to L; else
 // the 15 are chosen among them alone, each compared with all of them in shared memory.
-// 5980 tokens of 4 heads over up to 512 blocks: 24 us, 1.1 TB/s of scores.  (A search bit by
+// 5980 tokens of 4 heads over up to 512 blocks: 18 us, 1.4 TB/s of scores.  (A search bit by
 // bit, 31 rounds of a count over the warp, took 83 us; several heads of a token in one
-// warp, with the next row's scores on their way, 26 to 28.)  A row with more than 64 keys above L (they would have to lie in few lanes) is
+// warp, with the next row's scores on their way, was slower.)  A row with more than 64 keys above L (they would have to lie in few lanes) is
 // left to the search of msa_select.cuh, as are rows of more than 2048 blocks.
 #include "msa_device.cuh"
 #include "msa_launch.h"
@@ -29,51 +29,62 @@ constexpr int kWarps = 4;
 constexpr int kShort = 512;   // blocks of a row that the short form takes
 constexpr int kAbove = 64;    // keys above L that are compared with each other
 
-// select::order_key in fewer steps: -0 becomes 0 by the addition.
-__device__ __forceinline__ uint32_t key_of(float x, bool& nan) {
-  const bool bad = x != x;
-  nan |= bad;
-  const uint32_t u = __float_as_uint(x + 0.f);
-  return bad ? 0x007FFFFFu : u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+// Smallest of a float across the warp, NaN ignored.
+__device__ __forceinline__ float warp_min_f32(float x) {
+  float r;
+  asm volatile("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 // The kept blocks of a row of 16 .. 32 NK candidates, as select::select_row returns them;
-// false where it has to do it.  above: shared scratch of this warp, 2 kAbove words.
+// false where it has to do it.  Scores are compared as they are (-0 equals 0); a NaN score
+// counts as -inf, and a NaN of this function's own stands for no block at all: no
+// comparison holds with it.  scratch: shared words of this warp, at most 1024.
 template <int NK>
 __device__ __forceinline__ bool select_by_maxima(const float* __restrict__ srow, int64_t stride_n,
-                                                 int cur, int lane, uint32_t* above, int* slots,
+                                                 int cur, int lane, uint32_t* scratch, int* slots,
                                                  bool& nan, int& kept) {
   constexpr unsigned kAll = 0xffffffffu;
   constexpr int kSel = select::kSel;
-  uint32_t k[NK];
-  uint32_t m = 0;
-  {
-    float f[NK];
+  const float none = __uint_as_float(0x7FFFFFFFu);
+  constexpr int kRoom = NK <= 16 ? 32 * NK : kAbove;   // scores above L that are kept
+  float* above = reinterpret_cast<float*>(scratch);
+  uint32_t* block = scratch + kRoom;
+  float f[NK];
+  const float* at = srow + lane * stride_n;
+  const int64_t step = 32 * stride_n;
 #pragma unroll
-    for (int e = 0; e < NK; ++e) f[e] = lane + 32 * e < cur ? srow[(lane + 32 * e) * stride_n] : 0.f;
+  for (int e = 0; e < NK; ++e, at += step) f[e] = 32 * e < cur - lane ? __ldg(at) : none;
+  float m = none;
 #pragma unroll
-    for (int e = 0; e < NK; ++e) {
-      k[e] = lane + 32 * e < cur ? key_of(f[e], nan) : 0u;   // 0 ranks below every real key
-      m = max(m, k[e]);
-    }
+  for (int e = 0; e < NK; ++e) {
+    const bool bad = f[e] != f[e] && 32 * e < cur - lane;
+    nan |= bad;
+    f[e] = bad ? -INFINITY : f[e];
+    m = fmaxf(m, f[e]);
   }
-  // L: the smallest of the maxima that fewer than 15 are larger than
+  // L: the smallest of the lanes' maxima that fewer than 15 are larger than
+  above[lane] = m;
+  __syncwarp();
   int larger = 0;
 #pragma unroll
-  for (int o = 1; o < 32; ++o) larger += __shfl_xor_sync(kAll, m, o) > m;
-  const uint32_t low = __reduce_min_sync(kAll, larger < kSel ? m : kAll);
-  // the keys above L and their blocks, in ascending order
+  for (int j = 0; j < 32; j += 4) {
+    const float4 v = *reinterpret_cast<const float4*>(above + j);
+    larger += (v.x > m) + (v.y > m) + (v.z > m) + (v.w > m);
+  }
+  const float low = warp_min_f32(larger < kSel ? m : none);
+  __syncwarp();
+  // the scores above L and their blocks, in ascending order of the blocks
   const unsigned lt = (1u << lane) - 1u;
-  uint32_t* block = above + kAbove;
   int n = 0;
 #pragma unroll
   for (int e = 0; e < NK; ++e) {
-    const bool over = k[e] > low;
+    const bool over = f[e] > low;
     const unsigned b = __ballot_sync(kAll, over);
-    const int at = n + __popc(b & lt);
-    if (over && at < kAbove) {
-      above[at] = k[e];
-      block[at] = lane + 32 * e;
+    const int k = n + __popc(b & lt);
+    if (over && (kRoom == 32 * NK || k < kRoom)) {
+      above[k] = f[e];
+      block[k] = lane + 32 * e;
     }
     n += __popc(b);
   }
@@ -82,20 +93,22 @@ __device__ __forceinline__ bool select_by_maxima(const float* __restrict__ srow,
   if (n >= kSel) {
     // tau: the smallest of them that fewer than 15 are larger than; all larger ones are kept, and
     // of its equals as many of the first as there is room for
-    const uint32_t a = lane < n ? above[lane] : 0u, b = 32 + lane < n ? above[32 + lane] : 0u;
+    const bool two = n > 32;
+    const float a = lane < n ? above[lane] : none, b = 32 + lane < n ? above[32 + lane] : none;
     int a_gt = 0, b_gt = 0;
-    for (int j = 0; j < n; j += 4) {      // (words at and past n: not counted)
-      const uint4 v = *reinterpret_cast<const uint4*>(above + j);
-      const uint32_t x[4] = {v.x, j + 1 < n ? v.y : 0u, j + 2 < n ? v.z : 0u, j + 3 < n ? v.w : 0u};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        a_gt += x[i] > a;
-        b_gt += x[i] > b;
+    for (int j = 0; j < n; j += 4) {
+      float4 v = *reinterpret_cast<const float4*>(above + j);
+      if (j + 4 > n) {                     // (what lies past the n-th is not counted)
+        v.y = j + 1 < n ? v.y : none;
+        v.z = j + 2 < n ? v.z : none;
+        v.w = none;
       }
+      a_gt += (v.x > a) + (v.y > a) + (v.z > a) + (v.w > a);
+      if (two) b_gt += (v.x > b) + (v.y > b) + (v.z > b) + (v.w > b);
     }
-    const uint32_t tau = __reduce_min_sync(kAll, min(a_gt < kSel ? a : kAll, b != 0u && b_gt < kSel ? b : kAll));
-    const unsigned gt_a = __ballot_sync(kAll, a > tau), gt_b = __ballot_sync(kAll, b > tau);
-    const unsigned eq_a = __ballot_sync(kAll, a == tau), eq_b = __ballot_sync(kAll, b == tau);
+    const float tau = warp_min_f32(fminf(a_gt < kSel ? a : none, two && b_gt < kSel ? b : none));
+    const unsigned gt_a = __ballot_sync(kAll, a > tau), eq_a = __ballot_sync(kAll, a == tau);
+    const unsigned gt_b = __ballot_sync(kAll, b > tau), eq_b = __ballot_sync(kAll, b == tau);
     const int need = kSel - __popc(gt_a) - __popc(gt_b);
     const bool take_a = a > tau || (a == tau && __popc(eq_a & lt) < need);
     const bool take_b = b > tau || (b == tau && __popc(eq_a) + __popc(eq_b & lt) < need);
@@ -103,14 +116,14 @@ __device__ __forceinline__ bool select_by_maxima(const float* __restrict__ srow,
     if (take_a) slots[__popc(t_a & lt)] = block[lane];
     if (take_b) slots[__popc(t_a) + __popc(t_b & lt)] = block[32 + lane];
   } else {
-    // all keys above L, and of those equal to it the first
+    // all scores above L, and of those equal to it the first
     const int need = kSel - n;
     int written = 0, ties = 0;
 #pragma unroll
     for (int e = 0; e < NK; ++e) {
-      const bool eq = k[e] == low;             // (L is a real key: not 0)
+      const bool eq = f[e] == low;
       const unsigned be = __ballot_sync(kAll, eq);
-      const bool take = k[e] > low || (eq && ties + __popc(be & lt) < need);
+      const bool take = f[e] > low || (eq && ties + __popc(be & lt) < need);
       const unsigned bs = __ballot_sync(kAll, take);
       if (take) slots[written + __popc(bs & lt)] = lane + 32 * e;
       ties += __popc(be);
@@ -128,7 +141,7 @@ __device__ __forceinline__ bool select_by_maxima(const float* __restrict__ srow,
 // 8 KiB, and the GPU holds half as many.
 template <bool kVarlen, bool kLong>
 __global__ void __launch_bounds__(kWarps * 32) topk_kernel(const TopkParams p) {
-  constexpr int kCache = kLong ? 2048 : kShort;   // candidates cached per warp
+  constexpr int kCache = kLong ? 2048 : 1024;     // words of shared memory a warp
   __shared__ __align__(16) uint32_t s_keys[kWarps][kCache];
   __shared__ int s_slots[kWarps][kTopK];
   pdl_trigger();
