@@ -817,7 +817,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const PrefillPa
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const float w = k + x < have ? __shfl_sync(0xffffffffu, mine, (k + x) & 31) : 0.f;
-        if (w == 0.f) continue;
+        // (a weight that vanishes does not keep a NaN out; an empty part is zeros)
         l = fmaf(w, __shfl_sync(0xffffffffu, ml.y, (k + x) & 31), l);
         o.x = fmaf(w, v[x].x, o.x);
         o.y = fmaf(w, v[x].y, o.y);

@@ -272,3 +272,26 @@ def test_empty_batches_and_refusals():
     with pytest.raises(msa.MSAError):
         msa.dense_prefill(x.q, x.kv, x.bt, x.lens, x.cu, -1.0)
     assert msa.get_error() == 0
+
+
+def test_nan_reaches_across_parts():
+    """A row that many CTAs share, with NaN in keys and values whose parts weigh nothing
+    beside the rest: 0 times NaN is NaN however the row was cut."""
+    n = 9000
+    x = Batch([n], [20], 2, 17)
+    x.q[:] = 0
+    x.q[..., 0] = 2048.0
+    k = x.kv.view(F8)
+    k[..., :D] = 0
+    for page in x.bt[0, :-(-n // PAGE)].tolist():
+        k[page, :, :, 0] = -448.0
+    k[int(x.bt[0, 60]), :, 7, 0] = 448.0      # 448 * 2048 * 0.0071 / D^1/2 = 576 against -576
+    for key, g, d in [(3, 0, D + 5), (2000, 0, D + 9), (4100, 1, D + 127), (8999, 1, D)]:
+        x.kv[int(x.bt[0, key // PAGE]), g, key % PAGE, d] = 0x7F
+    want, tol = every_with_nan(x)
+    assert 0 < int(torch.isnan(want).sum()) < want.numel() // 16
+    check(run(x), want, tol)
+    x.kv[int(x.bt[0, 2]), 1, 44, 17] = 0xFF   # a key: the whole of its heads
+    got = run(x)
+    assert bool(torch.isnan(got[:, GROUP:]).all())
+    assert torch.equal(torch.isnan(got[:, :GROUP]), torch.isnan(want[:, :GROUP]))
