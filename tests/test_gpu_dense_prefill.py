@@ -295,3 +295,12 @@ def test_nan_reaches_across_parts():
     got = run(x)
     assert bool(torch.isnan(got[:, GROUP:]).all())
     assert torch.equal(torch.isnan(got[:, :GROUP]), torch.isnan(want[:, :GROUP]))
+
+
+@pytest.mark.parametrize("sm,k_scale", [(1e-25, 1e-25), (1e-30, 1e-12)])
+def test_scales_that_vanish(sm, k_scale):
+    """Logits that are all 0 in fp32, the factors' product too: every visible key counts alike."""
+    x = Batch([300, 130], [50, 130], 1, 18)
+    x.sm, x.k_scale = sm, k_scale
+    x.q *= 2.0 ** -100
+    check(run(x), *every(x))
