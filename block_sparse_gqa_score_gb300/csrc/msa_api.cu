@@ -900,9 +900,13 @@ int check_caches(const msa_cache_t* caches, int num_caches) {
   return MSA_OK;
 }
 
+// `overlap`: the input-overlap setting.  With it on, the next call's first kernel reads
+// tables and caches before it waits for the kernel just before it, so an empty kernel
+// stands in between.  pdl: whether the first copy kernel may overlap what is before it.
 int enqueue_copies(const int32_t* copies, int n, const msa_cache_t* caches, int num_caches,
-                   int64_t num_blocks, const DeviceState& dev, cudaStream_t stream, bool pdl) {
-  if (n == 0) return MSA_OK;
+                   int64_t num_blocks, const DeviceState& dev, cudaStream_t stream, bool pdl,
+                   bool overlap) {
+  if (n == 0) num_caches = 0;
   for (int c0 = 0; c0 < num_caches; c0 += msa::kMaxCopyCaches) {
     msa::CopyParams p{};
     p.copies = copies;
@@ -918,7 +922,7 @@ int enqueue_copies(const int32_t* copies, int n, const msa_cache_t* caches, int 
     const int st = from_cuda(msa::launch_copy(p, stream, pdl || c0 > 0));
     if (st != MSA_OK) return st;
   }
-  return MSA_OK;
+  return overlap ? from_cuda(msa::launch_order(stream)) : MSA_OK;
 }
 
 }  // namespace
@@ -1031,8 +1035,9 @@ int msa_fork_pages(const int32_t* block_table, const int32_t* seq_lens, const in
                           seq_lens_out, refs_out, copies,  dev->err, B, rows, S,
                           static_cast<int>(num_blocks)};
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if ((st = from_cuda(msa::launch_fork(p, s, input_overlap()))) != MSA_OK) return st;
-  return enqueue_copies(copies, rows, caches, num_caches, num_blocks, *dev, s, true);
+  const bool overlap = input_overlap();
+  if ((st = from_cuda(msa::launch_fork(p, s, overlap))) != MSA_OK) return st;
+  return enqueue_copies(copies, rows, caches, num_caches, num_blocks, *dev, s, true, overlap);
 }
 
 int msa_compact_pages(const int32_t* block_table, const int32_t* seq_lens, const int32_t* refs,
@@ -1055,9 +1060,10 @@ int msa_compact_pages(const int32_t* block_table, const int32_t* seq_lens, const
   const msa::CompactParams p{block_table, seq_lens, refs, block_table_out, refs_out, copies,
                              dev->err, B, S, static_cast<int>(num_blocks)};
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if ((st = from_cuda(msa::launch_compact(p, s, input_overlap()))) != MSA_OK) return st;
+  const bool overlap = input_overlap();
+  if ((st = from_cuda(msa::launch_compact(p, s, overlap))) != MSA_OK) return st;
   return enqueue_copies(copies, static_cast<int>(num_blocks / 2), caches, num_caches, num_blocks,
-                        *dev, s, true);
+                        *dev, s, true, overlap);
 }
 
 int msa_copy_pages(const int32_t* copies, int n, int64_t num_blocks, const msa_cache_t* caches,
@@ -1068,8 +1074,9 @@ int msa_copy_pages(const int32_t* copies, int n, int64_t num_blocks, const msa_c
   if (st != MSA_OK || n == 0 || num_caches == 0) return st;
   DeviceState* dev;
   if ((st = device_state(&dev)) != MSA_OK) return st;
+  const bool overlap = input_overlap();
   return enqueue_copies(copies, n, caches, num_caches, num_blocks, *dev,
-                        reinterpret_cast<cudaStream_t>(stream), input_overlap());
+                        reinterpret_cast<cudaStream_t>(stream), overlap, overlap);
 }
 
 int msa_test_wait_timeout(unsigned long long limit_ns, msa_stream_t stream) {

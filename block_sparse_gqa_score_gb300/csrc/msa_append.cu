@@ -462,10 +462,14 @@ __global__ void __launch_bounds__(kThreads, kScaled && kW == 1 ? 2 : 3)
       p, (static_cast<int64_t>(blockIdx.x) - unit_blocks) * kWarps + warp, per, lane);
 }
 
-// Nothing: stands between an append and a call that may start early (see launch_append).
+// Nothing: stands between a call and one that may start early (see launch_order).
 __global__ void order_kernel() {}
 
 }  // namespace
+
+cudaError_t launch_order(cudaStream_t stream) {
+  return launch_pdl(order_kernel, dim3(1), dim3(1), 0, stream, false);
+}
 
 cudaError_t launch_append(const AppendParams& p, cudaStream_t stream, bool pdl) {
   const bool scaled = p.kv_scales != nullptr, varlen = p.cu_q != nullptr;
@@ -502,8 +506,7 @@ cudaError_t launch_append(const AppendParams& p, cudaStream_t stream, bool pdl) 
   // With input overlap on, the next call's first kernel reads the cache and
   // the query before it waits for the kernel just before it.  An empty kernel
   // that starts only after this one has finished stands between them.
-  if (e == cudaSuccess && pdl)
-    e = launch_pdl(order_kernel, dim3(1), dim3(1), 0, stream, false);
+  if (e == cudaSuccess && pdl) e = launch_order(stream);
   return e;
 }
 

@@ -165,6 +165,9 @@ struct AppendParams {
   int sms;
 };
 cudaError_t launch_append(const AppendParams& p, cudaStream_t stream, bool pdl);
+// An empty kernel that starts behind all that is enqueued: what a call wrote is complete
+// before a later call's first kernel starts, early as it may.
+cudaError_t launch_order(cudaStream_t stream);
 
 // Prefill batches over every visible page: dense attention (msa_dense_prefill.cu)
 // and the block scorer (msa_score_prefill.cu).

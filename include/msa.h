@@ -796,12 +796,12 @@ int msa_set_union_tile(int enable);
  * that call's inputs: a kernel that wrote them could otherwise be read
  * before its writes are visible.  Outputs are always ordered: no library
  * kernel writes a buffer before the previous kernel has finished.
- * msa_dense_prefill, msa_score_prefill, msa_topk_prefill and the calls on pages
- * read nothing early.
- * msa_append_kv(_prefill), whose outputs are the other calls' inputs, reads
- * nothing early and, enqueued with the setting on, has finished before a kernel
- * enqueued after it starts (enqueued with it off, it is like any other kernel
- * that wrote the inputs: turn the setting on before the append).
+ * msa_dense_prefill, msa_score_prefill and msa_topk_prefill read nothing early.
+ * msa_append_kv(_prefill) and the calls on pages (fork, compact, copy), whose
+ * outputs are the other calls' inputs, read nothing early and, enqueued with the
+ * setting on, have finished before a kernel enqueued after them starts (enqueued
+ * with it off, they are like any other kernel that wrote the inputs: turn the
+ * setting on before them).
  * Process-wide; returns the previous setting (0 or 1).
  */
 int msa_set_input_overlap(int enable);

@@ -365,6 +365,52 @@ def test_prefill_of_new_rows_together():
     assert msa.get_error() == 0
 
 
+def test_overlapped_calls_keep_their_order():
+    """With input overlap on, calls that read tables, lengths and caches right behind the
+    calls on pages find what these wrote: tables and caches that are rewritten in turn."""
+    B, S, Hkv, sm = 32, 40, 2, D ** -0.5
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    x = Pool([4700 + 3 * b for b in range(B)], S, 2 * B * S, 15, Hkv=Hkv)
+    t0, n0, r0 = x.gpu()
+    kv0 = torch.randn(x.caches[0].shape, device="cuda", generator=gen).mul(50).to(F8).view(torch.uint8)
+    q = torch.randn((B, GROUP * Hkv, D), device="cuda", generator=gen).to(torch.bfloat16)
+    orders = [i32([(a * b + 1) % B // k * k for b in range(B)]) for a, k in ((5, 1), (7, 4), (11, 2))]
+    one = i32([1] * B)
+    t = t0.clamp(0, x.NB - 1)
+    n, r, co = n0.clone(), r0.clone(), torch.full((B, 3), -1, dtype=torch.int32, device="cuda")
+    t2, r2 = t.clone(), r0.clone()
+    moves = torch.full((x.NB // 2, 3), -1, dtype=torch.int32, device="cuda")
+    moves[:, 2] = 0
+
+    def run(sync):
+        kv = kv0.clone()
+        torch.cuda.synchronize()
+        out = []
+        for p in orders:
+            for f in (lambda: msa.fork_pages(t0, n0, p, r0, [kv], grow=one, block_table_out=t,
+                                             seq_lens_out=n, refs_out=r, copies=co),
+                      lambda: out.append(msa.score(q, kv, t, n, 1, sm)),
+                      lambda: msa.compact_pages(t, n, r, [kv], block_table_out=t2, refs_out=r2, copies=moves),
+                      lambda: out.append(msa.dense_decode(q, kv, t2, n, 1, sm, 0.01, 0.01)),
+                      lambda: out.append(msa.decode_step(q, kv, t2, n, 1, sm, 0.01, 0.01)[2])):
+                f()
+                if sync:
+                    torch.cuda.synchronize()
+            kv.copy_(kv0)
+        torch.cuda.synchronize()
+        return out
+
+    want = run(True)
+    was = msa.set_input_overlap(True)
+    try:
+        for _ in range(5):
+            for a, b in zip(run(False), want):
+                assert torch.equal(a, b)
+    finally:
+        msa.set_input_overlap(was)
+    assert msa.get_error() == 0
+
+
 def test_refusals():
     x = Pool([300, 5], 4, 20, 14)
     t0, n0, r0 = x.gpu()
