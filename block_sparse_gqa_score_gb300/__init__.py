@@ -51,7 +51,8 @@ MAX_QLEN = 32
 __all__ = ["score", "topk", "sparse_decode", "sparse_decode_select", "sparse_prefill",
            "sparse_prefill_select", "dense_decode", "dense_splits",
            "combine", "decode_step", "append_kv", "append_kv_prefill", "score_prefill",
-           "topk_prefill", "dense_prefill", "dense_prefill_workspace_bytes", "fork_pages", "compact_pages", "copy_pages",
+           "topk_prefill", "dense_prefill", "dense_prefill_workspace_bytes", "fork_pages",
+           "compact_pages", "copy_pages",
            "fused_selection", "FUSED_MAX_BLOCKS", "workspace_bytes",
            "choose_splits", "get_error", "set_input_overlap", "set_union_tile", "DecodeBuffers",
            "MSAError"]
@@ -520,8 +521,10 @@ def dense_prefill(q, kv, block_table, seq_lens, cu_seqlens_q, sm_scale: float,
     need = dense_prefill_workspace_bytes(dev)
     if workspace is None or workspace.numel() * workspace.element_size() < need:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev:
-        raise ValueError(f"workspace must be on {dev}")
+        if stream is not None:      # not given to another tensor before that stream is through
+            workspace.record_stream(stream)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {dev}")
     st = _lib().msa_dense_prefill(
         q.data_ptr(), float(q_scale) if _fp8(q, q_scale) else 0.0, kv.data_ptr(), sc,
         block_table.data_ptr(), seq_lens.data_ptr(), cu_seqlens_q.data_ptr(), workspace.data_ptr(),

@@ -856,7 +856,9 @@ int prepare_prefill(const void* q, float q_scale, const void* kv, const float* k
   if (!(q_scale == 0.f || finite_pos(q_scale)) || !finite_pos(sm_scale) || !finite_pos(k_scale) ||
       !aligned(kv_scales, k_only ? 4 : 8))
     return MSA_EINVAL;
-  if (!cu_q || !aligned(cu_q, 4) || T < 0 || T > INT_MAX / 4 || (B == 0) != (T == 0)) return MSA_EINVAL;
+  if (!cu_q || !aligned(cu_q, 4) || T < 0 || T > INT_MAX / 4 || (B == 0) != (T == 0) ||
+      S > msa::kMaxPrefillStride)
+    return MSA_EINVAL;
   if (T == 0) return MSA_OK;
   int st = check_common(q, kv, block_table, seq_lens, B, 1, Hq, Hkv, S, num_blocks);
   if (st != MSA_OK) return st;

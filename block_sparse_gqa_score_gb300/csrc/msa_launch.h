@@ -193,6 +193,9 @@ struct PrefillParams {
   float logit_scale;           // dense: sm_scale * k_scale * log2(e); scorer: sm_scale * k_scale
   float v_scale;
 };
+// Columns of a block table: some waits of these kernels last while a CTA goes through a
+// unit's pages (at 1.6 us a page 0.8 s of the 2 s that a wait may take).
+constexpr int kMaxPrefillStride = 1 << 19;
 // Bytes of the dense kernel's part_o, part_ml and cut together.
 size_t dense_prefill_workspace(int ctas);
 cudaError_t launch_dense_prefill(const CUtensorMap& kv_map, const PrefillParams& p,

@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster)
 
   // a run of `run` neighbouring pages a thread
   const int threads = kCluster * kThreads;
-  const int run = (p.num_blocks + threads - 1) / threads;
+  const int run = (p.num_blocks - 1) / threads + 1;
   const int64_t lo64 = static_cast<int64_t>(cta * kThreads + tid) * run;
   const int lo = static_cast<int>(min(lo64, static_cast<int64_t>(p.num_blocks)));
   const int hi = static_cast<int>(min(lo64 + run, static_cast<int64_t>(p.num_blocks)));
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster)
   pdl_trigger();
   pdl_wait();
   const int threads = kCluster * kThreads;
-  const int run = (p.num_blocks + threads - 1) / threads;
+  const int run = (p.num_blocks - 1) / threads + 1;
   const int64_t lo64 = static_cast<int64_t>(cta * kThreads + tid) * run;
   const int lo = static_cast<int>(min(lo64, static_cast<int64_t>(p.num_blocks)));
   const int hi = static_cast<int>(min(lo64 + run, static_cast<int64_t>(p.num_blocks)));

@@ -625,7 +625,7 @@ int msa_decode_step_scaled(const void *q, float q_scale, const void *kv, const f
  *   k_only     non-zero: kv is a K-only cache [num_blocks, Hkv, 128, 128]
  * Numerics as msa_score: exact fp8 parts of the query, fp32 sums.
  * Errors: as msa_score, cu_seqlens_q, B and T as msa_sparse_prefill, no bound on
- * the query length, q_scale < 0 or not finite, misaligned kv_scales (MSA_EINVAL).
+ * the query length, S > 2^19, q_scale < 0 or not finite, misaligned kv_scales (MSA_EINVAL).
  * Device: MSA_ERR_PAGE_RANGE, MSA_ERR_SCALE (K's: block scored -inf),
  * MSA_ERR_SEQ_RANGE: a request with q_len_b > seq_lens[b], bad seq_lens[b] or a
  * range of tokens outside 0 .. T, and tokens before cu_seqlens_q[0] or past
@@ -654,7 +654,7 @@ int msa_topk_prefill(const float *scores, int64_t stride_h, int64_t stride_t, in
  * key: the dense layers of the model.  The operation of msa_dense_decode with one
  * query length per request: token j of request b, at pos = seq_lens[b] - q_len_b
  * + j, attends keys 0 .. pos (the chunk's own are in the cache: msa_append_kv_prefill
- * comes first).  cu_seqlens_q, B and T as msa_sparse_prefill; any S.
+ * comes first).  cu_seqlens_q, B and T as msa_sparse_prefill.
  *   q_scale    0: q is bf16; > 0: fp8 e4m3 of value q * q_scale
  *   kv_scales  NULL: keys K8 * k_scale, values V8 * v_scale; else page scales
  *              [num_blocks, Hkv, 2] that multiply them, as the msa_*_scaled calls
@@ -736,7 +736,7 @@ int msa_copy_pages(const int32_t *copies, int n, int64_t num_blocks, const msa_c
  * equals refs), MSA_ERR_ROW_RANGE (a parent outside -1 .. B - 1: the row is
  * empty), MSA_ERR_SEQ_RANGE (a parent's length outside 0 .. 128 S: taken as 0;
  * growth below 0 or past 128 S: taken as 0), MSA_ERR_PAGE_RANGE (an entry outside
- * the pool: -1 in the new row, no copy), MSA_ERR_REFS (a page of a row whose count
+ * the pool: -1 in the new row, or a page without the copy), MSA_ERR_REFS (a page of a row whose count
  * changes was counted as free: it may have been given away).
  */
 int msa_fork_pages(const int32_t *block_table, const int32_t *seq_lens, const int32_t *parents,

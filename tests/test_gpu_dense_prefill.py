@@ -304,3 +304,23 @@ def test_scales_that_vanish(sm, k_scale):
     x.sm, x.k_scale = sm, k_scale
     x.q *= 2.0 ** -100
     check(run(x), *every(x))
+
+
+def test_workspace_of_the_call_on_another_stream():
+    """A call on a given stream without a workspace: its own is not handed to other tensors
+    while that stream works with it."""
+    x = Batch([9000, 300], [40, 300], 2, 19)
+    want = run(x)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    need = msa.dense_prefill_workspace_bytes("cuda")
+    for _ in range(4):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(2000000)
+        out = msa.dense_prefill(*x.args(), x.v_scale, stream=side, **x.kw())
+        junk = torch.full((need,), 0x55, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and int(junk[0]) == 0x55
+    wide = torch.zeros(1, dtype=torch.uint8, device="cuda").expand(need)
+    with pytest.raises(ValueError):
+        msa.dense_prefill(*x.args(), x.v_scale, workspace=wide, **x.kw())

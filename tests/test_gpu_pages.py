@@ -365,6 +365,27 @@ def test_prefill_of_new_rows_together():
     assert msa.get_error() == 0
 
 
+def test_most_rows():
+    """As many rows as a fork takes, on both sides."""
+    n = 8192
+    r = random.Random(16)
+    x = Pool([r.choice([0, 1, 127, 128, 129, 200, 256]) for _ in range(n)], 3, 4 * n, 16, Hkv=1)
+    parents = [r.randrange(-1, n) for _ in range(n)]
+    grow = [r.choice([0, 1, 128]) for _ in range(n)]
+    free = [p for p in range(x.NB) if x.refs[p] == 0]
+    assert len(free) > 2 * n
+    t0, n0, r0 = x.gpu()
+    t, lens, refs, copies = msa.fork_pages(t0, n0, i32(parents), r0, grow=i32(grow))
+    rows, want_n, want_r, want_c = x.fork(parents, grow)
+    same(t, full(rows, 3))
+    same(lens, want_n)
+    same(refs, want_r)
+    same(copies, [list(c) for c in want_c])
+    with pytest.raises(msa.MSAError):
+        msa.fork_pages(t0, n0, i32(parents + [0]), r0)
+    assert msa.get_error() == 0
+
+
 def test_overlapped_calls_keep_their_order():
     """With input overlap on, calls that read tables, lengths and caches right behind the
     calls on pages find what these wrote: tables and caches that are rewritten in turn."""

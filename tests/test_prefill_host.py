@@ -65,6 +65,13 @@ def test_prefill_rejects(lib, kw):
     assert score(lib, **kw) == EINVAL
 
 
+def test_prefill_rejects_rows_longer_than_a_wait(lib):
+    for f in (dense, score):
+        assert f(lib, B=1, S=(1 << 19) + 1) == EINVAL
+        if not torch.cuda.is_available():
+            assert f(lib, B=1, S=1 << 19) == _native.ECUDA
+
+
 def test_prefill_more_rejections(lib):
     assert dense(lib, v_s=float("nan")) == EINVAL and dense(lib, out=off(8)) == EINVAL
     assert score(lib, k_only=1, sc=off(2)) == EINVAL
