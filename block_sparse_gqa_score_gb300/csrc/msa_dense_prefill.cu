@@ -76,7 +76,7 @@ constexpr uint32_t kColS = 0, kColO = 256;      // [half] of 128 columns each
 
 constexpr float kShift = 8.f;                   // P = 2^kShift at the largest u when M is set
 constexpr float kTop = 15.f;                    // M moves when some P would pass 2^kTop
-constexpr float kTiny = 0x1p-120f;              // a logit's factor below this leaves every logit 0
+constexpr float kTiny = 0x1p-108f;              // 2^-40 of it is not 0, and 2^40 leaves every logit 0
 
 struct PageInfo {
   float k, lv, iv;      // K scale, log2 and reciprocal of the V scale
@@ -505,11 +505,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const PageInfo in = tail->info[t % kInfo];
-        if (n == sg.n0) zs = tail->zs[i & 3][j];
+        if (n == sg.n0) zs = fmaxf(tail->zs[i & 3][j], kTiny);   // (0 times a masked -inf is NaN)
         tc::fence_after_thread_sync();
         const int lim = in.block < 0 ? -1 : pos - n * kPage;  // keys <= lim are visible
         const bool edge = __any_sync(0xffffffffu, lim < kPage - 1);
-        const float zt = fmaxf(zs * in.k, kTiny);           // (0 times a masked -inf is NaN)
+        const float zt = zs * in.k;
         float nl = M == -INFINITY ? 0.f : in.lv - M + kShift;
         float a0 = 0.f, a1 = 0.f, b0 = 0.f, b1 = 0.f;
 #pragma unroll 1
