@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The first query tile: nobody but warp 0, which loads the first pages, has anything else
   // to do yet.
   if (warp > 0 && tail->seg[0].ntok > 0 && tail->seg[0].n0 < tail->seg[0].n1) {
-    (void)load_query_tile<2>(p, tail->seg[0], warp - 1, 15, smem, tail->zs[0], lane, [] { return true; });
+    (void)load_query_tile<2, 2>(p, tail->seg[0], warp - 1, 15, smem, tail->zs[0], lane, [] { return true; });
     named_barrier(1, 32 * 15);
   }
 
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (sg.ntok > 0 && sg.n0 < sg.n1) {
           // tokens 8 + h, 10 + h, .. (warps 12..15 take the first eight)
           if (i > 0)
-            ok = load_query_tile<4>(p, sg, kHalfTokens + h, 2, smem, tail->zs[i & 3], lane, [&] {
+            ok = load_query_tile<4, 2>(p, sg, kHalfTokens + h, 2, smem, tail->zs[i & 3], lane, [&] {
               return __all_sync(0xffffffffu, tiles == 0 || wait_for(&tail->q_empty, (tiles - 1) & 1)) != 0;
             });
           if (!ok) break;
@@ -547,6 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             a0 *= al, a1 *= al, b0 *= al, b1 *= al;
             // this page's P so far
             tc::wait_st();
+#pragma unroll 1
             for (int k = 0; k < c / 2; k += 8) {
               uint32_t w[8];
               tc::ld_32x32b_x8(s_at + k, w);
@@ -560,6 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (n > sg.n0) {
               // the products so far are complete: S(n) was issued behind them
+#pragma unroll 1
               for (int k = 0; k < kHeadDim; k += 8) {
                 uint32_t w[8];
                 tc::ld_32x32b_x8(o_at + k, w);
@@ -696,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float z[2];
 #pragma unroll
           for (int k = 0; k < 2; ++k)
-            if (2 * w4 + k < sg.ntok) z[k] = rows[k].split(p);
+            if (2 * w4 + k < sg.ntok) z[k] = rows[k].split<2>(p);
           ok = __all_sync(0xffffffffu, tiles == 0 || wait_for(&tail->q_empty, (tiles - 1) & 1));
           if (!ok) break;
 #pragma unroll
@@ -737,31 +739,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint8_t* from = smem + kOffV8 + sv * kHalfTile;
         uint8_t* to = smem + kOffV + b * kVTile;
         bool nan = false;
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const int key = 32 * w4 + 8 * (x >> 1) + 2 * (lane >> 3) + ((lane >> 2) & 1);
-          const int c = (lane & 3) + 4 * (((lane >> 2) & 1) ^ (x & 1));
-          uint4 r = *reinterpret_cast<const uint4*>(from + sw128(key, c));
-          if (key > all) {
-            if (key > last) {
-              r = make_uint4(0u, 0u, 0u, 0u);
-            } else {
-              uint32_t* q = reinterpret_cast<uint32_t*>(&r);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t m = nan_bytes(q[e]);
-                if (m) {
-                  nan = true;
-                  q[e] &= ~((m >> 7) * 0xFFu);
-                }
-              }
-            }
-          }
+        // chunk x of this lane: which key of the page and which 16 bytes of its row
+        auto key_of = [&](int x) { return 32 * w4 + 8 * (x >> 1) + 2 * (lane >> 3) + ((lane >> 2) & 1); };
+        auto piece_of = [&](int x) { return (lane & 3) + 4 * (((lane >> 2) & 1) ^ (x & 1)); };
+        auto convert = [&](const uint4& r, int key, int c) {
           const uint2 f0 = e4m3x4_to_f16x4(r.x), f1 = e4m3x4_to_f16x4(r.y);
           const uint2 f2 = e4m3x4_to_f16x4(r.z), f3 = e4m3x4_to_f16x4(r.w);
           uint8_t* half = to + (c >> 2) * kHalfTile;
           *reinterpret_cast<uint4*>(half + sw128(key, 2 * (c & 3))) = make_uint4(f0.x, f0.y, f1.x, f1.y);
           *reinterpret_cast<uint4*>(half + sw128(key, 2 * (c & 3) + 1)) = make_uint4(f2.x, f2.y, f3.x, f3.y);
+        };
+        if (all >= kPage - 1) {
+#pragma unroll 4
+          for (int x = 0; x < 8; ++x)
+            convert(*reinterpret_cast<const uint4*>(from + sw128(key_of(x), piece_of(x))), key_of(x), piece_of(x));
+        } else {
+#pragma unroll 1
+          for (int x = 0; x < 8; ++x) {
+            const int key = key_of(x), c = piece_of(x);
+            uint4 r = *reinterpret_cast<const uint4*>(from + sw128(key, c));
+            if (key > last) {
+              r = make_uint4(0u, 0u, 0u, 0u);
+            } else if (key > all) {
+              uint32_t* q = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t m = nan_bytes(q[e]);
+                nan |= m != 0;
+                q[e] &= ~((m >> 7) * 0xFFu);
+              }
+            }
+            convert(r, key, c);
+          }
         }
         if (nan) tail->nan_seen[i & 3] = 1;
         tc::fence_proxy_async_smem();

@@ -271,8 +271,24 @@ struct QueryRows {
     }
   }
 
+  // Eight bf16 values times sd: hi and lo parts.
+  static __device__ __forceinline__ uint4 parts(uint4 v, float sd) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t h[2], l[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const float f[4] = {bf16_bits_to_f32(w[2 * x] & 0xFFFF) * sd,
+                          __uint_as_float(w[2 * x] & 0xFFFF0000u) * sd,
+                          bf16_bits_to_f32(w[2 * x + 1] & 0xFFFF) * sd,
+                          __uint_as_float(w[2 * x + 1] & 0xFFFF0000u) * sd};
+      split_e4m3x4(f, h[x], l[x]);
+    }
+    return make_uint4(h[0], h[1], l[0], l[1]);
+  }
+
   // A bf16 row's values to their parts, in place: v[k].x, .y hi and .z, .w lo of the lane's eight
   // elements.  Returns the dot products' factor.
+  template <int kTurn>
   __device__ __forceinline__ float split(const PrefillParams& p) {
     if (p.q8) return p.logit_scale * p.q_scale;
     uint32_t m = 0;                       // the largest magnitudes as bf16 bits, two at a time
@@ -288,19 +304,15 @@ struct QueryRows {
     int e = (biased == 0 || biased == 0xFF) ? 0 : biased - 127 - 7;   // largest in [2^7, 2^8)
     e = e < -100 ? -100 : (e > 100 ? 100 : e);
     const float sd = exp2i(-e);
+    // (in a loop, the array turned by kTurn at a time: in line it was 6 KiB of code a token, and the
+    // warps of these kernels wait for instructions when their parts do not fit the SM's cache)
+#pragma unroll 1
+    for (int k = 0; k < 8; k += kTurn) {
+      uint4 r[kTurn];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-      uint32_t h[2], l[2];
+      for (int x = 0; x < kTurn; ++x) r[x] = parts(v[x], sd);
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const float f[4] = {bf16_bits_to_f32(w[2 * x] & 0xFFFF) * sd,
-                            __uint_as_float(w[2 * x] & 0xFFFF0000u) * sd,
-                            bf16_bits_to_f32(w[2 * x + 1] & 0xFFFF) * sd,
-                            __uint_as_float(w[2 * x + 1] & 0xFFFF0000u) * sd};
-        split_e4m3x4(f, h[x], l[x]);
-      }
-      v[k] = make_uint4(h[0], h[1], l[0], l[1]);
+      for (int x = 0; x < 8; ++x) v[x] = x + kTurn < 8 ? v[x + kTurn] : r[x + kTurn - 8];
     }
     return p.logit_scale * exp2i(e);
   }
@@ -328,22 +340,22 @@ struct QueryRows {
 // products' factors zs[16].  One warp, which takes at most kMost tokens; wait() returns,
 // false to give up, when the tile's last readers are through: the rows are loaded and split
 // by then.
-template <int kMost, typename Wait>
+template <int kMost, int kTurn, typename Wait>
 __device__ __forceinline__ bool load_query_tile(const PrefillParams& p, const Segment& sg, int first,
                                                 int step, uint8_t* tile, float* zs, int lane,
                                                 Wait&& wait) {
   constexpr int kAhead = kMost < 2 ? kMost : 2;    // tokens in registers at a time
   QueryRows rows[kAhead];
-  float z[kAhead];
 #pragma unroll
   for (int k = 0; k < kAhead; ++k)
     if (first + k * step < sg.ntok) rows[k].load(p, sg.tok0 + first + k * step, sg.g, lane);
-#pragma unroll
-  for (int k = 0; k < kAhead; ++k)
-    if (first + k * step < sg.ntok) z[k] = rows[k].split(p);
-  if (!wait()) return false;
 #pragma unroll 1
   for (int j0 = first; j0 < kTile; j0 += kAhead * step) {
+    float z[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (j0 + k * step < sg.ntok) z[k] = rows[k].split<kTurn>(p);
+    if (j0 == first && !wait()) return false;
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       const int j = j0 + k * step;
@@ -361,11 +373,6 @@ __device__ __forceinline__ bool load_query_tile(const PrefillParams& p, const Se
         if (!p.q8) zero_query_rows(row0, lo, lane);
         if (lane == 0) zs[j] = 0.f;
       }
-    }
-    if (kMost > kAhead) {
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k)
-        if (j0 + (kAhead + k) * step < sg.ntok) z[k] = rows[k].split(p);
     }
   }
   fence_proxy_async();

@@ -68,7 +68,7 @@ static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 // Token x of a segment's query tile.  Not in line: its registers are not the search's.
 __device__ __noinline__ void load_token(const PrefillParams& p, const Segment* sg, int x, uint8_t* tile,
                                         float* zs) {
-  (void)load_query_tile<1>(p, *sg, x, kTile, tile, zs, threadIdx.x & 31, [] { return true; });
+  (void)load_query_tile<1, 4>(p, *sg, x, kTile, tile, zs, threadIdx.x & 31, [] { return true; });
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         ++parted;
       } else if (sg.ntok > 0)
-        (void)load_query_tile<kTile / 2>(p, sg, h, 2, smem + (i & 1) * kQTile, tail->zs[i & 1], lane,
+        (void)load_query_tile<kTile / 2, 4>(p, sg, h, 2, smem + (i & 1) * kQTile, tail->zs[i & 1], lane,
                                          [] { return true; });
       __syncwarp();
       if (lane == 0) {
