@@ -42,6 +42,20 @@
 //   warps 12..15  values to fp16
 // One CTA an SM, each an equal share of all pages (msa_prefill.cuh); what several CTAs
 // work on is merged by a second kernel from their parts, in the order of the pages.
+//
+// Measured, 64/4 heads: four chunks of up to 1k tokens over 4k .. 16k 694 us (1420 TFLOP/s),
+// with an fp8 query 651; one chunk of 1.4k tokens over 128k on one KV head with page scales
+// 752 us (1490 TFLOP/s); eight prompts of 1k 205 us; two chunks of 24 tokens over 2k .. 3k on
+// one KV head 22.6 us, a third of it the launches, the first tiles and the merge.
+// A page takes some 3000 cycles, of which the products alone need 2250 (2048 at the tensor
+// core's rate): the rest is the round of one half, S 900 cycles, softmax 1400 (the two halves'
+// warps share the issue slots), P handed on 300, O 500, of which the other half's products
+// hide most but not all.  S ahead of P would break the round, but two S and a P for each half
+// beside O do not fit 512 columns.  Slower were: sixteen softmax warps with two threads a row
+// (registers spill), a product warp for each half, pieces of 32 columns, a check of the sum in
+// place of the maxima, P handed on in halves.  The warps' code has to stay small: seven
+// different loops share the SM's instruction cache, and with the query tiles' split and the
+// converter in line (191 KiB) short units took half as long again.
 #include <cstddef>
 
 #include "msa_device.cuh"
@@ -60,8 +74,9 @@ constexpr int kSlots = 3;                       // K tiles in flight
 constexpr int kVSlots = 2;                      // V tiles as stored, in flight
 constexpr int kInfo = 16;                       // pages' factors in flight
 constexpr int kSegs = 4;                        // segments known at a time
-// A unit's query and output, in pages' time: an fp8 query is copied, a bf16 one split.
-__device__ __forceinline__ int extra_steps(const PrefillParams& p) { return p.q8 ? 3 : 6; }
+// A unit's query and output, in pages' time: an fp8 query is copied, a bf16 one split (the four
+// chunks above with 4: 693 us; 5: 696, 6: 700, 7: 702).
+__device__ __forceinline__ int extra_steps(const PrefillParams& p) { return p.q8 ? 3 : 4; }
 constexpr int kMinSteps = 2;
 constexpr int kRows = kGroup * kTile;           // query rows of a unit
 constexpr int kQTile = 4 * kHalfTile;           // two halves, hi and lo parts

@@ -12,12 +12,18 @@
 // query row: the largest of a page's 128 columns is 64 three-input maxima without an
 // exchange, and a token's 16 heads are 16 lanes.  (Two pages, N = 256: A is read once for
 // both, 12 KiB of operands in 128 cycles; with a page at a time, 8 KiB in 64 cycles, shared
-// memory was the limit and there were twice the products to issue: 340 us for the listed
-// four chunks.)  A bf16 query is two exact e4m3 parts (two products a half, which cost what
+// memory was the limit and there were twice the products to issue: 340 us where two take 251.)
+// A bf16 query is two exact e4m3 parts (two products a half, which cost what
 // one bf16 product would, and the keys need no conversion), an fp8 query is one.  Each half
 // has its 256 columns of tensor memory: while one is searched the other is multiplied.  One
 // CTA an SM, each an equal share of all pages (msa_prefill.cuh); the next unit's query tile
 // is prepared while the current one is worked on.
+// Measured: four chunks of up to 1k tokens over 4k .. 16k, 64/4 heads, page scales 252 us,
+// 1950 TFLOP/s (the tensor core is active 95 % of the time); an fp8 query of 200 tokens, K-only
+// cache, 46 us (1590 TFLOP/s); eight prompts of 1k 113 us (scores are written at 0.9 TB/s, and
+// units of some five pages pay for their query tiles); three chunks of 40 tokens on one KV
+// head 13.6 us, of which 2 are products.  With the query tiles' split in line (118 KiB of code,
+// the warps waited for instructions) the four chunks took 277 us.
 //   warp 0       page look-ups, TMA of K tiles
 //   warp 1       products (owns tensor memory)
 //   warps 2, 3   segments and query tiles, a token each in turn (behind a short unit: warps
@@ -39,9 +45,9 @@ using namespace prefill;
 constexpr int kThreads = 640;
 constexpr int kPairs = 3;                       // pairs of K tiles in flight
 constexpr int kInfo = 8;                        // pairs' factors in flight
-constexpr int kExtra = 3;                       // a unit's query tile, in pages
+constexpr int kExtra = 4;                       // a unit's query tile, in pages
 constexpr int kMinSteps = 1;
-constexpr int kShort = 16;                      // pages of a unit too few to hide the next one's query tile
+constexpr int kShort = 10;                      // pages of a unit too few to hide the next one's query tile
 constexpr int kQTile = 4 * kHalfTile;           // two halves, hi and lo parts
 constexpr int kOffK = 2 * kQTile;
 constexpr int kOffTail = kOffK + kPairs * 2 * kHalfTile;

@@ -10,13 +10,14 @@
 //
 // What bounds it: the issue slots, some 600 instructions a row (its scores are a few hundred
 // floats).  The kept blocks are found from the lanes' own maxima: L, the 15th largest of
-// the 32, has at least 15 keys at or above it, and few keys are above it (some 20 of 256
-// random ones).  If fewer than 15 are, they are kept with the first keys equal to L; else
-// the 15 are chosen among them alone, each compared with all of them in shared memory.
+// the 32, has at least 15 scores at or above it, and few are above it (some 20 of 256
+// random ones).  If fewer than 15 are, they are kept with the first scores equal to L; else
+// the 15 are chosen among them alone, each compared with all of them in shared memory.  A row
+// with more than 64 scores above L (they would have to lie in few lanes) is left to the search
+// of msa_select.cuh, as are rows of more than 2048 blocks.
 // 5980 tokens of 4 heads over up to 512 blocks: 18 us, 1.4 TB/s of scores.  (A search bit by
-// bit, 31 rounds of a count over the warp, took 83 us; several heads of a token in one
-// warp, with the next row's scores on their way, was slower.)  A row with more than 64 keys above L (they would have to lie in few lanes) is
-// left to the search of msa_select.cuh, as are rows of more than 2048 blocks.
+// bit, 31 rounds of a count over the warp, took 83 us; several heads of a token in one warp,
+// with the next row's scores on their way, was slower.)
 #include "msa_device.cuh"
 #include "msa_launch.h"
 #include "msa_select.cuh"
@@ -27,7 +28,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kShort = 512;   // blocks of a row that the short form takes
-constexpr int kAbove = 64;    // keys above L that are compared with each other
+constexpr int kAbove = 64;    // scores above L that are compared with each other
 
 // Smallest of a float across the warp, NaN ignored.
 __device__ __forceinline__ float warp_min_f32(float x) {
