@@ -19,7 +19,7 @@
 // CTA an SM, each an equal share of all pages (msa_prefill.cuh); the next unit's query tile
 // is prepared while the current one is worked on.
 // Measured: four chunks of up to 1k tokens over 4k .. 16k, 64/4 heads, page scales 252 us,
-// 1950 TFLOP/s (the tensor core is active 95 % of the time); an fp8 query of 200 tokens, K-only
+// 1950 TFLOP/s (the tensor core is active in 87 % of the cycles); an fp8 query of 200 tokens, K-only
 // cache, 46 us (1590 TFLOP/s); eight prompts of 1k 113 us (scores are written at 0.9 TB/s, and
 // units of some five pages pay for their query tiles); three chunks of 40 tokens on one KV
 // head 13.6 us, of which 2 are products.  With the query tiles' split in line (118 KiB of code,
