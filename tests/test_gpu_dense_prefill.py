@@ -324,3 +324,22 @@ def test_workspace_of_the_call_on_another_stream():
     wide = torch.zeros(1, dtype=torch.uint8, device="cuda").expand(need)
     with pytest.raises(ValueError):
         msa.dense_prefill(*x.args(), x.v_scale, workspace=wide, **x.kw())
+
+
+def test_a_million_tokens():
+    """As many requests as a call takes, rows of q and out past 2^31 elements: every copy of
+    a batch of 4 gives what the batch gives."""
+    x = Batch([17, 40, 130, 1], [17, 40, 20, 1], 1, 20)
+    want, tol = every(x)
+    n = 16368
+    lens = list(x.q_lens) * n
+    q = x.q.repeat(n, 1, 1)
+    cus = cu(lens)
+    bt, sl = x.bt.repeat(n, 1), x.lens.repeat(n)
+    assert sl.numel() == 65472 and q.numel() > 1 << 31
+    out = msa.dense_prefill(q, x.kv, bt, sl, cus, x.sm, x.k_scale, x.v_scale)
+    for k in (0, 1, n // 2, n - 2, n - 1):
+        check(out[k * x.T:(k + 1) * x.T], want, tol)
+    s = msa.score_prefill(q, x.kv, bt, sl, cus, x.sm, x.k_scale)
+    assert torch.equal(s.view(1, n, x.T, x.S), s[:, -x.T:].view(1, 1, x.T, x.S).expand(1, n, x.T, x.S))
+    assert msa.get_error() == 0

@@ -259,3 +259,14 @@ def test_overlapped_calls_keep_their_order():
     finally:
         msa.set_input_overlap(was)
     assert msa.get_error() == 0
+
+
+def test_scores_past_four_billion_bytes():
+    """The widest table: scores and lists whose offsets pass 2^31 elements."""
+    wide, narrow = (Batch([300], [300], 16, 22, min_cols=m) for m in (1 << 19, 1))
+    s, want = score(wide), score(narrow)
+    assert s.numel() > 1 << 31 and torch.equal(s[:, :, :narrow.S], want)
+    assert bool(torch.isneginf(s[15, :, narrow.S:]).all()) and bool(torch.isneginf(s[0, 299, narrow.S:]).all())
+    lists = msa.topk_prefill(s, wide.lens, wide.cu)
+    assert torch.equal(lists, msa.topk_prefill(want, narrow.lens, narrow.cu))
+    assert msa.get_error() == 0
