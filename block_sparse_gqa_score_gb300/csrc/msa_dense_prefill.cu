@@ -52,11 +52,11 @@
 // warps share the issue slots), P handed on 300, O 500, of which the other half's products
 // hide most but not all.  S ahead of P would break the round, but two S and a P for each half
 // beside O do not fit 512 columns, and with S of 64 keys at a time, where they do, the products
-// take as long as those of 128 (856 us for the four chunks).  Slower were too: sixteen softmax warps with two threads a row
-// (registers spill), a product warp for each half, pieces of 32 columns, a check of the sum in
-// place of the maxima, P handed on in halves.  The warps' code has to stay small: seven
-// different loops share the SM's instruction cache, and with the query tiles' split and the
-// converter in line (191 KiB) short units took half as long again.
+// take as long as those of 128 (856 us for the four chunks).  Slower were too: sixteen softmax
+// warps with two threads a row (registers spill), a product warp for each half, pieces of 32
+// columns, a check of the sum in place of the maxima, P handed on in halves.  The warps' code
+// has to stay small: seven different loops share the SM's instruction cache, and with the query
+// tiles' split and the converter in line (191 KiB) short units took half as long again.
 #include <cstddef>
 
 #include "msa_device.cuh"
