@@ -24,10 +24,11 @@
 // the products of a thread execute in the order they are issued.
 //
 // P = 2^(u - M + kShift) is relative to a running reference M of the row, the largest u
-// rounded up when M is set; M stays until some P would pass 2^kTop (fp16 holds 2^16), so
-// that O is rescaled in a row's first pages and then hardly ever.  So a page needs no
-// exact maximum before its first exponential: S is read 64 columns at a time, and where a
-// piece moves M, what was made of the pieces before it is rescaled, by a power of two.
+// rounded up when M is set; M stays until 64 P sum to more than kMost (fp16 holds 65504), so
+// that O is rescaled in a row's first pages and then hardly ever, by a power of two, and what
+// was made of the page so far with it.  No maximum is taken on the way: S is read 64 columns at
+// a time, and only a unit's first piece and one whose sum says so are searched (and, the
+// latter, done again).  With the maximum of every piece the four chunks below took 697 us.
 // P is rounded to fp16: 2^-11 of itself down to 2^-21 of the row's largest, and at most
 // 2^-32 of that below.  Sums are of the unrounded P, in fp32, page by page.
 //
@@ -43,18 +44,18 @@
 // One CTA an SM, each an equal share of all pages (msa_prefill.cuh); what several CTAs
 // work on is merged by a second kernel from their parts, in the order of the pages.
 //
-// Measured, 64/4 heads: four chunks of up to 1k tokens over 4k .. 16k 694 us (1420 TFLOP/s),
-// with an fp8 query 651; one chunk of 1.4k tokens over 128k on one KV head with page scales
-// 752 us (1490 TFLOP/s); eight prompts of 1k 205 us; two chunks of 24 tokens over 2k .. 3k on
-// one KV head 22.6 us, a third of it the launches, the first tiles and the merge.
-// A page takes some 3000 cycles, of which the products alone need 2250 (2048 at the tensor
-// core's rate): the rest is the round of one half, S 900 cycles, softmax 1400 (the two halves'
+// Measured, 64/4 heads: four chunks of up to 1k tokens over 4k .. 16k 678 us (1455 TFLOP/s),
+// with an fp8 query 638; one chunk of 1.4k tokens over 128k on one KV head with page scales
+// 741 us (1515 TFLOP/s); eight prompts of 1k 212 us; two chunks of 24 tokens over 2k .. 3k on
+// one KV head 22.3 us, a third of it the launches, the first tiles and the merge.
+// A page takes some 2950 cycles, of which the products alone need 2250 (2048 at the tensor
+// core's rate): the rest is the round of one half, S 900 cycles, softmax 1300 (the two halves'
 // warps share the issue slots), P handed on 300, O 500, of which the other half's products
 // hide most but not all.  S ahead of P would break the round, but two S and a P for each half
 // beside O do not fit 512 columns, and with S of 64 keys at a time, where they do, the products
 // take as long as those of 128 (856 us for the four chunks).  Slower were too: sixteen softmax
 // warps with two threads a row (registers spill), a product warp for each half, pieces of 32
-// columns, a check of the sum in place of the maxima, P handed on in halves.  The warps' code
+// columns, P handed on in halves.  The warps' code
 // has to stay small: seven different loops share the SM's instruction cache, and with the query
 // tiles' split and the converter in line (191 KiB) short units took half as long again.
 #include <cstddef>
@@ -91,7 +92,7 @@ constexpr int kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;      // [half] of 128 columns each
 
 constexpr float kShift = 8.f;                   // P = 2^kShift at the largest u when M is set
-constexpr float kTop = 15.f;                    // M moves when some P would pass 2^kTop
+constexpr float kMost = 60000.f;                // M moves when 64 P sum to more
 constexpr float kTiny = 0x1p-108f;              // 2^-40 of it is not 0, and 2^40 leaves every logit 0
 
 struct PageInfo {
@@ -526,83 +527,95 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int lim = in.block < 0 ? -1 : pos - n * kPage;  // keys <= lim are visible
         const bool edge = __any_sync(0xffffffffu, lim < kPage - 1);
         const float zt = zs * in.k;
-        float nl = M == -INFINITY ? 0.f : in.lv - M + kShift;
-        float a0 = 0.f, a1 = 0.f, b0 = 0.f, b1 = 0.f;
+        // (no reference yet, of a row that has seen no key: every P comes out as infinity or NaN)
+        float nl = M == -INFINITY ? INFINITY : in.lv - M + kShift;
+        float lp = 0.f;           // the page's sum
 #pragma unroll 1
         for (int c = 0; c < kPage; c += 64) {
-          float s[64];
-          {
-            uint32_t v[2][32];
-            tc::ld_32x32b_x32(s_at + c, v[0]);
-            tc::ld_32x32b_x32(s_at + c + 32, v[1]);
-            tc::wait_ld();
+          uint32_t w[32];
+          float sum = INFINITY;
+#pragma unroll 1
+          for (bool known = n > sg.n0 || c > 0, last = false;; known = last = true) {
+            if (known) {
+              float a0 = 0.f, a1 = 0.f, b0 = 0.f, b1 = 0.f;
+              float s[64];
+              {
+                uint32_t v[2][32];
+                tc::ld_32x32b_x32(s_at + c, v[0]);
+                tc::ld_32x32b_x32(s_at + c + 32, v[1]);
+                tc::wait_ld();
 #pragma unroll
-            for (int e = 0; e < 64; ++e) s[e] = __uint_as_float(v[e >> 5][e & 31]);
-          }
-          if (edge) {
-            const int to = lim - c;
+                for (int e = 0; e < 64; ++e) s[e] = __uint_as_float(v[e >> 5][e & 31]);
+              }
+              if (edge) {
+                const int to = lim - c;
 #pragma unroll
-            for (int e = 0; e < 64; ++e) s[e] = e <= to ? s[e] : -INFINITY;
-          }
-          float top[4];
+                for (int e = 0; e < 64; ++e) s[e] = e <= to ? s[e] : -INFINITY;
+              }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            top[k] = fmaxf(s[16 * k], s[16 * k + 1]);
+              for (int e = 0; e < 64; e += 4) {
+                float x0, x1, x2, x3;
+                fma2(x0, x1, s[e], s[e + 1], zt, nl);
+                fma2(x2, x3, s[e + 2], s[e + 3], zt, nl);
+                x0 = ex2(x0), x1 = ex2(x1), x2 = ex2(x2), x3 = ex2(x3);
+                add2(a0, a1, x0, x1);
+                add2(b0, b1, x2, x3);
+                w[e / 2] = pack_f16x2(x0, x1);
+                w[e / 2 + 1] = pack_f16x2(x2, x3);
+              }
+              sum = (a0 + a1) + (b0 + b1);
+              if (last || __all_sync(0xffffffffu, sum <= kMost)) break;
+            }
+            // the first piece, or some P may have passed fp16: M moves to the row's largest
+            float top = -INFINITY;          // -inf: no visible key
+#pragma unroll 1
+            for (int k = c; k < c + 64; k += 32) {
+              uint32_t v[32];
+              tc::ld_32x32b_x32(s_at + k, v);
+              tc::wait_ld();
 #pragma unroll
-            for (int e = 2; e < 16; e += 2) top[k] = fmax3f(top[k], s[16 * k + e], s[16 * k + e + 1]);
-          }
-          // -inf: no visible key
-          const float u = fmaf(fmaxf(fmax3f(top[0], top[1], top[2]), top[3]), zt, in.lv);
-          const bool move = u - M > kTop - kShift;             // true while the row has no reference
-          if (__any_sync(0xffffffffu, move)) {
+              for (int e = 0; e < 32; ++e)
+                if (k + e <= lim) top = fmaxf(top, __uint_as_float(v[e]));
+            }
+            const float u = fmaf(top, zt, in.lv);
+            const bool move = u > M && !(sum <= kMost);
             const float to = move ? ceilf(u) : M;
             const float al = move ? ex2(M - to) : 1.f;         // a power of two; 0 at the first
             M = to;
             nl = M == -INFINITY ? 0.f : in.lv - M + kShift;
             l *= al;
-            a0 *= al, a1 *= al, b0 *= al, b1 *= al;
+            lp *= al;
             // this page's P so far
             tc::wait_st();
 #pragma unroll 1
             for (int k = 0; k < c / 2; k += 8) {
-              uint32_t w[8];
-              tc::ld_32x32b_x8(s_at + k, w);
+              uint32_t v[8];
+              tc::ld_32x32b_x8(s_at + k, v);
               tc::wait_ld();
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
-                w[e] = pack_f16x2(f.x * al, f.y * al);
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v[e]));
+                v[e] = pack_f16x2(f.x * al, f.y * al);
               }
-              tc::st_32x32b_x8(s_at + k, w);
+              tc::st_32x32b_x8(s_at + k, v);
             }
             if (n > sg.n0) {
               // the products so far are complete: S(n) was issued behind them
 #pragma unroll 1
               for (int k = 0; k < kHeadDim; k += 8) {
-                uint32_t w[8];
-                tc::ld_32x32b_x8(o_at + k, w);
+                uint32_t v[8];
+                tc::ld_32x32b_x8(o_at + k, v);
                 tc::wait_ld();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * al);
-                tc::st_32x32b_x8(o_at + k, w);
+                for (int e = 0; e < 8; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * al);
+                tc::st_32x32b_x8(o_at + k, v);
               }
             }
           }
-          uint32_t w[32];
-#pragma unroll
-          for (int e = 0; e < 64; e += 4) {
-            float x0, x1, x2, x3;
-            fma2(x0, x1, s[e], s[e + 1], zt, nl);
-            fma2(x2, x3, s[e + 2], s[e + 3], zt, nl);
-            x0 = ex2(x0), x1 = ex2(x1), x2 = ex2(x2), x3 = ex2(x3);
-            add2(a0, a1, x0, x1);
-            add2(b0, b1, x2, x3);
-            w[e / 2] = pack_f16x2(x0, x1);
-            w[e / 2 + 1] = pack_f16x2(x2, x3);
-          }
+          lp += sum;
           tc::st_32x32b_x32(s_at + c / 2, w);    // over columns that have been read
         }
-        l = fmaf((a0 + a1) + (b0 + b1), in.iv, l);
+        l = fmaf(lp, in.iv, l);
         tc::wait_st();
         tc::fence_before_thread_sync();
         __syncwarp();
