@@ -745,67 +745,67 @@ def append_kv_prefill(k, v, kv, block_table, seq_lens, cu_seqlens_q, k_scale: fl
                    q_scale, stream)
 
 
+_CACHE_DTYPES = _KV_DTYPES + (torch.float32,)
+
+
 def _caches(caches, num_blocks, dev):
-    """msa_cache_t of each tensor [num_blocks, ...]: rows of tokens in [.., 128, bytes]
-    of 8-bit types, else whole pages."""
-    out = (_native.Cache * max(1, len(caches)))()
+    """The bytes of an msa_cache_t for each tensor [num_blocks, ...]: rows of tokens in
+    [.., 128, bytes] of 8-bit types, else whole pages."""
+    out = []
     for i, c in enumerate(caches):
-        _need(c, f"caches[{i}]", _KV_DTYPES + (torch.float32,), dev)
+        if not (isinstance(c, torch.Tensor) and c.dtype in _CACHE_DTYPES and c.device == dev
+                and c.is_contiguous()):
+            _need(c, f"caches[{i}]", _CACHE_DTYPES, dev)
         shape = c.shape
         if len(shape) < 2 or shape[0] != num_blocks:
             raise ValueError(f"caches[{i}] must be [num_blocks, ...] of the pool's pages")
-        h = out[i]
-        h.base, h.units = c.data_ptr(), shape[1]
         if c.dtype is torch.float32:          # page scales [NB, Hkv, sides]
             if len(shape) != 3:
                 raise ValueError(f"caches[{i}]: page scales are [num_blocks, Hkv, sides]")
-            h.rows, h.row_bytes = 1, 4 * shape[2]
+            rows, row_bytes = 1, 4 * shape[2]
         else:
             if len(shape) != 4 or shape[2] != PAGE_SIZE:
                 raise ValueError(f"caches[{i}] must be [num_blocks, Hkv, 128, row bytes]")
-            h.rows, h.row_bytes = PAGE_SIZE, shape[3]
-    return out
+            rows, row_bytes = PAGE_SIZE, shape[3]
+        out.append(_native.pack_cache(c.data_ptr(), shape[1], rows, row_bytes))
+    return b"".join(out)
 
 
 def _int32(t, name: str, shape, dev):
-    """Checks int32 `t` of `shape` (None: any length of a vector) and returns its address
-    and end."""
+    """Checks int32 `t` of `shape` (None: any length of a vector) on `dev`, which is a CUDA
+    device, and returns its address."""
     try:
-        if (t.dtype is torch.int32 and t.is_cuda and t.is_contiguous() and t.device == dev
+        if (t.dtype is torch.int32 and t.device == dev and t.is_contiguous()
                 and (t.shape == shape or (shape is None and t.dim() == 1))):
-            at = t.data_ptr()
-            return at, at + 4 * t.numel()
+            return t.data_ptr()
     except AttributeError:
         pass
     _need(t, name, (torch.int32,), dev)
     raise ValueError(f"{name} must be " + ("a vector" if shape is None else str(list(shape))))
 
 
-def _outputs(given, inputs, dev):
-    """Tensors and addresses of the outputs [(tensor or None, name, shape)], which must
-    not overlap the inputs."""
+def _outputs(given, dev):
+    """Tensors and addresses of the outputs [(tensor or None, name, shape)]."""
     out, at = [], []
     for t, name, shape in given:
         if t is None:
             t = torch.empty(shape, dtype=torch.int32, device=dev)
-        lo, hi = _int32(t, name, shape, dev)
-        for i_lo, i_hi in inputs:
-            if lo < i_hi and i_lo < hi:
-                raise ValueError("outputs must not overlap the inputs")
+            at.append(t.data_ptr())
+        else:
+            at.append(_int32(t, name, shape, dev))
         out.append(t)
-        at.append(lo)
     return out, at
 
 
 def _table(block_table, seq_lens, refs):
     if not isinstance(block_table, torch.Tensor) or not isinstance(refs, torch.Tensor):
         raise TypeError("block_table and refs must be torch.Tensors")
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, S]")
+    if block_table.dim() != 2 or not block_table.is_cuda:
+        raise ValueError("block_table must be a CUDA tensor [B, S]")
     dev, (B, S) = block_table.device, block_table.shape
     return (dev, B, S, refs.shape[0] if refs.dim() else 0,
-            [_int32(block_table, "block_table", (B, S), dev), _int32(seq_lens, "seq_lens", (B,), dev),
-             _int32(refs, "refs", None, dev)])
+            _int32(block_table, "block_table", (B, S), dev), _int32(seq_lens, "seq_lens", (B,), dev),
+            _int32(refs, "refs", None, dev))
 
 
 def fork_pages(block_table, seq_lens, parents, refs, caches=(), grow=None, block_table_out=None,
@@ -817,18 +817,16 @@ def fork_pages(block_table, seq_lens, parents, refs, caches=(), grow=None, block
     of `caches` (kv [NB, Hkv, 128, 256], K-only caches, page scales, of any number of
     layers).  refs [NB]: how many rows hold each page; free pages (0) are taken in
     ascending order.  Returns (block_table, seq_lens, refs, copies [rows, 3])."""
-    dev, B, S, NB, ins = _table(block_table, seq_lens, refs)
-    ins.append(_int32(parents, "parents", None, dev))
+    dev, B, S, NB, table, lens, counts = _table(block_table, seq_lens, refs)
+    follows = _int32(parents, "parents", None, dev)
     rows = parents.shape[0]
-    if grow is not None:
-        ins.append(_int32(grow, "grow", (rows,), dev))
+    more = None if grow is None else _int32(grow, "grow", (rows,), dev)
     handles = _caches(caches, NB, dev)
     out, at = _outputs(((block_table_out, "block_table_out", (rows, S)),
                         (seq_lens_out, "seq_lens_out", (rows,)), (refs_out, "refs_out", (NB,)),
-                        (copies, "copies", (rows, 3))), ins, dev)
-    st = _lib().msa_fork_pages(
-        ins[0][0], ins[1][0], ins[3][0], None if grow is None else ins[4][0], ins[2][0], *at, B,
-        rows, S, NB, handles, len(caches), _stream(dev, stream))
+                        (copies, "copies", (rows, 3))), dev)
+    st = _lib().msa_fork_pages(table, lens, follows, more, counts, *at, B, rows, S, NB, handles,
+                               len(caches), _stream(dev, stream))
     _native.check(st, "msa_fork_pages")
     return tuple(out)
 
@@ -838,12 +836,12 @@ def compact_pages(block_table, seq_lens, refs, caches=(), block_table_out=None, 
     """Pages in use moved to the lowest indices (msa_compact_pages), in every tensor of
     `caches` as fork_pages() takes them.  Returns (block_table, refs, copies [NB // 2,
     3]): copies lists the moves (from, to, 128), then (-1, -1, 0)."""
-    dev, B, S, NB, ins = _table(block_table, seq_lens, refs)
+    dev, B, S, NB, table, lens, counts = _table(block_table, seq_lens, refs)
     handles = _caches(caches, NB, dev)
     out, at = _outputs(((block_table_out, "block_table_out", (B, S)), (refs_out, "refs_out", (NB,)),
-                        (copies, "copies", (NB // 2, 3))), ins, dev)
-    st = _lib().msa_compact_pages(ins[0][0], ins[1][0], ins[2][0], *at, B, S, NB, handles,
-                                  len(caches), _stream(dev, stream))
+                        (copies, "copies", (NB // 2, 3))), dev)
+    st = _lib().msa_compact_pages(table, lens, counts, *at, B, S, NB, handles, len(caches),
+                                  _stream(dev, stream))
     _native.check(st, "msa_compact_pages")
     return tuple(out)
 

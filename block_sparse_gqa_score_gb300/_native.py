@@ -5,6 +5,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 from . import build as _build
@@ -27,6 +28,9 @@ class Cache(ctypes.Structure):
     """msa_cache_t."""
     _fields_ = [("base", ctypes.c_void_p), ("units", ctypes.c_int), ("rows", ctypes.c_int),
                 ("row_bytes", ctypes.c_int)]
+
+
+pack_cache = struct.Struct("P3i4x").pack    # a Cache's bytes, in half the time of its fields
 
 
 #: Every symbol include/msa.h declares.
@@ -134,7 +138,7 @@ def load(path: str | None = None):
                                           i64, f32, f32, P]
         lib.msa_topk_prefill.argtypes = [P, i64, i64, i64, P, P, P, i32, i32, i32, i32, i32, P]
         # the cache's pages
-        caches = [ctypes.POINTER(Cache), i32]
+        caches = [P, i32]      # an array of Cache, or its bytes
         lib.msa_fork_pages.argtypes = [P] * 9 + [i32, i32, i32, i64] + caches + [P]
         lib.msa_compact_pages.argtypes = [P] * 6 + [i32, i32, i64] + caches + [P]
         lib.msa_copy_pages.argtypes = [P, i32, i64] + caches + [P]

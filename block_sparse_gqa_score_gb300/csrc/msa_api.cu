@@ -890,6 +890,20 @@ int prepare_prefill(const void* q, float q_scale, const void* kv, const float* k
   return MSA_OK;
 }
 
+// int32 arrays: whether some output shares memory with some input.
+struct Ints {
+  const int32_t* at;
+  int64_t n;
+};
+bool overlap(std::initializer_list<Ints> outs, std::initializer_list<Ints> ins) {
+  auto lo = [](const Ints& x) { return reinterpret_cast<uintptr_t>(x.at); };
+  auto hi = [&](const Ints& x) { return lo(x) + 4 * static_cast<uintptr_t>(x.n); };
+  for (const Ints& o : outs)
+    for (const Ints& i : ins)
+      if (o.at && i.at && lo(o) < hi(i) && lo(i) < hi(o)) return true;
+  return false;
+}
+
 // The copies of a fork or a compaction, or the caller's own, over all of its caches.
 int check_caches(const msa_cache_t* caches, int num_caches) {
   if (num_caches < 0 || (num_caches > 0 && !caches)) return MSA_EINVAL;
@@ -1031,6 +1045,10 @@ int msa_fork_pages(const int32_t* block_table, const int32_t* seq_lens, const in
                         static_cast<const void*>(seq_lens_out), static_cast<const void*>(refs_out),
                         static_cast<const void*>(copies)})
     if (!aligned(x, 4)) return MSA_EINVAL;
+  const int64_t in = static_cast<int64_t>(B) * S, out = static_cast<int64_t>(rows) * S;
+  if (overlap({{block_table_out, out}, {seq_lens_out, rows}, {refs_out, num_blocks}, {copies, 3 * int64_t{rows}}},
+              {{block_table, in}, {seq_lens, B}, {parents, rows}, {grow, rows}, {refs, num_blocks}}))
+    return MSA_EINVAL;
   DeviceState* dev;
   if ((st = device_state(&dev)) != MSA_OK) return st;
   const msa::ForkParams p{block_table,  seq_lens, parents, grow, refs, block_table_out,
@@ -1057,6 +1075,10 @@ int msa_compact_pages(const int32_t* block_table, const int32_t* seq_lens, const
                         static_cast<const void*>(refs), static_cast<const void*>(block_table_out),
                         static_cast<const void*>(refs_out), static_cast<const void*>(copies)})
     if (!aligned(x, 4)) return MSA_EINVAL;
+  const int64_t table = static_cast<int64_t>(B) * S;
+  if (overlap({{block_table_out, table}, {refs_out, num_blocks}, {copies, 3 * (num_blocks / 2)}},
+              {{block_table, table}, {seq_lens, B}, {refs, num_blocks}}))
+    return MSA_EINVAL;
   DeviceState* dev;
   if ((st = device_state(&dev)) != MSA_OK) return st;
   const msa::CompactParams p{block_table, seq_lens, refs, block_table_out, refs_out, copies,

@@ -730,8 +730,8 @@ int msa_copy_pages(const int32_t *copies, int n, int64_t num_blocks, const msa_c
  * With caches the copies are made by this call too.  The inputs are only read,
  * and outputs must not overlap them.
  * Errors: MSA_EINVAL for B or rows outside 0 .. 8192, S < 1, sizes past 2^31 - 1,
- * null or misaligned pointers (an input of no rows may be null), an output that is
- * the input, bad caches.  Device: MSA_ERR_NO_PAGES (more pages needed than free:
+ * null or misaligned pointers (an input of no rows may be null), an output that
+ * overlaps an input, bad caches.  Device: MSA_ERR_NO_PAGES (more pages needed than free:
  * nothing is forked; every new row is empty, its table -1, its length 0, refs_out
  * equals refs), MSA_ERR_ROW_RANGE (a parent outside -1 .. B - 1: the row is
  * empty), MSA_ERR_SEQ_RANGE (a parent's length outside 0 .. 128 S: taken as 0;
@@ -755,7 +755,8 @@ int msa_fork_pages(const int32_t *block_table, const int32_t *seq_lens, const in
  * page that moved away are left as they were).  The inputs are only read, and
  * outputs must not overlap them.
  * Errors: MSA_EINVAL for B < 0, S < 1, sizes past 2^31 - 1, null or misaligned
- * pointers (tables of no rows may be null), an output that is the input, bad caches.
+ * pointers (tables of no rows may be null), an output that overlaps an input, bad
+ * caches.
  * Device: MSA_ERR_SEQ_RANGE (a row's length outside 0 .. 128 S: taken as 0),
  * MSA_ERR_PAGE_RANGE, MSA_ERR_REFS (an entry outside the pool, or a page counted
  * as free: -1 in the new table).

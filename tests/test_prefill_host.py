@@ -155,6 +155,22 @@ def test_pages_reject(lib):
         assert compact(lib, NB=1, co=None) == _native.ECUDA
 
 
+@pytest.mark.parametrize("f,outs,ins", [
+    (fork, dict(bt2=5 * 8, sl2=5, refs2=100, co=15), dict(bt=4 * 8, sl=4, pa=5, gr=5, refs=100)),
+    (compact, dict(bt2=4 * 8, refs2=100, co=150), dict(bt=4 * 8, sl=4, refs=100))])
+def test_pages_reject_outputs_over_inputs(lib, f, outs, ins):
+    """An output that begins at an input's last word or ends at its first; and, next to
+    them, those that just do not."""
+    apart = {k: ctypes.c_void_p((2 + i) << 20) for i, k in enumerate((*ins, *outs))}
+    for o, n in outs.items():
+        for k, m in ins.items():
+            at = apart[k].value
+            for x, y in ((at + 4 * (m - 1), at + 4 * m), (at - 4 * (n - 1), at - 4 * n)):
+                assert f(lib, **dict(apart, **{o: ctypes.c_void_p(x)})) == EINVAL, (o, k)
+                if not torch.cuda.is_available():
+                    assert f(lib, **dict(apart, **{o: ctypes.c_void_p(y)})) == _native.ECUDA, (o, k)
+
+
 def test_python_rejects_host_tensors():
     q = torch.zeros((2, 16, 128), dtype=torch.bfloat16)
     kv = torch.zeros((3, 1, 128, 256), dtype=torch.uint8)
