@@ -14,10 +14,11 @@
 // random ones).  If fewer than 15 are, they are kept with the first scores equal to L; else
 // the 15 are chosen among them alone, each compared with all of them in shared memory.  A row
 // with more than 64 scores above L (they would have to lie in few lanes) is left to the search
-// of msa_select.cuh, as are rows of more than 2048 blocks.
+// of msa_select.cuh.  Rows of up to 2048 blocks are held in registers, longer ones read again.
 // 5980 tokens of 4 heads over up to 512 blocks: 18 us, 1.4 TB/s of scores.  (A search bit by
 // bit, 31 rounds of a count over the warp, took 83 us; several heads of a token in one warp,
-// with the next row's scores on their way, was slower.)
+// with the next row's scores on their way, was slower.)  A decode step's 256 rows of 2048
+// blocks 7.5 us (bit by bit 31), 32 rows of 4096 13.5 (98).
 #include "msa_device.cuh"
 #include "msa_launch.h"
 #include "msa_select.cuh"
@@ -40,7 +41,8 @@ __device__ __forceinline__ float warp_min_f32(float x) {
 // The kept blocks of a row of 16 .. 32 NK candidates, as select::select_row returns them;
 // false where it has to do it.  Scores are compared as they are (-0 equals 0); a NaN score
 // counts as -inf, and a NaN of this function's own stands for no block at all: no
-// comparison holds with it.  scratch: shared words of this warp, at most 1024.
+// comparison holds with it.  NK 0: rows of any length, read again in place of being held.
+// scratch: shared words of this warp, at most 1024.
 template <int NK>
 __device__ __forceinline__ bool select_by_maxima(const float* __restrict__ srow, int64_t stride_n,
                                                  int cur, int lane, uint32_t* scratch, int* slots,
@@ -48,22 +50,46 @@ __device__ __forceinline__ bool select_by_maxima(const float* __restrict__ srow,
   constexpr unsigned kAll = 0xffffffffu;
   constexpr int kSel = select::kSel;
   const float none = __uint_as_float(0x7FFFFFFFu);
-  constexpr int kRoom = NK <= 16 ? 32 * NK : kAbove;   // scores above L that are kept
+  constexpr int kRoom = NK > 0 && NK <= 16 ? 32 * NK : kAbove;   // scores above L that are kept
+  constexpr int kUnroll = NK > 0 ? NK : 8;
+  const int groups = NK > 0 ? NK : (cur + 31) / 32;
   float* above = reinterpret_cast<float*>(scratch);
   uint32_t* block = scratch + kRoom;
-  float f[NK];
-  const float* at = srow + lane * stride_n;
-  const int64_t step = 32 * stride_n;
-#pragma unroll
-  for (int e = 0; e < NK; ++e, at += step) f[e] = 32 * e < cur - lane ? __ldg(at) : none;
+  float f[kUnroll];
+  // the score of block lane + 32 e
+  auto load = [&](int e) {
+    return 32 * e < cur - lane ? __ldg(srow + (lane + 32 * static_cast<int64_t>(e)) * stride_n) : none;
+  };
   float m = none;
+  if constexpr (NK > 0) {
+    const float* at = srow + lane * stride_n;
+    const int64_t step = 32 * stride_n;
 #pragma unroll
-  for (int e = 0; e < NK; ++e) {
-    const bool bad = f[e] != f[e] && 32 * e < cur - lane;
-    nan |= bad;
-    f[e] = bad ? -INFINITY : f[e];
-    m = fmaxf(m, f[e]);
+    for (int e = 0; e < NK; ++e, at += step) f[e] = 32 * e < cur - lane ? __ldg(at) : none;
+#pragma unroll
+    for (int e = 0; e < NK; ++e) {
+      const bool bad = f[e] != f[e] && 32 * e < cur - lane;
+      nan |= bad;
+      f[e] = bad ? -INFINITY : f[e];
+      m = fmaxf(m, f[e]);
+    }
+  } else {
+    for (int e0 = 0; e0 < groups; e0 += kUnroll) {
+#pragma unroll
+      for (int e = 0; e < kUnroll; ++e) f[e] = load(e0 + e);
+#pragma unroll
+      for (int e = 0; e < kUnroll; ++e) {
+        const bool bad = f[e] != f[e] && 32 * (e0 + e) < cur - lane;
+        nan |= bad;
+        m = fmaxf(m, bad ? -INFINITY : f[e]);
+      }
+    }
   }
+  auto value = [&](int e) {
+    if constexpr (NK > 0) return f[e];
+    const float x = load(e);
+    return x != x && 32 * e < cur - lane ? -INFINITY : x;
+  };
   // L: the smallest of the lanes' maxima that fewer than 15 are larger than
   above[lane] = m;
   __syncwarp();
@@ -78,13 +104,14 @@ __device__ __forceinline__ bool select_by_maxima(const float* __restrict__ srow,
   // the scores above L and their blocks, in ascending order of the blocks
   const unsigned lt = (1u << lane) - 1u;
   int n = 0;
-#pragma unroll
-  for (int e = 0; e < NK; ++e) {
-    const bool over = f[e] > low;
+#pragma unroll kUnroll
+  for (int e = 0; e < groups; ++e) {
+    const float x = value(e);
+    const bool over = x > low;
     const unsigned b = __ballot_sync(kAll, over);
     const int k = n + __popc(b & lt);
     if (over && (kRoom == 32 * NK || k < kRoom)) {
-      above[k] = f[e];
+      above[k] = x;
       block[k] = lane + 32 * e;
     }
     n += __popc(b);
@@ -120,11 +147,12 @@ __device__ __forceinline__ bool select_by_maxima(const float* __restrict__ srow,
     // all scores above L, and of those equal to it the first
     const int need = kSel - n;
     int written = 0, ties = 0;
-#pragma unroll
-    for (int e = 0; e < NK; ++e) {
-      const bool eq = f[e] == low;
+#pragma unroll kUnroll
+    for (int e = 0; e < groups; ++e) {
+      const float x = value(e);
+      const bool eq = x == low;
       const unsigned be = __ballot_sync(kAll, eq);
-      const bool take = f[e] > low || (eq && ties + __popc(be & lt) < need);
+      const bool take = x > low || (eq && ties + __popc(be & lt) < need);
       const unsigned bs = __ballot_sync(kAll, take);
       if (take) slots[written + __popc(bs & lt)] = lane + 32 * e;
       ties += __popc(be);
@@ -185,6 +213,8 @@ __global__ void __launch_bounds__(kWarps * 32) topk_kernel(const TopkParams p) {
     done = select_by_maxima<32>(srow, p.stride_n, cur, lane, s_keys[warp], s_slots[warp], nan, v);
   else if (kLong && cur > 32 * 32 && cur <= 32 * 64)
     done = select_by_maxima<64>(srow, p.stride_n, cur, lane, s_keys[warp], s_slots[warp], nan, v);
+  else if (kLong && cur > 32 * 64)
+    done = select_by_maxima<0>(srow, p.stride_n, cur, lane, s_keys[warp], s_slots[warp], nan, v);
   if (!done)
     v = select::select_row<kLong ? 64 : 16>(srow, p.stride_n, pos, lane, s_keys[warp], kCache,
                                             s_slots[warp], nan);

@@ -270,3 +270,30 @@ def test_scores_past_four_billion_bytes():
     lists = msa.topk_prefill(s, wide.lens, wide.cu)
     assert torch.equal(lists, msa.topk_prefill(want, narrow.lens, narrow.cu))
     assert msa.get_error() == 0
+
+
+@pytest.mark.parametrize("n,S", [(2048, 2049), (2049, 2060), (2079, 2080), (5000, 5003), (70001, 70010)])
+@pytest.mark.parametrize("lanes", [0, 1, 15, 31])
+def test_long_rows(n, S, lanes):
+    """Rows of more blocks than a warp holds, beside shorter ones: drawn, with ties, alike, in
+    few columns, with NaN and with -inf."""
+    gen = torch.Generator().manual_seed(n + lanes)
+    x = torch.randn((2, 14, S), generator=gen)
+    if lanes:
+        x[:, ::2] = torch.where(torch.arange(S) % 32 < lanes, x[:, ::2] + 100, x[:, ::2])
+    x[0, 3] = 1.0
+    x[:, 4:6] = (x[:, 4:6] * 2).round()
+    x[:, 6, 20:] = -math.inf
+    x[1, 7] = -math.inf
+    x[:, 8, ::3] = float("nan")
+    lens = torch.tensor([n * PAGE + 60, 3000], dtype=torch.int32, device="cuda")
+    at = cu([12, 2])
+    got = msa.topk_prefill(x.cuda(), lens, at)
+    assert torch.equal(got.cpu(), select(x, lens.tolist(), [12, 2]))
+    assert msa.get_error() == _native.ERR_SCORE_NAN
+    clean = x[:, :12].nan_to_num(nan=-math.inf, neginf=-math.inf).cuda()
+    assert torch.equal(msa.topk(clean, lens[:1], 12), got[:12])
+    wide = torch.empty((2, 12, S, 2), device="cuda")
+    wide[..., 1] = clean
+    assert torch.equal(msa.topk(wide[..., 1], lens[:1], 12), got[:12])
+    assert msa.get_error() == 0
