@@ -31,6 +31,16 @@ __device__ __forceinline__ unsigned cluster_rank() {
   return r;
 }
 
+// The cluster's CTAs have all started, behind the wait: only then may another CTA's shared
+// memory be touched.  (Arrived at first thing and waited for just ahead of the first store
+// over there, so that it runs beside the reads of the counts.)
+__device__ __forceinline__ void cluster_started_arrive() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_started_wait() {
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+
 // All of the cluster's threads: what any of them wrote, to shared or global memory, is
 // seen by all behind it.
 __device__ __forceinline__ void cluster_sync() {
@@ -135,6 +145,7 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster)
   ForkRow* facts = reinterpret_cast<ForkRow*>(before + p.rows + 1);   // [rows]
   const int tid = threadIdx.x, lane = tid & 31;
   const unsigned cta = cluster_rank();
+  cluster_started_arrive();
   pdl_trigger();
   pdl_wait();
 
@@ -161,6 +172,7 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster)
   for (int b = r0; b < r1; ++b) facts[b] = load_fork_row(p, b, bad);
   int cta_free;
   const int at = block_scan(mine, sh.scan_a, cta_free);
+  cluster_started_wait();
   if (tid < kCluster) store_remote(&sh.total[cta], tid, cta_free);
   for (int b = r0; b < r1; ++b) {
     const int q = facts[b].parent;
@@ -275,6 +287,7 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster)
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31;
   const unsigned cta = cluster_rank();
+  cluster_started_arrive();
   pdl_trigger();
   pdl_wait();
   const int threads = kCluster * kThreads;
@@ -286,6 +299,7 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster)
   for (int i = lo; i < hi; ++i) mine += p.refs[i] != 0;
   int cta_live;
   const int at = block_scan(mine, sh.scan_a, cta_live);
+  cluster_started_wait();
   if (tid < kCluster) store_remote(&sh.total[cta], tid, cta_live);
   if (tid == 0) sh.below = 0;
   cluster_sync();
