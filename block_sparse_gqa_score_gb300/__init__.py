@@ -813,9 +813,9 @@ def fork_pages(block_table, seq_lens, parents, refs, caches=(), grow=None, block
     """The next step's rows of a block table (msa_fork_pages): new row b continues row
     parents[b] of block_table [B, S], seq_lens [B] (-1: a new, empty row) and has room
     for grow[b] more tokens; rows without a child are freed.  Full pages are shared, a
-    begun page goes to the first child and is copied for the others, in every tensor
-    of `caches` (kv [NB, Hkv, 128, 256], K-only caches, page scales, of any number of
-    layers).  refs [NB]: how many rows hold each page; free pages (0) are taken in
+    begun page goes to the first child (where nobody else holds it) and is copied for
+    the others, in every tensor of `caches` (kv [NB, Hkv, 128, 256], K-only caches, page
+    scales, of any number of layers).  refs [NB]: how many rows hold each page; free pages (0) are taken in
     ascending order.  Returns (block_table, seq_lens, refs, copies [rows, 3])."""
     dev, B, S, NB, table, lens, counts = _table(block_table, seq_lens, refs)
     follows = _int32(parents, "parents", None, dev)

@@ -110,7 +110,8 @@ struct ForkRow {
   int parent;     // -1: none
   int n, grow;
   __device__ __forceinline__ bool copied(const int* first, int b) const {
-    // the parent's begun page goes to another row: entry held() is a copy
+    // the parent's begun page goes to another row or stays with other holders: entry held()
+    // is a copy
     return n % kPage != 0 && first[parent] != b;
   }
   // entries taken over from the parent (all but a page to be copied), and entries of the row
@@ -139,7 +140,8 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster)
     fork_kernel(const ForkParams p) {
   extern __shared__ int dyn[];
   __shared__ Shared sh;
-  int* first = dyn;                 // [B] the lowest row that follows this one
+  int* first = dyn;                 // [B] the lowest row that follows this one; -1: its begun
+                                    // page has other holders, and is taken over by nobody
   int* children = first + p.B;      // [B] how many do
   int* before = children + p.B;     // [rows + 1] pages that the rows before need
   ForkRow* facts = reinterpret_cast<ForkRow*>(before + p.rows + 1);   // [rows]
@@ -161,8 +163,16 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster)
     p.refs_out[i] = r;
     mine += r == 0;
   }
-  for (int b = tid; b < p.B; b += kThreads) {
-    first[b] = INT_MAX;
+  // (the last threads' first: with few rows they are not the threads that load the new rows)
+  for (int b = kThreads - 1 - tid; b < p.B; b += kThreads) {
+    bool seq = false;
+    const int n = row_tokens(p.lens, b, p.S, seq);
+    bool others = false;
+    if (n % kPage != 0) {
+      const int page = p.table[static_cast<int64_t>(b) * p.S + n / kPage];
+      others = page >= 0 && page < p.num_blocks && p.refs[page] > 1;
+    }
+    first[b] = others ? -1 : INT_MAX;
     children[b] = 0;
   }
   // `each` neighbouring rows a thread
@@ -264,7 +274,8 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster)
     const int32_t* from = p.table + static_cast<int64_t>(b) * p.S;
     const int all = pages_of(n), full = n / kPage;
     for (int e = lane; e < all; e += 32) {
-      const int more = e < full ? c - 1 : min(c, 1) - 1;   // the begun page goes to one child
+      // the begun page goes to one child, or to none
+      const int more = e < full ? c - 1 : (first[b] < 0 ? 0 : min(c, 1)) - 1;
       if (more == 0) continue;
       const int page = from[e];
       if (page < 0 || page >= p.num_blocks) {

@@ -720,8 +720,11 @@ int msa_copy_pages(const int32_t *copies, int n, int64_t num_blocks, const msa_c
  * New row b has seq_lens_out[b] = seq_lens[parents[b]] + grow[b] tokens (the
  * convention of msa_append_kv: the new tokens are counted) and the pages for them.
  * Full pages are shared by all children.  A parent's last, not full page goes to
- * its first child (the lowest b); every other child gets a page of its own and a
- * copy of the rows that are filled.  The pages needed, in the order of the new
+ * its first child (the lowest b), unless it has another holder (refs above 1: another
+ * row, a prefix cache), who goes on reading it; every other child, and that one then,
+ * gets a page of its own and a copy of the rows that are filled.  So a new row's begun
+ * page is its own, and what it appends reaches nobody else.  (A kept prefix is taken
+ * over by a parent: give it a row of block_table.)  The pages needed, in the order of the new
  * rows and of their entries, are the free ones (refs 0) in ascending order; pages
  * that this call frees are free from the next call on.
  *   block_table_out [rows, S]   -1 behind a row's last page
