@@ -68,6 +68,25 @@ def _stream(device: torch.device, stream) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
+def _own(shape, dtype, device, stream):
+    """A buffer that only a call's kernels use, memory of their stream (None: the current
+    one): nothing that is still queued on another stream can write to it, and it goes to
+    others of that stream alone."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _empty(shape, dtype, device, stream):
+    """An output of a call on `stream`: memory of that stream, which is not given away either
+    before what the current stream does with it until it is freed."""
+    t = _own(shape, dtype, device, stream)
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _need(t: torch.Tensor, name: str, dtypes, device=None):
     try:   # what every call passes; the checks below name what is wrong
         if (t.is_cuda and t.dtype in dtypes and t.is_contiguous()
@@ -146,7 +165,7 @@ def _page_scales(kv_scales, name: str, dev, num_blocks: int, num_kv_heads: int, 
 
 
 def _parts(num_splits: int, kv_scales, batch: int, qlen: int, num_q_heads: int, num_kv_heads: int,
-           workspace, dev):
+           workspace, dev, stream):
     """(split count, workspace, its address and bytes) of an attend on lists: with
     page scales the library cuts a row by itself and needs no workspace."""
     if num_splits <= 0 and kv_scales is not None:
@@ -154,7 +173,7 @@ def _parts(num_splits: int, kv_scales, batch: int, qlen: int, num_q_heads: int, 
     splits = num_splits if num_splits > 0 else choose_splits(batch, qlen, num_kv_heads)
     need = workspace_bytes(batch, qlen, num_q_heads, splits)
     if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _own(need, torch.uint8, dev, stream)
     if workspace is None:
         return splits, None, None, 0
     return splits, workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -169,7 +188,7 @@ def score(q, kv, block_table, seq_lens, qlen: int, sm_scale: float, k_scale: flo
     kv_scales: page scales [NB, Hkv, 2] ([NB, Hkv, 1] of a K-only cache)."""
     dev, B, S, Hq, Hkv, NB = _geometry(q, kv, block_table, seq_lens, qlen, k_only_ok=True)
     if scores is None:
-        scores = torch.empty((Hkv, B * qlen, S), dtype=torch.float32, device=dev)
+        scores = _empty((Hkv, B * qlen, S), torch.float32, dev, stream)
     _need(scores, "scores", (torch.float32,), dev)
     if tuple(scores.shape) != (Hkv, B * qlen, S):
         raise ValueError("scores must be [Hkv, T, S]")
@@ -203,7 +222,7 @@ def topk(scores: torch.Tensor, seq_lens: torch.Tensor, qlen: int, k: int = TOPK,
     if T != B * qlen:
         raise ValueError("scores' token dim must be B*qlen")
     if out is None:
-        out = torch.empty((T, Hkv, k), dtype=torch.int32, device=dev)
+        out = _empty((T, Hkv, k), torch.int32, dev, stream)
     _need(out, "out", (torch.int32,), dev)
     sh, stt, sn = scores.stride()
     st = _lib().msa_topk(scores.data_ptr(), sh, stt, sn, seq_lens.data_ptr(), out.data_ptr(), B,
@@ -225,10 +244,10 @@ def sparse_decode(q, kv, block_table, seq_lens, topk_idx, qlen: int, sm_scale: f
     if tuple(topk_idx.shape) != (B * qlen, Hkv, TOPK):
         raise ValueError("topk must be [T, Hkv, 16]")
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        out = _empty(q.shape, torch.bfloat16, dev, stream)
     _need(out, "out", (torch.bfloat16,), dev)
     splits, workspace, ws_ptr, ws_bytes = _parts(num_splits, kv_scales, B, qlen, Hq, Hkv,
-                                                 workspace, dev)
+                                                 workspace, dev, stream)
     args = (kv.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), topk_idx.data_ptr(), ws_ptr,
             ws_bytes, out.data_ptr(), B, qlen, Hq, Hkv, S, NB, float(sm_scale), float(k_scale),
             float(v_scale), splits, _stream(dev, stream))
@@ -259,14 +278,14 @@ def dense_decode(q, kv, block_table, seq_lens, qlen: int, sm_scale: float, k_sca
     page scales [NB, Hkv, 2]."""
     dev, B, S, Hq, Hkv, NB = _geometry(q, kv, block_table, seq_lens, qlen)
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        out = _empty(q.shape, torch.bfloat16, dev, stream)
     _need(out, "out", (torch.bfloat16,), dev)
     splits = dense_splits(S)
     if splits == 0:
         raise ValueError("dense_decode takes block tables of at most 2048 columns")
     need = workspace_bytes(B, qlen, Hq, splits)
     if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _own(need, torch.uint8, dev, stream)
     ws_ptr = workspace.data_ptr() if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     args = (kv.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), ws_ptr, ws_bytes,
@@ -315,13 +334,13 @@ def sparse_decode_select(q, kv, block_table, seq_lens, scores, qlen: int, sm_sca
             or scores.shape[2] < S:
         raise ValueError("scores must be [Hkv, T, >= S]")
     if topk_out is None:
-        topk_out = torch.empty((B * qlen, Hkv, TOPK), dtype=torch.int32, device=dev)
+        topk_out = _empty((B * qlen, Hkv, TOPK), torch.int32, dev, stream)
     _need(topk_out, "topk_out", (torch.int32,), dev)
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        out = _empty(q.shape, torch.bfloat16, dev, stream)
     _need(out, "out", (torch.bfloat16,), dev)
     splits, workspace, ws_ptr, ws_bytes = _parts(num_splits, kv_scales, B, qlen, Hq, Hkv,
-                                                 workspace, dev)
+                                                 workspace, dev, stream)
     sh, st, sn = scores.stride()
     args = (kv.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), scores.data_ptr(), sh, st,
             sn, topk_out.data_ptr(), ws_ptr, ws_bytes, out.data_ptr(), B, qlen, Hq, Hkv, S, NB,
@@ -368,11 +387,11 @@ def sparse_prefill(q, kv, block_table, seq_lens, cu_seqlens_q, topk_idx, sm_scal
     if tuple(topk_idx.shape) != (T, Hkv, TOPK):
         raise ValueError("topk must be [T, Hkv, 16]")
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        out = _empty(q.shape, torch.bfloat16, dev, stream)
     _need(out, "out", (torch.bfloat16,), dev)
     # one CTA per token: the single-token rule, choose_splits(T, 1, ...)
     splits, workspace, ws_ptr, ws_bytes = _parts(num_splits, kv_scales, max(T, 1), 1, Hq, Hkv,
-                                                 workspace, dev)
+                                                 workspace, dev, stream)
     args = (kv.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), cu_seqlens_q.data_ptr(),
             topk_idx.data_ptr(), ws_ptr, ws_bytes, out.data_ptr(), B, T, Hq, Hkv, S, NB,
             float(sm_scale), float(k_scale), float(v_scale), splits, _stream(dev, stream))
@@ -406,14 +425,14 @@ def sparse_prefill_select(q, kv, block_table, seq_lens, cu_seqlens_q, scores, sm
             or scores.shape[2] < S:
         raise ValueError("scores must be [Hkv, T, >= S]")
     if topk_out is None:
-        topk_out = torch.empty((T, Hkv, TOPK), dtype=torch.int32, device=dev)
+        topk_out = _empty((T, Hkv, TOPK), torch.int32, dev, stream)
     _need(topk_out, "topk_out", (torch.int32,), dev)
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        out = _empty(q.shape, torch.bfloat16, dev, stream)
     _need(out, "out", (torch.bfloat16,), dev)
     # one CTA per token: the single-token rule, choose_splits(T, 1, ...)
     splits, workspace, ws_ptr, ws_bytes = _parts(num_splits, kv_scales, max(T, 1), 1, Hq, Hkv,
-                                                 workspace, dev)
+                                                 workspace, dev, stream)
     sh, st, sn = scores.stride()
     args = (kv.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), cu_seqlens_q.data_ptr(),
             scores.data_ptr(), sh, st, sn, topk_out.data_ptr(), ws_ptr, ws_bytes, out.data_ptr(),
@@ -441,7 +460,7 @@ def score_prefill(q, kv, block_table, seq_lens, cu_seqlens_q, sm_scale: float,
     dev, B, S, Hq, Hkv, NB = _geometry(q, kv, block_table, seq_lens, None, k_only_ok=True)
     T = _cu_seqlens(cu_seqlens_q, B, dev, q)
     if scores is None:
-        scores = torch.empty((Hkv, T, S), dtype=torch.float32, device=dev)
+        scores = _empty((Hkv, T, S), torch.float32, dev, stream)
     _need(scores, "scores", (torch.float32,), dev)
     if scores.shape != (Hkv, T, S):
         raise ValueError("scores must be [Hkv, T, S]")
@@ -474,7 +493,7 @@ def topk_prefill(scores: torch.Tensor, seq_lens: torch.Tensor, cu_seqlens_q: tor
     B = seq_lens.shape[0]
     _cu_seqlens(cu_seqlens_q, B, dev)
     if out is None:
-        out = torch.empty((T, Hkv, k), dtype=torch.int32, device=dev)
+        out = _empty((T, Hkv, k), torch.int32, dev, stream)
     _need(out, "out", (torch.int32,), dev)
     if out.shape != (T, Hkv, k):
         raise ValueError("out must be [T, Hkv, 16]")
@@ -511,7 +530,7 @@ def dense_prefill(q, kv, block_table, seq_lens, cu_seqlens_q, sm_scale: float,
     kv_scales: page scales [NB, Hkv, 2]."""
     dev, B, T, S, Hq, Hkv, NB = _prefill_geometry(q, kv, block_table, seq_lens, cu_seqlens_q)
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        out = _empty(q.shape, torch.bfloat16, dev, stream)
     _need(out, "out", (torch.bfloat16,), dev)
     if out.shape != q.shape:
         raise ValueError("out must be [T, Hq, 128]")
@@ -520,9 +539,7 @@ def dense_prefill(q, kv, block_table, seq_lens, cu_seqlens_q, sm_scale: float,
         return out
     need = dense_prefill_workspace_bytes(dev)
     if workspace is None or workspace.numel() * workspace.element_size() < need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        if stream is not None:      # not given to another tensor before that stream is through
-            workspace.record_stream(stream)
+        workspace = _own(need, torch.uint8, dev, stream)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {dev}")
     st = _lib().msa_dense_prefill(
@@ -541,7 +558,7 @@ def combine(workspace: torch.Tensor, tokens: int, num_q_heads: int, num_splits: 
         raise TypeError("workspace must be a CUDA tensor")
     dev = workspace.device
     if out is None:
-        out = torch.empty((tokens, num_q_heads, HEAD_DIM), dtype=torch.bfloat16, device=dev)
+        out = _empty((tokens, num_q_heads, HEAD_DIM), torch.bfloat16, dev, stream)
     _need(out, "out", (torch.bfloat16,), dev)
     st = _lib().msa_combine(workspace.data_ptr(), out.data_ptr(), tokens, num_q_heads, num_splits,
                             _stream(dev, stream))
@@ -563,15 +580,15 @@ class DecodeBuffers:
 
     @staticmethod
     def allocate(batch: int, qlen: int, num_q_heads: int, num_kv_heads: int, stride: int,
-                 device, num_splits: int = 0) -> "DecodeBuffers":
+                 device, num_splits: int = 0, stream=None) -> "DecodeBuffers":
         T = batch * qlen
         splits = num_splits if num_splits > 0 else choose_splits(batch, qlen, num_kv_heads)
         need = workspace_bytes(batch, qlen, num_q_heads, splits)
-        ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+        ws = _own(need, torch.uint8, device, stream) if need else None
         return DecodeBuffers(
-            scores=torch.empty((num_kv_heads, T, stride), dtype=torch.float32, device=device),
-            topk=torch.empty((T, num_kv_heads, TOPK), dtype=torch.int32, device=device),
-            out=torch.empty((T, num_q_heads, HEAD_DIM), dtype=torch.bfloat16, device=device),
+            scores=_empty((num_kv_heads, T, stride), torch.float32, device, stream),
+            topk=_empty((T, num_kv_heads, TOPK), torch.int32, device, stream),
+            out=_empty((T, num_q_heads, HEAD_DIM), torch.bfloat16, device, stream),
             workspace=ws, num_splits=splits, chosen=num_splits > 0)
 
 
@@ -591,7 +608,7 @@ def decode_step(q, kv, block_table, seq_lens, qlen: int, sm_scale: float, k_scal
     Returns (scores, topk, out)."""
     dev, B, S, Hq, Hkv, NB = _geometry(q, kv, block_table, seq_lens, qlen)
     if buffers is None:
-        buffers = DecodeBuffers.allocate(B, qlen, Hq, Hkv, S, dev)
+        buffers = DecodeBuffers.allocate(B, qlen, Hq, Hkv, S, dev, stream=stream)
     if index_k is not None:
         _need(index_k, "index_k", _KV_DTYPES, dev)
         if (index_k.dim() != 4 or index_k.shape[1] != Hkv or index_k.shape[2] != PAGE_SIZE
@@ -676,7 +693,7 @@ def _append(fn, k, v, kv, block_table, seq_lens, tokens, cu, qlen, k_scale, v_sc
     if q is not None:
         qs, qp = _rows(q, "q", Hq, tokens, dev), q.data_ptr()
         if q_out is None:
-            q_out = torch.empty((tokens, Hq, HEAD_DIM), dtype=torch.bfloat16, device=dev)
+            q_out = _empty((tokens, Hq, HEAD_DIM), torch.bfloat16, dev, stream)
         _need(q_out, "q_out", (torch.bfloat16,) + ((_FP8_Q,) if _FP8_Q is not None else ()), dev)
         if q_out.shape != (tokens, Hq, HEAD_DIM):
             raise ValueError("q_out must be [T, Hq, 128]")
@@ -784,12 +801,12 @@ def _int32(t, name: str, shape, dev):
     raise ValueError(f"{name} must be " + ("a vector" if shape is None else str(list(shape))))
 
 
-def _outputs(given, dev):
+def _outputs(given, dev, stream):
     """Tensors and addresses of the outputs [(tensor or None, name, shape)]."""
     out, at = [], []
     for t, name, shape in given:
         if t is None:
-            t = torch.empty(shape, dtype=torch.int32, device=dev)
+            t = _empty(shape, torch.int32, dev, stream)
             at.append(t.data_ptr())
         else:
             at.append(_int32(t, name, shape, dev))
@@ -824,7 +841,7 @@ def fork_pages(block_table, seq_lens, parents, refs, caches=(), grow=None, block
     handles = _caches(caches, NB, dev)
     out, at = _outputs(((block_table_out, "block_table_out", (rows, S)),
                         (seq_lens_out, "seq_lens_out", (rows,)), (refs_out, "refs_out", (NB,)),
-                        (copies, "copies", (rows, 3))), dev)
+                        (copies, "copies", (rows, 3))), dev, stream)
     st = _lib().msa_fork_pages(table, lens, follows, more, counts, *at, B, rows, S, NB, handles,
                                len(caches), _stream(dev, stream))
     _native.check(st, "msa_fork_pages")
@@ -839,7 +856,7 @@ def compact_pages(block_table, seq_lens, refs, caches=(), block_table_out=None, 
     dev, B, S, NB, table, lens, counts = _table(block_table, seq_lens, refs)
     handles = _caches(caches, NB, dev)
     out, at = _outputs(((block_table_out, "block_table_out", (B, S)), (refs_out, "refs_out", (NB,)),
-                        (copies, "copies", (NB // 2, 3))), dev)
+                        (copies, "copies", (NB // 2, 3))), dev, stream)
     st = _lib().msa_compact_pages(table, lens, counts, *at, B, S, NB, handles, len(caches),
                                   _stream(dev, stream))
     _native.check(st, "msa_compact_pages")
