@@ -116,8 +116,8 @@ __device__ __forceinline__ bool select_by_maxima(const float* __restrict__ srow,
     }
     n += __popc(b);
   }
+  __syncwarp();     // (ahead of the return too: who searches the row writes the same words)
   if (n > kAbove) return false;
-  __syncwarp();
   if (n >= kSel) {
     // tau: the smallest of them that fewer than 15 are larger than; all larger ones are kept, and
     // of its equals as many of the first as there is room for

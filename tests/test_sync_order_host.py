@@ -38,3 +38,13 @@ def test_remote_stores_wait_for_the_cluster(kernel):
     assert body.count("cluster_started_arrive()") == body.count("cluster_started_wait()") == 1
     # nobody leaves while others may still store to it
     assert body.rindex("cluster_sync()") > body.rindex("store_remote(")
+
+
+def test_scratch_of_a_given_up_row_is_ordered():
+    """select_by_maxima leaves a row to select_row, which writes the same shared words from
+    other lanes: what it wrote itself is ordered before."""
+    body = function(source("msa_topk.cu"), "select_by_maxima")
+    left = body.index("return false")
+    wrote = body.rindex("block[k] =", 0, left)
+    assert body.count("return false") == 1
+    assert "__syncwarp()" in body[wrote:left]
