@@ -230,6 +230,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int pages = __reduce_max_sync(0xffffffffu, tail->seg[i & 1].n1 - tail->seg[i & 1].n0);
       if (ntok == 0) break;
       ok = wait(&tail->q_full[i & 1], (i >> 1) & 1);
+      // Behind a unit of two halves, the pages of a unit of one: nothing else holds them back
+      // until the other half's warps have read their last pair and its factors, whose places
+      // (and phases) come round.
+      if (ok && ntok <= kHalfTokens && n_1 > 0) ok = wait(&tail->s_empty[1], (n_1 - 1) & 1);
       for (int x = 0; x < pages && ok; x += 2) {
         const uint32_t idesc = x + 1 < pages ? tc::idesc_e4m3_f32(128, 2 * kPage) : tc::idesc_e4m3_f32(128, kPage);
         ok = wait(&tail->k_full[s], k_par);
@@ -329,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float keep = 0.f;                   // the score of block n with n % 16 == lane % 16
       for (int n = sg.n0 + pg; n < sg.n1 + pg; n += 2, ++t, ++mine) {
         // (the products first: a half that skipped units may be many pages early, and
-        // info_full's phases come round)
+        // info_full's phases come round; it is never late, see the products)
         ok = wait_for(&tail->s_full[h], mine & 1) && wait_for(&tail->info_full[t % kInfo], (t / kInfo) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;

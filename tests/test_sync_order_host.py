@@ -48,3 +48,14 @@ def test_scratch_of_a_given_up_row_is_ordered():
     wrote = body.rindex("block[k] =", 0, left)
     assert body.count("return false") == 1
     assert "__syncwarp()" in body[wrote:left]
+
+
+def test_scorer_waits_for_the_half_that_a_unit_leaves_out():
+    """A unit of at most eight tokens uses one half of the tile; its pages' factors take the
+    places of those that the other half's warps may still be reading, unless the products
+    wait until these have handed back their last pair."""
+    body = function(source("msa_score_prefill.cu"), "score_prefill_kernel")
+    unit = body[body.index("tail->q_full[i & 1], (i >> 1) & 1"):]
+    before = unit[:unit.index("x < pages")]
+    assert re.search(r"ntok <= kHalfTokens[^;]*n_1 > 0[^;]*wait\(&tail->s_empty\[1\], \(n_1 - 1\) & 1\)",
+                     before)
