@@ -353,11 +353,14 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster)
     c[2] = 0;
   }
   cluster_sync();
+  // (what is read back is checked: outputs that share memory must not lead out of the pool)
+  unsigned bad = 0;
   for (int k = t; k < moves; k += threads) {
     const int32_t* c = p.copies + 3 * static_cast<int64_t>(k);
-    p.refs_out[__ldcg(c + 1)] = p.refs[__ldcg(c)];
+    const int src = __ldcg(c), dst = __ldcg(c + 1);
+    if (src >= 0 && src < p.num_blocks && dst >= 0 && dst < p.num_blocks) p.refs_out[dst] = p.refs[src];
+    else bad |= MSA_ERR_REFS;
   }
-  unsigned bad = 0;
   const int warps = threads / 32;
   for (int b = t / 32; b < p.B; b += warps) {
     bool seq = false;
@@ -375,7 +378,13 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster)
           bad |= MSA_ERR_REFS;
           page = -1;
         } else if (page >= live) {
-          page = __ldcg(p.copies + 3 * static_cast<int64_t>(__ldcg(p.refs_out + page)) + 1);
+          const int k = __ldcg(p.refs_out + page);
+          if (k >= 0 && k < moves) {
+            page = __ldcg(p.copies + 3 * static_cast<int64_t>(k) + 1);
+          } else {
+            bad |= MSA_ERR_REFS;
+            page = -1;
+          }
         }
       }
       p.table_out[row + e] = page;

@@ -731,7 +731,8 @@ int msa_copy_pages(const int32_t *copies, int n, int64_t num_blocks, const msa_c
  *   seq_lens_out [rows], refs_out [num_blocks]   (a page nobody holds: 0)
  *   copies [rows, 3]            row b's copy as msa_copy_pages takes it, or (-1, -1, 0)
  * With caches the copies are made by this call too.  The inputs are only read,
- * and outputs must not overlap them.
+ * and outputs must not overlap them, each other or the caches (the last two are not
+ * looked for here, and give results without meaning).
  * Errors: MSA_EINVAL for B or rows outside 0 .. 8192, S < 1, sizes past 2^31 - 1,
  * null or misaligned pointers (an input of no rows may be null), an output that
  * overlaps an input, bad caches.  Device: MSA_ERR_NO_PAGES (more pages needed than free:
@@ -756,7 +757,7 @@ int msa_fork_pages(const int32_t *block_table, const int32_t *seq_lens, const in
  * order, 128 token rows each, then (-1, -1, 0): whoever else holds pages finds their
  * new places there.  With caches the moves are made by this call too (the bytes of a
  * page that moved away are left as they were).  The inputs are only read, and
- * outputs must not overlap them.
+ * outputs must not overlap them, each other or the caches, as in msa_fork_pages.
  * Errors: MSA_EINVAL for B < 0, S < 1, sizes past 2^31 - 1, null or misaligned
  * pointers (tables of no rows may be null), an output that overlaps an input, bad
  * caches.
