@@ -63,9 +63,17 @@ def _lib():
 
 
 def _stream(device: torch.device, stream) -> int:
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    """The handle of the stream of a call on tensors of `device`.  The library launches on the
+    current device, so that has to be theirs."""
+    index = device.index
+    if index != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on {device}, which is not the current device: call "
+                         f"under torch.cuda.device({index})")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    if stream.device_index != index:
+        raise ValueError(f"the stream is not one of {device}")
+    return stream.cuda_stream
 
 
 def _own(shape, dtype, device, stream):

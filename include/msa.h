@@ -34,6 +34,8 @@
  *  - Every call only enqueues work on `stream` (a cudaStream_t; NULL is the
  *    legacy default stream) and returns without waiting.  No call
  *    synchronises the host except msa_get_error.
+ *  - Kernels are launched on the current device: it has to be the one of the
+ *    pointers and of `stream`.
  *  - Stream order: by default each call's work starts only after all work
  *    enqueued earlier on `stream` has completed, so its inputs may be written
  *    by any kernel or copy just before it.  Inside one call (and inside
