@@ -904,6 +904,10 @@ bool overlap(std::initializer_list<Ints> outs, std::initializer_list<Ints> ins) 
   return false;
 }
 
+// Entries of a table of the calls on pages: their kernels count rows and columns in 32 bits, by
+// up to a cluster's 8192 threads a step.
+constexpr int64_t kMaxTable = INT_MAX - 8192;
+
 // The copies of a fork or a compaction, or the caller's own, over all of its caches.
 int check_caches(const msa_cache_t* caches, int num_caches) {
   if (num_caches < 0 || (num_caches > 0 && !caches)) return MSA_EINVAL;
@@ -1030,7 +1034,7 @@ int msa_fork_pages(const int32_t* block_table, const int32_t* seq_lens, const in
                    int S, int64_t num_blocks, const msa_cache_t* caches, int num_caches,
                    msa_stream_t stream) {
   if (B < 0 || B > msa::kMaxForkRows || rows < 0 || rows > msa::kMaxForkRows || S < 1 ||
-      static_cast<int64_t>(B > rows ? B : rows) * S > INT_MAX || num_blocks < 1 || num_blocks > INT_MAX)
+      static_cast<int64_t>(B > rows ? B : rows) * S > kMaxTable || num_blocks < 1 || num_blocks > INT_MAX)
     return MSA_EINVAL;
   int st = check_caches(caches, num_caches);
   if (st != MSA_OK) return st;
@@ -1064,7 +1068,7 @@ int msa_compact_pages(const int32_t* block_table, const int32_t* seq_lens, const
                       int32_t* block_table_out, int32_t* refs_out, int32_t* copies, int B, int S,
                       int64_t num_blocks, const msa_cache_t* caches, int num_caches,
                       msa_stream_t stream) {
-  if (B < 0 || S < 1 || static_cast<int64_t>(B) * S > INT_MAX || num_blocks < 1 || num_blocks > INT_MAX)
+  if (B < 0 || S < 1 || static_cast<int64_t>(B) * S > kMaxTable || num_blocks < 1 || num_blocks > INT_MAX)
     return MSA_EINVAL;
   int st = check_caches(caches, num_caches);
   if (st != MSA_OK) return st;

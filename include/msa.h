@@ -735,7 +735,8 @@ int msa_copy_pages(const int32_t *copies, int n, int64_t num_blocks, const msa_c
  * With caches the copies are made by this call too.  The inputs are only read,
  * and outputs must not overlap them, each other or the caches (the last two are not
  * looked for here, and give results without meaning).
- * Errors: MSA_EINVAL for B or rows outside 0 .. 8192, S < 1, sizes past 2^31 - 1,
+ * Errors: MSA_EINVAL for B or rows outside 0 .. 8192, S < 1, tables of more than 2^31 -
+ * 8193 entries, more than 2^31 - 1 pages,
  * null or misaligned pointers (an input of no rows may be null), an output that
  * overlaps an input, bad caches.  Device: MSA_ERR_NO_PAGES (more pages needed than free:
  * nothing is forked; every new row is empty, its table -1, its length 0, refs_out
@@ -760,7 +761,7 @@ int msa_fork_pages(const int32_t *block_table, const int32_t *seq_lens, const in
  * new places there.  With caches the moves are made by this call too (the bytes of a
  * page that moved away are left as they were).  The inputs are only read, and
  * outputs must not overlap them, each other or the caches, as in msa_fork_pages.
- * Errors: MSA_EINVAL for B < 0, S < 1, sizes past 2^31 - 1, null or misaligned
+ * Errors: MSA_EINVAL for B < 0, S < 1, sizes as msa_fork_pages, null or misaligned
  * pointers (tables of no rows may be null), an output that overlaps an input, bad
  * caches.
  * Device: MSA_ERR_SEQ_RANGE (a row's length outside 0 .. 128 S: taken as 0),
