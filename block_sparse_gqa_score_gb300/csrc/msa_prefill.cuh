@@ -15,6 +15,7 @@
 
 #include "msa_device.cuh"
 #include "msa_launch.h"
+#include "msa_tcgen05.cuh"
 
 namespace msa {
 namespace prefill {
@@ -30,11 +31,6 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, unsigned parity) {
   while (!mbar_try_wait_sleep(bar, parity, 1000000u))
     if (global_ns() - t0 > kWaitLimitNs) return false;
   return true;
-}
-
-// Makes generic-proxy shared-memory writes visible to the tensor core.
-__device__ __forceinline__ void fence_proxy_async() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
 // A request's query tokens, and whether they can be worked on.
@@ -375,7 +371,7 @@ __device__ __forceinline__ bool load_query_tile(const PrefillParams& p, const Se
       }
     }
   }
-  fence_proxy_async();
+  tc::fence_proxy_async_smem();   // read by the tensor core
   __syncwarp();
   return true;
 }
