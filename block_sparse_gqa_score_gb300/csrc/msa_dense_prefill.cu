@@ -45,9 +45,11 @@
 // work on is merged by a second kernel from their parts, in the order of the pages.
 //
 // Measured, 64/4 heads: four chunks of up to 1k tokens over 4k .. 16k 678 us (1455 TFLOP/s),
-// with an fp8 query 638; one chunk of 1.4k tokens over 128k on one KV head with page scales
-// 741 us (1515 TFLOP/s); eight prompts of 1k 212 us; two chunks of 24 tokens over 2k .. 3k on
-// one KV head 22.3 us, a third of it the launches, the first tiles and the merge.
+// with an fp8 query 635 (the products of both need 512 and 384); one chunk of 1050 tokens over
+// 128k on one KV head with page scales 741 us (1515 TFLOP/s); eight prompts of 1024 tokens 241 us
+// (72: units of 4.5 pages, whose query tiles, outputs and masked last pages take longer than the
+// pages); two chunks of 18 and 27 tokens over 2k .. 3k on one KV head 22.4 us, at most two
+// pages a CTA and the rest latency: two launches, the first tiles, each loop's first run, the merge.
 // A page takes some 2950 cycles, of which the products alone need 2250 (2048 at the tensor
 // core's rate): the rest is the round of one half, S 900 cycles, softmax 1300 (the two halves'
 // warps share the issue slots), P handed on 300, O 500, of which the other half's products

@@ -19,11 +19,13 @@
 // CTA an SM, each an equal share of all pages (msa_prefill.cuh); the next unit's query tile
 // is prepared while the current one is worked on.
 // Measured: four chunks of up to 1k tokens over 4k .. 16k, 64/4 heads, page scales 252 us,
-// 1950 TFLOP/s (the tensor core is active in 87 % of the cycles); an fp8 query of 200 tokens, K-only
-// cache, 46 us (1590 TFLOP/s); eight prompts of 1k 113 us (scores are written at 0.9 TB/s, and
-// units of some five pages pay for their query tiles); three chunks of 40 tokens on one KV
-// head 13.6 us, of which 2 are products.  With the query tiles' split in line (118 KiB of code,
-// the warps waited for instructions) the four chunks took 277 us.
+// 1950 TFLOP/s (the tensor core is active in 87 % of the cycles); with an fp8 query on a K-only
+// cache 196 us (its products need 128: each half's search, four loads from tensor memory in turn,
+// is no longer hidden behind them); four chunks of some 200 tokens over 2k .. 8k on it 35.6 us (16),
+// with a bf16 query 49.5 (32); eight prompts of 1024 tokens 114 us (36: units of 4.5 pages pay
+// for their query tiles); three chunks of some 40 tokens on one KV head 13.7 us, of which 2 are
+// products.  With the query tiles' split in line (118 KiB of code, the warps waited for
+// instructions) the four chunks took 277 us.
 //   warp 0       page look-ups, TMA of K tiles
 //   warp 1       products (owns tensor memory)
 //   warps 2, 3   segments and query tiles, a token each in turn (behind a short unit: warps

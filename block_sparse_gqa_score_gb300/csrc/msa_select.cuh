@@ -1,6 +1,6 @@
 // msa_select.cuh -- the block selector of one (token, KV head) row, run by
-// one warp; used by the selector kernel and by the attend kernel's fused
-// select-then-attend mode.
+// one warp; used by the attend kernels' fused select-then-attend modes, and by the
+// selector kernel for rows that its own way leaves over.
 //
 // Keep the current block cur = pos/128 and the 15 best earlier blocks in the
 // order (score descending, block index ascending); the kept ids come out

@@ -8,17 +8,20 @@
 // scorer's [head, token, block] buffer through a transposed view.  One warp
 // per row.
 //
-// What bounds it: the issue slots, some 600 instructions a row (its scores are a few hundred
+// What bounds it: the issue slots, some 720 instructions a row (its scores are a few hundred
 // floats).  The kept blocks are found from the lanes' own maxima: L, the 15th largest of
 // the 32, has at least 15 scores at or above it, and few are above it (some 20 of 256
 // random ones).  If fewer than 15 are, they are kept with the first scores equal to L; else
 // the 15 are chosen among them alone, each compared with all of them in shared memory.  A row
 // with more than 64 scores above L (they would have to lie in few lanes) is left to the search
 // of msa_select.cuh.  Rows of up to 2048 blocks are held in registers, longer ones read again.
-// 5980 tokens of 4 heads over up to 512 blocks: 18 us, 1.4 TB/s of scores.  (A search bit by
-// bit, 31 rounds of a count over the warp, took 83 us; several heads of a token in one warp,
-// with the next row's scores on their way, was slower.)  A decode step's 256 rows of 2048
-// blocks 7.5 us (bit by bit 31), 32 rows of 4096 13.5 (98).
+// 5999 tokens of 4 heads over up to 512 blocks: 18.6 us, 1.4 TB/s of scores; the same rows in
+// a table of more than 512 columns, which the long form takes, 29.8; over 1024 .. 2048 blocks
+// 91.8.  (A search bit by bit, 31 rounds of a count over the warp, took 83 us for the first;
+// several heads of a token in one warp, with the next row's scores on their way, was slower.)
+// A decode step's 256 rows of 2000 blocks 7.6 us (bit by bit 31), 32 rows of 4000 13.3 (106);
+// rows whose best scores all lie in three lanes, which are searched after all, 31.8 and 126
+// (31 and 116).
 #include "msa_device.cuh"
 #include "msa_launch.h"
 #include "msa_select.cuh"
@@ -166,8 +169,8 @@ __device__ __forceinline__ bool select_by_maxima(const float* __restrict__ srow,
 }
 
 // kVarlen: a prefill-style batch, the tokens' requests looked up in cu_q.  kLong: rows may
-// have more than kShort blocks; without it a warp has 64 registers and 2 KiB, with it 168 and
-// 8 KiB, and the GPU holds half as many.
+// have more than kShort blocks; without it a thread has 48 or 56 registers and a warp 4 KiB,
+// with it 154 and 8 KiB, and an SM holds 12 warps in place of 36.
 template <bool kVarlen, bool kLong>
 __global__ void __launch_bounds__(kWarps * 32) topk_kernel(const TopkParams p) {
   constexpr int kCache = kLong ? 2048 : 1024;     // words of shared memory a warp
