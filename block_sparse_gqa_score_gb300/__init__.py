@@ -809,29 +809,16 @@ def _int32(t, name: str, shape, dev):
     raise ValueError(f"{name} must be " + ("a vector" if shape is None else str(list(shape))))
 
 
-def _apart(spans):
-    """Raises where two of the outputs [(first byte, past the last, name)] share memory."""
-    end = 0
-    for span in sorted(spans):
-        if span[0] < end:
-            raise ValueError(f"{name} and {span[2]} share memory")
-        _, end, name = span
-
-
 def _outputs(given, dev, stream):
     """Tensors and addresses of the outputs [(tensor or None, name, shape)]."""
-    out, at, spans = [], [], []
+    out, at = [], []
     for t, name, shape in given:
         if t is None:
             t = _empty(shape, torch.int32, dev, stream)
             at.append(t.data_ptr())
         else:
-            a = _int32(t, name, shape, dev)
-            at.append(a)
-            spans.append((a, a + t.nbytes, name))      # (0, 0) of an empty tensor
+            at.append(_int32(t, name, shape, dev))
         out.append(t)
-    if len(spans) > 1:
-        _apart(spans)
     return out, at
 
 

@@ -904,6 +904,26 @@ bool overlap(std::initializer_list<Ints> outs, std::initializer_list<Ints> ins) 
   return false;
 }
 
+// Whether outputs share memory with each other, or any of the arrays with a cache, whose bytes
+// the copies write.
+bool arrays_meet(std::initializer_list<Ints> outs, std::initializer_list<Ints> ins,
+                 const msa_cache_t* caches, int num_caches, int64_t num_blocks) {
+  for (const Ints* a = outs.begin(); a != outs.end(); ++a)
+    for (const Ints* b = outs.begin(); b != a; ++b)
+      if (overlap({*a}, {*b})) return true;
+  for (int c = 0; c < num_caches; ++c) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(caches[c].base);
+    const uintptr_t hi = lo + static_cast<uintptr_t>(num_blocks) * caches[c].units * caches[c].rows *
+                                  static_cast<uintptr_t>(caches[c].row_bytes);
+    for (const auto& list : {outs, ins})
+      for (const Ints& x : list) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(x.at);
+        if (x.at && x.n > 0 && at < hi && lo < at + 4 * static_cast<uintptr_t>(x.n)) return true;
+      }
+  }
+  return false;
+}
+
 // Entries of a table of the calls on pages: their kernels count rows and columns in 32 bits, by
 // up to a cluster's 8192 threads a step.
 constexpr int64_t kMaxTable = INT_MAX - 8192;
@@ -1050,11 +1070,14 @@ int msa_fork_pages(const int32_t* block_table, const int32_t* seq_lens, const in
                         static_cast<const void*>(copies)})
     if (!aligned(x, 4)) return MSA_EINVAL;
   const int64_t in = static_cast<int64_t>(B) * S, out = static_cast<int64_t>(rows) * S;
-  if (overlap({{block_table_out, out}, {seq_lens_out, rows}, {refs_out, num_blocks}, {copies, 3 * int64_t{rows}}},
-              {{block_table, in}, {seq_lens, B}, {parents, rows}, {grow, rows}, {refs, num_blocks}}))
-    return MSA_EINVAL;
+  const std::initializer_list<Ints> outs = {{block_table_out, out}, {seq_lens_out, rows},
+                                            {refs_out, num_blocks}, {copies, 3 * int64_t{rows}}};
+  const std::initializer_list<Ints> ins = {{block_table, in}, {seq_lens, B}, {parents, rows},
+                                           {grow, rows}, {refs, num_blocks}};
+  if (overlap(outs, ins)) return MSA_EINVAL;
   DeviceState* dev;
   if ((st = device_state(&dev)) != MSA_OK) return st;
+  if (arrays_meet(outs, ins, caches, num_caches, num_blocks)) return MSA_EINVAL;
   const msa::ForkParams p{block_table,  seq_lens, parents, grow, refs, block_table_out,
                           seq_lens_out, refs_out, copies,  dev->err, B, rows, S,
                           static_cast<int>(num_blocks)};
@@ -1080,11 +1103,13 @@ int msa_compact_pages(const int32_t* block_table, const int32_t* seq_lens, const
                         static_cast<const void*>(refs_out), static_cast<const void*>(copies)})
     if (!aligned(x, 4)) return MSA_EINVAL;
   const int64_t table = static_cast<int64_t>(B) * S;
-  if (overlap({{block_table_out, table}, {refs_out, num_blocks}, {copies, 3 * (num_blocks / 2)}},
-              {{block_table, table}, {seq_lens, B}, {refs, num_blocks}}))
-    return MSA_EINVAL;
+  const std::initializer_list<Ints> outs = {{block_table_out, table}, {refs_out, num_blocks},
+                                            {copies, 3 * (num_blocks / 2)}};
+  const std::initializer_list<Ints> ins = {{block_table, table}, {seq_lens, B}, {refs, num_blocks}};
+  if (overlap(outs, ins)) return MSA_EINVAL;
   DeviceState* dev;
   if ((st = device_state(&dev)) != MSA_OK) return st;
+  if (arrays_meet(outs, ins, caches, num_caches, num_blocks)) return MSA_EINVAL;
   const msa::CompactParams p{block_table, seq_lens, refs, block_table_out, refs_out, copies,
                              dev->err, B, S, static_cast<int>(num_blocks)};
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -1102,6 +1127,7 @@ int msa_copy_pages(const int32_t* copies, int n, int64_t num_blocks, const msa_c
   if (st != MSA_OK || n == 0 || num_caches == 0) return st;
   DeviceState* dev;
   if ((st = device_state(&dev)) != MSA_OK) return st;
+  if (arrays_meet({}, {{copies, 3 * int64_t{n}}}, caches, num_caches, num_blocks)) return MSA_EINVAL;
   const bool overlap = input_overlap();
   return enqueue_copies(copies, n, caches, num_caches, num_blocks, *dev,
                         reinterpret_cast<cudaStream_t>(stream), overlap, overlap);

@@ -705,8 +705,9 @@ typedef struct msa_cache {
  * rows) each: the first `token rows` rows of the page's units, and the whole of
  * caches with rows 1, to the destination, in every cache given.  (-1, -1, x) is no
  * copy, nor is 0 token rows.  No page may be the destination of two copies, or of one and the
- * source of another.  Errors: MSA_EINVAL for bad sizes or caches (above).  Device:
- * MSA_ERR_PAGE_RANGE (a page outside the pool, or rows outside 0 .. 128: skipped).
+ * source of another.  Errors: MSA_EINVAL for bad sizes or caches (above), or
+ * copies that overlap a cache.  Device: MSA_ERR_PAGE_RANGE (a page outside the pool, or
+ * rows outside 0 .. 128: skipped).
  */
 int msa_copy_pages(const int32_t *copies, int n, int64_t num_blocks, const msa_cache_t *caches,
                    int num_caches, msa_stream_t stream);
@@ -733,12 +734,11 @@ int msa_copy_pages(const int32_t *copies, int n, int64_t num_blocks, const msa_c
  *   seq_lens_out [rows], refs_out [num_blocks]   (a page nobody holds: 0)
  *   copies [rows, 3]            row b's copy as msa_copy_pages takes it, or (-1, -1, 0)
  * With caches the copies are made by this call too.  The inputs are only read,
- * and outputs must not overlap them, each other or the caches (the last two are not
- * looked for here, and give results without meaning).
+ * and outputs must not overlap them or each other, nor any of these the caches.
  * Errors: MSA_EINVAL for B or rows outside 0 .. 8192, S < 1, tables of more than 2^31 -
  * 8193 entries, more than 2^31 - 1 pages,
- * null or misaligned pointers (an input of no rows may be null), an output that
- * overlaps an input, bad caches.  Device: MSA_ERR_NO_PAGES (more pages needed than free:
+ * null or misaligned pointers (an input of no rows may be null), arrays that overlap
+ * so, bad caches.  Device: MSA_ERR_NO_PAGES (more pages needed than free:
  * nothing is forked; every new row is empty, its table -1, its length 0, refs_out
  * equals refs), MSA_ERR_ROW_RANGE (a parent outside -1 .. B - 1: the row is
  * empty), MSA_ERR_SEQ_RANGE (a parent's length outside 0 .. 128 S: taken as 0;
@@ -759,11 +759,10 @@ int msa_fork_pages(const int32_t *block_table, const int32_t *seq_lens, const in
  * row's last page), refs_out the counts, copies [num_blocks / 2, 3] the moves in
  * order, 128 token rows each, then (-1, -1, 0): whoever else holds pages finds their
  * new places there.  With caches the moves are made by this call too (the bytes of a
- * page that moved away are left as they were).  The inputs are only read, and
- * outputs must not overlap them, each other or the caches, as in msa_fork_pages.
+ * page that moved away are left as they were).  The inputs are only read; what must not
+ * overlap is as in msa_fork_pages.
  * Errors: MSA_EINVAL for B < 0, S < 1, sizes as msa_fork_pages, null or misaligned
- * pointers (tables of no rows may be null), an output that overlaps an input, bad
- * caches.
+ * pointers (tables of no rows may be null), arrays that overlap so, bad caches.
  * Device: MSA_ERR_SEQ_RANGE (a row's length outside 0 .. 128 S: taken as 0),
  * MSA_ERR_PAGE_RANGE, MSA_ERR_REFS (an entry outside the pool, or a page counted
  * as free: -1 in the new table).
