@@ -13,6 +13,8 @@ import block_sparse_gqa_score_gb300 as msa
 @pytest.fixture
 def two_devices(monkeypatch):
     now = [0]
+    monkeypatch.setattr(torch.cuda, "device_count", lambda: 2)
+    monkeypatch.setattr(msa, "_devices", 0)
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: now[0], raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 100 + i, raising=False)
     return now
