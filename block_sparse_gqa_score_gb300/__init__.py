@@ -86,7 +86,7 @@ def _own(shape, dtype, device, stream):
     """A buffer that only a call's kernels use, memory of their stream (None: the current
     one): nothing that is still queued on another stream can write to it, and it goes to
     others of that stream alone."""
-    if stream is None:
+    if stream is None or stream == torch.cuda.current_stream(device):
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
@@ -846,8 +846,8 @@ def fork_pages(block_table, seq_lens, parents, refs, caches=(), grow=None, block
     for grow[b] more tokens; rows without a child are freed.  Full pages are shared, a
     begun page goes to the first child (where nobody else holds it) and is copied for
     the others, in every tensor of `caches` (kv [NB, Hkv, 128, 256], K-only caches, page
-    scales, of any number of layers).  refs [NB]: how many rows hold each page; free pages (0) are taken in
-    ascending order.  Returns (block_table, seq_lens, refs, copies [rows, 3])."""
+    scales, of any number of layers).  refs [NB]: how many rows hold each page; free
+    pages (0) are taken in ascending order.  Returns (block_table, seq_lens, refs, copies [rows, 3])."""
     dev, B, S, NB, table, lens, counts = _table(block_table, seq_lens, refs)
     follows = _int32(parents, "parents", None, dev)
     rows = parents.shape[0]

@@ -727,20 +727,19 @@ int msa_copy_pages(const int32_t *copies, int n, int64_t num_blocks, const msa_c
  * row, a prefix cache), who goes on reading it; every other child, and that one then,
  * gets a page of its own and a copy of the rows that are filled.  So a new row's begun
  * page is its own, and what it appends reaches nobody else.  (A kept prefix is taken
- * over by a parent: give it a row of block_table.)  The pages needed, in the order of the new
- * rows and of their entries, are the free ones (refs 0) in ascending order; pages
- * that this call frees are free from the next call on.
+ * over by a parent: give it a row of block_table.)  The pages needed, in the order of
+ * the new rows and of their entries, are the free ones (refs 0) in ascending order;
+ * pages that this call frees are free from the next call on.
  *   block_table_out [rows, S]   -1 behind a row's last page
  *   seq_lens_out [rows], refs_out [num_blocks]   (a page nobody holds: 0)
  *   copies [rows, 3]            row b's copy as msa_copy_pages takes it, or (-1, -1, 0)
  * With caches the copies are made by this call too.  The inputs are only read,
  * and outputs must not overlap them or each other, nor any of these the caches.
- * Errors: MSA_EINVAL for B or rows outside 0 .. 8192, S < 1, tables of more than 2^31 -
- * 8193 entries, more than 2^31 - 1 pages,
- * null or misaligned pointers (an input of no rows may be null), arrays that overlap
- * so, bad caches.  Device: MSA_ERR_NO_PAGES (more pages needed than free:
- * nothing is forked; every new row is empty, its table -1, its length 0, refs_out
- * equals refs), MSA_ERR_ROW_RANGE (a parent outside -1 .. B - 1: the row is
+ * Errors: MSA_EINVAL for B or rows outside 0 .. 8192, S < 1, tables of more than
+ * 2^31 - 8193 entries, more than 2^31 - 1 pages, null or misaligned pointers (an input
+ * of no rows may be null), arrays that overlap so, bad caches.
+ * Device: MSA_ERR_NO_PAGES (more pages needed than free: nothing is forked; every new
+ * row is empty, its table -1, its length 0, refs_out equals refs), MSA_ERR_ROW_RANGE (a parent outside -1 .. B - 1: the row is
  * empty), MSA_ERR_SEQ_RANGE (a parent's length outside 0 .. 128 S: taken as 0;
  * growth below 0 or past 128 S: taken as 0), MSA_ERR_PAGE_RANGE (an entry outside
  * the pool: -1 in the new row, or a page without the copy), MSA_ERR_REFS (a page of a row whose count
